@@ -9,7 +9,8 @@ Entry points (same names as the C ABI, without the ``ep_`` prefix):
 ``dispatch_layout``, ``dispatch_layout_routed``, ``dispatch_layout_noalloc``, ``dispatch_nvfp4``,
 ``dispatch_layout_nvfp4``, ``dispatch_layout_padded_nvfp4``, ``dispatch_bf16``, ``dispatch_fp8``, ``combine``, ``combine_bwd``,
 ``dispatch_bwd``, ``routing_map_to_topk``, ``indices_to_multihot``, ``rows_max``,
-``read_status``, ``cvt_e2m1``, ``cvt_e4m3``.
+``read_status``, ``cvt_e2m1``, ``cvt_e4m3``; around the dispatch: ``layer_norm``, ``layer_norm_bwd``,
+``router_topk``, ``router_topk_bwd`` and ``expert_matvec``.
 """
 from __future__ import annotations
 
@@ -35,6 +36,8 @@ NOALLOC_WORKSPACE_BYTES = 1 << 20
 STATUS_OVERFLOW = 1
 STATUS_BAD_EXPERT = 2
 STATUS_BOUNDS = 8
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # ep_dtype_t
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 class EPError(RuntimeError):
@@ -65,6 +68,7 @@ class _Layout(ctypes.Structure):
 
 
 _P, _I, _L, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_long, ctypes.c_size_t
+_LL, _F = ctypes.c_longlong, ctypes.c_float
 _LP = ctypes.POINTER(_Layout)
 
 # name -> (restype, argtypes); must match include/ep.h
@@ -85,6 +89,12 @@ SIGNATURES = {
     "ep_combine": (_I, [_P, _P, _I, _LP, _P, _P]),
     "ep_combine_bwd": (_I, [_P, _P, _P, _I, _LP, _P, _P, _P]),
     "ep_dispatch_bwd": (_I, [_P, _I, _LP, _P, _P]),
+    "ep_layer_norm": (_I, [_P, _LL, _I, _P, _P, _I, _I, _I, _F, _I, _P, _P, _P, _P]),
+    "ep_layer_norm_bwd_workspace_bytes": (_Z, [_I, _I]),
+    "ep_layer_norm_bwd": (_I, [_P, _LL, _P, _LL, _I, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
+    "ep_router_topk": (_I, [_P, _LL, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "ep_router_topk_bwd": (_I, [_P, _P, _LL, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P]),
+    "ep_expert_matvec": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _LP, _P, _P]),
     "ep_read_status": (_I, [_LP, _P, ctypes.POINTER(ctypes.c_int32)]),
     "ep_strerror": (ctypes.c_char_p, [_I]),
     "ep_cvt_e2m1": (_I, [_P, _P, _L, _P]),
@@ -549,6 +559,171 @@ def dispatch_bwd(grad_rows: torch.Tensor, L: Layout, out: torch.Tensor | None = 
         out = torch.empty(max(L.T, 1), H, dtype=torch.bfloat16, device=grad_rows.device)
     _need(out, L.T, H, _BF16, "grad_input")
     _check(_lib.ep_dispatch_bwd(_bits(grad_rows), H, L.ref, _bits(out), _stream(stream)), "ep_dispatch_bwd")
+    return out
+
+
+def _matrix(t: torch.Tensor, what: str):
+    """Pointer, row stride and element type of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a 2-D tensor, got {tuple(t.shape)}")
+    if t.dtype not in DTYPES:
+        raise TypeError(f"{what}: dtype {t.dtype} not in {tuple(DTYPES)}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    rows, cols = t.shape
+    stride, step = t.stride()
+    if rows <= 1:
+        stride = cols
+    if (cols > 1 and step != 1) or stride < cols:
+        raise ValueError(f"{what}: rows must be contiguous and not overlap, got strides {t.stride()}")
+    return t.data_ptr(), stride, DTYPES[t.dtype]
+
+
+def _vector(t: torch.Tensor, n: int, dtypes, what: str):
+    """Pointer of a contiguous CUDA tensor [n]."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: dtype {t.dtype} not in {dtypes}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{what}: expected [{n}], got {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _dense(t: torch.Tensor, rows: int, cols: int, dtype: torch.dtype, what: str):
+    """Pointer of a contiguous CUDA tensor [rows, cols]."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype} is not {dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what}: expected {(rows, cols)}, got {tuple(t.shape)}")
+    return _ptr(t)
+
+
+_F32 = (torch.float32,)
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5,
+               rms: bool = False, out=None, stream=None):
+    """ep_layer_norm -> (y [T, H] in x's dtype, mean fp32 [T] or None when rms, rstd fp32 [T]).
+
+    x [T, H] bf16 / fp16 / fp32 (rows may have a stride); weight and bias [H] in x's dtype or
+    fp32.  ``out``: the three buffers."""
+    px, ld, dt = _matrix(x, "x")
+    T, H = x.shape
+    params = (x.dtype, torch.float32)
+    pw = _vector(weight, H, params, "weight")
+    pb = None if bias is None else _vector(bias, H, (weight.dtype,), "bias")
+    if out is None:
+        f32 = dict(dtype=torch.float32, device=x.device)
+        out = (torch.empty(T, H, dtype=x.dtype, device=x.device), None if rms else torch.empty(T, **f32),
+               torch.empty(T, **f32))
+    y, mean, rstd = out
+    rc = _lib.ep_layer_norm(px, ld, dt, pw, pb, DTYPES[weight.dtype], T, H, eps, int(bool(rms)),
+                            _dense(y, T, H, x.dtype, "y"), None if rms else _vector(mean, T, _F32, "mean"),
+                            _vector(rstd, T, _F32, "rstd"), _stream(stream))
+    _check(rc, "ep_layer_norm")
+    return y, None if rms else mean, rstd
+
+
+def layer_norm_bwd_workspace_bytes(T: int, H: int) -> int:
+    """ep_layer_norm_bwd_workspace_bytes: scratch bytes of ``layer_norm_bwd``."""
+    n = int(_lib.ep_layer_norm_bwd_workspace_bytes(T, H))
+    if n == 0:
+        raise EPError(EP_ERR_INVALID_ARG, "layer_norm_bwd sizes")
+    return n
+
+
+def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | None,
+                   rstd: torch.Tensor, rms: bool = False, bias: bool = False, out=None,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """ep_layer_norm_bwd -> (grad_x [T, H] in x's dtype, grad_weight fp32 [H], grad_bias fp32 [H] or
+    None without ``bias``).  mean (None when rms) and rstd come from ``layer_norm``.  ``workspace``: a
+    uint8 buffer of ``layer_norm_bwd_workspace_bytes`` to reuse."""
+    px, ldx, dt = _matrix(x, "x")
+    T, H = x.shape
+    pg, ldg, gdt = _matrix(grad_y, "grad_y")
+    if grad_y.shape != x.shape or gdt != dt:
+        raise ValueError("grad_y and x differ in shape or dtype")
+    pw = _vector(weight, H, (x.dtype, torch.float32), "weight")
+    if out is None:
+        f32 = dict(dtype=torch.float32, device=x.device)
+        out = (torch.empty(T, H, dtype=x.dtype, device=x.device), torch.empty(H, **f32),
+               torch.empty(H, **f32) if bias else None)
+    if workspace is None:
+        workspace = torch.empty(layer_norm_bwd_workspace_bytes(T, H), dtype=torch.uint8, device=x.device)
+    dx, dw, db = out
+    rc = _lib.ep_layer_norm_bwd(pg, ldg, px, ldx, dt, pw, DTYPES[weight.dtype],
+                                None if rms else _vector(mean, T, _F32, "mean"), _vector(rstd, T, _F32, "rstd"), T, H,
+                                int(bool(rms)), _dense(dx, T, H, x.dtype, "grad_x"), _vector(dw, H, _F32, "grad_weight"),
+                                _vector(db, H, _F32, "grad_bias") if bias else None, _ptr(workspace),
+                                workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "ep_layer_norm_bwd")
+    return dx, dw, db if bias else None
+
+
+def _score(score: str) -> int:
+    if score not in SCORES:
+        raise ValueError(f"score {score!r} not in {tuple(SCORES)}")
+    return SCORES[score]
+
+
+def router_topk(logits: torch.Tensor, K: int, bias: torch.Tensor | None = None, score: str = "softmax",
+                renormalize: bool = True, scale: float = 1.0, out=None, stream=None):
+    """ep_router_topk -> (topk_ids int32 [T, K], probs fp32 [T, K]) from logits [T, E] bf16 / fp16 /
+    fp32 (rows may have a stride): the K largest of logit + bias (fp32 [E]), ties to the lower id; -1
+    with probability 0 where only -inf is left."""
+    pl, ld, dt = _matrix(logits, "logits")
+    T, E = logits.shape
+    if out is None:
+        out = (torch.empty(T, K, dtype=torch.int32, device=logits.device),
+               torch.empty(T, K, dtype=torch.float32, device=logits.device))
+    ids, probs = out
+    rc = _lib.ep_router_topk(pl, ld, dt, None if bias is None else _vector(bias, E, _F32, "bias"), T, E, K,
+                             _score(score), int(bool(renormalize)), scale, _dense(ids, T, K, torch.int32, "topk_ids"),
+                             _dense(probs, T, K, torch.float32, "probs"), _stream(stream))
+    _check(rc, "ep_router_topk")
+    return ids, probs
+
+
+def router_topk_bwd(grad_probs: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor, score: str = "softmax",
+                    renormalize: bool = True, scale: float = 1.0, out: torch.Tensor | None = None, stream=None):
+    """ep_router_topk_bwd -> grad_logits [T, E] in the logits' dtype; the arguments of the forward
+    call, its ids, and grad_probs fp32 [T, K]."""
+    pl, ld, dt = _matrix(logits, "logits")
+    T, E = logits.shape
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be [T, K]")
+    K = topk_ids.shape[1]
+    if out is None:
+        out = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
+    rc = _lib.ep_router_topk_bwd(_dense(grad_probs, T, K, torch.float32, "grad_probs"), pl, ld, dt,
+                                 _dense(topk_ids, T, K, torch.int32, "topk_ids"), T, E, K, _score(score),
+                                 int(bool(renormalize)), scale, _dense(out, T, E, logits.dtype, "grad_logits"),
+                                 _stream(stream))
+    _check(rc, "ep_router_topk_bwd")
+    return out
+
+
+def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, row_scale: torch.Tensor, L: Layout,
+                  by_token: bool = True, swiglu: bool = False, out: torch.Tensor | None = None, stream=None):
+    """ep_expert_matvec -> bf16 [R_max, N] (or [R_max, N/2] with swiglu): each row of the layout times
+    its group's 4-bit weights, codes uint8 [G, N, H/2], scales uint8 [G, N, H/16] (E4M3) and row_scale
+    fp32 [G, N].  x bf16 is [T, H] when by_token (rows take their token's vector), else [R_max, H]."""
+    if codes.dim() != 3 or codes.dtype != torch.uint8 or codes.shape[0] != L.G:
+        raise ValueError(f"codes: expected uint8 [{L.G}, N, H/2], got {codes.dtype} {tuple(codes.shape)}")
+    N, H = codes.shape[1], 2 * codes.shape[2]
+    if scales.dtype != torch.uint8 or scales.shape != (L.G, N, H // 16):
+        raise ValueError(f"scales: expected uint8 {(L.G, N, H // 16)}, got {scales.dtype} {tuple(scales.shape)}")
+    _need(row_scale, None, N, _F32, "row_scale", exact_rows=L.G)
+    if by_token:
+        _need(x, None, H, _BF16, "x", exact_rows=L.T)
+    else:
+        _need(x, L.R_max, H, _BF16, "x")
+    n_out = N // 2 if swiglu else N
+    if out is None:
+        out = torch.empty(max(L.R_max, 1), n_out, dtype=torch.bfloat16, device=x.device)
+    _need(out, L.R_max, n_out, _BF16, "out")
+    rc = _lib.ep_expert_matvec(_bits(x), int(bool(by_token)), _ptr(codes), _ptr(scales), _ptr(row_scale), H, N,
+                               int(bool(swiglu)), L.ref, _bits(out), _stream(stream))
+    _check(rc, "ep_expert_matvec")
     return out
 
 

@@ -8,6 +8,7 @@
 #include <stdlib.h>
 
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "ep.h"
@@ -43,6 +44,7 @@ constexpr int kMaxK = 32;
 constexpr int kMaxE = 1024;
 constexpr int kMaxT = 1 << 24;
 constexpr int kMaxH = 32768;
+constexpr int kMaxN = 65536;   // output rows of an expert's weights
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

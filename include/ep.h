@@ -398,6 +398,110 @@ int ep_dispatch_layout_noalloc(const int32_t *topk_ids, int T, int K, int n_expe
                                int n_parts, int capacity, int fused_shared, ep_layout_t *L,
                                void *stream);
 
+/* Element types of the norm and router calls (bf16 and fp16 tensors as their 16-bit patterns). */
+typedef enum { EP_BF16 = 0, EP_F16 = 1, EP_F32 = 2 } ep_dtype_t;
+
+/*
+ * The norm and router calls differ from the other calls in two conventions: their matrix inputs
+ * may have a row stride (in elements, at least the row's length), and pointers marked (e) need
+ * only their element's alignment.  Rows and parameters on 16-byte boundaries are read 16 bytes
+ * at a time, others element by element.
+ */
+
+/*
+ * ep_layer_norm -- layer norm (or RMS norm) of every token, in front of the router and the
+ * dispatch.
+ *   x       [T, H] of type dtype, row stride x_stride (e); 1 <= H <= 32768, 0 <= T <= 2^24.
+ *   weight  [H] and bias [H] or NULL, of type param_dtype: dtype itself or EP_F32 (e).
+ *   rms     0: mean = sum(x)/H; 1: mean = 0 (RMS norm; `mean` is not written and may be NULL).
+ *   -> rstd [T] fp32 = 1/sqrt(sum((x - mean)^2)/H + eps), mean [T] fp32 (e): what the backward
+ *      pass takes;
+ *   -> y    [T*H] dtype, dense (e) = (x - mean) * rstd * weight + bias.
+ * All arithmetic is fp32, rounded once into y; the variance is summed over x - mean.  eps >= 0 (with
+ * eps = 0 a constant row gives NaN).  A NaN or infinity in a row makes that row NaN and no other.
+ */
+int ep_layer_norm(const void *x, long long x_stride, int dtype, const void *weight, const void *bias,
+                  int param_dtype, int T, int hidden_size, float eps, int rms, void *y, float *mean,
+                  float *rstd, void *stream);
+
+/* Scratch bytes ep_layer_norm_bwd needs (0 on invalid sizes). */
+size_t ep_layer_norm_bwd_workspace_bytes(int T, int hidden_size);
+
+/*
+ * ep_layer_norm_bwd -- backward of ep_layer_norm.  With xh = (x - mean) * rstd and a = grad_y * weight:
+ *   -> grad_x      [T*H] dtype, dense (e): rstd * (a - sum(a)/H - xh * sum(a*xh)/H), without the
+ *                  sum(a)/H when rms is 1;
+ *   -> grad_weight [H] fp32 (e): sum over tokens of grad_y * xh;
+ *   -> grad_bias   [H] fp32 (e) or NULL: sum over tokens of grad_y.
+ *   grad_y [T, H] dtype, row stride grad_stride (e); x, weight, mean (NULL allowed when rms is 1) and
+ *   rstd as in the forward call.
+ *   workspace: ep_layer_norm_bwd_workspace_bytes(T, H) bytes, 16-byte aligned; needs no
+ *   initialisation, and calls that share one must not overlap on the GPU.
+ * Sums are fp32 in an order fixed by the sizes and the GPU's SM count: results repeat bit for
+ * bit.  T = 0 writes zero parameter gradients.
+ */
+int ep_layer_norm_bwd(const void *grad_y, long long grad_stride, const void *x, long long x_stride,
+                      int dtype, const void *weight, int param_dtype, const float *mean,
+                      const float *rstd, int T, int hidden_size, int rms, void *grad_x,
+                      float *grad_weight, float *grad_bias, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Scores of the router calls. */
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
+
+/*
+ * ep_router_topk -- the experts and probabilities of every token from its router logits: the
+ * topk_ids the layout calls take and the probs ep_combine takes.
+ *   logits [T, E] of type dtype, row stride `stride` (e); bias [E] fp32 or NULL (e).
+ *   Selection: the K experts with the largest fp32 logit + bias, in descending order, ties to the
+ *   lower id (K <= E, K <= 32).  An expert whose sum is -inf is not selectable; slots for
+ *   which no expert is left get id -1 and probability 0, so a fully masked row routes nowhere.
+ *   Any finite value, the type's lowest among them, is selectable.  A NaN sorts above every
+ *   number, so that it shows in the outputs.
+ *   Probabilities, of the logits without bias, fp32: exp(l) (EP_SCORE_SOFTMAX) or 1/(1 + exp(-l))
+ *   (EP_SCORE_SIGMOID), divided by the sum over the selected experts when renormalize is 1; a
+ *   softmax that is not renormalised is divided by the sum over all experts of the row.  Then
+ *   times scale (positive and finite).
+ *   -> topk_ids [T*K] int32, topk_probs [T*K] fp32.
+ */
+int ep_router_topk(const void *logits, long long stride, int dtype, const float *bias, int T,
+                   int n_experts, int K, int score, int renormalize, float scale,
+                   int32_t *topk_ids, float *topk_probs, void *stream);
+
+/*
+ * ep_router_topk_bwd -- gradient of the logits from the gradient of the probabilities
+ * (ep_combine_bwd's grad_probs); the ids are constants.
+ *   grad_probs [T*K] fp32, logits [T, E] and topk_ids [T*K] as in and from the forward call, and the
+ *   same score, renormalize and scale.
+ *   -> grad_logits [T*E] dtype, dense.  0 for an expert that is not selected (except under a
+ *      softmax over all experts) or masked.  grad_probs of a -1 slot is not used.  Ids outside
+ *      [0, E) count as -1; slots that name the same expert add up.
+ */
+int ep_router_topk_bwd(const float *grad_probs, const void *logits, long long stride, int dtype,
+                       const int32_t *topk_ids, int T, int n_experts, int K, int score,
+                       int renormalize, float scale, void *grad_logits, void *stream);
+
+/*
+ * ep_expert_matvec -- the experts' products for batches of few tokens: every row of a layout times
+ * the 4-bit weights of its group.
+ *   x          [T*H] bf16 when x_by_token is 1: row r takes the token of src_info (the rows need
+ *              not be dispatched); [R_max*H] bf16 in row order when it is 0.
+ *   codes      [G * N * H/2] uint8, scales [G * N * H/16] uint8, row_scale [G * N] fp32 for the
+ *              G = E + S groups: element k of weight row n is E2M1(code) * E4M3(scale of its
+ *              16-element block) * row_scale[n].  Codes, block scales and bytes are those of
+ *              ep_dispatch_nvfp4, so quantising a weight matrix as N tokens with one expert
+ *              gives this format, with row_scale = its inverse scales widened to fp32.
+ *   N          out_rows, 1 <= N <= 65536; with swiglu 1 even: N/2 gate rows, then N/2 up rows.
+ *   -> out     [R_max * N] bf16: out[r, n] = weight row n . x, or with swiglu [R_max * N/2] bf16:
+ *              silu(gate) * up, silu(v) = v / (1 + exp(-v)); fp32 sums, rounded once.
+ * The rows [0, row_offsets[G]) are written; a padding row is the product of a zero row.  Nothing
+ * is written while the layout's status word is non-zero.
+ */
+int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t *codes, const uint8_t *scales,
+                     const float *row_scale, int hidden_size, int out_rows, int swiglu,
+                     const ep_layout_t *L, uint16_t *out, void *stream);
+
 /* Human-readable name of a return code. */
 const char *ep_strerror(int code);
 

@@ -1,0 +1,225 @@
+"""Layer norm and RMS norm, forward and backward, against the 64-bit definition: every type, widths that no
+vector divides, strided rows, rows that are constant or hold infinities, one token and none."""
+import numpy as np
+import pytest
+import torch
+
+import operator_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32), (torch.float16, torch.float16),
+         (torch.float16, torch.float32), (torch.float32, torch.float32)]
+# (T, H): one element, odd widths, each register layout's edges, the widest rows, ragged row counts
+SIZES = [(1, 1), (3, 2), (5, 8), (7, 33), (2, 255), (9, 256), (400, 256), (33, 264), (700, 511), (600, 512), (310, 520),
+         (1, 2048), (320, 2048), (37, 2056), (5, 4096), (3, 4097), (311, 1111), (6, 7168), (610, 7168), (2, 8192),
+         (3, 8200), (330, 8200), (2, 16384), (2, 32767), (3, 32768)]
+
+
+def make(T, H, dt, wdt, seed, bias=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, H, generator=g) * (1 + torch.arange(T)[:, None] % 5) + 0.5
+    w = 1 + 0.2 * torch.randn(H, generator=g)
+    b = 0.3 * torch.randn(H, generator=g) if bias else None
+    gy = torch.randn(T, H, generator=g)
+    to = lambda t, d: t.to(d).cuda()
+    return to(x, dt), to(w, wdt), None if b is None else to(b, wdt), to(gy, dt)
+
+
+def check_forward(ep, x, w, b, eps, rms, out=None):
+    y, mean, rstd = ep.layer_norm(x, w, b, eps=eps, rms=rms, out=out)
+    ry, rmean, rrstd = ref.norm(x, w, b, eps, rms)
+    ty, tmean, trstd = ref.norm_tol(x, w, b, eps, rms, x.dtype)
+    ref.assert_within(y, ry, ty, "y")
+    ref.assert_within(rstd, rrstd, trstd, "rstd")
+    if rms:
+        assert mean is None
+    else:
+        ref.assert_within(mean, rmean, tmean, "mean")
+    return y, mean, rstd
+
+
+def check_backward(ep, gy, x, w, mean, rstd, rms, bias=True):
+    dx, dw, db = ep.layer_norm_bwd(gy, x, w, mean, rstd, rms=rms, bias=bias)
+    rx, rw, rb = ref.norm_bwd(gy, x, w, mean, rstd, rms)
+    tx, tw, tb = ref.norm_bwd_tol(gy, x, w, mean, rstd, rms, x.dtype)
+    assert dw.dtype == torch.float32
+    ref.assert_within(dx, rx, tx, "dx")
+    ref.assert_within(dw, rw, tw, "dw")
+    if bias:
+        ref.assert_within(db, rb, tb, "db")
+    else:
+        assert db is None
+
+
+@pytest.mark.parametrize("T,H", SIZES)
+@pytest.mark.parametrize("rms", [False, True])
+def test_sizes_bf16(T, H, rms):
+    import combine_topk_ids_histogram_gb300 as ep
+    x, w, b, gy = make(T, H, torch.bfloat16, torch.bfloat16, T * 7 + H, bias=not rms)
+    _, mean, rstd = check_forward(ep, x, w, b, 1e-5, rms)
+    check_backward(ep, gy, x, w, mean, rstd, rms, bias=not rms)
+
+
+@pytest.mark.parametrize("dt,wdt", TYPES[1:])
+@pytest.mark.parametrize("T,H", [(1, 7), (35, 100), (340, 132), (320, 2048), (61, 2049), (5, 4100), (320, 7168), (2, 8196),
+                                 (2, 32768)])
+def test_types(dt, wdt, T, H):
+    import combine_topk_ids_histogram_gb300 as ep
+    x, w, b, gy = make(T, H, dt, wdt, T + 3 * H)
+    _, mean, rstd = check_forward(ep, x, w, b, 1e-6, False)
+    check_backward(ep, gy, x, w, mean, rstd, False)
+    _, mean, rstd = check_forward(ep, x, w, b, 1e-6, True)            # RMS with a bias
+    check_backward(ep, gy, x, w, mean, rstd, True)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("offset,extra", [(0, 8), (0, 3), (1, 7), (8, 24), (5, 0)])
+def test_strided_and_unaligned_rows(dt, offset, extra):
+    """Rows inside a wider matrix, on and off 16-byte boundaries, give the dense rows' bits where both take
+    the same path, and stay within the bound everywhere."""
+    import combine_topk_ids_histogram_gb300 as ep
+    T, H = 45, 256
+    x, w, b, gy = make(T, H, dt, dt, offset + extra)
+    wide = torch.full((T, offset + H + extra), float("nan"), dtype=dt, device="cuda")
+    wide[:, offset:offset + H] = x
+    gwide = torch.full((T, 2 * H + 1), float("nan"), dtype=dt, device="cuda")
+    gwide[:, H:2 * H] = gy
+    xs, gs = wide[:, offset:offset + H], gwide[:, H:2 * H]
+    _, mean, rstd = check_forward(ep, xs, w, b, 1e-5, False)
+    check_backward(ep, gs, xs, w, mean, rstd, False)
+
+
+def test_no_write_outside_outputs():
+    import combine_topk_ids_histogram_gb300 as ep
+    for T, H in ((3, 33), (310, 64), (9, 2048), (2, 8200)):
+        x, w, b, gy = make(T, H, torch.bfloat16, torch.bfloat16, T)
+        buf = torch.full((T * H + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
+        f = torch.full((3, T + H + 64), 7.0, device="cuda")
+        y = buf[64:64 + T * H].view(T, H)
+        ep.layer_norm(x, w, b, out=(y, f[0, 8:8 + T], f[1, 8:8 + T]))
+        assert (buf[:64] == 7).all() and (buf[64 + T * H:] == 7).all()
+        assert (f[:, :8] == 7).all() and (f[:2, 8 + T:] == 7).all()
+        mean, rstd = f[0, 8:8 + T].clone(), f[1, 8:8 + T].clone()
+        nws = ep.layer_norm_bwd_workspace_bytes(T, H)
+        ws = torch.full((nws + 256,), 7, dtype=torch.uint8, device="cuda")
+        f.fill_(7)
+        ep.layer_norm_bwd(gy, x, w, mean, rstd, bias=True, out=(y, f[0, 8:8 + H], f[1, 8:8 + H]),
+                          workspace=ws[:nws])
+        assert (buf[:64] == 7).all() and (buf[64 + T * H:] == 7).all()
+        assert (f[:, :8] == 7).all() and (f[:2, 8 + H:] == 7).all() and (ws[nws:] == 7).all()
+
+
+def test_constant_rows_and_large_means():
+    """A constant row has variance 0: y = bias, and rstd = 1/sqrt(eps).  A large mean costs no digits of the
+    variance."""
+    import combine_topk_ids_histogram_gb300 as ep
+    x = torch.zeros(4, 512, device="cuda")
+    x[1] = 3.0
+    x[2] = 1e4 + torch.arange(512, device="cuda") / 64
+    x[3] = -1e30
+    w = torch.ones(512, device="cuda")
+    b = torch.full((512,), 0.25, device="cuda")
+    y, mean, rstd = check_forward(ep, x, w, b, 1e-5, False)
+    assert (y[:2] == 0.25).all() and (y[3] == 0.25).all()
+    # in-bound at the large mean is not enough: the two-pass variance is within 1e-6 of 64 bits
+    r = ref.norm(x, w, b, 1e-5, False)[2]
+    assert abs(rstd[2].item() / r[2].item() - 1) < 1e-6
+
+
+def test_non_finite_rows_stay_in_their_rows():
+    import combine_topk_ids_histogram_gb300 as ep
+    x, w, b, gy = make(8, 300, torch.float32, torch.float32, 5)
+    clean = ep.layer_norm(x, w, b)
+    bad = x.clone()
+    bad[2, 7] = float("inf")
+    bad[5, 299] = float("nan")
+    y, mean, rstd = ep.layer_norm(bad, w, b)
+    rows = [0, 1, 3, 4, 6, 7]
+    assert torch.equal(y[rows], clean[0][rows]) and torch.equal(rstd[rows], clean[2][rows])
+    assert torch.isnan(y[2]).all() and torch.isnan(y[5]).all()
+    dx, dw, db = ep.layer_norm_bwd(gy, bad, w, mean, rstd, bias=True)
+    want = ep.layer_norm_bwd(gy, x, w, clean[1], clean[2], bias=True)
+    assert torch.equal(dx[rows], want[0][rows])
+    assert torch.isnan(dx[2]).all() and torch.isnan(dx[5]).all()
+    assert torch.equal(db, want[2])
+
+
+def test_no_tokens():
+    import combine_topk_ids_histogram_gb300 as ep
+    x = torch.empty(0, 96, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(96, dtype=torch.bfloat16, device="cuda")
+    y, mean, rstd = ep.layer_norm(x, w, w)
+    assert y.shape == (0, 96) and mean.numel() == 0
+    dw, db = torch.full((96,), 5.0, device="cuda"), torch.full((96,), 5.0, device="cuda")
+    ep.layer_norm_bwd(x, x, w, mean, rstd, bias=True, out=(y, dw, db))
+    torch.cuda.synchronize()
+    assert (dw == 0).all() and (db == 0).all()
+
+
+@pytest.mark.parametrize("rms", [False, True])
+def test_gradient_against_differences(rms):
+    """<dx, v> + <dw, u> + <db, z> against central differences of the 64-bit forward form.  With step 1e-5
+    the difference's own error is below 1e-8 of the gradient's magnitude."""
+    import combine_topk_ids_histogram_gb300 as ep
+    T, H, eps = 6, 200, 1e-5
+    x, w, b, gy = make(T, H, torch.float32, torch.float32, 11)
+    _, mean, rstd = ep.layer_norm(x, w, b, eps=eps, rms=rms)
+    dx, dw, db = ep.layer_norm_bwd(gy, x, w, mean, rstd, rms=rms, bias=True)
+    tx, tw, tb = ref.norm_bwd_tol(gy, x, w, mean, rstd, rms, torch.float32)
+    g = torch.Generator().manual_seed(3)
+    for _ in range(5):
+        v, u, z = (torch.randn(*s, generator=g, dtype=torch.float64) for s in ((T, H), (H,), (H,)))
+        loss = lambda s: (ref.norm(ref.d64(x) + s * v, ref.d64(w) + s * u, ref.d64(b) + s * z, eps, rms)[0] * ref.d64(gy)).sum()
+        diff = (loss(1e-5) - loss(-1e-5)) / 2e-5
+        got = (ref.d64(dx) * v).sum() + (ref.d64(dw) * u).sum() + (ref.d64(db) * z).sum()
+        # the saved statistics are fp32: their relative error of 128 * 2^-24 moves every term by as much
+        mag = (ref.d64(dx).abs() * v.abs()).sum() + (ref.d64(dw).abs() * u.abs()).sum()
+        tol = (tx * v.abs()).sum() + (tw * u.abs()).sum() + (tb * z.abs()).sum() + (4 * ref.ROW + 1e-8) * mag
+        assert abs(got - diff) <= tol
+
+
+def test_repeatable_and_on_a_side_stream():
+    import combine_topk_ids_histogram_gb300 as ep
+    x, w, b, gy = make(1500, 1024, torch.bfloat16, torch.bfloat16, 2)
+    y, mean, rstd = ep.layer_norm(x, w, b)
+    first = ep.layer_norm_bwd(gy, x, w, mean, rstd, bias=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y2, m2, r2 = ep.layer_norm(x, w, b)
+        second = ep.layer_norm_bwd(gy, x, w, m2, r2, bias=True)
+    s.synchronize()
+    assert torch.equal(y, y2) and all(torch.equal(p, q) for p, q in zip(first, second))
+
+
+def test_refusals():
+    import combine_topk_ids_histogram_gb300 as ep
+    x, w, b, gy = make(4, 64, torch.bfloat16, torch.bfloat16, 1)
+    y, mean, rstd = ep.layer_norm(x, w, b)
+    with pytest.raises(TypeError):
+        ep.layer_norm(x.double(), w, b)
+    with pytest.raises(TypeError):
+        ep.layer_norm(x, w.half(), b)                      # parameters in x's type or fp32
+    with pytest.raises(TypeError):
+        ep.layer_norm(x, w, b.float())                     # bias in the weight's type
+    with pytest.raises(ValueError):
+        ep.layer_norm(x, w[:32], b)
+    with pytest.raises(ValueError):
+        ep.layer_norm(x.t(), w[:4], None)                  # columns are not contiguous
+    with pytest.raises(ValueError):
+        ep.layer_norm(x[0], w, b)
+    with pytest.raises(ValueError):
+        ep.layer_norm(x.cpu(), w, b)
+    with pytest.raises(ep.EPError):
+        ep.layer_norm(x, w, b, eps=-1.0)
+    with pytest.raises(ep.EPError):
+        ep.layer_norm(x, w, b, eps=float("nan"))
+    with pytest.raises(ValueError):
+        ep.layer_norm_bwd(gy[:3], x, w, mean, rstd)
+    with pytest.raises(ValueError):
+        ep.layer_norm_bwd(gy, x, w, mean[:3], rstd)
+    with pytest.raises(ep.EPError):
+        ep.layer_norm_bwd(gy, x, w, mean, rstd, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ep.EPError):
+        ep.layer_norm(torch.zeros(1, 40000, device="cuda"), torch.zeros(40000, device="cuda"))
