@@ -94,7 +94,8 @@ SIGNATURES = {
     "ep_layer_norm_bwd": (_I, [_P, _LL, _P, _LL, _I, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
     "ep_router_topk": (_I, [_P, _LL, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
     "ep_router_topk_bwd": (_I, [_P, _P, _LL, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P]),
-    "ep_expert_matvec": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _LP, _P, _P]),
+    "ep_expert_matvec_workspace_bytes": (_Z, [_LP, _I]),
+    "ep_expert_matvec": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _LP, _P, _P, _Z, _P]),
     "ep_read_status": (_I, [_LP, _P, ctypes.POINTER(ctypes.c_int32)]),
     "ep_strerror": (ctypes.c_char_p, [_I]),
     "ep_cvt_e2m1": (_I, [_P, _P, _L, _P]),
@@ -702,11 +703,22 @@ def router_topk_bwd(grad_probs: torch.Tensor, logits: torch.Tensor, topk_ids: to
     return out
 
 
+def expert_matvec_workspace_bytes(L: Layout, H: int) -> int:
+    """ep_expert_matvec_workspace_bytes: scratch bytes of ``expert_matvec`` on this layout's sizes."""
+    n = int(_lib.ep_expert_matvec_workspace_bytes(L.ref, H))
+    if n == 0:
+        raise EPError(EP_ERR_INVALID_ARG, "expert_matvec sizes")
+    return n
+
+
 def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, row_scale: torch.Tensor, L: Layout,
-                  by_token: bool = True, swiglu: bool = False, out: torch.Tensor | None = None, stream=None):
+                  by_token: bool = True, swiglu: bool = False, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
     """ep_expert_matvec -> bf16 [R_max, N] (or [R_max, N/2] with swiglu): each row of the layout times
     its group's 4-bit weights, codes uint8 [G, N, H/2], scales uint8 [G, N, H/16] (E4M3) and row_scale
-    fp32 [G, N].  x bf16 is [T, H] when by_token (rows take their token's vector), else [R_max, H]."""
+    fp32 [G, N].  x bf16 is [T, H] when by_token (rows take their token's vector), else [R_max, H].
+    ``workspace``: a uint8 buffer of ``expert_matvec_workspace_bytes`` to reuse; without one a call
+    allocates its own on the stream it runs on."""
     if codes.dim() != 3 or codes.dtype != torch.uint8 or codes.shape[0] != L.G:
         raise ValueError(f"codes: expected uint8 [{L.G}, N, H/2], got {codes.dtype} {tuple(codes.shape)}")
     N, H = codes.shape[1], 2 * codes.shape[2]
@@ -721,8 +733,12 @@ def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ro
     if out is None:
         out = torch.empty(max(L.R_max, 1), n_out, dtype=torch.bfloat16, device=x.device)
     _need(out, L.R_max, n_out, _BF16, "out")
+    if workspace is None:
+        with torch.cuda.stream(stream):     # a buffer of that stream's, so that its reuse is ordered behind this call
+            workspace = torch.empty(expert_matvec_workspace_bytes(L, H), dtype=torch.uint8, device=x.device)
     rc = _lib.ep_expert_matvec(_bits(x), int(bool(by_token)), _ptr(codes), _ptr(scales), _ptr(row_scale), H, N,
-                               int(bool(swiglu)), L.ref, _bits(out), _stream(stream))
+                               int(bool(swiglu)), L.ref, _bits(out), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc, "ep_expert_matvec")
     return out
 

@@ -1,76 +1,459 @@
 // ep_experts.cu -- products of the experts' 4-bit weights with the rows of a dispatch layout, for
 // batches of few tokens (decode), optionally with the gated activation silu(gate) * up.
 //
-// Weights are in the format the NVFP4 dispatch writes: E2M1 codes, two per byte, with an E4M3 scale
-// per 16 elements, and an fp32 scale per output row.
+//   out[r, n] = row_scale[n] * sum over k of E2M1(code[n, k]) * E4M3(scale[n, k/16]) * x[r, k]
+//
+// Weights are in the format the NVFP4 dispatch writes.  A group's weights are read from HBM once for
+// all of its rows, so HBM bounds the call while an expert has few rows: 9/16 byte per weight.
+//
+// The products run on mma.sync.m16n8k16 with weight rows as M and layout rows as N: at 8 rows
+// or fewer per expert the tensor cores are far from their rate, and operands that a thread builds in
+// its own registers need no pass through shared memory, which would carry four times the
+// weights' bytes.  An E2M1 value times an E4M3 scale has 6 significant bits and lies in
+// [2^-10, 2688], so it is exact in fp16; a row of x is scaled by the power of two that puts its
+// largest magnitude in [2^14, 2^15), where a bf16 is exact in fp16 too unless it is below 2^-32 of
+// that magnitude.  The contraction may take its k in any order as long as both operands take the same
+// one: a thread reads 64 consecutive codes of a weight row (32 bytes) and feeds them to 16 steps of the
+// tensor cores, and a first kernel writes x as fp16 in that order.
+#include <math.h>
+
 #include "ep_host.h"
 #include "ep_types.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kExpertThreads = 256;
-
-__device__ __forceinline__ float e2m1_value(unsigned c) {
-    const float mag = (c & 4u) ? (float)((2u | (c & 1u)) << ((c >> 1) & 1u)) : 0.5f * (float)(c & 3u);
-    return (c & 8u) ? -mag : mag;
-}
-__device__ __forceinline__ float e4m3_value(unsigned c) {
-    const unsigned e = (c >> 3) & 15u, m = c & 7u;
-    const float mag = e == 0u ? (float)m * 0x1p-9f : __uint_as_float(((e + 120u) << 23) | (m << 20));
-    return (c & 0x80u) ? -mag : mag;
-}
+constexpr int kStepK = 256;              // k per warp step: 64 per thread of a quad
+constexpr int kPackThreads = 256;
 
 struct ExpertArgs {
     const uint16_t *x;
     const uint8_t *codes, *scales;
     const float *row_scale;
     int H, N, by_token, swiglu, T, G, R_max;
+    int KS;                              // warps that share a tile and split its k: 1, 2 or 4
     const int32_t *row_offsets, *src_info, *status;
+    uint4 *xw;                           // [R_max][step][word][quad thread] x as fp16, 16-byte pieces
+    float *xs;                           // [R_max] what a row's sums are multiplied by
     uint16_t *out;
 };
 
-// Product of weight row n of group g with the row x (one warp; the same value in every lane).
-__device__ __forceinline__ float row_product(const ExpertArgs &a, int g, int n, const uint16_t *x, int lane) {
-    const size_t r = (size_t)g * a.N + n;
-    const uint8_t *c = a.codes + r * (a.H / 2), *s = a.scales + r * (a.H / 16);
-    float sum = 0.0f;
-    for (int k = lane; k < a.H / 2; k += 32) {
-        const unsigned b = c[k];
-        const float sc = e4m3_value(s[k / 8]);
-        sum = fmaf(e2m1_value(b & 15u) * sc, bf16_lo(x[2 * k]), sum);
-        sum = fmaf(e2m1_value(b >> 4) * sc, bf16_lo(x[2 * k + 1]), sum);
-    }
-    return warp_sum(sum) * a.row_scale[r];
+__device__ __forceinline__ void cp_async4(void *smem, const void *gmem) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(smem)), "l"(gmem) : "memory");
 }
 
-// One warp per output element.
-__global__ void __launch_bounds__(kExpertThreads)
-ep_expert_matvec_kernel(ExpertArgs a) {
-    pdl_wait();
-    if (cta_status(a.status)) return;
-    const int lane = threadIdx.x & 31;
-    const int n_out = a.swiglu ? a.N / 2 : a.N;
-    const int n = blockIdx.x * (kExpertThreads / 32) + (threadIdx.x >> 5);
-    if (n >= n_out) return;
-    int g = 0;
-    const int R = a.row_offsets[a.G];
-    for (int row = blockIdx.y; row < R && row < a.R_max; row += gridDim.y) {
-        while (g < a.G && a.row_offsets[g + 1] <= row) ++g;
-        const int src = a.by_token ? a.src_info[2 * (size_t)row] : row;
-        float v = 0.0f;
-        if (src >= 0 && src < (a.by_token ? a.T : a.R_max)) {
-            const uint16_t *x = a.x + (size_t)src * a.H;
-            v = row_product(a, g, n, x, lane);
-            if (a.swiglu) {
-                const float up = row_product(a, g, n_out + n, x, lane);
-                v = v / (1.0f + expf(-v)) * up;
+inline int pack_steps(int H) { return (H + kStepK - 1) / kStepK; }
+
+__device__ __forceinline__ void cp_async16(void *smem, const void *gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(smem)), "l"(gmem) : "memory");
+}
+
+// Eight codes of a word to four fp16 pairs (consecutive codes), times the scale of their block.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t scale2, uint32_t (&o)[4]) {
+    asm("{.reg .b8 b0, b1, b2, b3;\n"
+        " mov.b32 {b0, b1, b2, b3}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+        " cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, b2;\n"
+        " cvt.rn.f16x2.e2m1x2 %3, b3;}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[i]) : "r"(scale2));
+}
+
+// Four E4M3 scales to fp16.
+__device__ __forceinline__ void scales_to_f16(uint32_t w, uint32_t (&s)[2]) {
+    asm("{.reg .b16 h0, h1;\n mov.b32 {h0, h1}, %2;\n cvt.rn.f16x2.e4m3x2 %0, h0;\n cvt.rn.f16x2.e4m3x2 %1, h1;}"
+        : "=r"(s[0]), "=r"(s[1])
+        : "r"(w));
+}
+// Scale i of them in both halves of a word.
+__device__ __forceinline__ uint32_t scale_pair(const uint32_t (&s)[2], int i) {
+    return __byte_perm(s[i >> 1], 0, i & 1 ? 0x3232 : 0x1010);
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// What a thread holds of one step: for each of its 2 * MT weight rows 64 codes and their scales.
+template <int MT> struct Weights {
+    uint32_t w[2 * MT][8];
+    uint32_t s[2 * MT];
+};
+
+// k of word wi (8 codes) of quad thread q within a step.  WIDE: 64 consecutive codes per thread, one 32-byte
+// load per row; else four runs of 16 codes, 8-byte loads, for rows that are only 8-byte aligned.
+template <bool WIDE> __device__ __forceinline__ int word_k(int q, int wi) {
+    return WIDE ? q * 64 + wi * 8 : (wi >> 1) * 64 + q * 16 + (wi & 1) * 8;
+}
+
+template <bool WIDE, int MT>
+__device__ __forceinline__ void load_weights(Weights<MT> &d, const uint8_t *codes, const uint8_t *scales,
+                                             const unsigned (&row)[2 * MT], int half, int step, int q, int H) {
+    if constexpr (WIDE) {
+        const int k = step * kStepK + q * 64;
+        if (k < H) {
+#pragma unroll
+            for (int r = 0; r < 2 * MT; ++r) {
+                const unsigned long long at = (unsigned long long)row[r] * half + (k >> 1);
+                asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(d.w[r][0]), "=r"(d.w[r][1]), "=r"(d.w[r][2]), "=r"(d.w[r][3]), "=r"(d.w[r][4]),
+                               "=r"(d.w[r][5]), "=r"(d.w[r][6]), "=r"(d.w[r][7])
+                             : "l"(codes + at));
+                d.s[r] = __ldg(reinterpret_cast<const uint32_t *>(scales + (at >> 3)));
             }
-        } else if (src != -1) {
-            bounds_fail(a.status);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 2 * MT; ++r) {
+                d.s[r] = 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d.w[r][i] = 0u;
+            }
         }
-        if (lane == 0) a.out[(size_t)row * n_out + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    } else {
+#pragma unroll
+        for (int r = 0; r < 2 * MT; ++r) {
+            d.s[r] = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = step * kStepK + j * 64 + q * 16;
+                uint2 v = make_uint2(0u, 0u);
+                if (k < H) {
+                    const unsigned long long at = (unsigned long long)row[r] * half + (k >> 1);
+                    v = __ldg(reinterpret_cast<const uint2 *>(codes + at));
+                    d.s[r] |= (uint32_t)__ldg(scales + (at >> 3)) << (8 * j);
+                }
+                d.w[r][2 * j] = v.x;
+                d.w[r][2 * j + 1] = v.y;
+            }
+        }
     }
+}
+
+// One step of a warp: MT * 16 weight rows x 256 k x NT * 8 layout rows.  x: the step's pieces of this thread's
+// layout row in shared memory, xo: how far on its row of the second block of 8 is.
+template <int MT, int NT>
+__device__ __forceinline__ void mma_step(const Weights<MT> &d, const uint4 *x, const int (&xo)[NT],
+                                         float (&acc)[MT][NT][4]) {
+    uint32_t sc[2 * MT][2];
+#pragma unroll
+    for (int r = 0; r < 2 * MT; ++r) scales_to_f16(d.s[r], sc[r]);
+#pragma unroll
+    for (int wi = 0; wi < 8; ++wi) {
+        uint4 b[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) b[t] = x[xo[t] + wi * 4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            uint32_t lo[4], hi[4];   // weight rows g and g + 8 of the tile
+            codes_to_f16(d.w[2 * mt][wi], scale_pair(sc[2 * mt], wi >> 1), lo);
+            codes_to_f16(d.w[2 * mt + 1][wi], scale_pair(sc[2 * mt + 1], wi >> 1), hi);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                mma_f16(acc[mt][t], lo[0], hi[0], lo[1], hi[1], b[t].x, b[t].y);
+                mma_f16(acc[mt][t], lo[2], hi[2], lo[3], hi[3], b[t].z, b[t].w);
+            }
+        }
+    }
+}
+
+// x of one layout row, scaled to fp16 and reordered: one CTA per row.
+template <bool WIDE>
+__global__ void __launch_bounds__(kPackThreads)
+ep_expert_pack_kernel(const ExpertArgs a) {
+    __shared__ unsigned s_top[kPackThreads / 32];
+    pdl_begin();
+    const int row = blockIdx.x, tid = threadIdx.x;
+    const int R = a.row_offsets[a.G];                               // these three loads go out together
+    const int src = a.by_token ? a.src_info[2 * (size_t)row] : row;
+    if (cta_status(a.status) || row >= R) return;
+    const bool real = src >= 0 && src < (a.by_token ? a.T : a.R_max);
+    if (!real && src != -1) bounds_fail(a.status);
+    const uint4 *x = reinterpret_cast<const uint4 *>(a.x + (real ? (size_t)src * a.H : 0));
+    unsigned top = 0u;                                              // largest finite magnitude, as bf16 bits
+    for (int p = tid; real && p < a.H / 8; p += kPackThreads) {
+        const uint4 v = __ldg(x + p);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned mag = u[i] & 0x7fff7fffu;
+            top = __vmaxu2(top, mag & ~__vcmpgeu2(mag, 0x7f807f80u));
+        }
+    }
+    top = __reduce_max_sync(kFullMask, max(top & 0xffffu, top >> 16));
+    if ((tid & 31) == 0) s_top[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPackThreads / 32; ++w) top = max(top, s_top[w]);
+    const int e = max((int)(top >> 7), 15);                         // biased exponent; both powers stay normal
+    const float up = __uint_as_float((unsigned)(268 - e) << 23);    // 2^(141 - e)
+    if (tid == 0) a.xs[row] = __uint_as_float((unsigned)(e - 14) << 23);
+    const int pieces = (a.H + kStepK - 1) / kStepK * 32;
+    uint4 *dst = a.xw + (size_t)row * pieces;
+    for (int p = tid; p < pieces; p += kPackThreads) {
+        const int k = (p >> 5) * kStepK + word_k<WIDE>(p & 3, (p >> 2) & 7);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (real && k < a.H) {
+            float f[8];
+            unpack8(__ldg(x + (k >> 3)), f);
+            __half2 h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i] * up, f[2 * i + 1] * up);
+            __builtin_memcpy(&v, h, 16);
+        }
+        dst[p] = v;
+    }
+}
+
+// How a kernel is built: MT m16 tiles of weight rows per warp and NT blocks of 8 layout rows per pass, for THREADS threads
+// and CTAS CTAs per SM; P steps of x fill one of the two shared-memory buffers, in rows PITCH pieces apart, half a
+// 128-byte line beyond whole lines so that two rows' reads miss each other's banks.
+template <int MT_, int NT_, int THREADS_, int CTAS_, int P_> struct Shape {
+    static constexpr int MT = MT_, NT = NT_, THREADS = THREADS_, CTAS = CTAS_, P = P_;
+    static constexpr int WARPS = THREADS / 32, ROWS = 8 * NT, PITCH = P * 32 + 4;
+    static constexpr size_t SMEM = (size_t)2 * ROWS * PITCH * sizeof(uint4);
+};
+
+// Work is cut into items: a tile of weight rows of a group and a chunk of up to 8 * NT of the group's rows, chunks of
+// a tile next to each other so that L2 serves the second reading of its weights.  CTAs take items in
+// turn.  KS of a CTA's warps share each 32-row tile and split its k; their sums meet in shared memory in
+// a fixed order.  Nothing drains at an item's end: x of the next part of 8 / NT steps, of the next item too, is
+// copied to shared memory while the present one is computed, and a warp has its next step's weights on their
+// way to registers.  The first weights start before x is there, because the weights, like every argument,
+// were complete before the first kernel started.
+template <bool WIDE, typename S>
+__global__ void __launch_bounds__(S::THREADS, S::CTAS)
+ep_expert_matvec_kernel(const ExpertArgs a) {
+    constexpr int kChunkRows = S::ROWS, P = S::P, PITCH = S::PITCH, MT = S::MT, NT = S::NT;
+    constexpr int kExpertThreads = S::THREADS, kExpertWarps = S::WARPS, kTileRows = 16 * MT;
+    extern __shared__ uint4 s_x[];                                  // [2][8 * NT][PITCH]
+    __shared__ float s_red[kExpertWarps][4 * MT * NT][32];               // partial sums, [warp][register][lane]
+    __shared__ float s_xs[2][kChunkRows], s_rs[2][kExpertThreads];  // scales of an item's rows of x and of W (the up rows last)
+    __shared__ int s_first[kMaxE + 2];                              // chunks before each group
+    __shared__ int s_row[kMaxE + 2];                                // first row of each group
+    __shared__ int s_warp[kExpertWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gl = lane >> 2, q = lane & 3;
+    if (cta_status(a.status)) return;
+
+    // chunks before each group: thread i scans a run of groups
+    for (int g = tid; g <= a.G; g += kExpertThreads) s_row[g] = min(max(a.row_offsets[g], 0), a.R_max);
+    __syncthreads();
+    {
+        const int per = (a.G + kExpertThreads - 1) / kExpertThreads;
+        const int g0 = min(tid * per, a.G), g1 = min(g0 + per, a.G);
+        int n = 0, prev = s_row[g0];
+        for (int g = g0; g < g1; ++g) {
+            const int next = s_row[g + 1];
+            s_first[g] = n;                                         // within the thread's run
+            n += next > prev ? (next - prev + kChunkRows - 1) / kChunkRows : 0;
+            prev = next;
+        }
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFullMask, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        int base = incl - n;
+        for (int w = 0; w < warp; ++w) base += s_warp[w];
+        for (int g = g0; g < g1; ++g) s_first[g] += base;
+        if (tid == kExpertThreads - 1) s_first[a.G] = base + n;
+        __syncthreads();
+    }
+    const int KS = a.KS, NS = kExpertWarps / KS;
+    const int kw = warp & (KS - 1), nw = warp / KS;
+    const int n_out = a.swiglu ? a.N >> 1 : a.N;
+    const int per_warp = a.swiglu ? kTileRows / 2 : kTileRows;
+    const int rows_out = per_warp * NS;                             // output columns of an item
+    const int blocks = (n_out + rows_out - 1) / rows_out;
+    const int items = s_first[a.G] * blocks;                        // the output holds 128 elements per item: fits an int
+    const int half = a.H >> 1;
+    const int steps = (a.H + kStepK - 1) / kStepK;
+
+    struct Cursor {
+        int item, g, chunk, block;                                  // chunk: of the group
+    };
+    const auto locate = [&](Cursor &c) {                            // from c.item: the last group that begins at or before it
+        int lo = 0, hi = a.G;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_first[mid] * blocks <= c.item) lo = mid;
+            else hi = mid;
+        }
+        const int of_group = c.item - s_first[lo] * blocks, n = s_first[lo + 1] - s_first[lo];
+        c.g = lo;
+        c.block = n == 1 ? of_group : of_group / n;
+        c.chunk = of_group - c.block * n;
+    };
+    // the weight rows of this thread in an item, clamped to the matrix (the excess is not stored).  Rows g and g + 8 of a
+    // tile are output columns 8 apart, or a gate row and its up row.
+    const auto weight_rows = [&](const Cursor &c, unsigned (&row)[2 * MT]) {
+        const unsigned base = (unsigned)c.g * (unsigned)a.N;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int n = c.block * rows_out + nw * per_warp + mt * (a.swiglu ? 8 : 16) + gl;
+            row[2 * mt] = base + (unsigned)min(n, n_out - 1);
+            row[2 * mt + 1] = base + (unsigned)(a.swiglu ? n_out + min(n, n_out - 1) : min(n + 8, n_out - 1));
+        }
+    };
+    Cursor cur = {(int)blockIdx.x, 0, 0, 0};
+    if (cur.item >= items) return;
+    locate(cur);
+    Cursor pf = cur;
+    unsigned pf_row[2 * MT];
+    weight_rows(pf, pf_row);
+    int pf_step = kw;
+    Weights<MT> nxt;
+    // past the last item this loads the last step once more: no branch around the loads
+    const auto prefetch = [&]() {
+        load_weights<WIDE, MT>(nxt, a.codes, a.scales, pf_row, half, pf_step, q, a.H);
+        if (pf_step + KS < steps) {
+            pf_step += KS;
+        } else if (pf.item + (int)gridDim.x < items) {
+            pf_step = kw;
+            pf.item += gridDim.x;
+            locate(pf);
+            weight_rows(pf, pf_row);
+        }
+    };
+    const auto row_of_chunk = [&](const Cursor &c) { return s_row[c.g] + c.chunk * kChunkRows; };
+    const auto rows_of_chunk = [&](const Cursor &c) { return min(s_row[c.g + 1] - row_of_chunk(c), kChunkRows); };
+    // starts the copy of x for steps [from, from + P) of an item, a warp taking a step of a row at a time, and with the
+    // first ones that of what the item's sums are multiplied by
+    const auto copy_x = [&](const Cursor &c, int from, uint4 *buf, int parity) {
+        const int n = min(P, steps - from), m = rows_of_chunk(c);
+        const uint4 *src = a.xw + ((size_t)row_of_chunk(c) * steps + from) * 32 + lane;
+        for (int u = warp; u < m * n; u += kExpertWarps) {
+            const int r = u / n, st = u - r * n;
+            cp_async16(buf + r * PITCH + st * 32 + lane, src + ((size_t)r * steps + st) * 32);
+        }
+        if (from == 0) {
+            if (tid < m) cp_async4(&s_xs[parity][tid], a.xs + row_of_chunk(c) + tid);
+            if (tid < kTileRows * NS) {
+                const int up = a.swiglu && tid >= rows_out, n = min(c.block * rows_out + tid - (up ? rows_out : 0), n_out - 1);
+                cp_async4(&s_rs[parity][tid], a.row_scale + (size_t)c.g * a.N + (up ? n_out : 0) + n);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    prefetch();
+    pdl_begin();                                                    // x is there
+    copy_x(cur, 0, s_x, 0);
+
+    int buf = 0;
+    for (int parity = 0; cur.item < items; parity ^= 1) {
+        const int row0 = row_of_chunk(cur), m = rows_of_chunk(cur);
+        Cursor nx = cur;
+        nx.item += gridDim.x;
+        if (nx.item < items) locate(nx);
+        float acc[MT][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[mt][t][i] = 0.0f;
+        // columns past the chunk's rows repeat its last row; their sums are not stored
+        const int x_at = min(gl, m - 1) * PITCH + q;
+        int xo[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xo[t] = (min(t * 8 + gl, m - 1) - min(gl, m - 1)) * PITCH;
+        for (int from = 0; from < steps; from += P, buf ^= 1) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();                                        // this part is there, and every warp is done with the other
+            uint4 *other = s_x + (buf ^ 1) * kChunkRows * PITCH;
+            if (from + P < steps) copy_x(cur, from + P, other, parity);
+            else if (nx.item < items) copy_x(nx, 0, other, parity ^ 1);
+            const int to = min(P, steps - from);
+            const uint4 *x = s_x + buf * kChunkRows * PITCH + x_at;
+            for (int st = kw; st < to; st += KS) {
+                const Weights<MT> w = nxt;
+                prefetch();
+                mma_step<MT, NT>(w, x + st * 32, xo, acc);
+            }
+        }
+
+        // join the KS partial sums; the warps of a tile share the (row of x, weight row) pairs
+        if (KS > 1) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s_red[warp][mt * 4 * NT + t * 4 + i][lane] = acc[mt][t][i];
+            __syncthreads();
+        }
+#pragma unroll
+        for (int u = 0; u < 2 * MT * NT; ++u) {                     // u = (mt, t, column of the pair)
+            if ((u & (KS - 1)) != kw) continue;
+            const int mt = u / (2 * NT), t = u / 2 % NT, i = u & 1;
+            const int r = t * 8 + q * 2 + i;
+            if (r >= m) continue;
+            float v[2] = {acc[mt][t][i], acc[mt][t][2 + i]};        // weight rows g and g + 8
+            if (KS > 1) {
+                v[0] = v[1] = 0.0f;
+                for (int w = 0; w < KS; ++w) {
+                    v[0] += s_red[nw * KS + w][mt * 4 * NT + t * 4 + i][lane];
+                    v[1] += s_red[nw * KS + w][mt * 4 * NT + t * 4 + 2 + i][lane];
+                }
+            }
+            const int at = nw * per_warp + mt * (a.swiglu ? 8 : 16) + gl, n = cur.block * rows_out + at;
+            const float xs = s_xs[parity][r], *rs = s_rs[parity] + at;
+            uint16_t *out = a.out + (size_t)(row0 + r) * n_out;
+            if (a.swiglu) {
+                if (n < n_out) {
+                    const float gate = v[0] * xs * rs[0], up = v[1] * xs * rs[rows_out];
+                    out[n] = __bfloat16_as_ushort(__float2bfloat16_rn(gate / (1.0f + expf(-gate)) * up));
+                }
+            } else {
+                if (n < n_out) out[n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0] * xs * rs[0]));
+                if (n + 8 < n_out) out[n + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(v[1] * xs * rs[8]));
+            }
+        }
+        cur = nx;
+    }
+}
+
+template <bool WIDE, typename S>
+int launch_expert_matvec(const ExpertArgs &a, cudaStream_t st) {
+    const auto kern = ep_expert_matvec_kernel<WIDE, S>;
+    const int rc = launch_pdl(ep_expert_pack_kernel<WIDE>, dim3(a.R_max), dim3(kPackThreads), 0, st, a);
+    if (rc != EP_OK) return rc;
+    static const cudaError_t set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+    if (set != cudaSuccess) return launch_result(set);
+    const int grid = resident_blocks(kern, S::THREADS, S::SMEM);
+    if (grid <= 0) return EP_ERR_CUDA;
+    return launch_pdl(kern, dim3(grid), dim3(S::THREADS), S::SMEM, st, a);
+}
+
+using FewRows = Shape<2, 1, 256, 2, 8>;
+using MoreRows = Shape<2, 2, 384, 1, 8>;
+
+// KS: the split that ends soonest when every CTA takes its rounds of items one after another, a round lasting its
+// warps' steps and about one more to begin and end an item (half a step more to join sums).
+template <typename S>
+int choose_split(const ExpertArgs &a, int steps, float chunks) {
+    const int n_out = a.swiglu ? a.N / 2 : a.N, per_warp = S::MT * (a.swiglu ? 8 : 16);
+    int best = 1;
+    float best_time = 0.0f;
+    for (int ks = 1; ks <= 4 && ks <= steps; ks *= 2) {
+        const int rows = per_warp * (S::WARPS / ks);
+        const float items = chunks * (float)((n_out + rows - 1) / rows);
+        const float time = ceilf(items / (152.0f * S::CTAS)) * ((float)((steps + ks - 1) / ks) + (ks > 1 ? 1.5f : 1.0f));
+        if (ks == 1 || time < best_time) {
+            best = ks;
+            best_time = time;
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -78,25 +461,47 @@ ep_expert_matvec_kernel(ExpertArgs a) {
 
 using namespace ep;
 
+extern "C" size_t ep_expert_matvec_workspace_bytes(const ep_layout_t *L, int hidden_size) {
+    if (!layout_ok(L) || !hidden_ok(hidden_size)) return 0;
+    const size_t R = layout_rows(L);
+    return R * pack_steps(hidden_size) * 512 + (R + 3) / 4 * 16 + 16;
+}
+
 extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t *codes, const uint8_t *scales,
                                 const float *row_scale, int hidden_size, int out_rows, int swiglu,
-                                const ep_layout_t *L, uint16_t *out, void *stream) {
+                                const ep_layout_t *L, uint16_t *out, void *workspace, size_t workspace_bytes,
+                                void *stream) {
     EP_NVTX_RANGE("ep_expert_matvec");
     const int H = hidden_size, N = out_rows;
     if (!layout_ok(L) || !hidden_ok(H) || N < 1 || N > kMaxN || (swiglu != 0 && swiglu != 1)) return EP_ERR_INVALID_ARG;
     if ((x_by_token != 0 && x_by_token != 1) || (swiglu && N % 2 != 0)) return EP_ERR_INVALID_ARG;
-    const void *ptrs[] = {x, codes, scales, row_scale, out};
+    const void *ptrs[] = {x, codes, scales, row_scale, out, workspace};
     for (const void *p : ptrs)
         if (!aligned16(p)) return EP_ERR_INVALID_ARG;
     if (L->T == 0) return EP_OK;
     for (const void *p : ptrs)
         if (!p) return EP_ERR_INVALID_ARG;
     if (x_by_token && !L->src_info) return EP_ERR_INVALID_ARG;
-    ExpertArgs a = {x, codes, scales, row_scale, H, N, x_by_token, swiglu, L->T, L->E + L->fused_shared,
-                    layout_rows(L), L->row_offsets, L->src_info, L->status, out};
-    const int n_out = swiglu ? N / 2 : N;
-    const int warps = kExpertThreads / 32;
-    const int rows = a.R_max < 256 ? a.R_max : 256;
-    return launch_pdl(ep_expert_matvec_kernel, dim3((n_out + warps - 1) / warps, rows), dim3(kExpertThreads), 0,
-                      as_stream(stream), a);
+    if (workspace_bytes < ep_expert_matvec_workspace_bytes(L, H)) return EP_ERR_INVALID_ARG;
+    ExpertArgs a = {};
+    a.x = x; a.codes = codes; a.scales = scales; a.row_scale = row_scale;
+    a.H = H; a.N = N; a.by_token = x_by_token; a.swiglu = swiglu;
+    a.T = L->T; a.G = L->E + L->fused_shared; a.R_max = layout_rows(L);
+    a.row_offsets = L->row_offsets; a.src_info = L->src_info; a.status = L->status;
+    const int steps = pack_steps(H);
+    a.xw = (uint4 *)workspace;
+    a.xs = (float *)(a.xw + (size_t)a.R_max * steps * 32);
+    a.out = out;
+    // rows that share weights: up to 8 per expert take the kernel whose passes serve 8
+    const float per_expert = (float)L->T * L->K / L->E;
+    const bool few = per_expert <= 6.0f;
+    // chunks that a layout of this many rows has, if the router spreads them evenly
+    const float active = L->E * (1.0f - expf(-per_expert));
+    const float rows = few ? 8.0f : 16.0f;
+    const float chunks = active * fmaxf(1.0f, per_expert / rows + 0.5f) + (L->fused_shared ? ceilf(L->T / rows) : 0.0f);
+    a.KS = few ? choose_split<FewRows>(a, steps, chunks) : choose_split<MoreRows>(a, steps, chunks);
+    const bool wide = H % 64 == 0 && (reinterpret_cast<uintptr_t>(codes) & 31u) == 0;
+    cudaStream_t st = as_stream(stream);
+    if (few) return wide ? launch_expert_matvec<true, FewRows>(a, st) : launch_expert_matvec<false, FewRows>(a, st);
+    return wide ? launch_expert_matvec<true, MoreRows>(a, st) : launch_expert_matvec<false, MoreRows>(a, st);
 }

@@ -482,6 +482,9 @@ int ep_router_topk_bwd(const float *grad_probs, const void *logits, long long st
                        const int32_t *topk_ids, int T, int n_experts, int K, int score,
                        int renormalize, float scale, void *grad_logits, void *stream);
 
+/* Scratch bytes ep_expert_matvec needs for this layout's sizes (0 on invalid sizes). */
+size_t ep_expert_matvec_workspace_bytes(const ep_layout_t *L, int hidden_size);
+
 /*
  * ep_expert_matvec -- the experts' products for batches of few tokens: every row of a layout times
  * the 4-bit weights of its group.
@@ -495,12 +498,16 @@ int ep_router_topk_bwd(const float *grad_probs, const void *logits, long long st
  *   N          out_rows, 1 <= N <= 65536; with swiglu 1 even: N/2 gate rows, then N/2 up rows.
  *   -> out     [R_max * N] bf16: out[r, n] = weight row n . x, or with swiglu [R_max * N/2] bf16:
  *              silu(gate) * up, silu(v) = v / (1 + exp(-v)); fp32 sums, rounded once.
+ *   workspace  ep_expert_matvec_workspace_bytes(L, H) bytes (about 2H bytes per row of R_max), 16-byte
+ *              aligned; needs no initialisation, and calls that share
+ *              one must not overlap on the GPU.
  * The rows [0, row_offsets[G]) are written; a padding row is the product of a zero row.  Nothing
  * is written while the layout's status word is non-zero.
  */
 int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t *codes, const uint8_t *scales,
                      const float *row_scale, int hidden_size, int out_rows, int swiglu,
-                     const ep_layout_t *L, uint16_t *out, void *stream);
+                     const ep_layout_t *L, uint16_t *out, void *workspace,
+                     size_t workspace_bytes, void *stream);
 
 /* Human-readable name of a return code. */
 const char *ep_strerror(int code);

@@ -38,7 +38,10 @@ def check(ep, L, w, by_token, swiglu, seed, zero=()):
     n_out = N // 2 if swiglu else N
     buf = torch.full(((L.R_max + 2) * n_out + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
     out = buf[:L.R_max * n_out].view(L.R_max, n_out)
-    got = ep.expert_matvec(x, codes, scales, row_scale, L, by_token=by_token, swiglu=swiglu, out=out)
+    nws = ep.expert_matvec_workspace_bytes(L, H) if L.T else 16
+    ws = torch.full((nws + 256,), 0xFF, dtype=torch.uint8, device="cuda")        # NaN where nothing is written
+    got = ep.expert_matvec(x, codes, scales, row_scale, L, by_token=by_token, swiglu=swiglu, out=out, workspace=ws[:nws])
+    assert (ws[nws:] == 0xFF).all()
     assert ep.read_status(L) == 0
     off = L.row_offsets.cpu().numpy()
     src = L.src_info.cpu().numpy()
@@ -218,3 +221,5 @@ def test_no_tokens_and_refusals():
         ep.expert_matvec(x, *odd, L, swiglu=True)                             # gate and up rows: an even number
     with pytest.raises(ValueError):
         ep.expert_matvec(x, codes, scales, row_scale, L, out=torch.empty(3, 24, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ep.EPError):
+        ep.expert_matvec(x, codes, scales, row_scale, L, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))

@@ -76,15 +76,18 @@ def test_expert_refusals():
                      workspace=256, workspace_bytes=1 << 20, T=4, K=2, E=8, P=1, capacity=4, fused_shared=0,
                      pad_multiple=1, row_capacity=0)
     ref_ = ctypes.byref(lay)
-    ok = dict(x=256, by_token=1, codes=256, scales=256, rs=256, H=64, N=32, swiglu=0, L=ref_, out=256)
+    ok = dict(x=256, by_token=1, codes=256, scales=256, rs=256, H=64, N=32, swiglu=0, L=ref_, out=256, ws=256, nws=1 << 20)
 
     def call(**kw):
         return L.ep_expert_matvec(*{**ok, **kw}.values(), None)
 
     for kw in (dict(x=None), dict(codes=None), dict(scales=None), dict(rs=None), dict(out=None), dict(x=264), dict(out=258),
-               dict(codes=257), dict(H=24), dict(H=0), dict(H=32784), dict(N=0), dict(N=65537), dict(N=33, swiglu=1),
+               dict(codes=257), dict(ws=None), dict(ws=264), dict(nws=8 * 512 + 47), dict(H=24), dict(H=0), dict(H=32784), dict(N=0), dict(N=65537), dict(N=33, swiglu=1),
                dict(swiglu=2), dict(by_token=2), dict(L=None), dict(L=ctypes.byref(ep._Layout()))):
         assert call(**kw) == bad, kw
+    # 8 rows x 256 k in fp16, and 8 scales
+    assert L.ep_expert_matvec_workspace_bytes(ref_, 64) == 8 * 512 + 32 + 16
+    assert L.ep_expert_matvec_workspace_bytes(ref_, 24) == 0
     lay.src_info = None
     assert call() == bad                       # token gathering needs src_info
     lay.src_info = 256
