@@ -132,7 +132,13 @@ def _check(rc: int, what: str):
         raise EPError(rc, what)
 
 
+# the current stream's handle without the Stream object around it (2.6 us of a call's host time on GB300's host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
+    if stream is None and _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -217,6 +223,7 @@ class Layout:
             raise EPError(EP_ERR_INVALID_ARG, "layout sizes")
         self.workspace = torch.zeros(nb, dtype=torch.uint8, device=dev)
         self.capacity = T
+        self.matvec_bytes = {}                   # expert_matvec's workspace size by H: set by the sizes alone
         self.c = _Layout(
             row_offsets=self.row_offsets.data_ptr(), expert_ids=self.expert_ids.data_ptr(),
             src_info=self.src_info.data_ptr(), row_of=self.row_of.data_ptr(),
@@ -564,10 +571,11 @@ def dispatch_bwd(grad_rows: torch.Tensor, L: Layout, out: torch.Tensor | None = 
 
 
 def _matrix(t: torch.Tensor, what: str):
-    """Pointer, row stride and element type of a 2-D CUDA tensor whose rows are contiguous."""
+    """Pointer, rows, columns, row stride and element type of a 2-D CUDA tensor whose rows are contiguous."""
     if t.dim() != 2:
         raise ValueError(f"{what}: expected a 2-D tensor, got {tuple(t.shape)}")
-    if t.dtype not in DTYPES:
+    dt = DTYPES.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{what}: dtype {t.dtype} not in {tuple(DTYPES)}")
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
@@ -577,27 +585,23 @@ def _matrix(t: torch.Tensor, what: str):
         stride = cols
     if (cols > 1 and step != 1) or stride < cols:
         raise ValueError(f"{what}: rows must be contiguous and not overlap, got strides {t.stride()}")
-    return t.data_ptr(), stride, DTYPES[t.dtype]
+    return t.data_ptr(), rows, cols, stride, dt
 
 
-def _vector(t: torch.Tensor, n: int, dtypes, what: str):
-    """Pointer of a contiguous CUDA tensor [n]."""
+def _buffer(t: torch.Tensor, shape: tuple, dtypes, what: str) -> int:
+    """Pointer of a contiguous CUDA tensor of this shape."""
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype} not in {dtypes}")
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{what}: expected [{n}], got {tuple(t.shape)}")
-    return _ptr(t)
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected {shape}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
 
 
-def _dense(t: torch.Tensor, rows: int, cols: int, dtype: torch.dtype, what: str):
-    """Pointer of a contiguous CUDA tensor [rows, cols]."""
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: dtype {t.dtype} is not {dtype}")
-    if t.shape != (rows, cols):
-        raise ValueError(f"{what}: expected {(rows, cols)}, got {tuple(t.shape)}")
-    return _ptr(t)
-
-
+_I32, _U8 = (torch.int32,), (torch.uint8,)
 _F32 = (torch.float32,)
 
 
@@ -607,19 +611,18 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
 
     x [T, H] bf16 / fp16 / fp32 (rows may have a stride); weight and bias [H] in x's dtype or
     fp32.  ``out``: the three buffers."""
-    px, ld, dt = _matrix(x, "x")
-    T, H = x.shape
-    params = (x.dtype, torch.float32)
-    pw = _vector(weight, H, params, "weight")
-    pb = None if bias is None else _vector(bias, H, (weight.dtype,), "bias")
+    px, T, H, ld, dt = _matrix(x, "x")
+    xt, wt = x.dtype, weight.dtype
+    pw = _buffer(weight, (H,), (xt, torch.float32), "weight")
+    pb = None if bias is None else _buffer(bias, (H,), (wt,), "bias")
     if out is None:
         f32 = dict(dtype=torch.float32, device=x.device)
-        out = (torch.empty(T, H, dtype=x.dtype, device=x.device), None if rms else torch.empty(T, **f32),
+        out = (torch.empty(T, H, dtype=xt, device=x.device), None if rms else torch.empty(T, **f32),
                torch.empty(T, **f32))
     y, mean, rstd = out
-    rc = _lib.ep_layer_norm(px, ld, dt, pw, pb, DTYPES[weight.dtype], T, H, eps, int(bool(rms)),
-                            _dense(y, T, H, x.dtype, "y"), None if rms else _vector(mean, T, _F32, "mean"),
-                            _vector(rstd, T, _F32, "rstd"), _stream(stream))
+    rc = _lib.ep_layer_norm(px, ld, dt, pw, pb, DTYPES[wt], T, H, eps, 1 if rms else 0, _buffer(y, (T, H), (xt,), "y"),
+                            None if rms else _buffer(mean, (T,), _F32, "mean"), _buffer(rstd, (T,), _F32, "rstd"),
+                            _stream(stream))
     _check(rc, "ep_layer_norm")
     return y, None if rms else mean, rstd
 
@@ -632,38 +635,48 @@ def layer_norm_bwd_workspace_bytes(T: int, H: int) -> int:
     return n
 
 
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A call's own workspace, allocated on the stream it runs on so that its reuse is ordered behind the call."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | None,
                    rstd: torch.Tensor, rms: bool = False, bias: bool = False, out=None,
                    workspace: torch.Tensor | None = None, stream=None):
     """ep_layer_norm_bwd -> (grad_x [T, H] in x's dtype, grad_weight fp32 [H], grad_bias fp32 [H] or
     None without ``bias``).  mean (None when rms) and rstd come from ``layer_norm``.  ``workspace``: a
-    uint8 buffer of ``layer_norm_bwd_workspace_bytes`` to reuse."""
-    px, ldx, dt = _matrix(x, "x")
-    T, H = x.shape
-    pg, ldg, gdt = _matrix(grad_y, "grad_y")
-    if grad_y.shape != x.shape or gdt != dt:
+    uint8 buffer of ``layer_norm_bwd_workspace_bytes`` to reuse; without one a call allocates its own."""
+    px, T, H, ldx, dt = _matrix(x, "x")
+    pg, Tg, Hg, ldg, gdt = _matrix(grad_y, "grad_y")
+    if Tg != T or Hg != H or gdt != dt:
         raise ValueError("grad_y and x differ in shape or dtype")
-    pw = _vector(weight, H, (x.dtype, torch.float32), "weight")
+    xt = x.dtype
+    pw = _buffer(weight, (H,), (xt, torch.float32), "weight")
     if out is None:
         f32 = dict(dtype=torch.float32, device=x.device)
-        out = (torch.empty(T, H, dtype=x.dtype, device=x.device), torch.empty(H, **f32),
+        out = (torch.empty(T, H, dtype=xt, device=x.device), torch.empty(H, **f32),
                torch.empty(H, **f32) if bias else None)
     if workspace is None:
-        workspace = torch.empty(layer_norm_bwd_workspace_bytes(T, H), dtype=torch.uint8, device=x.device)
+        workspace = _scratch(layer_norm_bwd_workspace_bytes(T, H), x.device, stream)
     dx, dw, db = out
     rc = _lib.ep_layer_norm_bwd(pg, ldg, px, ldx, dt, pw, DTYPES[weight.dtype],
-                                None if rms else _vector(mean, T, _F32, "mean"), _vector(rstd, T, _F32, "rstd"), T, H,
-                                int(bool(rms)), _dense(dx, T, H, x.dtype, "grad_x"), _vector(dw, H, _F32, "grad_weight"),
-                                _vector(db, H, _F32, "grad_bias") if bias else None, _ptr(workspace),
+                                None if rms else _buffer(mean, (T,), _F32, "mean"), _buffer(rstd, (T,), _F32, "rstd"), T,
+                                H, 1 if rms else 0, _buffer(dx, (T, H), (xt,), "grad_x"),
+                                _buffer(dw, (H,), _F32, "grad_weight"),
+                                _buffer(db, (H,), _F32, "grad_bias") if bias else None, _ptr(workspace),
                                 workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc, "ep_layer_norm_bwd")
     return dx, dw, db if bias else None
 
 
 def _score(score: str) -> int:
-    if score not in SCORES:
+    n = SCORES.get(score)
+    if n is None:
         raise ValueError(f"score {score!r} not in {tuple(SCORES)}")
-    return SCORES[score]
+    return n
 
 
 def router_topk(logits: torch.Tensor, K: int, bias: torch.Tensor | None = None, score: str = "softmax",
@@ -671,15 +684,14 @@ def router_topk(logits: torch.Tensor, K: int, bias: torch.Tensor | None = None, 
     """ep_router_topk -> (topk_ids int32 [T, K], probs fp32 [T, K]) from logits [T, E] bf16 / fp16 /
     fp32 (rows may have a stride): the K largest of logit + bias (fp32 [E]), ties to the lower id; -1
     with probability 0 where only -inf is left."""
-    pl, ld, dt = _matrix(logits, "logits")
-    T, E = logits.shape
+    pl, T, E, ld, dt = _matrix(logits, "logits")
     if out is None:
         out = (torch.empty(T, K, dtype=torch.int32, device=logits.device),
                torch.empty(T, K, dtype=torch.float32, device=logits.device))
     ids, probs = out
-    rc = _lib.ep_router_topk(pl, ld, dt, None if bias is None else _vector(bias, E, _F32, "bias"), T, E, K,
-                             _score(score), int(bool(renormalize)), scale, _dense(ids, T, K, torch.int32, "topk_ids"),
-                             _dense(probs, T, K, torch.float32, "probs"), _stream(stream))
+    rc = _lib.ep_router_topk(pl, ld, dt, None if bias is None else _buffer(bias, (E,), _F32, "bias"), T, E, K,
+                             _score(score), 1 if renormalize else 0, scale, _buffer(ids, (T, K), _I32, "topk_ids"),
+                             _buffer(probs, (T, K), _F32, "probs"), _stream(stream))
     _check(rc, "ep_router_topk")
     return ids, probs
 
@@ -688,16 +700,15 @@ def router_topk_bwd(grad_probs: torch.Tensor, logits: torch.Tensor, topk_ids: to
                     renormalize: bool = True, scale: float = 1.0, out: torch.Tensor | None = None, stream=None):
     """ep_router_topk_bwd -> grad_logits [T, E] in the logits' dtype; the arguments of the forward
     call, its ids, and grad_probs fp32 [T, K]."""
-    pl, ld, dt = _matrix(logits, "logits")
-    T, E = logits.shape
+    pl, T, E, ld, dt = _matrix(logits, "logits")
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be [T, K]")
     K = topk_ids.shape[1]
     if out is None:
         out = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
-    rc = _lib.ep_router_topk_bwd(_dense(grad_probs, T, K, torch.float32, "grad_probs"), pl, ld, dt,
-                                 _dense(topk_ids, T, K, torch.int32, "topk_ids"), T, E, K, _score(score),
-                                 int(bool(renormalize)), scale, _dense(out, T, E, logits.dtype, "grad_logits"),
+    rc = _lib.ep_router_topk_bwd(_buffer(grad_probs, (T, K), _F32, "grad_probs"), pl, ld, dt,
+                                 _buffer(topk_ids, (T, K), _I32, "topk_ids"), T, E, K, _score(score),
+                                 1 if renormalize else 0, scale, _buffer(out, (T, E), (logits.dtype,), "grad_logits"),
                                  _stream(stream))
     _check(rc, "ep_router_topk_bwd")
     return out
@@ -705,9 +716,12 @@ def router_topk_bwd(grad_probs: torch.Tensor, logits: torch.Tensor, topk_ids: to
 
 def expert_matvec_workspace_bytes(L: Layout, H: int) -> int:
     """ep_expert_matvec_workspace_bytes: scratch bytes of ``expert_matvec`` on this layout's sizes."""
-    n = int(_lib.ep_expert_matvec_workspace_bytes(L.ref, H))
-    if n == 0:
-        raise EPError(EP_ERR_INVALID_ARG, "expert_matvec sizes")
+    n = L.matvec_bytes.get(H)
+    if n is None:
+        n = int(_lib.ep_expert_matvec_workspace_bytes(L.ref, H))
+        if n == 0:
+            raise EPError(EP_ERR_INVALID_ARG, "expert_matvec sizes")
+        L.matvec_bytes[H] = n
     return n
 
 
@@ -719,26 +733,26 @@ def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ro
     fp32 [G, N].  x bf16 is [T, H] when by_token (rows take their token's vector), else [R_max, H].
     ``workspace``: a uint8 buffer of ``expert_matvec_workspace_bytes`` to reuse; without one a call
     allocates its own on the stream it runs on."""
-    if codes.dim() != 3 or codes.dtype != torch.uint8 or codes.shape[0] != L.G:
-        raise ValueError(f"codes: expected uint8 [{L.G}, N, H/2], got {codes.dtype} {tuple(codes.shape)}")
-    N, H = codes.shape[1], 2 * codes.shape[2]
-    if scales.dtype != torch.uint8 or scales.shape != (L.G, N, H // 16):
-        raise ValueError(f"scales: expected uint8 {(L.G, N, H // 16)}, got {scales.dtype} {tuple(scales.shape)}")
-    _need(row_scale, None, N, _F32, "row_scale", exact_rows=L.G)
+    if codes.dim() != 3:
+        raise ValueError(f"codes: expected [{L.G}, N, H/2], got {tuple(codes.shape)}")
+    G, N, half = codes.shape
+    H = 2 * half
+    pc = _buffer(codes, (L.G, N, half), _U8, "codes")
+    ps = _buffer(scales, (L.G, N, H // 16), _U8, "scales")
+    pr = _buffer(row_scale, (L.G, N), _F32, "row_scale")
     if by_token:
-        _need(x, None, H, _BF16, "x", exact_rows=L.T)
+        px = _buffer(x, (L.T, H), _BF16, "x")
     else:
         _need(x, L.R_max, H, _BF16, "x")
+        px = _bits(x)
     n_out = N // 2 if swiglu else N
     if out is None:
         out = torch.empty(max(L.R_max, 1), n_out, dtype=torch.bfloat16, device=x.device)
     _need(out, L.R_max, n_out, _BF16, "out")
     if workspace is None:
-        with torch.cuda.stream(stream):     # a buffer of that stream's, so that its reuse is ordered behind this call
-            workspace = torch.empty(expert_matvec_workspace_bytes(L, H), dtype=torch.uint8, device=x.device)
-    rc = _lib.ep_expert_matvec(_bits(x), int(bool(by_token)), _ptr(codes), _ptr(scales), _ptr(row_scale), H, N,
-                               int(bool(swiglu)), L.ref, _bits(out), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), _stream(stream))
+        workspace = _scratch(expert_matvec_workspace_bytes(L, H), x.device, stream)
+    rc = _lib.ep_expert_matvec(px, 1 if by_token else 0, pc, ps, pr, H, N, 1 if swiglu else 0, L.ref, _bits(out),
+                               _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc, "ep_expert_matvec")
     return out
 

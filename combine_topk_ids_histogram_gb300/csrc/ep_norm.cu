@@ -8,70 +8,352 @@
 //
 // Statistics and sums are fp32.  The variance is summed over (x - mean) in a second pass over
 // registers, so rows with a large mean lose nothing.  Both passes are bound by HBM: each row is
-// read once, kept in registers, and written once.
+// read once and written once.
+//
+// Many rows: one CTA per SM whose threads form groups, a group holding 32 elements of a row per thread, and
+// looping over rows.  Rows arrive in a ring of shared-memory stages by asynchronous copies, so that the
+// bytes in flight (about 170 KB per SM) do not depend on registers, and each group's barriers leave the
+// other groups running.
 #include "ep_host.h"
 #include "ep_types.cuh"
 
 namespace ep {
 namespace {
 
+constexpr int kFwdEpt = 32, kBwdEpt = 32;     // elements of a row per thread in the pipelined kernels
+constexpr int kFwdThreads = 672, kBwdThreads = 512;
+constexpr int kBwdStages = 3;
+template <typename T> constexpr int kFwdStages = sizeof(T) == 4 ? 3 : 4;
+constexpr int kSharedBytes = 226 * 1024; // shared memory for stages and parameters
+constexpr int kBwdMaxH = 8192;
+constexpr int kPartials = 304;           // rows of partial column sums a workspace has room for
+// Few rows.  Forward: one CTA per row while all of them are resident at once (bf16, us against the pipelined kernel: H = 2048,
+// T = 1000 4.2 against 4.7, T = 2000 6.5 against 6.4; H = 7168, T = 304 5.1 against 5.4, T = 600 9.5 against 7.6; H = 256,
+// T = 8000 5.7 against 6.8).  Backward: one launch that reads x and g twice (H = 2048, T = 64 2.4 against 10.1, T = 304 5.5
+// against 10.5, T = 1021 14.9 against 11.1).
+constexpr int kResidentThreads = 152 * 2048;
+constexpr int kFewBwdRows = 456;
+
+constexpr int round_up(int n, int to) { return (n + to - 1) / to * to; }
+
+// Sum of one or two values over the threads of a group of G threads (a whole number of warps); ty is the
+// group's index in its CTA and names its barrier (1 to 15: a CTA has at most 15 groups of several warps).  `red` has
+// room for 32 values, zero past the group's warps, and is not written again before the next barrier of the group.
+__device__ __forceinline__ void group_barrier(int G, int ty) {
+    if (G == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(ty + 1), "r"(G) : "memory");
+}
+__device__ __forceinline__ float group_sum(float a, float *red, int G, int ty) {
+    a = warp_sum(a);
+    if (G == 32) return a;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    group_barrier(G, ty);
+    float s = 0.0f;
+    for (int i = 0; i < (G >> 5); i += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(red + i);
+        s += (v.x + v.y) + (v.z + v.w);
+    }
+    return s;
+}
+__device__ __forceinline__ float2 group_sum2(f32x2 a, f32x2 *red, int G, int ty) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float2 v = f2_get(a);
+        a = f2_add(a, f2(__shfl_xor_sync(kFullMask, v.x, o), __shfl_xor_sync(kFullMask, v.y, o)));
+    }
+    if (G == 32) return f2_get(a);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    group_barrier(G, ty);
+    f32x2 s = f2(0.0f, 0.0f);
+    for (int i = 0; i < (G >> 5); i += 2) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(red + i);
+        s = f2_add(s, f2_add(v.x, v.y));
+    }
+    return f2_get(s);
+}
+
+// How the rows of all matrices of a call lie.
+//   kAligned  on 16-byte boundaries;
+//   kShifted  off them, row for row by the same amount in every matrix (dense matrices of any width): work is by the
+//             aligned 16-byte pieces that cover a row, the first and last of them in part.  The amount repeats every
+//             `period` rows, and a group takes rows that share one, so its columns stay the same;
+//   kAny      anything else: element by element.
+enum Lay { kAligned, kShifted, kAny };
+
+// How a thread of a pipelined kernel holds its EPT elements of a row: in units of E elements as E/2 pairs.  Unit i is
+// piece tid + i * G of 16 bytes (kAny: the elements tid + (i * E + j) * G).  Units past the row's end read its last piece or
+// element instead, which costs no branch (another thread may still be copying it: any value does); what lies outside the
+// row is left out of sums (add) and not stored.
+template <typename T, int EPT, int LAY> struct Units {
+    static constexpr int VEC = 16 / (int)sizeof(T), E = LAY == kAny ? 4 : VEC, N = EPT / E;
+    int tid, G, H, shift;                // shift: elements by which rows follow a 16-byte boundary
+    __device__ __forceinline__ int first(int i) const { return (tid + i * G) * VEC - shift; }   // column of the unit's first element
+    __device__ __forceinline__ int col(int i, int j) const { return LAY == kAny ? tid + (i * E + j) * G : first(i) + j; }
+    __device__ __forceinline__ bool has(int i, int j) const {
+        const int c = col(i, LAY == kAligned ? 0 : j);
+        return c < H && (LAY != kShifted || c >= 0);
+    }
+    __device__ __forceinline__ bool whole(int i) const {            // not for kAny
+        return LAY == kAligned ? has(i, 0) : first(i) >= 0 && first(i) + VEC <= H;
+    }
+    // row: where column 0 is (kAny), or the piece that column 0 is in
+    template <typename P> __device__ __forceinline__ void load(const P *row, int i, f32x2 (&v)[E / 2]) const {
+        float f[E];
+        if constexpr (LAY != kAny) {
+            ld_pack<P, VEC>(row + min(tid + i * G, (H + shift - 1) / VEC) * VEC).unpack(f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j) f[j] = to_f32(row[min(col(i, j), H - 1)]);
+        }
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) v[j] = f2(f[2 * j], f[2 * j + 1]);
+    }
+    __device__ __forceinline__ void store(T *row, int i, const f32x2 (&v)[E / 2]) const {      // row: where column 0 is
+        float f[E];
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) {
+            const float2 p = f2_get(v[j]);
+            f[2 * j] = p.x;
+            f[2 * j + 1] = p.y;
+        }
+        bool vector = false;
+        if constexpr (LAY != kAny) {
+            vector = whole(i);
+            if (vector) st_pack_stream<T, VEC>(row + first(i), f);
+        }
+        if constexpr (LAY != kAligned) {
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (!vector && has(i, j)) row[col(i, j)] = from_f32<T>(f[j]);
+        }
+    }
+    __device__ __forceinline__ void store_sums(float *row, int i, const f32x2 (&v)[E / 2]) const {
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) {
+            const float2 p = f2_get(v[j]);
+            if (has(i, 2 * j)) row[col(i, 2 * j)] = p.x;
+            if (has(i, 2 * j + 1)) row[col(i, 2 * j + 1)] = p.y;
+        }
+    }
+    // sum + the unit's values that are in the row
+    __device__ __forceinline__ f32x2 add(f32x2 sum, int i, const f32x2 (&v)[E / 2]) const {
+        bool done = false;
+        if constexpr (LAY != kAny) {
+            done = whole(i);
+            if (done) {
+                f32x2 s = v[0];
+#pragma unroll
+                for (int j = 1; j < E / 2; ++j) s = f2_add(s, v[j]);
+                sum = f2_add(sum, s);
+            }
+        }
+        if constexpr (LAY != kAligned) {
+            if (!done)
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j) {
+                    const float2 p = f2_get(v[j]);
+                    sum = f2_add(sum, f2(has(i, 2 * j) ? p.x : 0.0f, has(i, 2 * j + 1) ? p.y : 0.0f));
+                }
+        }
+        return sum;
+    }
+};
+
+// The rows of a group: gi-th of n groups.
+struct Rows {
+    int first, step;
+    __device__ __forceinline__ Rows(int gi, int n, int period) {
+        const int kind = gi % period, k = gi / period;              // groups of a kind take the rows of that kind in turn
+        first = kind + k * period;
+        step = (n - kind + period - 1) / period * period;
+    }
+};
+
+// A matrix whose rows a group copies to shared memory as the aligned 16-byte pieces that cover them; a piece that would
+// reach outside the matrix, before its first or after its last row, is copied by elements.  A thread copies pieces tid,
+// tid + G, ...: those it will read itself, so that it has only its own copies to wait for (kAny: the group meets at a
+// barrier).
+template <typename T, int EPT, int LAY> struct RowSource {
+    static constexpr int VEC = 16 / (int)sizeof(T);
+    const T *base, *end;                 // the matrix: end is past the last row's last element
+    long long ld;
+    int H;
+    __device__ __forceinline__ RowSource(const T *m, long long ld_, int rows, int H_)
+        : base(m), end(m + (size_t)(rows - 1) * ld_ + H_), ld(ld_), H(H_) {}
+    static __host__ __device__ __forceinline__ int stage_bytes(int H) { return ((int)sizeof(T) * H + 15) / 16 * 16 + (LAY == kAligned ? 0 : 16); }
+    __device__ __forceinline__ int shift(int row) const {            // elements by which a row follows a 16-byte boundary
+        return LAY == kAligned ? 0 : (int)(reinterpret_cast<uintptr_t>(base + (size_t)row * ld) & 15u) / (int)sizeof(T);
+    }
+    __device__ __forceinline__ void copy(int row, char *stage, int tid, int G) const {
+        const unsigned to = (unsigned)__cvta_generic_to_shared(stage) + tid * 16;
+        const int before = shift(row);
+        const T *from = base + (size_t)row * ld - before + tid * VEC;
+        if constexpr (LAY == kAligned) {
+#pragma unroll
+            for (int i = 0; i < EPT / VEC; ++i)
+                if ((tid + i * G) * VEC < H)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * G * 16), "l"(from + i * G * VEC) : "memory");
+        } else {
+            const int pieces = (before + H + VEC - 1) / VEC;
+            for (int i = 0; tid + i * G < pieces; ++i, from += G * VEC) {
+                if (from >= base && from + VEC <= end) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * G * 16), "l"(from) : "memory");
+                } else {
+                    for (int j = 0; j < VEC; ++j)
+                        if (from + j >= base && from + j < end) reinterpret_cast<T *>(stage)[(tid + i * G) * VEC + j] = from[j];
+                }
+            }
+        }
+    }
+};
+
+// Shared memory of a parameter.
+template <typename W> constexpr __host__ __device__ int param_bytes(int H) { return ((int)sizeof(W) * H + 15) / 16 * 16; }
+// Copies of the parameters: one for all groups, or one behind each group's own boundary.
+constexpr __host__ __device__ int param_copies(int lay, int R) { return lay == kShifted ? R : 1; }
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // ---------------------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------------------
-// Sum over the threads of one row: a warp (WARP) or the whole CTA.  `red` holds one float per
-// warp; two calls in a row use different halves, so one barrier each is enough.
-template <bool WARP>
-__device__ __forceinline__ float row_sum(float v, float *red) {
-    v = warp_sum(v);
-    if (WARP) return v;
-    const int nw = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+template <typename T, typename W, int LAY>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, const W *__restrict__ b,
+               int rows, int H, float eps, int rms, int period, T *__restrict__ y, float *__restrict__ mean_out,
+               float *__restrict__ rstd_out) {
+    constexpr int D = kFwdStages<T>;
+    using U = Units<T, kFwdEpt, LAY>;
+    extern __shared__ __align__(16) char smem[];                    // [copy][weight, bias], [group][stage]
+    __shared__ __align__(16) float s_red[2][32][4];                 // a group's values lie in whole rows of 4
+    const int G = blockDim.x, R = blockDim.y, tid = threadIdx.x, ty = threadIdx.y;
+    if (ty * G + tid < 128) s_red[0][0][ty * G + tid] = s_red[1][0][ty * G + tid] = 0.0f;
+    pdl_begin();
+    const RowSource<T, kFwdEpt, LAY> src(x, ldx, rows, H);
+    const Rows mine(blockIdx.x * R + ty, gridDim.x * R, period);
+    const int step = mine.step, shift = LAY == kShifted && mine.first < rows ? src.shift(mine.first) : 0;
+    const U un{tid, G, H, shift};
+    const int bytes = src.stage_bytes(H), params = param_bytes<W>(H + 2 * U::VEC);
+    char *stages = smem + param_copies(LAY, R) * 2 * params + (size_t)ty * D * bytes;
+    int row = mine.first;
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) {
+        if (row + i * step < rows) src.copy(row + i * step, stages + i * bytes, tid, G);
+        copies_commit();
+    }
+    const float inv_h = 1.0f / (float)H;
+    // the parameters, as far behind a 16-byte boundary as the group's rows (L1 is too small beside the stages to keep them)
+    W *s_w = reinterpret_cast<W *>(smem + (LAY == kShifted ? ty : 0) * 2 * params), *s_b = s_w + params / sizeof(W);
+    for (int c = LAY == kShifted ? tid : ty * G + tid; c < H; c += LAY == kShifted ? G : R * G) {
+        s_w[c + shift] = w[c];
+        if (b) s_b[c + shift] = b[c];
+    }
+    const int red_rows = ((G >> 5) + 3) / 4;
+    float *red0 = &s_red[0][ty * red_rows][0], *red1 = &s_red[1][ty * red_rows][0];
     __syncthreads();
-    float s = 0.0f;
-    for (int i = 0; i < nw; ++i) s += red[i];
-    return s;
+    for (int at = 0, buf = 0; row < rows; row += step, at = at + 1 == D ? 0 : at + 1, buf ^= 1) {
+        copies_wait<D - 2>();
+        if (LAY == kAny) group_barrier(G, ty);
+        // the stage before this one was read before the group's last barrier (or by this thread alone)
+        if (row + (D - 1) * step < rows) src.copy(row + (D - 1) * step, stages + (at == 0 ? D - 1 : at - 1) * bytes, tid, G);
+        copies_commit();
+        const T *s_row = reinterpret_cast<const T *>(stages + at * bytes) + (LAY == kAny ? src.shift(row) : 0);
+        f32x2 d[U::N][U::E / 2];
+#pragma unroll
+        for (int i = 0; i < U::N; ++i) un.load(s_row, i, d[i]);
+        float mean = 0.0f;
+        if (!rms) {
+            f32x2 s = f2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < U::N; ++i) s = un.add(s, i, d[i]);
+            const float2 p = f2_get(s);
+            mean = group_sum(p.x + p.y, red0, G, ty) * inv_h;
+            const f32x2 neg = f2(-mean, -mean);
+#pragma unroll
+            for (int i = 0; i < U::N; ++i)
+#pragma unroll
+                for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_add(d[i][j], neg);
+        }
+        f32x2 q = f2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < U::N; ++i) {
+            f32x2 sq[U::E / 2];
+#pragma unroll
+            for (int j = 0; j < U::E / 2; ++j) sq[j] = f2_mul(d[i][j], d[i][j]);
+            q = un.add(q, i, sq);
+        }
+        const float2 p = f2_get(q);
+        const float rstd = rsqrtf(fmaf(group_sum(p.x + p.y, rms && buf ? red0 : red1, G, ty), inv_h, eps));
+        if (tid == 0) {
+            if (!rms) mean_out[row] = mean;
+            rstd_out[row] = rstd;
+        }
+        const f32x2 r2 = f2(rstd, rstd);
+        T *yr = y + (size_t)row * H;
+#pragma unroll
+        for (int i = 0; i < U::N; ++i) {
+            f32x2 u[U::E / 2];
+            un.load(s_w, i, u);
+#pragma unroll
+            for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_mul(f2_mul(d[i][j], r2), u[j]);
+            if (b) {
+                un.load(s_b, i, u);
+#pragma unroll
+                for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_add(d[i][j], u[j]);
+            }
+            un.store(yr, i, d[i]);
+        }
+    }
 }
 
-// NV vectors of VEC elements per thread, one row per warp or per CTA.
-template <typename T, typename W, int VEC, int NV, bool WARP>
-__global__ void __launch_bounds__(1024)
-ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, const W *__restrict__ b,
-               int rows, int H, float eps, int rms, int one_wave, T *__restrict__ y,
-               float *__restrict__ mean_out, float *__restrict__ rstd_out) {
-    __shared__ float red[2][32];
+// Few rows, or rows wider than the pipelined kernel's: one CTA per row, NV vectors per thread straight from memory.
+template <typename T, typename W, int VEC, int NV>
+__global__ void __launch_bounds__(1024, 1)
+ep_norm_row_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, const W *__restrict__ b,
+                   int H, float eps, int rms, int one_wave, T *__restrict__ y, float *__restrict__ mean_out,
+                   float *__restrict__ rstd_out) {
+    __shared__ __align__(16) float s_red[2][32];
+    if (threadIdx.x < 32) s_red[0][threadIdx.x] = s_red[1][threadIdx.x] = 0.0f;
+    __syncthreads();
     pdl_begin_if(one_wave);
-    const int group = WARP ? 32 : blockDim.x;
-    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int row = WARP ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-    if (WARP && row >= rows) return;
-    const int nv = H / VEC;
+    const int G = blockDim.x, tid = threadIdx.x, row = blockIdx.x, nv = H / VEC;
     const T *xr = x + (size_t)row * ldx;
-    Pack<T, VEC> d[NV];
+    float d[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int v = tid + i * group;
-        if (v < nv) d[i] = ld_pack_stream<T, VEC>(xr + (size_t)v * VEC);
+        const int v = tid + i * G;
+        if (v < nv) {
+            ld_pack_stream<T, VEC>(xr + (size_t)v * VEC).unpack(d[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) d[i][j] = 0.0f;
+        }
+    }
+    Pack<W, VEC> w0, b0;                 // one vector per thread: the parameters are on their way while the row is reduced
+    if (NV == 1 && tid < nv) {
+        w0 = ld_pack<W, VEC>(w + (size_t)tid * VEC);
+        if (b) b0 = ld_pack<W, VEC>(b + (size_t)tid * VEC);
     }
     float mean = 0.0f;
     if (!rms) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (tid + i * group < nv)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) s += d[i].f(j);
-        mean = row_sum<WARP>(s, red[0]) / (float)H;
+            for (int j = 0; j < VEC; ++j) s += d[i][j];
+        mean = group_sum(s, s_red[0], G, 0) / (float)H;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) d[i][j] = tid + i * G < nv ? d[i][j] - mean : 0.0f;
     }
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (tid + i * group < nv)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float c = d[i].f(j) - mean;
-                q = fmaf(c, c, q);
-            }
-    const float rstd = 1.0f / sqrtf(row_sum<WARP>(q, red[1]) / (float)H + eps);
+        for (int j = 0; j < VEC; ++j) q = fmaf(d[i][j], d[i][j], q);
+    const float rstd = 1.0f / sqrtf(group_sum(q, s_red[1], G, 0) / (float)H + eps);
     if (tid == 0) {
         if (!rms) mean_out[row] = mean;
         rstd_out[row] = rstd;
@@ -79,143 +361,215 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
     T *yr = y + (size_t)row * H;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int v = tid + i * group;
-        if (v >= nv) break;
-        const Pack<W, VEC> wv = ld_pack<W, VEC>(w + (size_t)v * VEC);
-        float o[VEC];
+        const int v = tid + i * G;
+        if (v < nv) {
+            float o[VEC];
+            if (NV > 1) w0 = ld_pack<W, VEC>(w + (size_t)v * VEC);
+            w0.unpack(o);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = (d[i].f(j) - mean) * rstd * wv.f(j);
-        if (b) {
-            const Pack<W, VEC> bv = ld_pack<W, VEC>(b + (size_t)v * VEC);
+            for (int j = 0; j < VEC; ++j) o[j] *= d[i][j] * rstd;
+            if (b) {
+                float c[VEC];
+                if (NV > 1) b0 = ld_pack<W, VEC>(b + (size_t)v * VEC);
+                b0.unpack(c);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) o[j] += bv.f(j);
+                for (int j = 0; j < VEC; ++j) o[j] += c[j];
+            }
+            st_pack_stream<T, VEC>(yr + (size_t)v * VEC, o);
         }
-        st_pack_stream<T, VEC>(yr + (size_t)v * VEC, o);
     }
 }
 
 // ---------------------------------------------------------------------------------------
-// backward, rows of up to kFusedH elements: a group of threads keeps one row of x and g in
-// registers and the sums of its columns over all its rows beside them, so x and g are read once
-// for dx, dw and db.  Group sums are joined per CTA in shared memory, CTA sums by
+// backward, rows of up to kBwdMaxH elements: x and g are read once for dx, dw and db.  A thread keeps the sums of
+// its columns over all the group's rows in registers; groups are joined per CTA in shared memory, CTAs by
 // ep_norm_cols_kernel, both in a fixed order.
 // ---------------------------------------------------------------------------------------
-constexpr int kFusedH = 8192;
-constexpr int kFusedThreads = 512;
-constexpr int kPartials = 304;   // rows of partial column sums: two CTAs on each of 152 SMs
-
-// Sum of two values over the threads of a group of G threads (ty: the group's index in the CTA).
-__device__ __forceinline__ float2 group_sum2(float a, float b, float2 *red, int G, int ty) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (G == 32) return make_float2(a, b);
-    const int nw = G >> 5;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
-    asm volatile("bar.sync %0, %1;" ::"r"(ty + 1), "r"(G) : "memory");
-    float2 s = make_float2(0.0f, 0.0f);
-    for (int i = 0; i < nw; ++i) {
-        s.x += red[i].x;
-        s.y += red[i].y;
-    }
-    return s;
-}
-
-template <typename T, typename W, int VEC, int NV>
-__global__ void __launch_bounds__(kFusedThreads)
+template <typename T, typename W, int LAY>
+__global__ void __launch_bounds__(kBwdThreads, 1)
 ep_norm_bwd_kernel(const T *__restrict__ g, long long ldg, const T *__restrict__ x, long long ldx,
                    const W *__restrict__ w, const float *__restrict__ mean_in,
-                   const float *__restrict__ rstd_in, int rows, int H, int rms, int want_db,
+                   const float *__restrict__ rstd_in, int rows, int H, int rms, int want_db, int period,
                    T *__restrict__ dx, float *__restrict__ part) {
-    extern __shared__ float s_cols[];   // [2][H], with more than one group per CTA
-    __shared__ float2 s_red[2][kFusedThreads / 32];
-    pdl_begin();
+    constexpr int D = kBwdStages;
+    using U = Units<T, kBwdEpt, LAY>;
+    extern __shared__ __align__(16) char smem[];                    // [copy] weight, [group][stage][x, g]; at the end [group][2][H] sums
+    __shared__ __align__(16) f32x2 s_red[2][32][2];                 // a group's values lie in whole rows of 2
     const int G = blockDim.x, R = blockDim.y, tid = threadIdx.x, ty = threadIdx.y;
-    const int nv = H / VEC;
-    float dw[NV][VEC], db[NV][VEC];
+    if (ty * G + tid < 64) s_red[0][0][ty * G + tid] = s_red[1][0][ty * G + tid] = f2(0.0f, 0.0f);
+    pdl_begin();
+    const RowSource<T, kBwdEpt, LAY> sx(x, ldx, rows, H), sg(g, ldg, rows, H);
+    const Rows mine(blockIdx.x * R + ty, gridDim.x * R, period);
+    const int step = mine.step, shift = LAY == kShifted && mine.first < rows ? sx.shift(mine.first) : 0;
+    const U un{tid, G, H, shift};
+    const int bytes = sx.stage_bytes(H), params = param_bytes<W>(H + 2 * U::VEC);
+    char *stages = smem + param_copies(LAY, R) * params + (size_t)ty * D * 2 * bytes;
+    W *s_w = reinterpret_cast<W *>(smem + (LAY == kShifted ? ty : 0) * params);
+    for (int c = LAY == kShifted ? tid : ty * G + tid; c < H; c += LAY == kShifted ? G : R * G) s_w[c + shift] = w[c];
+    int row = mine.first;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) dw[i][j] = db[i][j] = 0.0f;
-    int buf = 0;
-    for (int row = blockIdx.x * R + ty; row < rows; row += gridDim.x * R, buf ^= 1) {
-        Pack<T, VEC> xv[NV], gv[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = tid + i * G;
-            if (v < nv) {
-                xv[i] = ld_pack_stream<T, VEC>(x + (size_t)row * ldx + (size_t)v * VEC);
-                gv[i] = ld_pack_stream<T, VEC>(g + (size_t)row * ldg + (size_t)v * VEC);
-            }
+    for (int i = 0; i < D - 1; ++i) {
+        if (row + i * step < rows) {
+            sx.copy(row + i * step, stages + 2 * i * bytes, tid, G);
+            sg.copy(row + i * step, stages + (2 * i + 1) * bytes, tid, G);
         }
+        copies_commit();
+    }
+    f32x2 dw[U::N][U::E / 2], db[U::N][U::E / 2];
+#pragma unroll
+    for (int i = 0; i < U::N; ++i)
+#pragma unroll
+        for (int j = 0; j < U::E / 2; ++j) dw[i][j] = db[i][j] = f2(0.0f, 0.0f);
+    const float inv_h = 1.0f / (float)H;
+    float next_mean = 0.0f, next_rstd = 0.0f;                       // a row ahead
+    if (row < rows) {
+        if (!rms) next_mean = mean_in[row];
+        next_rstd = rstd_in[row];
+    }
+    f32x2 *red[2] = {&s_red[0][ty * (((G >> 5) + 1) / 2)][0], &s_red[1][ty * (((G >> 5) + 1) / 2)][0]};
+    __syncthreads();
+    for (int at = 0, buf = 0; row < rows; row += step, at = at + 1 == D ? 0 : at + 1, buf ^= 1) {
+        const float mean = next_mean, rstd = next_rstd;
+        if (row + step < rows) {
+            if (!rms) next_mean = mean_in[row + step];
+            next_rstd = rstd_in[row + step];
+        }
+        copies_wait<D - 2>();
+        if (LAY == kAny) group_barrier(G, ty);
+        // the stage before this one was read to the end before (kAny: before the barrier just passed)
+        if (row + (D - 1) * step < rows) {
+            char *to = stages + 2 * (at == 0 ? D - 1 : at - 1) * bytes;
+            sx.copy(row + (D - 1) * step, to, tid, G);
+            sg.copy(row + (D - 1) * step, to + bytes, tid, G);
+        }
+        copies_commit();
+        const T *xr = reinterpret_cast<const T *>(stages + 2 * at * bytes) + (LAY == kAny ? sx.shift(row) : 0);
+        const T *gr = reinterpret_cast<const T *>(stages + (2 * at + 1) * bytes) + (LAY == kAny ? sg.shift(row) : 0);
+        const f32x2 neg_mean = f2(-mean, -mean), r2 = f2(rstd, rstd);
+        f32x2 sa = f2(0.0f, 0.0f), sax = sa;
+#pragma unroll
+        for (int i = 0; i < U::N; ++i) {
+            f32x2 xe[U::E / 2], ge[U::E / 2], u[U::E / 2];
+            un.load(xr, i, xe);
+            un.load(gr, i, ge);
+            un.load(s_w, i, u);
+#pragma unroll
+            for (int j = 0; j < U::E / 2; ++j) {
+                const f32x2 xh = f2_mul(f2_add(xe[j], neg_mean), r2);
+                dw[i][j] = f2_fma(ge[j], xh, dw[i][j]);
+                if (want_db) db[i][j] = f2_add(db[i][j], ge[j]);
+                u[j] = f2_mul(ge[j], u[j]);
+                xe[j] = f2_mul(u[j], xh);
+            }
+            sa = un.add(sa, i, u);
+            sax = un.add(sax, i, xe);
+        }
+        const float2 pa = f2_get(sa), px = f2_get(sax);
+        const float2 s = group_sum2(f2(pa.x + pa.y, px.x + px.y), red[buf], G, ty);
+        const float ma = rms ? 0.0f : s.x * inv_h, max_ = s.y * inv_h;
+        const f32x2 neg_ma = f2(-ma, -ma), neg_max = f2(-max_, -max_);
+        T *out = dx + (size_t)row * H;
+#pragma unroll
+        for (int i = 0; i < U::N; ++i) {
+            f32x2 xe[U::E / 2], ge[U::E / 2], u[U::E / 2];
+            un.load(xr, i, xe);
+            un.load(gr, i, ge);
+            un.load(s_w, i, u);
+#pragma unroll
+            for (int j = 0; j < U::E / 2; ++j) {
+                const f32x2 xh = f2_mul(f2_add(xe[j], neg_mean), r2);
+                xe[j] = f2_mul(f2_fma(xh, neg_max, f2_fma(ge[j], u[j], neg_ma)), r2);
+            }
+            un.store(out, i, xe);
+        }
+    }
+    // the CTA's column sums
+    copies_wait<0>();
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(smem) + (size_t)ty * 2 * H;
+#pragma unroll
+    for (int i = 0; i < U::N; ++i) {
+        un.store_sums(sums, i, dw[i]);
+        un.store_sums(sums + H, i, db[i]);
+    }
+    sums = reinterpret_cast<float *>(smem);
+    __syncthreads();
+    const int n = want_db ? 2 * H : H;
+    for (int c = ty * G + tid; c < n; c += R * G) {
+        float s = 0.0f;
+        for (int r = 0; r < R; ++r) s += sums[(size_t)r * 2 * H + c];
+        part[(size_t)blockIdx.x * 2 * H + c] = s;
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// backward, few rows: one launch, whose first `rows` CTAs make dx (a row each, read again from L1 for the second pass) and
+// whose other CTAs make dw and db of 32 columns each (mean and rstd are inputs, so columns need no row sums).  x and g
+// are read twice, the second time from L2; no partial sums and no second kernel.
+// ---------------------------------------------------------------------------------------
+constexpr int kFewThreads = 1024, kColRows = kFewThreads / 32;
+
+template <typename T, typename W, int VEC>
+__global__ void __launch_bounds__(kFewThreads)
+ep_norm_bwd_few_kernel(const T *__restrict__ g, long long ldg, const T *__restrict__ x, long long ldx,
+                       const W *__restrict__ w, const float *__restrict__ mean_in, const float *__restrict__ rstd_in,
+                       int rows, int H, int rms, T *__restrict__ dx, float *__restrict__ dw, float *__restrict__ db) {
+    __shared__ __align__(16) f32x2 s_red[32];
+    __shared__ float s_col[2][kColRows][33];
+    pdl_wait();
+    const int tid = threadIdx.x;
+    if ((int)blockIdx.x < rows) {
+        if (tid < 32) s_red[tid] = f2(0.0f, 0.0f);
+        const int row = blockIdx.x;
+        const T *xr = x + (size_t)row * ldx, *gr = g + (size_t)row * ldg;
         const float mean = rms ? 0.0f : mean_in[row], rstd = rstd_in[row];
         float sa = 0.0f, sax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = tid + i * G;
-            if (v < nv) {
-                const Pack<W, VEC> wv = ld_pack<W, VEC>(w + (size_t)v * VEC);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float gj = gv[i].f(j), xh = (xv[i].f(j) - mean) * rstd, a = gj * wv.f(j);
-                    sa += a;
-                    sax = fmaf(a, xh, sax);
-                    dw[i][j] = fmaf(gj, xh, dw[i][j]);
-                    db[i][j] += gj;
-                }
-            }
-        }
-        const float2 s = group_sum2(sa, sax, s_red[buf] + ty * (G >> 5), G, ty);
-        const float ma = rms ? 0.0f : s.x / (float)H, max_ = s.y / (float)H;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = tid + i * G;
-            if (v < nv) {
-                const Pack<W, VEC> wv = ld_pack<W, VEC>(w + (size_t)v * VEC);
-                float o[VEC];
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float xh = (xv[i].f(j) - mean) * rstd;
-                    o[j] = rstd * (gv[i].f(j) * wv.f(j) - ma - xh * max_);
-                }
-                st_pack_stream<T, VEC>(dx + (size_t)row * H + (size_t)v * VEC, o);
-            }
-        }
-    }
-    // the CTA's column sums: group 0 in registers, the other groups' added in order
-    for (int r = 1; r < R; ++r) {
-        __syncthreads();
-        if (ty == r) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (tid + i * G < nv)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        s_cols[(tid + i * G) * VEC + j] = dw[i][j];
-                        s_cols[H + (tid + i * G) * VEC + j] = db[i][j];
-                    }
-        }
-        __syncthreads();
-        if (ty == 0) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (tid + i * G < nv)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        dw[i][j] += s_cols[(tid + i * G) * VEC + j];
-                        db[i][j] += s_cols[H + (tid + i * G) * VEC + j];
-                    }
-        }
-    }
-    if (ty != 0) return;
-    float *pw = part + (size_t)blockIdx.x * 2 * H, *pb = pw + H;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (tid + i * G < nv)
+        for (int c = tid * VEC; c < H; c += kFewThreads * VEC) {
+            float xf[VEC], gf[VEC], wf[VEC];
+            ld_pack<T, VEC>(xr + c).unpack(xf);
+            ld_pack<T, VEC>(gr + c).unpack(gf);
+            ld_pack<W, VEC>(w + c).unpack(wf);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                pw[(tid + i * G) * VEC + j] = dw[i][j];
-                if (want_db) pb[(tid + i * G) * VEC + j] = db[i][j];
+                const float a = gf[j] * wf[j];
+                sa += a;
+                sax = fmaf(a, (xf[j] - mean) * rstd, sax);
             }
+        }
+        __syncthreads();
+        const float2 s = group_sum2(f2(sa, sax), s_red, kFewThreads, 0);
+        const float inv_h = 1.0f / (float)H, ma = rms ? 0.0f : s.x * inv_h, max_ = s.y * inv_h;
+        for (int c = tid * VEC; c < H; c += kFewThreads * VEC) {
+            float xf[VEC], gf[VEC], wf[VEC], o[VEC];
+            ld_pack<T, VEC>(xr + c).unpack(xf);
+            ld_pack<T, VEC>(gr + c).unpack(gf);
+            ld_pack<W, VEC>(w + c).unpack(wf);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) o[j] = rstd * (fmaf(gf[j], wf[j], -ma) - (xf[j] - mean) * rstd * max_);
+            st_pack_stream<T, VEC>(dx + (size_t)row * H + c, o);
+        }
+        return;
+    }
+    const int lane = tid & 31, part = tid >> 5, c = (blockIdx.x - rows) * 32 + lane;
+    float sw = 0.0f, sb = 0.0f;
+    if (c < H) {
+#pragma unroll 4
+        for (int row = part; row < rows; row += kColRows) {
+            const float gj = to_f32(g[(size_t)row * ldg + c]);
+            sw = fmaf(gj, (to_f32(x[(size_t)row * ldx + c]) - (rms ? 0.0f : mean_in[row])) * rstd_in[row], sw);
+            sb += gj;
+        }
+    }
+    s_col[0][part][lane] = sw;
+    s_col[1][part][lane] = sb;
+    __syncthreads();
+    // warp i joins column i: lane r holds part r
+    const int col = (blockIdx.x - rows) * 32 + part;
+    const float tw = warp_sum(s_col[0][lane][part]), tb = warp_sum(s_col[1][lane][part]);
+    if (lane == 0 && col < H) {
+        dw[col] = tw;
+        if (db) db[col] = tb;
+    }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -224,11 +578,11 @@ ep_norm_bwd_kernel(const T *__restrict__ g, long long ldg, const T *__restrict__
 // kernel of their own.
 // ---------------------------------------------------------------------------------------
 template <typename T, typename W>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(1024, 1)
 ep_norm_bwd_wide_kernel(const T *__restrict__ g, long long ldg, const T *__restrict__ x, long long ldx,
                         const W *__restrict__ w, const float *__restrict__ mean_in,
                         const float *__restrict__ rstd_in, int H, int rms, T *__restrict__ dx) {
-    __shared__ float2 s_red[32];
+    __shared__ __align__(16) f32x2 s_red[32];
     pdl_wait();
     const int row = blockIdx.x;
     const T *xr = x + (size_t)row * ldx, *gr = g + (size_t)row * ldg;
@@ -239,7 +593,7 @@ ep_norm_bwd_wide_kernel(const T *__restrict__ g, long long ldg, const T *__restr
         sa += a;
         sax = fmaf(a, (to_f32(xr[c]) - mean) * rstd, sax);
     }
-    const float2 s = group_sum2(sa, sax, s_red, blockDim.x, 0);
+    const float2 s = group_sum2(f2(sa, sax), s_red, blockDim.x, 0);
     const float ma = rms ? 0.0f : s.x / (float)H, max_ = s.y / (float)H;
     for (int c = threadIdx.x; c < H; c += blockDim.x) {
         const float xh = (to_f32(xr[c]) - mean) * rstd;
@@ -268,7 +622,6 @@ ep_norm_bwd_wide_cols_kernel(const T *__restrict__ g, long long ldg, const T *__
 
 // Column sums of the partial rows: 32 columns per CTA, kColRows partial rows at a time, joined
 // in shared memory in a fixed order.  blockIdx.y: 0 for dw, 1 for db.
-constexpr int kColRows = 32;
 __global__ void __launch_bounds__(32 * kColRows)
 ep_norm_cols_kernel(const float *__restrict__ part, int nparts, int H, float *__restrict__ dw,
                     float *__restrict__ db) {
@@ -296,37 +649,57 @@ struct NormArgs {
     long long ldx;
     const void *w, *b;
     const float *mean_in, *rstd_in;
-    int rows, H, rms;
+    int rows, H, rms, period;
     float eps;
     void *out;
     float *mean_out, *rstd_out, *part, *dw, *db;
     cudaStream_t st;
 };
 
-constexpr int round_up32(int n) { return (n + 31) / 32 * 32; }
-
 template <typename T, typename W, int VEC, int NV>
-int launch_fwd_nv(const NormArgs &a, int group) {
-    const auto launch = [&](auto kern, int grid, int threads) {
-        return launch_pdl(kern, dim3(grid), dim3(threads), 0, a.st, (const T *)a.x, a.ldx, (const W *)a.w,
-                          (const W *)a.b, a.rows, a.H, a.eps, a.rms, one_wave(grid), (T *)a.out, a.mean_out,
-                          a.rstd_out);
-    };
-    if (group == 32) return launch(ep_norm_kernel<T, W, VEC, NV, true>, (a.rows + 3) / 4, 128);
-    return launch(ep_norm_kernel<T, W, VEC, NV, false>, a.rows, group);
+int launch_fwd_rows(const NormArgs &a) {
+    return launch_pdl(ep_norm_row_kernel<T, W, VEC, NV>, dim3(a.rows), dim3(round_up((a.H / VEC + NV - 1) / NV, 32)), 0,
+                      a.st, (const T *)a.x, a.ldx, (const W *)a.w, (const W *)a.b, a.H, a.eps, a.rms, one_wave(a.rows),
+                      (T *)a.out, a.mean_out, a.rstd_out);
 }
 
-template <typename T, typename W, int VEC>
+// A pipelined kernel's CTA: groups of G threads that hold a row, as many as `threads` and the shared memory have room for
+// with row_bytes for each and params bytes per copy of the parameters; no groups (y = 0) where not even one fits.
+dim3 group_shape(int H, int ept, int threads, int lay, int params, int row_bytes) {
+    const int G = round_up((H + ept - 1) / ept, 32);
+    const int fit = lay == kShifted ? kSharedBytes / (row_bytes + params) : (kSharedBytes - params) / row_bytes;
+    return dim3(G, min(min(threads / G, fit), G == 32 ? 32 : 15));
+}
+// CTAs for a pipelined kernel: one per SM, or as many as the rows fill.
+int group_grid(int rows, int R) {
+    const int sms = device_sm_count(), full = (rows + R - 1) / R;
+    return sms > 0 && sms < full ? sms : full;
+}
+
+template <typename K> int set_smem(K kern, size_t bytes) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}
+
+// A piece more than the elements fill, for rows that begin and end inside one.
+constexpr int laid(int H, int lay, int vec) { return lay == kShifted ? H + 2 * (vec - 1) : H; }
+
+template <typename T, typename W, int LAY>
 int launch_fwd(const NormArgs &a) {
-    const int nv = a.H / VEC;
-    // few rows: as many threads per row as it has vectors; many rows: a warp for up to 8 vectors
-    // per lane, then as few warps as hold the row
-    if (a.rows <= 2 * 152 && nv <= 1024) return launch_fwd_nv<T, W, VEC, 1>(a, round_up32(nv));
-    if (nv <= 32) return launch_fwd_nv<T, W, VEC, 1>(a, 32);
-    if (nv <= 64) return launch_fwd_nv<T, W, VEC, 2>(a, 32);
-    if (nv <= 128) return launch_fwd_nv<T, W, VEC, 4>(a, 32);
-    if (nv <= 8 * 1024) return launch_fwd_nv<T, W, VEC, 8>(a, round_up32((nv + 7) / 8));
-    return launch_fwd_nv<T, W, VEC, 32>(a, round_up32((nv + 31) / 32));
+    constexpr int VEC = 16 / sizeof(T), RV = LAY == kAligned ? VEC : 1;   // the one-row kernel's vectors
+    const int nv = a.H / RV;
+    if ((long long)a.rows * round_up(nv <= 1024 ? nv : (nv + 7) / 8, 32) <= kResidentThreads) {
+        if (nv <= 1024) return launch_fwd_rows<T, W, RV, 1>(a);
+        if (nv <= 8192) return launch_fwd_rows<T, W, RV, 8>(a);
+    }
+    const int row_bytes = kFwdStages<T> * RowSource<T, kFwdEpt, LAY>::stage_bytes(a.H), params = 2 * param_bytes<W>(a.H + 2 * VEC);
+    const dim3 block = group_shape(laid(a.H, LAY, VEC), kFwdEpt, kFwdThreads, LAY, params, row_bytes);
+    if (block.y < 1) return launch_fwd_rows<T, W, RV, (RV == 1 ? 32 : 8)>(a);
+    const auto kern = ep_norm_kernel<T, W, LAY>;
+    static const int rc = set_smem(kern, kSharedBytes);
+    if (rc != EP_OK) return launch_result(cudaErrorInvalidValue);
+    const size_t smem = param_copies(LAY, block.y) * params + (size_t)block.y * row_bytes;
+    return launch_pdl(kern, dim3(group_grid(a.rows, block.y)), block, smem, a.st, (const T *)a.x, a.ldx, (const W *)a.w,
+                      (const W *)a.b, a.rows, a.H, a.eps, a.rms, a.period, (T *)a.out, a.mean_out, a.rstd_out);
 }
 
 int launch_cols(const NormArgs &a, int nparts) {
@@ -334,23 +707,29 @@ int launch_cols(const NormArgs &a, int nparts) {
                       (const float *)a.part, nparts, a.H, a.dw, a.db);
 }
 
-template <typename T, typename W, int VEC, int NV>
-int launch_bwd_nv(const NormArgs &a) {
-    const int G = round_up32((a.H / VEC + NV - 1) / NV);
-    const int R = G == 32 ? 16 : G < kFusedThreads ? kFusedThreads / G : 1;
-    const size_t smem = R > 1 ? (size_t)2 * a.H * sizeof(float) : 0;
-    const int grid = min((a.rows + R - 1) / R, kPartials);
-    const int rc = launch_pdl(ep_norm_bwd_kernel<T, W, VEC, NV>, dim3(grid), dim3(G, R), smem, a.st, (const T *)a.g,
-                              a.ldg, (const T *)a.x, a.ldx, (const W *)a.w, a.mean_in, a.rstd_in, a.rows, a.H, a.rms,
-                              a.db ? 1 : 0, (T *)a.out, a.part);
-    return rc != EP_OK ? rc : launch_cols(a, grid);
-}
-
-template <typename T, typename W, int VEC>
+template <typename T, typename W, int LAY>
 int launch_bwd(const NormArgs &a) {
-    if (a.rows == 0) return launch_cols(a, 0);
-    if (a.H <= kFusedH / 2) return launch_bwd_nv<T, W, VEC, 8 / VEC>(a);
-    if (a.H <= kFusedH) return launch_bwd_nv<T, W, VEC, 16 / VEC>(a);
+    if (a.rows <= kFewBwdRows) {
+        constexpr int VEC = LAY == kAligned ? 16 / sizeof(T) : 1;
+        return launch_pdl(ep_norm_bwd_few_kernel<T, W, VEC>, dim3(a.rows + (a.H + 31) / 32), dim3(kFewThreads), 0, a.st,
+                          (const T *)a.g, a.ldg, (const T *)a.x, a.ldx, (const W *)a.w, a.mean_in, a.rstd_in, a.rows, a.H,
+                          a.rms, (T *)a.out, a.dw, a.db);
+    }
+    if (a.H <= kBwdMaxH) {
+        constexpr int VEC = 16 / sizeof(T);
+        const int row_bytes = kBwdStages * 2 * RowSource<T, kBwdEpt, LAY>::stage_bytes(a.H), params = param_bytes<W>(a.H + 2 * VEC);
+        const dim3 block = group_shape(laid(a.H, LAY, VEC), kBwdEpt, kBwdThreads, LAY, params, row_bytes);
+        const auto kern = ep_norm_bwd_kernel<T, W, LAY>;
+        const size_t stages = param_copies(LAY, block.y) * params + (size_t)block.y * row_bytes;
+        const size_t sums = (size_t)block.y * 2 * a.H * sizeof(float);
+        static const int rc = set_smem(kern, kSharedBytes);
+        if (rc != EP_OK) return launch_result(cudaErrorInvalidValue);
+        const int grid = min(group_grid(a.rows, block.y), kPartials);
+        const int e = launch_pdl(kern, dim3(grid), block, stages > sums ? stages : sums, a.st, (const T *)a.g, a.ldg,
+                                 (const T *)a.x, a.ldx, (const W *)a.w, a.mean_in, a.rstd_in, a.rows, a.H, a.rms,
+                                 a.db ? 1 : 0, a.period, (T *)a.out, a.part);
+        return e != EP_OK ? e : launch_cols(a, grid);
+    }
     int rc = launch_pdl(ep_norm_bwd_wide_kernel<T, W>, dim3(a.rows), dim3(1024), 0, a.st, (const T *)a.g, a.ldg,
                         (const T *)a.x, a.ldx, (const W *)a.w, a.mean_in, a.rstd_in, a.H, a.rms, (T *)a.out);
     if (rc != EP_OK) return rc;
@@ -360,14 +739,25 @@ int launch_bwd(const NormArgs &a) {
     return rc != EP_OK ? rc : launch_cols(a, parts);
 }
 
-// Vectors of 16 bytes need every row and parameter on a 16-byte boundary.
-template <typename T, typename W>
-int launch_norm(const NormArgs &a) {
+// How the rows lie: x, y and, going backward, g.
+template <typename T>
+int lay_of(const NormArgs &a, int &period) {
     constexpr int VEC = 16 / sizeof(T);
-    const bool vec = a.H % VEC == 0 && a.ldx % VEC == 0 && (!a.g || a.ldg % VEC == 0) && aligned16(a.x) &&
-                     aligned16(a.g) && aligned16(a.w) && aligned16(a.b) && aligned16(a.out);
-    if (a.g) return vec ? launch_bwd<T, W, VEC>(a) : launch_bwd<T, W, 1>(a);
-    return vec ? launch_fwd<T, W, VEC>(a) : launch_fwd<T, W, 1>(a);
+    const auto off = [](const void *p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15u); };
+    period = 1;
+    if (off(a.x) != off(a.out) || a.ldx % VEC != a.H % VEC) return kAny;
+    if (a.g && (off(a.g) != off(a.x) || a.ldg % VEC != a.H % VEC)) return kAny;
+    if (off(a.x) == 0 && a.H % VEC == 0) return aligned16(a.w) && aligned16(a.b) ? kAligned : kShifted;
+    while (period * a.H % VEC) period *= 2;
+    return kShifted;
+}
+
+template <typename T, typename W>
+int launch_norm(NormArgs a) {
+    const int lay = lay_of<T>(a, a.period);
+    if (lay == kAny) a.period = 1;
+    if (a.g) return lay == kAligned ? launch_bwd<T, W, kAligned>(a) : lay == kShifted ? launch_bwd<T, W, kShifted>(a) : launch_bwd<T, W, kAny>(a);
+    return lay == kAligned ? launch_fwd<T, W, kAligned>(a) : lay == kShifted ? launch_fwd<T, W, kShifted>(a) : launch_fwd<T, W, kAny>(a);
 }
 
 int launch_norm(const NormArgs &a, int dtype, int wdtype) {

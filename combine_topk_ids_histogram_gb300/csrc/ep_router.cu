@@ -2,8 +2,11 @@
 // probabilities from its logits, and the gradient of the logits from the gradient of the
 // probabilities (what ep_combine_bwd returns).
 //
-// One warp per token; every lane holds E/32 of the row's selection scores as order-preserving
-// integer keys.
+// One warp per token.  A lane holds V = E/32 consecutive experts' scores as order-preserving integer keys, so that
+// lane order is id order.  The K-th largest of the lanes' largest keys bounds the K-th largest key from below;
+// the few keys at or above it (about K + 2 for independent scores) are gathered in id order and ranked
+// against one another.  Against K rounds of finding and striking out the largest of all keys this took the
+// instructions of a token from 660 to about 250 at E = 256, K = 8; instruction issue bounds the call there.
 #include "ep_host.h"
 #include "ep_types.cuh"
 
@@ -13,13 +16,30 @@ namespace {
 constexpr int kRouterThreads = 256;
 constexpr int kRouterWarps = kRouterThreads / 32;
 
-// Keys compare as unsigned integers the way the scores compare as numbers; +0 and -0 are equal,
-// a NaN is above everything, and 0 stands for "not selectable" (-inf, or taken already).
+// Keys compare as unsigned integers the way the scores compare as numbers: +0 and -0 are equal and a NaN is above
+// everything.
 __device__ __forceinline__ unsigned score_key(float s) {
-    if (s != s) return 0xffffffffu;
     const unsigned u = __float_as_uint(s + 0.0f);
-    const unsigned k = (u & 0x80000000u) ? ~u : u | 0x80000000u;
-    return k == 0x007fffffu ? 0u : k;   // the key of -inf
+    return s != s ? 0xffffffffu : u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+}
+constexpr unsigned kNoKey = 0x007fffffu;   // the key of -inf: not selectable, like every smaller one
+
+// V consecutive elements of a row from e0 on, `fill` past its end.  vec: rows lie on boundaries of 16 bytes.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T *row, int e0, int E, bool vec, float fill, float (&f)[V]) {
+    constexpr int VL = V * sizeof(T) > 16 ? 16 / sizeof(T) : V;
+#pragma unroll
+    for (int j = 0; j < V; j += VL) {
+        if (vec && e0 + j + VL <= E) {
+            float g[VL];
+            ld_pack<T, VL>(row + e0 + j).unpack(g);
+#pragma unroll
+            for (int i = 0; i < VL; ++i) f[j + i] = g[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < VL; ++i) f[j + i] = e0 + j + i < E ? to_f32(row[e0 + j + i]) : fill;
+        }
+    }
 }
 
 struct RouterScore {
@@ -31,8 +51,8 @@ struct RouterScore {
 // `row` gives the logits of all experts to a softmax over all of them.  Renormalised scores are
 // divided through by the largest of them first, exp(min(max l, 0)) for sigmoids, so that rows
 // of very negative logits keep their ratios.
-template <typename T, int NVAL>
-__device__ __forceinline__ float slot_prob(float l, bool used, const T *row, int E, int lane, RouterScore sc) {
+template <typename T, int V>
+__device__ __forceinline__ float slot_prob(float l, bool used, const T *row, int E, bool vec, int lane, RouterScore sc) {
     const float neg_inf = __int_as_float(0xff800000);
     if (sc.sigmoid) {
         if (!sc.renorm) return used ? sc.scale / (1.0f + expf(-l)) : 0.0f;
@@ -47,64 +67,108 @@ __device__ __forceinline__ float slot_prob(float l, bool used, const T *row, int
         const float total = warp_sum(e);
         return used ? sc.scale * (e / total) : 0.0f;
     }
+    float v[V];
+    load_row<T, V>(row, lane * V, E, vec, neg_inf, v);
     float m = neg_inf;
 #pragma unroll
-    for (int i = 0; i < NVAL; ++i) {
-        const int e = i * 32 + lane;
-        if (e < E) m = fmaxf(m, to_f32(row[e]));
-    }
+    for (int i = 0; i < V; ++i) m = fmaxf(m, v[i]);
     m = warp_max(m);
     if (m == neg_inf) return 0.0f;
     float total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NVAL; ++i) {
-        const int e = i * 32 + lane;
-        if (e < E) total += expf(to_f32(row[e]) - m);
-    }
+    for (int i = 0; i < V; ++i) total += expf(v[i] - m);
     total = warp_sum(total);
     return used ? sc.scale * (expf(l - m) / total) : 0.0f;
 }
 
-template <typename T, int NVAL>
+template <typename T, int V>
 __global__ void __launch_bounds__(kRouterThreads)
 ep_router_topk_kernel(const T *__restrict__ logits, long long ld, const float *__restrict__ bias, int tokens, int E,
-                      int K, RouterScore sc, int one_wave, int32_t *__restrict__ ids, float *__restrict__ probs) {
+                      int K, RouterScore sc, int vec, int vec_bias, int one_wave, int32_t *__restrict__ ids,
+                      float *__restrict__ probs) {
+    __shared__ unsigned s_key[kRouterWarps][32];
+    __shared__ int s_id[kRouterWarps][32], s_slot[kRouterWarps][32];
     pdl_begin_if(one_wave);
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kRouterWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x * kRouterWarps + warp;
     if (t >= tokens) return;
     const T *row = logits + (size_t)t * ld;
-    unsigned key[NVAL];
+    const float neg_inf = __int_as_float(0xff800000);
+    unsigned key[V];
+    {
+        float f[V];
+        load_row<T, V>(row, lane * V, E, vec, neg_inf, f);
+        if (bias) {
+            float b[V];
+            load_row<float, V>(bias, lane * V, E, vec_bias, 0.0f, b);
 #pragma unroll
-    for (int i = 0; i < NVAL; ++i) {
-        const int e = i * 32 + lane;
-        key[i] = 0u;
-        if (e < E) {
-            float s = to_f32(row[e]);
-            if (bias) s += bias[e];
-            key[i] = score_key(s);
+            for (int i = 0; i < V; ++i) f[i] += b[i];
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = score_key(f[i]);
     }
-    int my_id = -1;   // lane k: the expert of slot k
+    unsigned best = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    // a lower bound of the K-th largest key; lanes with equal maxima are struck out together, which only lowers it
+    unsigned bound = kNoKey + 1;
     for (int k = 0; k < K; ++k) {
-        unsigned best = 0u;
-#pragma unroll
-        for (int i = 0; i < NVAL; ++i) best = max(best, key[i]);
         const unsigned top = __reduce_max_sync(kFullMask, best);
-        if (top == 0u) break;   // nothing selectable is left
-        int e = E;
+        bound = max(top, kNoKey + 1);
+        if (top <= kNoKey) break;
+        if (best == top) best = 0u;
+    }
+    int mine = 0;
 #pragma unroll
-        for (int i = NVAL - 1; i >= 0; --i)
-            if (key[i] == top) e = i * 32 + lane;
-        const int first = __reduce_min_sync(kFullMask, e);   // ties to the lower id
+    for (int i = 0; i < V; ++i) mine += key[i] >= bound ? 1 : 0;
+    int at = mine;                                                  // candidates in the lanes up to this one
 #pragma unroll
-        for (int i = 0; i < NVAL; ++i)
-            if (first == i * 32 + lane) key[i] = 0u;
-        if (lane == k) my_id = first;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFullMask, at, o);
+        if (lane >= o) at += v;
+    }
+    const int n = __shfl_sync(kFullMask, at, 31);
+    at -= mine;
+    int my_id = -1;                                                 // lane k: the expert of slot k
+    if (n <= 32) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] >= bound) {
+                s_key[warp][at] = key[i];
+                s_id[warp][at] = lane * V + i;
+                ++at;
+            }
+        __syncwarp();
+        const unsigned mk = lane < n ? s_key[warp][lane] : 0u;
+        int rank = 0;
+        for (int j = 0; j < n; ++j) {
+            const unsigned other = s_key[warp][j];
+            if (other > mk || (other == mk && j < lane)) ++rank;    // ties to the lower id
+        }
+        if (lane < n && rank < K) s_slot[warp][rank] = s_id[warp][lane];
+        __syncwarp();
+        if (lane < min(n, K)) my_id = s_slot[warp][lane];
+    } else {                                                        // many equal keys: K rounds of the largest key
+        for (int k = 0; k < K; ++k) {
+            unsigned b = 0u;
+#pragma unroll
+            for (int i = 0; i < V; ++i) b = max(b, key[i]);
+            const unsigned top = __reduce_max_sync(kFullMask, b);
+            if (top <= kNoKey) break;
+            int e = E;
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i)
+                if (key[i] == top) e = lane * V + i;
+            const int first = __reduce_min_sync(kFullMask, e);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (first == lane * V + i) key[i] = 0u;
+            if (lane == k) my_id = first;
+        }
     }
     const bool used = my_id >= 0;
     const float l = used ? to_f32(row[my_id]) : 0.0f;
-    const float p = slot_prob<T, NVAL>(l, used, row, E, lane, sc);
+    const float p = slot_prob<T, V>(l, used, row, E, vec, lane, sc);
     if (lane < K) {
         ids[(size_t)t * K + lane] = my_id;
         probs[(size_t)t * K + lane] = p;
@@ -117,11 +181,11 @@ ep_router_topk_kernel(const T *__restrict__ logits, long long ld, const float *_
 //   sigmoid:                     dl[id_k] = g_k p_k (1 - sigmoid(l))
 //   softmax over all:            dl[e] = -P_e * scale * G, and + g_k p_k at e = id_k
 // Slots that name the same expert add up in slot order.
-template <typename T, int NVAL>
+template <typename T, int V>
 __global__ void __launch_bounds__(kRouterThreads)
 ep_router_topk_bwd_kernel(const float *__restrict__ grad_p, const T *__restrict__ logits, long long ld,
-                          const int32_t *__restrict__ ids, int tokens, int E, int K, RouterScore sc, int one_wave,
-                          T *__restrict__ grad) {
+                          const int32_t *__restrict__ ids, int tokens, int E, int K, RouterScore sc, int vec,
+                          int vec_out, int one_wave, T *__restrict__ grad) {
     pdl_begin_if(one_wave);
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * kRouterWarps + (threadIdx.x >> 5);
@@ -137,7 +201,7 @@ ep_router_topk_bwd_kernel(const float *__restrict__ grad_p, const T *__restrict_
     const bool used = id >= 0 && id < E;
     if (!used) g = 0.0f;
     const float l = used ? to_f32(row[id]) : 0.0f;
-    const float p = slot_prob<T, NVAL>(l, used, row, E, lane, sc);
+    const float p = slot_prob<T, V>(l, used, row, E, vec, lane, sc);
     const float G = warp_sum(g * p) / sc.scale;
     float d;
     if (sc.sigmoid) d = p * (sc.renorm ? g - G : g) / (1.0f + expf(l));
@@ -149,30 +213,41 @@ ep_router_topk_bwd_kernel(const float *__restrict__ grad_p, const T *__restrict_
         const float dk = __shfl_sync(kFullMask, d, k);
         if (ik == id) sum += dk;
     }
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.0f;
     if (!sc.sigmoid && !sc.renorm) {
         const float neg_inf = __int_as_float(0xff800000);
+        load_row<T, V>(row, lane * V, E, vec, neg_inf, v);
         float m = neg_inf, total = 0.0f;
-        float v[NVAL];
 #pragma unroll
-        for (int i = 0; i < NVAL; ++i) {
-            const int e = i * 32 + lane;
-            v[i] = e < E ? to_f32(row[e]) : neg_inf;
-            m = fmaxf(m, v[i]);
-        }
+        for (int i = 0; i < V; ++i) m = fmaxf(m, v[i]);
         m = warp_max(m);
         if (m == neg_inf) m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NVAL; ++i) total += v[i] = expf(v[i] - m);
+        for (int i = 0; i < V; ++i) total += v[i] = expf(v[i] - m);
         total = warp_sum(total);
         const float f = total > 0.0f ? -sc.scale * G / total : 0.0f;
 #pragma unroll
-        for (int i = 0; i < NVAL; ++i) {
-            const int e = i * 32 + lane;
-            if (e < E) out[e] = from_f32<T>(f * v[i]);
-        }
+        for (int i = 0; i < V; ++i) v[i] *= f;
         sum += f * expf(l - m);
-    } else {
-        for (int e = lane; e < E; e += 32) out[e] = from_f32<T>(0.0f);
+    }
+    constexpr int VL = V * sizeof(T) > 16 ? 16 / sizeof(T) : V;
+#pragma unroll
+    for (int j = 0; j < V; j += VL) {
+        const int e = lane * V + j;
+        if (vec_out && e + VL <= E) {
+            float g[VL];
+#pragma unroll
+            for (int i = 0; i < VL; ++i) g[i] = v[j + i];
+            Pack<T, VL> o;
+            o.pack(g);
+            *reinterpret_cast<Pack<T, VL> *>(out + e) = o;
+        } else {
+#pragma unroll
+            for (int i = 0; i < VL; ++i)
+                if (e + i < E) out[e + i] = from_f32<T>(v[j + i]);
+        }
     }
     __syncwarp();   // the row is written before its selected entries are
     if (used) out[id] = from_f32<T>(sum);
@@ -187,6 +262,11 @@ bool router_args_ok(int T, int E, int K, int dtype, long long ld, int score, int
 
 bool element_aligned(const void *p, int dtype) {
     return (reinterpret_cast<uintptr_t>(p) & (dtype == EP_F32 ? 3u : 1u)) == 0;
+}
+
+// Whether rows can be read (or written) 16 bytes at a time: a lane's run of experts starts on a boundary of its own size.
+bool rows_aligned(const void *p, long long stride, int dtype) {
+    return aligned16(p) && stride * (dtype == EP_F32 ? 4 : 2) % 16 == 0;
 }
 
 template <typename F>
@@ -225,11 +305,12 @@ extern "C" int ep_router_topk(const void *logits, long long stride, int dtype, c
     const int grid = (T + kRouterWarps - 1) / kRouterWarps;
     return by_type(dtype, [&](auto *tp) {
         using P = decltype(tp);
-        return by_width(n_experts, [&](auto nval) {
+        return by_width(n_experts, [&](auto v) {
             using E = std::remove_const_t<std::remove_pointer_t<P>>;
-            return launch_pdl(ep_router_topk_kernel<E, decltype(nval)::value>, dim3(grid), dim3(kRouterThreads), 0,
-                              as_stream(stream), (P)logits, stride, bias, T, n_experts, K, sc, one_wave(grid),
-                              topk_ids, topk_probs);
+            return launch_pdl(ep_router_topk_kernel<E, decltype(v)::value>, dim3(grid), dim3(kRouterThreads), 0,
+                              as_stream(stream), (P)logits, stride, bias, T, n_experts, K, sc,
+                              (int)rows_aligned(logits, stride, dtype), (int)aligned16(bias), one_wave(grid), topk_ids,
+                              topk_probs);
         });
     });
 }
@@ -247,10 +328,11 @@ extern "C" int ep_router_topk_bwd(const float *grad_probs, const void *logits, l
     const int grid = (T + kRouterWarps - 1) / kRouterWarps;
     return by_type(dtype, [&](auto *tp) {
         using P = decltype(tp);
-        return by_width(n_experts, [&](auto nval) {
+        return by_width(n_experts, [&](auto v) {
             using E = std::remove_const_t<std::remove_pointer_t<P>>;
-            return launch_pdl(ep_router_topk_bwd_kernel<E, decltype(nval)::value>, dim3(grid), dim3(kRouterThreads), 0,
+            return launch_pdl(ep_router_topk_bwd_kernel<E, decltype(v)::value>, dim3(grid), dim3(kRouterThreads), 0,
                               as_stream(stream), grad_probs, (P)logits, stride, topk_ids, T, n_experts, K, sc,
+                              (int)rows_aligned(logits, stride, dtype), (int)rows_aligned(grad_logits, n_experts, dtype),
                               one_wave(grid), (E *)grad_logits);
         });
     });

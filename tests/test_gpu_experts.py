@@ -211,6 +211,10 @@ def test_no_tokens_and_refusals():
     with pytest.raises(ValueError):
         ep.expert_matvec(x, codes, scales, row_scale[:, :20].contiguous(), L)
     with pytest.raises(TypeError):
+        ep.expert_matvec(x, codes.int(), scales, row_scale, L)
+    with pytest.raises(ValueError):
+        ep.expert_matvec(x.cpu(), codes, scales, row_scale, L)
+    with pytest.raises(TypeError):
         ep.expert_matvec(x.float(), codes, scales, row_scale, L)
     with pytest.raises(ValueError):
         ep.expert_matvec(x[:5], codes, scales, row_scale, L)

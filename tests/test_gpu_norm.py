@@ -75,11 +75,10 @@ def test_types(dt, wdt, T, H):
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("offset,extra", [(0, 8), (0, 3), (1, 7), (8, 24), (5, 0)])
-def test_strided_and_unaligned_rows(dt, offset, extra):
-    """Rows inside a wider matrix, on and off 16-byte boundaries, give the dense rows' bits where both take
-    the same path, and stay within the bound everywhere."""
+@pytest.mark.parametrize("T,H", [(45, 256), (450, 256), (330, 1030), (310, 4099), (2, 9000)])
+def test_strided_and_unaligned_rows(dt, offset, extra, T, H):
+    """Rows inside a wider matrix, on and off 16-byte boundaries."""
     import combine_topk_ids_histogram_gb300 as ep
-    T, H = 45, 256
     x, w, b, gy = make(T, H, dt, dt, offset + extra)
     wide = torch.full((T, offset + H + extra), float("nan"), dtype=dt, device="cuda")
     wide[:, offset:offset + H] = x
@@ -90,9 +89,31 @@ def test_strided_and_unaligned_rows(dt, offset, extra):
     check_backward(ep, gs, xs, w, mean, rstd, False)
 
 
+@pytest.mark.parametrize("T,H", [(1, 3), (7, 5), (310, 9), (500, 1111), (777, 2047), (40, 8191)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_dense_matrices_off_boundaries(dt, T, H):
+    """Dense matrices of odd width that all begin at the same distance from a 16-byte boundary."""
+    import combine_topk_ids_histogram_gb300 as ep
+    x, w, b, gy = make(T, H, dt, dt, T + H)
+    for off in (0, 1, 3):
+        bufs = [torch.full((off + T * H + 16,), float("nan"), dtype=dt, device="cuda") for _ in range(3)]
+        xs, gs, ys = (v[off:off + T * H].view(T, H) for v in bufs)
+        xs.copy_(x)
+        gs.copy_(gy)
+        f32 = dict(device="cuda")
+        out = ys, torch.empty(T, **f32), torch.empty(T, **f32)
+        _, mean, rstd = check_forward(ep, xs, w, b, 1e-5, False, out=out)
+        check_backward(ep, gs, xs, w, mean, rstd, False)
+        assert torch.isnan(bufs[2][:off]).all() and torch.isnan(bufs[2][off + T * H:]).all()
+        dx = ep.layer_norm_bwd(gs, xs, w, mean, rstd, bias=True, out=(ys, torch.empty(H, **f32), torch.empty(H, **f32)))[0]
+        ref.assert_within(dx, ref.norm_bwd(gs, xs, w, mean, rstd, False)[0],
+                          ref.norm_bwd_tol(gs, xs, w, mean, rstd, False, dt)[0], "dx")
+        assert torch.isnan(bufs[2][:off]).all() and torch.isnan(bufs[2][off + T * H:]).all()
+
+
 def test_no_write_outside_outputs():
     import combine_topk_ids_histogram_gb300 as ep
-    for T, H in ((3, 33), (310, 64), (9, 2048), (2, 8200)):
+    for T, H in ((3, 33), (310, 64), (9, 2048), (2, 8200), (330, 1111), (330, 1112)):
         x, w, b, gy = make(T, H, torch.bfloat16, torch.bfloat16, T)
         buf = torch.full((T * H + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
         f = torch.full((3, T + H + 64), 7.0, device="cuda")
