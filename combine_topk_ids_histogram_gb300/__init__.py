@@ -223,7 +223,7 @@ class Layout:
             raise EPError(EP_ERR_INVALID_ARG, "layout sizes")
         self.workspace = torch.zeros(nb, dtype=torch.uint8, device=dev)
         self.capacity = T
-        self.matvec_bytes = {}                   # expert_matvec's workspace size by H: set by the sizes alone
+        self._scratch = {}                       # expert_matvec's workspaces by (stream, H): see scratch
         self.c = _Layout(
             row_offsets=self.row_offsets.data_ptr(), expert_ids=self.expert_ids.data_ptr(),
             src_info=self.src_info.data_ptr(), row_of=self.row_of.data_ptr(),
@@ -233,6 +233,21 @@ class Layout:
     @property
     def ref(self):
         return ctypes.byref(self.c)
+
+    def scratch(self, H: int):
+        """expert_matvec's workspace for the current stream, as (pointer, bytes, tensor): calls on one stream run one
+        after another and share it, another stream gets its own, and a call that is captured into a graph gets one
+        of that graph's.  (Kept because a torch allocation between two launches adds 6 us to a call's host time.)"""
+        capturing = torch.cuda.is_current_stream_capturing()
+        key = (_stream().value, H)
+        w = None if capturing else self._scratch.get(key)
+        if w is None:
+            n = expert_matvec_workspace_bytes(self, H)
+            t = torch.empty(n, dtype=torch.uint8, device=self.status.device)
+            w = (t.data_ptr(), n, t)
+            if not capturing:
+                self._scratch[key] = w
+        return w
 
     def shape_key(self):
         return (self.T, self.K, self.E, self.P, self.S, self.pad, self.row_capacity)
@@ -601,6 +616,14 @@ def _buffer(t: torch.Tensor, shape: tuple, dtypes, what: str) -> int:
     return t.data_ptr()
 
 
+def _rows(t: torch.Tensor, rows: int, cols: int, what: str) -> int:
+    """Pointer of a contiguous bf16 CUDA tensor of at least `rows` rows."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows:
+        raise ValueError(f"{what}: needs at least {rows} rows of {cols}, got {tuple(shape)}")
+    return _buffer(t, (shape[0], cols), _BF16, what)
+
+
 _I32, _U8 = (torch.int32,), (torch.uint8,)
 _F32 = (torch.float32,)
 
@@ -716,12 +739,9 @@ def router_topk_bwd(grad_probs: torch.Tensor, logits: torch.Tensor, topk_ids: to
 
 def expert_matvec_workspace_bytes(L: Layout, H: int) -> int:
     """ep_expert_matvec_workspace_bytes: scratch bytes of ``expert_matvec`` on this layout's sizes."""
-    n = L.matvec_bytes.get(H)
-    if n is None:
-        n = int(_lib.ep_expert_matvec_workspace_bytes(L.ref, H))
-        if n == 0:
-            raise EPError(EP_ERR_INVALID_ARG, "expert_matvec sizes")
-        L.matvec_bytes[H] = n
+    n = int(_lib.ep_expert_matvec_workspace_bytes(L.ref, H))
+    if n == 0:
+        raise EPError(EP_ERR_INVALID_ARG, "expert_matvec sizes")
     return n
 
 
@@ -731,8 +751,8 @@ def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ro
     """ep_expert_matvec -> bf16 [R_max, N] (or [R_max, N/2] with swiglu): each row of the layout times
     its group's 4-bit weights, codes uint8 [G, N, H/2], scales uint8 [G, N, H/16] (E4M3) and row_scale
     fp32 [G, N].  x bf16 is [T, H] when by_token (rows take their token's vector), else [R_max, H].
-    ``workspace``: a uint8 buffer of ``expert_matvec_workspace_bytes`` to reuse; without one a call
-    allocates its own on the stream it runs on."""
+    ``workspace``: a uint8 buffer of ``expert_matvec_workspace_bytes`` to use; without one a call takes the
+    layout's for the current stream (``Layout.scratch``), or its own when a ``stream`` is given."""
     if codes.dim() != 3:
         raise ValueError(f"codes: expected [{L.G}, N, H/2], got {tuple(codes.shape)}")
     G, N, half = codes.shape
@@ -740,19 +760,19 @@ def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ro
     pc = _buffer(codes, (L.G, N, half), _U8, "codes")
     ps = _buffer(scales, (L.G, N, H // 16), _U8, "scales")
     pr = _buffer(row_scale, (L.G, N), _F32, "row_scale")
-    if by_token:
-        px = _buffer(x, (L.T, H), _BF16, "x")
-    else:
-        _need(x, L.R_max, H, _BF16, "x")
-        px = _bits(x)
+    px = _buffer(x, (L.T, H), _BF16, "x") if by_token else _rows(x, L.R_max, H, "x")
     n_out = N // 2 if swiglu else N
     if out is None:
         out = torch.empty(max(L.R_max, 1), n_out, dtype=torch.bfloat16, device=x.device)
-    _need(out, L.R_max, n_out, _BF16, "out")
-    if workspace is None:
-        workspace = _scratch(expert_matvec_workspace_bytes(L, H), x.device, stream)
-    rc = _lib.ep_expert_matvec(px, 1 if by_token else 0, pc, ps, pr, H, N, 1 if swiglu else 0, L.ref, _bits(out),
-                               _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    po = _rows(out, L.R_max, n_out, "out")
+    if workspace is None and stream is None:
+        pw, nw, _ = L.scratch(H)
+    else:
+        if workspace is None:
+            workspace = _scratch(expert_matvec_workspace_bytes(L, H), x.device, stream)
+        pw, nw = _ptr(workspace), workspace.numel() * workspace.element_size()
+    rc = _lib.ep_expert_matvec(px, 1 if by_token else 0, pc, ps, pr, H, N, 1 if swiglu else 0, L.ref, po, pw, nw,
+                               _stream(stream))
     _check(rc, "ep_expert_matvec")
     return out
 

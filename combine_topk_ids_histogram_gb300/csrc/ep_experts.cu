@@ -136,9 +136,9 @@ __device__ __forceinline__ void load_weights(Weights<MT> &d, const uint8_t *code
     }
 }
 
-// One step of a warp: MT * 16 weight rows x 256 k x NT * 8 layout rows.  x: the step's pieces of this thread's
+// One step of a warp: MT * 16 weight rows x 256 k x the first USE of NT blocks of 8 layout rows.  x: the step's pieces of this thread's
 // layout row in shared memory, xo: how far on its row of the second block of 8 is.
-template <int MT, int NT>
+template <int USE, int MT, int NT>
 __device__ __forceinline__ void mma_step(const Weights<MT> &d, const uint4 *x, const int (&xo)[NT],
                                          float (&acc)[MT][NT][4]) {
     uint32_t sc[2 * MT][2];
@@ -146,16 +146,16 @@ __device__ __forceinline__ void mma_step(const Weights<MT> &d, const uint4 *x, c
     for (int r = 0; r < 2 * MT; ++r) scales_to_f16(d.s[r], sc[r]);
 #pragma unroll
     for (int wi = 0; wi < 8; ++wi) {
-        uint4 b[NT];
+        uint4 b[USE];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) b[t] = x[xo[t] + wi * 4];
+        for (int t = 0; t < USE; ++t) b[t] = x[xo[t] + wi * 4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             uint32_t lo[4], hi[4];   // weight rows g and g + 8 of the tile
             codes_to_f16(d.w[2 * mt][wi], scale_pair(sc[2 * mt], wi >> 1), lo);
             codes_to_f16(d.w[2 * mt + 1][wi], scale_pair(sc[2 * mt + 1], wi >> 1), hi);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
+            for (int t = 0; t < USE; ++t) {
                 mma_f16(acc[mt][t], lo[0], hi[0], lo[1], hi[1], b[t].x, b[t].y);
                 mma_f16(acc[mt][t], lo[2], hi[2], lo[3], hi[3], b[t].z, b[t].w);
             }
@@ -377,7 +377,8 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
             for (int st = kw; st < to; st += KS) {
                 const Weights<MT> w = nxt;
                 prefetch();
-                mma_step<MT, NT>(w, x + st * 32, xo, acc);
+                if (NT > 1 && m <= 8) mma_step<1>(w, x + st * 32, xo, acc);
+                else mma_step<NT>(w, x + st * 32, xo, acc);
             }
         }
 

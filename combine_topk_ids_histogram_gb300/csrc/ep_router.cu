@@ -2,11 +2,10 @@
 // probabilities from its logits, and the gradient of the logits from the gradient of the
 // probabilities (what ep_combine_bwd returns).
 //
-// One warp per token.  A lane holds V = E/32 consecutive experts' scores as order-preserving integer keys, so that
-// lane order is id order.  The K-th largest of the lanes' largest keys bounds the K-th largest key from below;
-// the few keys at or above it (about K + 2 for independent scores) are gathered in id order and ranked
-// against one another.  Against K rounds of finding and striking out the largest of all keys this took the
-// instructions of a token from 660 to about 250 at E = 256, K = 8; instruction issue bounds the call there.
+// One warp per token.  Lane l holds the scores of experts l, l + 32, ... as order-preserving integer keys.  The K-th largest
+// of the lanes' largest keys bounds the K-th largest key from below; the few keys at or above it (about K + 2 for
+// independent scores) are gathered and ranked against one another.  Against K rounds of finding and
+// striking out the largest of all keys this takes half of the instructions, whose issue bounds the call.
 #include "ep_host.h"
 #include "ep_types.cuh"
 
@@ -16,11 +15,11 @@ namespace {
 constexpr int kRouterThreads = 256;
 constexpr int kRouterWarps = kRouterThreads / 32;
 
-// Keys compare as unsigned integers the way the scores compare as numbers: +0 and -0 are equal and a NaN is above
-// everything.
+// Keys compare as unsigned integers the way the scores compare as numbers: adding +0 makes one zero of the two and one
+// NaN of all, whose key is above every other.
 __device__ __forceinline__ unsigned score_key(float s) {
     const unsigned u = __float_as_uint(s + 0.0f);
-    return s != s ? 0xffffffffu : u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+    return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
 }
 constexpr unsigned kNoKey = 0x007fffffu;   // the key of -inf: not selectable, like every smaller one
 
@@ -47,8 +46,7 @@ struct RouterScore {
     float scale;
 };
 
-// Probabilities of the selected logits, lane k holding slot k (used: the slot has an expert).
-// `row` gives the logits of all experts to a softmax over all of them.  Renormalised scores are
+// Probabilities of the selected logits, lane k holding slot k (used: the slot has an expert).  `row` gives the logits of all experts to a softmax over all of them.  Renormalised scores are
 // divided through by the largest of them first, exp(min(max l, 0)) for sigmoids, so that rows
 // of very negative logits keep their ratios.
 template <typename T, int V>
@@ -57,7 +55,9 @@ __device__ __forceinline__ float slot_prob(float l, bool used, const T *row, int
     if (sc.sigmoid) {
         if (!sc.renorm) return used ? sc.scale / (1.0f + expf(-l)) : 0.0f;
         const float m = fminf(warp_max(used ? l : neg_inf), 0.0f);
-        const float s = !used ? 0.0f : l >= 0.0f ? 1.0f / (1.0f + expf(-l)) : expf(l - m) / (1.0f + expf(l));
+        // exp(l - m) / (1 + exp(l)) below 0 and 1 / (1 + exp(-l)) from there on (then m = 0)
+        const float e = expf(-fabsf(l)), top = l >= 0.0f ? 1.0f : m == 0.0f ? e : expf(l - m);
+        const float s = used ? __fdividef(top, 1.0f + e) : 0.0f;        // 1 <= 1 + e <= 2: good to 2 ulp
         const float total = warp_sum(s);
         return used ? sc.scale * (s / total) : 0.0f;
     }
@@ -84,85 +84,80 @@ __device__ __forceinline__ float slot_prob(float l, bool used, const T *row, int
 template <typename T, int V>
 __global__ void __launch_bounds__(kRouterThreads)
 ep_router_topk_kernel(const T *__restrict__ logits, long long ld, const float *__restrict__ bias, int tokens, int E,
-                      int K, RouterScore sc, int vec, int vec_bias, int one_wave, int32_t *__restrict__ ids,
+                      int K, RouterScore sc, int vec, int one_wave, int32_t *__restrict__ ids,
                       float *__restrict__ probs) {
-    __shared__ unsigned s_key[kRouterWarps][32];
-    __shared__ int s_id[kRouterWarps][32], s_slot[kRouterWarps][32];
+    __shared__ __align__(16) unsigned long long s_cand[kRouterWarps][32];
+    __shared__ int s_slot[kRouterWarps][32];
     pdl_begin_if(one_wave);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kRouterWarps + warp;
     if (t >= tokens) return;
     const T *row = logits + (size_t)t * ld;
-    const float neg_inf = __int_as_float(0xff800000);
     unsigned key[V];
-    {
-        float f[V];
-        load_row<T, V>(row, lane * V, E, vec, neg_inf, f);
-        if (bias) {
-            float b[V];
-            load_row<float, V>(bias, lane * V, E, vec_bias, 0.0f, b);
 #pragma unroll
-            for (int i = 0; i < V; ++i) f[i] += b[i];
+    for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = 0u;
+        if (e < E) {
+            float s = to_f32(row[e]);
+            if (bias) s += bias[e];
+            key[i] = score_key(s);
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = score_key(f[i]);
     }
-    unsigned best = 0u;
+    unsigned best = 0u, top = 0u;
 #pragma unroll
     for (int i = 0; i < V; ++i) best = max(best, key[i]);
     // a lower bound of the K-th largest key; lanes with equal maxima are struck out together, which only lowers it
-    unsigned bound = kNoKey + 1;
+#pragma unroll 4
     for (int k = 0; k < K; ++k) {
-        const unsigned top = __reduce_max_sync(kFullMask, best);
-        bound = max(top, kNoKey + 1);
-        if (top <= kNoKey) break;
+        top = __reduce_max_sync(kFullMask, best);
         if (best == top) best = 0u;
     }
-    int mine = 0;
+    const unsigned bound = max(top, kNoKey + 1);
+    unsigned mask = 0u;                                             // this lane's candidates
 #pragma unroll
-    for (int i = 0; i < V; ++i) mine += key[i] >= bound ? 1 : 0;
-    int at = mine;                                                  // candidates in the lanes up to this one
+    for (int i = 0; i < V; ++i) mask |= key[i] >= bound ? 1u << i : 0u;
+    int at = __popc(mask);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(kFullMask, at, o);
         if (lane >= o) at += v;
     }
     const int n = __shfl_sync(kFullMask, at, 31);
-    at -= mine;
     int my_id = -1;                                                 // lane k: the expert of slot k
     if (n <= 32) {
+        // the larger key, then the lower id, is the larger 64-bit number
+        s_cand[warp][lane] = 0ull;
+        __syncwarp();
+        unsigned long long *to = &s_cand[warp][at - __popc(mask)];
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (key[i] >= bound) {
-                s_key[warp][at] = key[i];
-                s_id[warp][at] = lane * V + i;
-                ++at;
-            }
+            if (mask >> i & 1u) *to++ = (unsigned long long)key[i] << 32 | (unsigned)~(i * 32 + lane);
         __syncwarp();
-        const unsigned mk = lane < n ? s_key[warp][lane] : 0u;
+        const unsigned long long own = s_cand[warp][lane];
         int rank = 0;
-        for (int j = 0; j < n; ++j) {
-            const unsigned other = s_key[warp][j];
-            if (other > mk || (other == mk && j < lane)) ++rank;    // ties to the lower id
+        for (int j = 0; j < n; j += 2) {                            // past the last candidate is 0
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(&s_cand[warp][j]);
+            rank += (o.x > own) + (o.y > own);
         }
-        if (lane < n && rank < K) s_slot[warp][rank] = s_id[warp][lane];
+        if (lane < n && rank < K) s_slot[warp][rank] = ~(int)(unsigned)own;
         __syncwarp();
         if (lane < min(n, K)) my_id = s_slot[warp][lane];
     } else {                                                        // many equal keys: K rounds of the largest key
         for (int k = 0; k < K; ++k) {
-            unsigned b = 0u;
+            unsigned m = 0u;
 #pragma unroll
-            for (int i = 0; i < V; ++i) b = max(b, key[i]);
-            const unsigned top = __reduce_max_sync(kFullMask, b);
-            if (top <= kNoKey) break;
+            for (int i = 0; i < V; ++i) m = max(m, key[i]);
+            const unsigned largest = __reduce_max_sync(kFullMask, m);
+            if (largest <= kNoKey) break;
             int e = E;
 #pragma unroll
             for (int i = V - 1; i >= 0; --i)
-                if (key[i] == top) e = lane * V + i;
+                if (key[i] == largest) e = i * 32 + lane;
             const int first = __reduce_min_sync(kFullMask, e);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (first == lane * V + i) key[i] = 0u;
+                if (first == i * 32 + lane) key[i] = 0u;
             if (lane == k) my_id = first;
         }
     }
@@ -309,7 +304,7 @@ extern "C" int ep_router_topk(const void *logits, long long stride, int dtype, c
             using E = std::remove_const_t<std::remove_pointer_t<P>>;
             return launch_pdl(ep_router_topk_kernel<E, decltype(v)::value>, dim3(grid), dim3(kRouterThreads), 0,
                               as_stream(stream), (P)logits, stride, bias, T, n_experts, K, sc,
-                              (int)rows_aligned(logits, stride, dtype), (int)aligned16(bias), one_wave(grid), topk_ids,
+                              (int)rows_aligned(logits, stride, dtype), one_wave(grid), topk_ids,
                               topk_probs);
         });
     });
