@@ -239,7 +239,6 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     __shared__ int s_row[kMaxE + 2];                                // first row of each group
     __shared__ int s_warp[kExpertWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gl = lane >> 2, q = lane & 3;
-    if (cta_status(a.status)) return;
 
     // chunks before each group: thread i scans a run of groups
     for (int g = tid; g <= a.G; g += kExpertThreads) s_row[g] = min(max(a.row_offsets[g], 0), a.R_max);
@@ -347,6 +346,10 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     prefetch();
     pdl_begin();                                                    // x is there
     copy_x(cur, 0, s_x, 0);
+    if (cta_status(a.status)) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        return;
+    }
 
     int buf = 0;
     for (int parity = 0; cur.item < items; parity ^= 1) {

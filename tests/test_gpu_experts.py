@@ -179,7 +179,8 @@ def test_status_repeat_and_streams():
 
 
 def test_rows_outside_the_layout_are_not_used():
-    """A src_info entry that names no token is a zero row, and row_offsets past R_max are cut there."""
+    """A src_info entry that names no token is a zero row, and row_offsets past R_max are cut there; the bounds-checked
+    build reports such an entry and writes nothing."""
     import combine_topk_ids_histogram_gb300 as ep
     L = ep.dispatch_layout(routing(6, 2, 4, 5), 4)
     w = weights(4, 24, 96, 3)
@@ -190,11 +191,12 @@ def test_rows_outside_the_layout_are_not_used():
     L.row_offsets[4] = L.R_max + 3
     ep.expert_matvec(x, *w, L, out=buf)
     torch.cuda.synchronize()
+    if ep.CHECKED:
+        assert ep.read_status(L) == ep.STATUS_BOUNDS and (buf == 7).all()
+        return
     keep = [r for r in range(L.R_max) if r not in (3, 5)]
     assert torch.equal(buf[keep], good[keep])
-    assert (buf[L.R_max:] == 7).all()
-    if not ep.CHECKED:
-        assert (buf[[3, 5]] == 0).all()
+    assert (buf[L.R_max:] == 7).all() and (buf[[3, 5]] == 0).all()
 
 
 def test_no_tokens_and_refusals():
