@@ -132,7 +132,7 @@ def _check(rc: int, what: str):
         raise EPError(rc, what)
 
 
-# the current stream's handle without the Stream object around it (2.6 us of a call's host time on GB300's host)
+# the current stream's handle without the Stream object around it (2.4 us less of a call's host time on GB300's host)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 

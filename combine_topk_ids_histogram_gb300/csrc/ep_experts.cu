@@ -428,16 +428,20 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
 
 template <bool WIDE, typename S>
 int launch_expert_matvec(const ExpertArgs &a, cudaStream_t st) {
-    const auto kern = ep_expert_matvec_kernel<WIDE, S>;
-    const int rc = launch_pdl(ep_expert_pack_kernel<WIDE>, dim3(a.R_max), dim3(kPackThreads), 0, st, a);
+    constexpr auto kern = ep_expert_matvec_kernel<WIDE, S>;
+    int rc = allow_smem<kern>(S::SMEM);
     if (rc != EP_OK) return rc;
-    static const cudaError_t set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
-    if (set != cudaSuccess) return launch_result(set);
+    rc = launch_pdl(ep_expert_pack_kernel<WIDE>, dim3(a.R_max), dim3(kPackThreads), 0, st, a);
+    if (rc != EP_OK) return rc;
     const int grid = resident_blocks(kern, S::THREADS, S::SMEM);
     if (grid <= 0) return EP_ERR_CUDA;
     return launch_pdl(kern, dim3(grid), dim3(S::THREADS), S::SMEM, st, a);
 }
 
+// Up to 8 rows per expert: two steps of weights in 128 registers, 16 warps per SM.  More: a pass serves 16 rows and 12 warps
+// have 168 registers each, since spilled prefetches would be waited for.  64 tokens over 8 experts, top-2 (14336 -> 4096 /
+// 4096 -> 2 x 4096 gated): 134 us with passes of 8 rows, 109 / 62 us with this shape; 120 / 70 with two CTAs of 6 warps,
+// 128 / 66 with 8 warps, 143 / 76 with passes of 32 rows.
 using FewRows = Shape<2, 1, 256, 2, 8>;
 using MoreRows = Shape<2, 2, 384, 1, 8>;
 

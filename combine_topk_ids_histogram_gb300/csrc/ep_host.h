@@ -7,6 +7,7 @@
 #include <stdint.h>
 #include <stdlib.h>
 
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 #include <utility>
@@ -142,6 +143,21 @@ inline int one_wave(int ctas) {
     return sms > 0 && ctas <= sms ? 1 : 0;
 }
 
+// Lets `kernel` have up to `bytes` of dynamic shared memory (always the same for a kernel); set once per device.
+template <auto kernel>
+inline int allow_smem(size_t bytes) {
+    constexpr int kMaxDev = 64;
+    static std::atomic<bool> set[kMaxDev];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return launch_result(cudaErrorInvalidDevice);
+    const bool cacheable = dev >= 0 && dev < kMaxDev;
+    if (cacheable && set[dev].load(std::memory_order_relaxed)) return EP_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return launch_result(e);
+    if (cacheable) set[dev].store(true, std::memory_order_relaxed);
+    return EP_OK;
+}
+
 // Blocks of `kernel` that fit on the device at once (SM count x resident blocks per SM),
 // for grids that loop over their work.  Cached per (device, kernel, block size, shared memory).
 template <typename K>
@@ -152,7 +168,7 @@ inline int resident_blocks(K kernel, int threads, size_t smem) {
         size_t smem;
         int blocks;
     };
-    constexpr int kSlots = 32;
+    constexpr int kSlots = 64;
     static Entry cache[kSlots];
     static std::mutex mu;
     int dev = 0;

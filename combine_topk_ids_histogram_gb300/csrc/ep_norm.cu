@@ -676,10 +676,6 @@ int group_grid(int rows, int R) {
     return sms > 0 && sms < full ? sms : full;
 }
 
-template <typename K> int set_smem(K kern, size_t bytes) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
-}
-
 // A piece more than the elements fill, for rows that begin and end inside one.
 constexpr int laid(int H, int lay, int vec) { return lay == kShifted ? H + 2 * (vec - 1) : H; }
 
@@ -694,9 +690,9 @@ int launch_fwd(const NormArgs &a) {
     const int row_bytes = kFwdStages<T> * RowSource<T, kFwdEpt, LAY>::stage_bytes(a.H), params = 2 * param_bytes<W>(a.H + 2 * VEC);
     const dim3 block = group_shape(laid(a.H, LAY, VEC), kFwdEpt, kFwdThreads, LAY, params, row_bytes);
     if (block.y < 1) return launch_fwd_rows<T, W, RV, (RV == 1 ? 32 : 8)>(a);
-    const auto kern = ep_norm_kernel<T, W, LAY>;
-    static const int rc = set_smem(kern, kSharedBytes);
-    if (rc != EP_OK) return launch_result(cudaErrorInvalidValue);
+    constexpr auto kern = ep_norm_kernel<T, W, LAY>;
+    const int rc = allow_smem<kern>(kSharedBytes);
+    if (rc != EP_OK) return rc;
     const size_t smem = param_copies(LAY, block.y) * params + (size_t)block.y * row_bytes;
     return launch_pdl(kern, dim3(group_grid(a.rows, block.y)), block, smem, a.st, (const T *)a.x, a.ldx, (const W *)a.w,
                       (const W *)a.b, a.rows, a.H, a.eps, a.rms, a.period, (T *)a.out, a.mean_out, a.rstd_out);
@@ -719,11 +715,11 @@ int launch_bwd(const NormArgs &a) {
         constexpr int VEC = 16 / sizeof(T);
         const int row_bytes = kBwdStages * 2 * RowSource<T, kBwdEpt, LAY>::stage_bytes(a.H), params = param_bytes<W>(a.H + 2 * VEC);
         const dim3 block = group_shape(laid(a.H, LAY, VEC), kBwdEpt, kBwdThreads, LAY, params, row_bytes);
-        const auto kern = ep_norm_bwd_kernel<T, W, LAY>;
+        constexpr auto kern = ep_norm_bwd_kernel<T, W, LAY>;
         const size_t stages = param_copies(LAY, block.y) * params + (size_t)block.y * row_bytes;
         const size_t sums = (size_t)block.y * 2 * a.H * sizeof(float);
-        static const int rc = set_smem(kern, kSharedBytes);
-        if (rc != EP_OK) return launch_result(cudaErrorInvalidValue);
+        const int rc = allow_smem<kern>(kSharedBytes);
+        if (rc != EP_OK) return rc;
         const int grid = min(group_grid(a.rows, block.y), kPartials);
         const int e = launch_pdl(kern, dim3(grid), block, stages > sums ? stages : sums, a.st, (const T *)a.g, a.ldg,
                                  (const T *)a.x, a.ldx, (const W *)a.w, a.mean_in, a.rstd_in, a.rows, a.H, a.rms,

@@ -404,8 +404,8 @@ typedef enum { EP_BF16 = 0, EP_F16 = 1, EP_F32 = 2 } ep_dtype_t;
 /*
  * The norm and router calls differ from the other calls in two conventions: their matrix inputs
  * may have a row stride (in elements, at least the row's length), and pointers marked (e) need
- * only their element's alignment.  Rows and parameters on 16-byte boundaries are read 16 bytes
- * at a time, others element by element.
+ * only their element's alignment.  Outputs and workspaces of these calls and of ep_expert_matvec must
+ * not overlap their inputs or one another.
  */
 
 /*

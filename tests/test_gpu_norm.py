@@ -131,9 +131,10 @@ def test_no_write_outside_outputs():
         assert (f[:, :8] == 7).all() and (f[:2, 8 + H:] == 7).all() and (ws[nws:] == 7).all()
 
 
-def test_constant_rows_and_large_means():
+@pytest.mark.parametrize("rep", [1, 500])
+def test_constant_rows_and_large_means(rep):
     """A constant row has variance 0: y = bias, and rstd = 1/sqrt(eps).  A large mean costs no digits of the
-    variance."""
+    variance.  (rep: in few rows, and in many.)"""
     import combine_topk_ids_histogram_gb300 as ep
     x = torch.zeros(4, 512, device="cuda")
     x[1] = 3.0
@@ -141,22 +142,24 @@ def test_constant_rows_and_large_means():
     x[3] = -1e30
     w = torch.ones(512, device="cuda")
     b = torch.full((512,), 0.25, device="cuda")
-    y, mean, rstd = check_forward(ep, x, w, b, 1e-5, False)
+    y, mean, rstd = check_forward(ep, x.repeat(rep, 1), w, b, 1e-5, False)
+    y, rstd = y[-4:], rstd[-4:]
     assert (y[:2] == 0.25).all() and (y[3] == 0.25).all()
     # in-bound at the large mean is not enough: the two-pass variance is within 1e-6 of 64 bits
     r = ref.norm(x, w, b, 1e-5, False)[2]
     assert abs(rstd[2].item() / r[2].item() - 1) < 1e-6
 
 
-def test_non_finite_rows_stay_in_their_rows():
+@pytest.mark.parametrize("T,H", [(8, 300), (1200, 300), (1200, 301)])
+def test_non_finite_rows_stay_in_their_rows(T, H):
     import combine_topk_ids_histogram_gb300 as ep
-    x, w, b, gy = make(8, 300, torch.float32, torch.float32, 5)
+    x, w, b, gy = make(T, H, torch.float32, torch.float32, 5)
     clean = ep.layer_norm(x, w, b)
     bad = x.clone()
     bad[2, 7] = float("inf")
-    bad[5, 299] = float("nan")
+    bad[5, H - 1] = float("nan")
     y, mean, rstd = ep.layer_norm(bad, w, b)
-    rows = [0, 1, 3, 4, 6, 7]
+    rows = [r for r in range(T) if r not in (2, 5)]
     assert torch.equal(y[rows], clean[0][rows]) and torch.equal(rstd[rows], clean[2][rows])
     assert torch.isnan(y[2]).all() and torch.isnan(y[5]).all()
     dx, dw, db = ep.layer_norm_bwd(gy, bad, w, mean, rstd, bias=True)
