@@ -81,69 +81,86 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// What a thread holds of one step: for each of its 2 * MT weight rows 64 codes and their scales.
-template <int MT> struct Weights {
+// What a thread holds of one step: for each of its 2 * MT weight rows 64 consecutive codes and their scales.  ALIGN is the
+// number of bytes that every weight row begins on a multiple of: 32, 16 or 8.
+template <int MT, int ALIGN> struct Weights {
     uint32_t w[2 * MT][8];
-    uint32_t s[2 * MT];
+    uint32_t s[2 * MT][ALIGN == 32 ? 1 : 2];
+    uint32_t at;                         // ALIGN 8: bits 2r, 2r + 1: the byte of s[r] that is the first scale; from bit 8: a mask's shift
 };
 
-// k of word wi (8 codes) of quad thread q within a step.  WIDE: 64 consecutive codes per thread, one 32-byte
-// load per row; else four runs of 16 codes, 8-byte loads, for rows that are only 8-byte aligned.
-template <bool WIDE> __device__ __forceinline__ int word_k(int q, int wi) {
-    return WIDE ? q * 64 + wi * 8 : (wi >> 1) * 64 + q * 16 + (wi & 1) * 8;
-}
+// k of word wi (8 codes) of quad thread q within a step.
+__device__ __forceinline__ int word_k(int q, int wi) { return q * 64 + wi * 8; }
 
-template <bool WIDE, int MT>
-__device__ __forceinline__ void load_weights(Weights<MT> &d, const uint8_t *codes, const uint8_t *scales,
-                                             const unsigned (&row)[2 * MT], int half, int step, int q, int H) {
-    if constexpr (WIDE) {
-        const int k = step * kStepK + q * 64;
-        if (k < H) {
+template <int ALIGN, int MT>
+__device__ __forceinline__ void load_weights(Weights<MT, ALIGN> &d, const uint8_t *codes, const uint8_t *scales,
+                                             const uint8_t *scales_end, const unsigned (&row)[2 * MT], int step, int q, int H) {
+    const int k = step * kStepK + q * 64;
 #pragma unroll
-            for (int r = 0; r < 2 * MT; ++r) {
-                const unsigned long long at = (unsigned long long)row[r] * half + (k >> 1);
-                asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                             : "=r"(d.w[r][0]), "=r"(d.w[r][1]), "=r"(d.w[r][2]), "=r"(d.w[r][3]), "=r"(d.w[r][4]),
-                               "=r"(d.w[r][5]), "=r"(d.w[r][6]), "=r"(d.w[r][7])
-                             : "l"(codes + at));
-                d.s[r] = __ldg(reinterpret_cast<const uint32_t *>(scales + (at >> 3)));
-            }
+    for (int r = 0; r < 2 * MT; ++r) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d.w[r][i] = 0u;
+        d.s[r][0] = 0u;
+        if constexpr (ALIGN != 32) d.s[r][1] = 0u;
+    }
+    if constexpr (ALIGN == 8) d.at = 0u;
+    if (k >= H) return;
+    if constexpr (ALIGN == 8) d.at = (unsigned)max(0, 64 - (H - k)) << 7;   // 8 * scales past the row's end, at bit 8
+#pragma unroll
+    for (int r = 0; r < 2 * MT; ++r) {
+        const unsigned long long at = (unsigned long long)row[r] * ((unsigned)H >> 1) + (unsigned)(k >> 1);
+        const uint8_t *c = codes + at, *s = scales + (at >> 3);
+        if constexpr (ALIGN == 32) {
+            asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(d.w[r][0]), "=r"(d.w[r][1]), "=r"(d.w[r][2]), "=r"(d.w[r][3]), "=r"(d.w[r][4]),
+                           "=r"(d.w[r][5]), "=r"(d.w[r][6]), "=r"(d.w[r][7])
+                         : "l"(c));
+            d.s[r][0] = __ldg(reinterpret_cast<const uint32_t *>(s));
+        } else if constexpr (ALIGN == 16) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (k + 32 * j < H) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(c + 16 * j));
+                    d.w[r][4 * j] = v.x; d.w[r][4 * j + 1] = v.y; d.w[r][4 * j + 2] = v.z; d.w[r][4 * j + 3] = v.w;
+                    d.s[r][j] = __ldg(reinterpret_cast<const uint16_t *>(s + 2 * j));
+                }
         } else {
 #pragma unroll
-            for (int r = 0; r < 2 * MT; ++r) {
-                d.s[r] = 0u;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d.w[r][i] = 0u;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int r = 0; r < 2 * MT; ++r) {
-            d.s[r] = 0u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = step * kStepK + j * 64 + q * 16;
-                uint2 v = make_uint2(0u, 0u);
-                if (k < H) {
-                    const unsigned long long at = (unsigned long long)row[r] * half + (k >> 1);
-                    v = __ldg(reinterpret_cast<const uint2 *>(codes + at));
-                    d.s[r] |= (uint32_t)__ldg(scales + (at >> 3)) << (8 * j);
+            for (int j = 0; j < 4; ++j)
+                if (k + 16 * j < H) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(c + 8 * j));
+                    d.w[r][2 * j] = v.x; d.w[r][2 * j + 1] = v.y;
                 }
-                d.w[r][2 * j] = v.x;
-                d.w[r][2 * j + 1] = v.y;
+            // the scales begin at any byte: the two aligned words around them, bytes where the scales' own end cuts one off
+            const unsigned off = (unsigned)(at >> 3) & 3u;
+            d.at |= off << (2 * r);
+            s -= off;
+            if (s + 8 <= scales_end) {
+                d.s[r][0] = __ldg(reinterpret_cast<const uint32_t *>(s));
+                d.s[r][1] = __ldg(reinterpret_cast<const uint32_t *>(s + 4));
+            } else {
+                for (int i = 0; i < 8; ++i)
+                    if (s + i < scales_end) d.s[r][i >> 2] |= (uint32_t)s[i] << (8 * (i & 3));
             }
         }
     }
 }
 
+// The four scales of row r, one per byte; zero past the row's end.
+template <int ALIGN, int MT> __device__ __forceinline__ uint32_t row_scales(const Weights<MT, ALIGN> &d, int r) {
+    if constexpr (ALIGN == 32) return d.s[r][0];
+    else if constexpr (ALIGN == 16) return __byte_perm(d.s[r][0], d.s[r][1], 0x5410);
+    else return __funnelshift_r(d.s[r][0], d.s[r][1], 8 * (d.at >> (2 * r) & 3u)) & (~0u >> (d.at >> 8));
+}
+
 // One step of a warp: MT * 16 weight rows x 256 k x the first USE of NT blocks of 8 layout rows.  x: the step's pieces of this thread's
 // layout row in shared memory, xo: how far on its row of the second block of 8 is.
-template <int USE, int MT, int NT>
-__device__ __forceinline__ void mma_step(const Weights<MT> &d, const uint4 *x, const int (&xo)[NT],
+template <int USE, int ALIGN, int MT, int NT>
+__device__ __forceinline__ void mma_step(const Weights<MT, ALIGN> &d, const uint4 *x, const int (&xo)[NT],
                                          float (&acc)[MT][NT][4]) {
     uint32_t sc[2 * MT][2];
 #pragma unroll
-    for (int r = 0; r < 2 * MT; ++r) scales_to_f16(d.s[r], sc[r]);
+    for (int r = 0; r < 2 * MT; ++r) scales_to_f16(row_scales(d, r), sc[r]);
 #pragma unroll
     for (int wi = 0; wi < 8; ++wi) {
         uint4 b[USE];
@@ -164,7 +181,6 @@ __device__ __forceinline__ void mma_step(const Weights<MT> &d, const uint4 *x, c
 }
 
 // x of one layout row, scaled to fp16 and reordered: one CTA per row.
-template <bool WIDE>
 __global__ void __launch_bounds__(kPackThreads)
 ep_expert_pack_kernel(const ExpertArgs a) {
     __shared__ unsigned s_top[kPackThreads / 32];
@@ -197,7 +213,7 @@ ep_expert_pack_kernel(const ExpertArgs a) {
     const int pieces = (a.H + kStepK - 1) / kStepK * 32;
     uint4 *dst = a.xw + (size_t)row * pieces;
     for (int p = tid; p < pieces; p += kPackThreads) {
-        const int k = (p >> 5) * kStepK + word_k<WIDE>(p & 3, (p >> 2) & 7);
+        const int k = (p >> 5) * kStepK + word_k(p & 3, (p >> 2) & 7);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (real && k < a.H) {
             float f[8];
@@ -227,7 +243,7 @@ template <int MT_, int NT_, int THREADS_, int CTAS_, int P_> struct Shape {
 // copied to shared memory while the present one is computed, and a warp has its next step's weights on their
 // way to registers.  The first weights start before x is there, because the weights, like every argument,
 // were complete before the first kernel started.
-template <bool WIDE, typename S>
+template <int ALIGN, typename S>
 __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 ep_expert_matvec_kernel(const ExpertArgs a) {
     constexpr int kChunkRows = S::ROWS, P = S::P, PITCH = S::PITCH, MT = S::MT, NT = S::NT;
@@ -274,7 +290,6 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     const int rows_out = per_warp * NS;                             // output columns of an item
     const int blocks = (n_out + rows_out - 1) / rows_out;
     const int items = s_first[a.G] * blocks;                        // the output holds 128 elements per item: fits an int
-    const int half = a.H >> 1;
     const int steps = (a.H + kStepK - 1) / kStepK;
 
     struct Cursor {
@@ -310,10 +325,11 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     unsigned pf_row[2 * MT];
     weight_rows(pf, pf_row);
     int pf_step = kw;
-    Weights<MT> nxt;
+    Weights<MT, ALIGN> nxt;
+    const uint8_t *const scales_end = a.scales + (size_t)a.G * a.N * (a.H >> 4);
     // past the last item this loads the last step once more: no branch around the loads
     const auto prefetch = [&]() {
-        load_weights<WIDE, MT>(nxt, a.codes, a.scales, pf_row, half, pf_step, q, a.H);
+        load_weights<ALIGN, MT>(nxt, a.codes, a.scales, scales_end, pf_row, pf_step, q, a.H);
         if (pf_step + KS < steps) {
             pf_step += KS;
         } else if (pf.item + (int)gridDim.x < items) {
@@ -378,7 +394,7 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
             const int to = min(P, steps - from);
             const uint4 *x = s_x + buf * kChunkRows * PITCH + x_at;
             for (int st = kw; st < to; st += KS) {
-                const Weights<MT> w = nxt;
+                const Weights<MT, ALIGN> w = nxt;
                 prefetch();
                 if (NT > 1 && m <= 8) mma_step<1>(w, x + st * 32, xo, acc);
                 else mma_step<NT>(w, x + st * 32, xo, acc);
@@ -426,24 +442,17 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     }
 }
 
-template <bool WIDE, typename S>
-int launch_expert_matvec(const ExpertArgs &a, cudaStream_t st) {
-    constexpr auto kern = ep_expert_matvec_kernel<WIDE, S>;
-    int rc = allow_smem<kern>(S::SMEM);
-    if (rc != EP_OK) return rc;
-    rc = launch_pdl(ep_expert_pack_kernel<WIDE>, dim3(a.R_max), dim3(kPackThreads), 0, st, a);
-    if (rc != EP_OK) return rc;
-    const int grid = resident_blocks(kern, S::THREADS, S::SMEM);
-    if (grid <= 0) return EP_ERR_CUDA;
-    return launch_pdl(kern, dim3(grid), dim3(S::THREADS), S::SMEM, st, a);
-}
-
 // Up to 8 rows per expert: two steps of weights in 128 registers, 16 warps per SM.  More: a pass serves 16 rows and 12 warps
 // have 168 registers each, since spilled prefetches would be waited for.  64 tokens over 8 experts, top-2 (14336 -> 4096 /
 // 4096 -> 2 x 4096 gated): 134 us with passes of 8 rows, 109 / 62 us with this shape; 120 / 70 with two CTAs of 6 warps,
 // 128 / 66 with 8 warps, 143 / 76 with passes of 32 rows.
 using FewRows = Shape<2, 1, 256, 2, 8>;
 using MoreRows = Shape<2, 2, 384, 1, 8>;
+
+// Rows on 8-byte boundaries only need more registers for their scales.  16 tokens, 64 experts, top-4, 2064 -> 2 x 2048 gated /
+// 7184 -> the same: 58 / 164 us with FewRows, which spills, 53 / 158 us with this.  On 16-byte boundaries FewRows holds: 53 us
+// at 2080, 60 with this.  (2048 takes 37 us: its rows fill whole steps of 256 k and one load brings each thread's 64 codes.)
+using FewUnaligned = Shape<2, 1, 384, 1, 8>;
 
 // KS: the split that ends soonest when every CTA takes its rounds of items one after another, a round lasting its
 // warps' steps and about one more to begin and end an item (half a step more to join sums).
@@ -462,6 +471,19 @@ int choose_split(const ExpertArgs &a, int steps, float chunks) {
         }
     }
     return best;
+}
+
+template <int ALIGN, typename S>
+int launch_expert_matvec(ExpertArgs a, float chunks, cudaStream_t st) {
+    constexpr auto kern = ep_expert_matvec_kernel<ALIGN, S>;
+    a.KS = choose_split<S>(a, pack_steps(a.H), chunks);
+    int rc = allow_smem<kern>(S::SMEM);
+    if (rc != EP_OK) return rc;
+    rc = launch_pdl(ep_expert_pack_kernel, dim3(a.R_max), dim3(kPackThreads), 0, st, a);
+    if (rc != EP_OK) return rc;
+    const int grid = resident_blocks(kern, S::THREADS, S::SMEM);
+    if (grid <= 0) return EP_ERR_CUDA;
+    return launch_pdl(kern, dim3(grid), dim3(S::THREADS), S::SMEM, st, a);
 }
 
 }  // namespace
@@ -507,9 +529,12 @@ extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t
     const float active = L->E * (1.0f - expf(-per_expert));
     const float rows = few ? 8.0f : 16.0f;
     const float chunks = active * fmaxf(1.0f, per_expert / rows + 0.5f) + (L->fused_shared ? ceilf(L->T / rows) : 0.0f);
-    a.KS = few ? choose_split<FewRows>(a, steps, chunks) : choose_split<MoreRows>(a, steps, chunks);
-    const bool wide = H % 64 == 0 && (reinterpret_cast<uintptr_t>(codes) & 31u) == 0;
     cudaStream_t st = as_stream(stream);
-    if (few) return wide ? launch_expert_matvec<true, FewRows>(a, st) : launch_expert_matvec<false, FewRows>(a, st);
-    return wide ? launch_expert_matvec<true, MoreRows>(a, st) : launch_expert_matvec<false, MoreRows>(a, st);
+    const bool by64 = H % 64 == 0 && (reinterpret_cast<uintptr_t>(codes) & 31u) == 0;
+    if (few) {
+        if (by64) return launch_expert_matvec<32, FewRows>(a, chunks, st);
+        return H % 32 == 0 ? launch_expert_matvec<16, FewRows>(a, chunks, st) : launch_expert_matvec<8, FewUnaligned>(a, chunks, st);
+    }
+    if (by64) return launch_expert_matvec<32, MoreRows>(a, chunks, st);
+    return H % 32 == 0 ? launch_expert_matvec<16, MoreRows>(a, chunks, st) : launch_expert_matvec<8, MoreRows>(a, chunks, st);
 }

@@ -95,6 +95,23 @@ def test_unused_slots_and_empty_groups(swiglu):
         check(ep, L, weights(32, 48, 160, 2), False, swiglu, 4)
 
 
+@pytest.mark.parametrize("H", [16, 48, 80, 272, 304, 1040])
+def test_a_nan_scale_stays_in_its_weight_row(H):
+    """Rows whose scales begin at any byte: the block after a row's last one is the next row's."""
+    import combine_topk_ids_histogram_gb300 as ep
+    N = 37
+    codes, scales, row_scale = weights(2, N, H, 9)
+    scales[0, 5, 0] = scales[1, 20, -1] = scales[1, N - 1, -1] = 0x7F
+    codes |= 0x11                                                       # no zero weight
+    L = ep.dispatch_layout(routing(4, 2, 2, 1), 2)
+    x = torch.randn(4, H, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    got = ep.expert_matvec(x, codes, scales, row_scale, L)
+    bad = torch.isnan(got)
+    want = torch.zeros_like(bad)
+    want[:4, 5] = want[4:, 20] = want[4:, N - 1] = True
+    assert torch.equal(bad, want)
+
+
 def test_all_rows_in_one_expert_and_negative_scales():
     import combine_topk_ids_histogram_gb300 as ep
     L = ep.dispatch_layout(routing(100, 2, 5, 1, only=3), 5)
