@@ -17,6 +17,8 @@
 // tensor cores, and a first kernel writes x as fp16 in that order.
 #include <math.h>
 
+#include <algorithm>
+
 #include "ep_host.h"
 #include "ep_types.cuh"
 
@@ -24,7 +26,7 @@ namespace ep {
 namespace {
 
 constexpr int kStepK = 256;              // k per warp step: 64 per thread of a quad
-constexpr int kPackThreads = 256;
+constexpr int kPackThreads = 1024;       // at most; a thread takes 8 values at a time
 
 struct ExpertArgs {
     const uint16_t *x;
@@ -193,7 +195,7 @@ ep_expert_pack_kernel(const ExpertArgs a) {
     if (!real && src != -1) bounds_fail(a.status);
     const uint4 *x = reinterpret_cast<const uint4 *>(a.x + (real ? (size_t)src * a.H : 0));
     unsigned top = 0u;                                              // largest finite magnitude, as bf16 bits
-    for (int p = tid; real && p < a.H / 8; p += kPackThreads) {
+    for (int p = tid; real && p < a.H / 8; p += blockDim.x) {
         const uint4 v = __ldg(x + p);
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -205,14 +207,13 @@ ep_expert_pack_kernel(const ExpertArgs a) {
     top = __reduce_max_sync(kFullMask, max(top & 0xffffu, top >> 16));
     if ((tid & 31) == 0) s_top[tid >> 5] = top;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kPackThreads / 32; ++w) top = max(top, s_top[w]);
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) top = max(top, s_top[w]);
     const int e = max((int)(top >> 7), 15);                         // biased exponent; both powers stay normal
     const float up = __uint_as_float((unsigned)(268 - e) << 23);    // 2^(141 - e)
     if (tid == 0) a.xs[row] = __uint_as_float((unsigned)(e - 14) << 23);
     const int pieces = (a.H + kStepK - 1) / kStepK * 32;
     uint4 *dst = a.xw + (size_t)row * pieces;
-    for (int p = tid; p < pieces; p += kPackThreads) {
+    for (int p = tid; p < pieces; p += blockDim.x) {
         const int k = (p >> 5) * kStepK + word_k(p & 3, (p >> 2) & 7);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (real && k < a.H) {
@@ -442,10 +443,11 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     }
 }
 
-// Up to 8 rows per expert: two steps of weights in 128 registers, 16 warps per SM.  More: a pass serves 16 rows and 12 warps
-// have 168 registers each, since spilled prefetches would be waited for.  64 tokens over 8 experts, top-2 (14336 -> 4096 /
-// 4096 -> 2 x 4096 gated): 134 us with passes of 8 rows, 109 / 62 us with this shape; 120 / 70 with two CTAs of 6 warps,
-// 128 / 66 with 8 warps, 143 / 76 with passes of 32 rows.
+// Fewer than 8 rows per expert: two steps of weights in 128 registers, 16 warps per SM, passes of 8 rows.  More: a pass serves
+// 16 rows and 12 warps have 168 registers each, since spilled prefetches would be waited for.  8 experts, top-2, 4096 -> 2 x
+// 2048 gated, with 4 / 6 / 8 / 10 rows per expert: 22 / 28 / 33 / 36 us with passes of 8 rows, 29 / 31 / 32 / 34 us with 16; with
+// 16 rows, 14336 -> 4096: 134 and 109 us.  Of the shapes for 16 rows this one is best there: 120 us with two CTAs of 6 warps,
+// 128 us with 8 warps, 143 us with passes of 32 rows.
 using FewRows = Shape<2, 1, 256, 2, 8>;
 using MoreRows = Shape<2, 2, 384, 1, 8>;
 
@@ -479,7 +481,8 @@ int launch_expert_matvec(ExpertArgs a, float chunks, cudaStream_t st) {
     a.KS = choose_split<S>(a, pack_steps(a.H), chunks);
     int rc = allow_smem<kern>(S::SMEM);
     if (rc != EP_OK) return rc;
-    rc = launch_pdl(ep_expert_pack_kernel, dim3(a.R_max), dim3(kPackThreads), 0, st, a);
+    const int pack = std::min(std::max((a.H / 8 + 31) / 32 * 32, 128), kPackThreads);
+    rc = launch_pdl(ep_expert_pack_kernel, dim3(a.R_max), dim3(pack), 0, st, a);
     if (rc != EP_OK) return rc;
     const int grid = resident_blocks(kern, S::THREADS, S::SMEM);
     if (grid <= 0) return EP_ERR_CUDA;
@@ -522,9 +525,8 @@ extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t
     a.xw = (uint4 *)workspace;
     a.xs = (float *)(a.xw + (size_t)a.R_max * steps * 32);
     a.out = out;
-    // rows that share weights: up to 8 per expert take the kernel whose passes serve 8
     const float per_expert = (float)L->T * L->K / L->E;
-    const bool few = per_expert <= 6.0f;
+    const bool few = per_expert < 8.0f;
     // chunks that a layout of this many rows has, if the router spreads them evenly
     const float active = L->E * (1.0f - expf(-per_expert));
     const float rows = few ? 8.0f : 16.0f;
