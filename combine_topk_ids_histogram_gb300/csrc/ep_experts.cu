@@ -37,6 +37,8 @@ struct ExpertArgs {
     const int32_t *row_offsets, *src_info, *status;
     uint4 *xw;                           // [R_max][step][word][quad thread] x as fp16, 16-byte pieces
     float *xs;                           // [R_max] what a row's sums are multiplied by
+    int draw;                            // CTAs draw their items; needs two steps or more of every warp in an item
+    unsigned *drawn;                     // items drawn beyond the first two of every CTA
     uint16_t *out;
 };
 
@@ -188,6 +190,7 @@ ep_expert_pack_kernel(const ExpertArgs a) {
     __shared__ unsigned s_top[kPackThreads / 32];
     pdl_begin();
     const int row = blockIdx.x, tid = threadIdx.x;
+    if (row == 0 && tid == 0) *a.drawn = 0u;
     const int R = a.row_offsets[a.G];                               // these three loads go out together
     const int src = a.by_token ? a.src_info[2 * (size_t)row] : row;
     if (cta_status(a.status) || row >= R) return;
@@ -238,12 +241,15 @@ template <int MT_, int NT_, int THREADS_, int CTAS_, int P_> struct Shape {
 };
 
 // Work is cut into items: a tile of weight rows of a group and a chunk of up to 8 * NT of the group's rows, chunks of
-// a tile next to each other so that L2 serves the second reading of its weights.  CTAs take items in
-// turn.  KS of a CTA's warps share each 32-row tile and split its k; their sums meet in shared memory in
-// a fixed order.  Nothing drains at an item's end: x of the next part of 8 / NT steps, of the next item too, is
-// copied to shared memory while the present one is computed, and a warp has its next step's weights on their
-// way to registers.  The first weights start before x is there, because the weights, like every argument,
-// were complete before the first kernel started.
+// a tile next to each other so that L2 serves the second reading of its weights.  A CTA begins with two
+// items and draws the others from a counter, each while it works on the one before the last, because SMs
+// differ in speed by a sixth while HBM is busy (items in turn / drawn: 271 / 265 us for 16 tokens, top-8 of 256, 7168 -> 2 x
+// 2048 gated; 116 / 106 us for 64 tokens, top-4 of 64, 4096 -> 2 x 2048).  Sums do not depend on who draws what.
+// KS of a CTA's warps share each 32-row tile and split its k; their sums meet in shared memory in a fixed
+// order.  Nothing drains at an item's end: x of the next part of P steps, of the next item too, is copied to
+// shared memory while the present one is computed, and a warp has its next step's weights on their way to
+// registers.  The first weights start before x is there, because the weights, like every argument, were
+// complete before the first kernel started.
 template <int ALIGN, typename S>
 __global__ void __launch_bounds__(S::THREADS, S::CTAS)
 ep_expert_matvec_kernel(const ExpertArgs a) {
@@ -255,6 +261,7 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     __shared__ int s_first[kMaxE + 2];                              // chunks before each group
     __shared__ int s_row[kMaxE + 2];                                // first row of each group
     __shared__ int s_warp[kExpertWarps];
+    __shared__ int s_next[2];                                       // the item after the present one, by its parity
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gl = lane >> 2, q = lane & 3;
 
     // chunks before each group: thread i scans a run of groups
@@ -325,7 +332,8 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     Cursor pf = cur;
     unsigned pf_row[2 * MT];
     weight_rows(pf, pf_row);
-    int pf_step = kw;
+    int pf_step = kw, parity = 0;
+    if (tid == 0) s_next[0] = cur.item + (int)gridDim.x;
     Weights<MT, ALIGN> nxt;
     const uint8_t *const scales_end = a.scales + (size_t)a.G * a.N * (a.H >> 4);
     // past the last item this loads the last step once more: no branch around the loads
@@ -333,11 +341,14 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
         load_weights<ALIGN, MT>(nxt, a.codes, a.scales, scales_end, pf_row, pf_step, q, a.H);
         if (pf_step + KS < steps) {
             pf_step += KS;
-        } else if (pf.item + (int)gridDim.x < items) {
-            pf_step = kw;
-            pf.item += gridDim.x;
-            locate(pf);
-            weight_rows(pf, pf_row);
+        } else {
+            const int n = a.draw ? s_next[parity] : pf.item + (int)gridDim.x;
+            if (n < items) {
+                pf_step = kw;
+                pf.item = n;
+                locate(pf);
+                weight_rows(pf, pf_row);
+            }
         }
     };
     const auto row_of_chunk = [&](const Cursor &c) { return s_row[c.g] + c.chunk * kChunkRows; };
@@ -369,11 +380,10 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     }
 
     int buf = 0;
-    for (int parity = 0; cur.item < items; parity ^= 1) {
+    for (; cur.item < items; parity ^= 1) {
         const int row0 = row_of_chunk(cur), m = rows_of_chunk(cur);
         Cursor nx = cur;
-        nx.item += gridDim.x;
-        if (nx.item < items) locate(nx);
+        unsigned drawn = 0u;
         float acc[MT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -389,6 +399,11 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
         for (int from = 0; from < steps; from += P, buf ^= 1) {
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncthreads();                                        // this part is there, and every warp is done with the other
+            if (from == 0) {
+                nx.item = a.draw ? s_next[parity] : cur.item + (int)gridDim.x;
+                if (nx.item < items) locate(nx);
+                if (a.draw && tid == 0) drawn = atomicAdd(a.drawn, 1u);
+            }
             uint4 *other = s_x + (buf ^ 1) * kChunkRows * PITCH;
             if (from + P < steps) copy_x(cur, from + P, other, parity);
             else if (nx.item < items) copy_x(nx, 0, other, parity ^ 1);
@@ -401,6 +416,8 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
                 else mma_step<NT>(w, x + st * 32, xo, acc);
             }
         }
+
+        if (a.draw && tid == 0) s_next[parity ^ 1] = (int)(drawn + 2 * gridDim.x);   // not before: the answer takes a microsecond
 
         // join the KS partial sums; the warps of a tile share the (row of x, weight row) pairs
         if (KS > 1) {
@@ -456,8 +473,12 @@ using MoreRows = Shape<2, 2, 384, 1, 8>;
 // at 2080, 60 with this.  (2048 takes 37 us: its rows fill whole steps of 256 k and one load brings each thread's 64 codes.)
 using FewUnaligned = Shape<2, 1, 384, 1, 8>;
 
-// KS: the split that ends soonest when every CTA takes its rounds of items one after another, a round lasting its
-// warps' steps and about one more to begin and end an item (half a step more to join sums).
+// KS: the split that ends soonest.  x is the number of items per CTA, and an item lasts its warps' steps and about one more to
+// begin and end it, a little longer where sums are joined.  Passes of 8 rows are bound by HBM, so CTAs that work alone on an SM
+// are faster, and the last drawn items end within about 0.6 of an item's time of x; passes of 16 rows are bound by their own
+// instructions and take whole rounds.  KS 1 / 2 / 4: 16 tokens, top-8 of 256, 7168 -> 2 x 2048 gated 274 / 265 / 277 us; 64
+// tokens, top-4 of 64, 4096 -> 2 x 2048 106 / 114 / 128; 1 token, top-8 of 128, 2048 -> 2 x 768 11.4 / 8.4 / 8.2; 64 tokens,
+// top-2 of 8, 14336 -> 4096 103 / 111 / 126.
 template <typename S>
 int choose_split(const ExpertArgs &a, int steps, float chunks) {
     const int n_out = a.swiglu ? a.N / 2 : a.N, per_warp = S::MT * (a.swiglu ? 8 : 16);
@@ -466,7 +487,9 @@ int choose_split(const ExpertArgs &a, int steps, float chunks) {
     for (int ks = 1; ks <= 4 && ks <= steps; ks *= 2) {
         const int rows = per_warp * (S::WARPS / ks);
         const float items = chunks * (float)((n_out + rows - 1) / rows);
-        const float time = ceilf(items / (152.0f * S::CTAS)) * ((float)((steps + ks - 1) / ks) + (ks > 1 ? 1.5f : 1.0f));
+        const float x = items / (152.0f * S::CTAS);
+        const float begin_end = ks == 1 ? 1.0f : ks == 2 ? 1.25f : 1.4f;
+        const float time = (S::NT > 1 ? ceilf(x) : fmaxf(x, 1.0f) + 0.6f) * ((float)((steps + ks - 1) / ks) + begin_end);
         if (ks == 1 || time < best_time) {
             best = ks;
             best_time = time;
@@ -479,6 +502,7 @@ template <int ALIGN, typename S>
 int launch_expert_matvec(ExpertArgs a, float chunks, cudaStream_t st) {
     constexpr auto kern = ep_expert_matvec_kernel<ALIGN, S>;
     a.KS = choose_split<S>(a, pack_steps(a.H), chunks);
+    a.draw = pack_steps(a.H) >= 2 * a.KS;
     int rc = allow_smem<kern>(S::SMEM);
     if (rc != EP_OK) return rc;
     const int pack = std::min(std::max((a.H / 8 + 31) / 32 * 32, 128), kPackThreads);
@@ -497,7 +521,7 @@ using namespace ep;
 extern "C" size_t ep_expert_matvec_workspace_bytes(const ep_layout_t *L, int hidden_size) {
     if (!layout_ok(L) || !hidden_ok(hidden_size)) return 0;
     const size_t R = layout_rows(L);
-    return R * pack_steps(hidden_size) * 512 + (R + 3) / 4 * 16 + 16;
+    return R * pack_steps(hidden_size) * 512 + 16 + R * sizeof(float);
 }
 
 extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t *codes, const uint8_t *scales,
@@ -523,12 +547,13 @@ extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t
     a.row_offsets = L->row_offsets; a.src_info = L->src_info; a.status = L->status;
     const int steps = pack_steps(H);
     a.xw = (uint4 *)workspace;
-    a.xs = (float *)(a.xw + (size_t)a.R_max * steps * 32);
+    a.drawn = (unsigned *)(a.xw + (size_t)a.R_max * steps * 32);
+    a.xs = (float *)(a.drawn + 4);
     a.out = out;
     const float per_expert = (float)L->T * L->K / L->E;
     const bool few = per_expert < 8.0f;
     // chunks that a layout of this many rows has, if the router spreads them evenly
-    const float active = L->E * (1.0f - expf(-per_expert));
+    const float active = L->E * (1.0f - powf(fmaxf(1.0f - (float)L->K / L->E, 0.0f), (float)L->T));
     const float rows = few ? 8.0f : 16.0f;
     const float chunks = active * fmaxf(1.0f, per_expert / rows + 0.5f) + (L->fused_shared ? ceilf(L->T / rows) : 0.0f);
     cudaStream_t st = as_stream(stream);
