@@ -460,16 +460,16 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     }
 }
 
-// Fewer than 8 rows per expert: two steps of weights in 128 registers, 16 warps per SM, passes of 8 rows.  More: a pass serves
-// 16 rows and 12 warps have 168 registers each, since spilled prefetches would be waited for.  8 experts, top-2, 4096 -> 2 x
-// 2048 gated, with 4 / 6 / 8 / 10 rows per expert: 22 / 28 / 33 / 36 us with passes of 8 rows, 29 / 31 / 32 / 34 us with 16; with
-// 16 rows, 14336 -> 4096: 134 and 109 us.  Of the shapes for 16 rows this one is best there: 120 us with two CTAs of 6 warps,
-// 128 us with 8 warps, 143 us with passes of 32 rows.
+// Up to 8 rows per expert: two steps of weights in 128 registers, 16 warps per SM, passes of 8 rows.  More: a pass serves 16
+// rows and 12 warps have 168 registers each, since spilled prefetches would be waited for.  8 experts, top-2, 4096 -> 2 x 2048
+// gated, with 4 / 6 / 8 / 10 rows per expert: 23 / 28 / 32 / 36 us with passes of 8 rows, 30 / 31 / 33 / 35 us with 16; 64
+// experts with 4 / 8: 105 / 156 against 119 / 161; 8 experts with 16 rows, 14336 -> 4096: 137 and 104 us.  Of the shapes for 16
+// rows this one is best there: 10 % more with two CTAs of 6 warps, 18 % with 8 warps, 31 % with passes of 32 rows.
 using FewRows = Shape<2, 1, 256, 2, 8>;
 using MoreRows = Shape<2, 2, 384, 1, 8>;
 
 // Rows on 8-byte boundaries only need more registers for their scales.  16 tokens, 64 experts, top-4, 2064 -> 2 x 2048 gated /
-// 7184 -> the same: 58 / 164 us with FewRows, which spills, 53 / 158 us with this.  On 16-byte boundaries FewRows holds: 53 us
+// 7184 -> the same: 58 / 164 us with FewRows, which spills, 54 / 156 us with this.  On 16-byte boundaries FewRows holds: 53 us
 // at 2080, 60 with this.  (2048 takes 37 us: its rows fill whole steps of 256 k and one load brings each thread's 64 codes.)
 using FewUnaligned = Shape<2, 1, 384, 1, 8>;
 
@@ -551,7 +551,7 @@ extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t
     a.xs = (float *)(a.drawn + 4);
     a.out = out;
     const float per_expert = (float)L->T * L->K / L->E;
-    const bool few = per_expert < 8.0f;
+    const bool few = per_expert <= 8.0f;
     // chunks that a layout of this many rows has, if the router spreads them evenly
     const float active = L->E * (1.0f - powf(fmaxf(1.0f - (float)L->K / L->E, 0.0f), (float)L->T));
     const float rows = few ? 8.0f : 16.0f;
