@@ -29,10 +29,12 @@ constexpr int kBwdMaxH = 8192;
 constexpr int kPartials = 304;           // rows of partial column sums a workspace has room for
 // Few rows.  Forward: one CTA per row while all of them are resident at once (bf16, us against the pipelined kernel: H = 2048,
 // T = 1000 4.2 against 4.7, T = 2000 6.5 against 6.4; H = 7168, T = 304 5.1 against 5.4, T = 600 9.5 against 7.6; H = 256,
-// T = 8000 5.7 against 6.8).  Backward: one launch that reads x and g twice (H = 2048, T = 64 2.4 against 10.1, T = 304 5.5
-// against 10.5, T = 1021 14.9 against 11.1).
+// T = 8000 5.7 against 6.8).  Backward: one launch that reads x and g twice, up to few_bwd_rows rows (us against the pipelined
+// kernel, bf16: H = 256, T = 400 5.5 against 6.0, T = 600 7.5 against 6.2; H = 2048, T = 200 4.2 against 10.8, T = 800 11.3
+// against 11.7, T = 1000 13.5 against 11.8; H = 8192, T = 800 22.0 against 26.6, T = 1500 38.4 against 33.6.  fp32: H = 2048,
+// T = 400 8.6 against 8.2; H = 8192, T = 400 20.2 against 25.4, T = 600 29.4 against 29.2).
 constexpr int kResidentThreads = 152 * 2048;
-constexpr int kFewBwdRows = 456;
+constexpr int few_bwd_rows(int H, int element) { return element == 2 && H > 256 ? 800 : 456; }
 
 constexpr int round_up(int n, int to) { return (n + to - 1) / to * to; }
 
@@ -245,6 +247,7 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
     const float inv_h = 1.0f / (float)H;
     // the parameters, as far behind a 16-byte boundary as the group's rows (L1 is too small beside the stages to keep them)
     W *s_w = reinterpret_cast<W *>(smem + (LAY == kShifted ? ty : 0) * 2 * params), *s_b = s_w + params / sizeof(W);
+#pragma unroll 8
     for (int c = LAY == kShifted ? tid : ty * G + tid; c < H; c += LAY == kShifted ? G : R * G) {
         s_w[c + shift] = w[c];
         if (b) s_b[c + shift] = b[c];
@@ -405,7 +408,6 @@ ep_norm_bwd_kernel(const T *__restrict__ g, long long ldg, const T *__restrict__
     const int bytes = sx.stage_bytes(H), params = param_bytes<W>(H + 2 * U::VEC);
     char *stages = smem + param_copies(LAY, R) * params + (size_t)ty * D * 2 * bytes;
     W *s_w = reinterpret_cast<W *>(smem + (LAY == kShifted ? ty : 0) * params);
-    for (int c = LAY == kShifted ? tid : ty * G + tid; c < H; c += LAY == kShifted ? G : R * G) s_w[c + shift] = w[c];
     int row = mine.first;
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) {
@@ -415,6 +417,8 @@ ep_norm_bwd_kernel(const T *__restrict__ g, long long ldg, const T *__restrict__
         }
         copies_commit();
     }
+#pragma unroll 8
+    for (int c = LAY == kShifted ? tid : ty * G + tid; c < H; c += LAY == kShifted ? G : R * G) s_w[c + shift] = w[c];
     f32x2 dw[U::N][U::E / 2], db[U::N][U::E / 2];
 #pragma unroll
     for (int i = 0; i < U::N; ++i)
@@ -705,7 +709,7 @@ int launch_cols(const NormArgs &a, int nparts) {
 
 template <typename T, typename W, int LAY>
 int launch_bwd(const NormArgs &a) {
-    if (a.rows <= kFewBwdRows) {
+    if (a.rows <= few_bwd_rows(a.H, sizeof(T))) {
         constexpr int VEC = LAY == kAligned ? 16 / sizeof(T) : 1;
         return launch_pdl(ep_norm_bwd_few_kernel<T, W, VEC>, dim3(a.rows + (a.H + 31) / 32), dim3(kFewThreads), 0, a.st,
                           (const T *)a.g, a.ldg, (const T *)a.x, a.ldx, (const W *)a.w, a.mean_in, a.rstd_in, a.rows, a.H,

@@ -13,7 +13,8 @@ TYPES = [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32), (tor
 # (T, H): one element, odd widths, each register layout's edges, the widest rows, ragged row counts
 SIZES = [(1, 1), (3, 2), (5, 8), (7, 33), (2, 255), (9, 256), (400, 256), (33, 264), (700, 511), (600, 512), (310, 520),
          (1, 2048), (320, 2048), (37, 2056), (5, 4096), (3, 4097), (311, 1111), (6, 7168), (610, 7168), (2, 8192),
-         (3, 8200), (330, 8200), (2, 16384), (2, 32767), (3, 32768)]
+         (3, 8200), (330, 8200), (2, 16384), (2, 32767), (3, 32768),
+         (457, 256), (801, 264), (830, 1111), (810, 7168), (820, 8192), (805, 8200), (4000, 40), (2500, 520)]
 
 
 def make(T, H, dt, wdt, seed, bias=True):
@@ -63,7 +64,7 @@ def test_sizes_bf16(T, H, rms):
 
 @pytest.mark.parametrize("dt,wdt", TYPES[1:])
 @pytest.mark.parametrize("T,H", [(1, 7), (35, 100), (340, 132), (320, 2048), (61, 2049), (5, 4100), (320, 7168), (2, 8196),
-                                 (2, 32768)])
+                                 (2, 32768), (457, 132), (820, 132), (815, 2048), (803, 2049), (810, 7168), (801, 8196)])
 def test_types(dt, wdt, T, H):
     import combine_topk_ids_histogram_gb300 as ep
     x, w, b, gy = make(T, H, dt, wdt, T + 3 * H)
@@ -75,7 +76,8 @@ def test_types(dt, wdt, T, H):
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("offset,extra", [(0, 8), (0, 3), (1, 7), (8, 24), (5, 0)])
-@pytest.mark.parametrize("T,H", [(45, 256), (450, 256), (330, 1030), (310, 4099), (2, 9000)])
+@pytest.mark.parametrize("T,H", [(45, 256), (450, 256), (330, 1030), (310, 4099), (2, 9000), (820, 256), (830, 1030),
+                                 (810, 4099), (802, 8185)])
 def test_strided_and_unaligned_rows(dt, offset, extra, T, H):
     """Rows inside a wider matrix, on and off 16-byte boundaries."""
     import combine_topk_ids_histogram_gb300 as ep
@@ -89,7 +91,8 @@ def test_strided_and_unaligned_rows(dt, offset, extra, T, H):
     check_backward(ep, gs, xs, w, mean, rstd, False)
 
 
-@pytest.mark.parametrize("T,H", [(1, 3), (7, 5), (310, 9), (500, 1111), (777, 2047), (40, 8191)])
+@pytest.mark.parametrize("T,H", [(1, 3), (7, 5), (310, 9), (500, 1111), (777, 2047), (40, 8191), (831, 9), (1003, 1111), (823, 2047),
+                                 (809, 8191)])
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_dense_matrices_off_boundaries(dt, T, H):
     """Dense matrices of odd width that all begin at the same distance from a 16-byte boundary."""
@@ -113,7 +116,8 @@ def test_dense_matrices_off_boundaries(dt, T, H):
 
 def test_no_write_outside_outputs():
     import combine_topk_ids_histogram_gb300 as ep
-    for T, H in ((3, 33), (310, 64), (9, 2048), (2, 8200), (330, 1111), (330, 1112)):
+    for T, H in ((3, 33), (310, 64), (9, 2048), (2, 8200), (330, 1111), (330, 1112), (830, 1111),
+                 (830, 1112)):
         x, w, b, gy = make(T, H, torch.bfloat16, torch.bfloat16, T)
         buf = torch.full((T * H + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
         f = torch.full((3, T + H + 64), 7.0, device="cuda")
