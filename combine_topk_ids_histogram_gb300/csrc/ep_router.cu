@@ -2,7 +2,7 @@
 // probabilities from its logits, and the gradient of the logits from the gradient of the
 // probabilities (what ep_combine_bwd returns).
 //
-// One warp per token.  Lane l holds the scores of experts l, l + 32, ... as order-preserving integer keys.  The K-th largest
+// One warp per token.  Lane l holds the scores of experts V * l to V * l + V - 1 as order-preserving integer keys.  The K-th largest
 // of the lanes' largest keys bounds the K-th largest key from below; the few keys at or above it (about K + 2 for
 // independent scores) are gathered and ranked against one another.  Against K rounds of finding and
 // striking out the largest of all keys this takes half of the instructions, whose issue bounds the call: 32768 tokens of 256
@@ -95,17 +95,19 @@ ep_router_topk_kernel(const T *__restrict__ logits, long long ld, const float *_
     const int t = blockIdx.x * kRouterWarps + warp;
     if (t >= tokens) return;
     const T *row = logits + (size_t)t * ld;
+    const float neg_inf = __int_as_float(0xff800000);
+    const int e0 = lane * V;
+    float f[V];
+    load_row<T, V>(row, e0, E, vec & 1, neg_inf, f);
+    if (bias) {
+        float b[V];
+        load_row<float, V>(bias, e0, E, vec & 2, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] += b[i];
+    }
     unsigned key[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        key[i] = 0u;
-        if (e < E) {
-            float s = to_f32(row[e]);
-            if (bias) s += bias[e];
-            key[i] = score_key(s);
-        }
-    }
+    for (int i = 0; i < V; ++i) key[i] = score_key(f[i]);
     unsigned best = 0u, top = 0u;
 #pragma unroll
     for (int i = 0; i < V; ++i) best = max(best, key[i]);
@@ -134,7 +136,7 @@ ep_router_topk_kernel(const T *__restrict__ logits, long long ld, const float *_
         unsigned long long *to = &s_cand[warp][at - __popc(mask)];
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (mask >> i & 1u) *to++ = (unsigned long long)key[i] << 32 | (unsigned)~(i * 32 + lane);
+            if (mask >> i & 1u) *to++ = (unsigned long long)key[i] << 32 | (unsigned)~(e0 + i);
         __syncwarp();
         const unsigned long long own = s_cand[warp][lane];
         int rank = 0;
@@ -155,17 +157,17 @@ ep_router_topk_kernel(const T *__restrict__ logits, long long ld, const float *_
             int e = E;
 #pragma unroll
             for (int i = V - 1; i >= 0; --i)
-                if (key[i] == largest) e = i * 32 + lane;
+                if (key[i] == largest) e = e0 + i;
             const int first = __reduce_min_sync(kFullMask, e);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (first == i * 32 + lane) key[i] = 0u;
+                if (first == e0 + i) key[i] = 0u;
             if (lane == k) my_id = first;
         }
     }
     const bool used = my_id >= 0;
     const float l = used ? to_f32(row[my_id]) : 0.0f;
-    const float p = slot_prob<T, V>(l, used, row, E, vec, lane, sc);
+    const float p = slot_prob<T, V>(l, used, row, E, vec & 1, lane, sc);
     if (lane < K) {
         ids[(size_t)t * K + lane] = my_id;
         probs[(size_t)t * K + lane] = p;
@@ -306,7 +308,7 @@ extern "C" int ep_router_topk(const void *logits, long long stride, int dtype, c
             using E = std::remove_const_t<std::remove_pointer_t<P>>;
             return launch_pdl(ep_router_topk_kernel<E, decltype(v)::value>, dim3(grid), dim3(kRouterThreads), 0,
                               as_stream(stream), (P)logits, stride, bias, T, n_experts, K, sc,
-                              (int)rows_aligned(logits, stride, dtype), one_wave(grid), topk_ids,
+                              (int)rows_aligned(logits, stride, dtype) | (aligned16(bias) ? 2 : 0), one_wave(grid), topk_ids,
                               topk_probs);
         });
     });
