@@ -234,12 +234,12 @@ class Layout:
     def ref(self):
         return ctypes.byref(self.c)
 
-    def scratch(self, H: int):
-        """expert_matvec's workspace for the current stream, as (pointer, bytes, tensor): calls on one stream run one
+    def scratch(self, H: int, stream: int):
+        """expert_matvec's workspace for the current stream, whose handle `stream` is, as (pointer, bytes, tensor): calls on one stream run one
         after another and share it, another stream gets its own, and a call that is captured into a graph gets one
         of that graph's.  (Kept because a torch allocation between two launches adds 6 us to a call's host time.)"""
         capturing = torch.cuda.is_current_stream_capturing()
-        key = (_stream().value, H)
+        key = (stream, H)
         w = None if capturing else self._scratch.get(key)
         if w is None:
             n = expert_matvec_workspace_bytes(self, H)
@@ -765,14 +765,14 @@ def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ro
     if out is None:
         out = torch.empty(max(L.R_max, 1), n_out, dtype=torch.bfloat16, device=x.device)
     po = _rows(out, L.R_max, n_out, "out")
+    handle = _stream(stream)
     if workspace is None and stream is None:
-        pw, nw, _ = L.scratch(H)
+        pw, nw, _ = L.scratch(H, handle.value)
     else:
         if workspace is None:
             workspace = _scratch(expert_matvec_workspace_bytes(L, H), x.device, stream)
         pw, nw = _ptr(workspace), workspace.numel() * workspace.element_size()
-    rc = _lib.ep_expert_matvec(px, 1 if by_token else 0, pc, ps, pr, H, N, 1 if swiglu else 0, L.ref, po, pw, nw,
-                               _stream(stream))
+    rc = _lib.ep_expert_matvec(px, 1 if by_token else 0, pc, ps, pr, H, N, 1 if swiglu else 0, L.ref, po, pw, nw, handle)
     _check(rc, "ep_expert_matvec")
     return out
 

@@ -6,8 +6,8 @@
 // Weights are in the format the NVFP4 dispatch writes.  A group's weights are read from HBM once for
 // all of its rows, so HBM bounds the call while an expert has few rows: 9/16 byte per weight.  16 tokens, top-8 of 256 and a
 // shared expert, 7168 -> 2 x 2048 gated: 265 us, 0.80 of the measured copy bandwidth (0.94 while all SMs work); 1 token, top-8 of
-// 128, 2048 -> 2 x 768: 8.2 us.  From about 16 rows per expert on the conversion and the products bound it: 64 tokens, top-2 of
-// 8, 14336 -> 4096: 104 us.
+// 128, 2048 -> 2 x 768: 6.7 us.  From about 16 rows per expert on the conversion and the products bound it: 64 tokens, top-2 of
+// 8, 14336 -> 4096: 100 us.
 //
 // The products run on mma.sync.m16n8k16 with weight rows as M and layout rows as N: at 8 rows
 // or fewer per expert the tensor cores are far from their rate, and operands that a thread builds in
@@ -37,7 +37,7 @@ struct ExpertArgs {
     const float *row_scale;
     int H, N, by_token, swiglu, T, G, R_max;
     int KS;                              // warps that share a tile and split its k: 1, 2 or 4
-    const int32_t *row_offsets, *src_info, *status;
+    const int32_t *row_offsets, *expert_ids, *src_info, *status;
     uint4 *xw;                           // [R_max][step][word][quad thread] x as fp16, 16-byte pieces
     float *xs;                           // [R_max] what a row's sums are multiplied by
     int draw;                            // CTAs draw their items; needs two steps or more of every warp in an item
@@ -187,21 +187,13 @@ __device__ __forceinline__ void mma_step(const Weights<MT, ALIGN> &d, const uint
     }
 }
 
-// x of one layout row, scaled to fp16 and reordered: one CTA per row.
-__global__ void __launch_bounds__(kPackThreads)
-ep_expert_pack_kernel(const ExpertArgs a) {
+// A row of x (null: no token) as fp16 in the order that the products take, and what its sums are multiplied by: all
+// threads of a CTA together.
+__device__ __forceinline__ float pack_row(const uint4 *x, int H, uint4 *dst) {
     __shared__ unsigned s_top[kPackThreads / 32];
-    pdl_begin();
-    const int row = blockIdx.x, tid = threadIdx.x;
-    if (row == 0 && tid == 0) *a.drawn = 0u;
-    const int R = a.row_offsets[a.G];                               // these three loads go out together
-    const int src = a.by_token ? a.src_info[2 * (size_t)row] : row;
-    if (cta_status(a.status) || row >= R) return;
-    const bool real = src >= 0 && src < (a.by_token ? a.T : a.R_max);
-    if (!real && src != -1) bounds_fail(a.status);
-    const uint4 *x = reinterpret_cast<const uint4 *>(a.x + (real ? (size_t)src * a.H : 0));
+    const int tid = threadIdx.x;
     unsigned top = 0u;                                              // largest finite magnitude, as bf16 bits
-    for (int p = tid; real && p < a.H / 8; p += blockDim.x) {
+    for (int p = tid; x && p < H / 8; p += blockDim.x) {
         const uint4 v = __ldg(x + p);
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -216,13 +208,11 @@ ep_expert_pack_kernel(const ExpertArgs a) {
     for (int w = 0; w < (int)blockDim.x / 32; ++w) top = max(top, s_top[w]);
     const int e = max((int)(top >> 7), 15);                         // biased exponent; both powers stay normal
     const float up = __uint_as_float((unsigned)(268 - e) << 23);    // 2^(141 - e)
-    if (tid == 0) a.xs[row] = __uint_as_float((unsigned)(e - 14) << 23);
-    const int pieces = (a.H + kStepK - 1) / kStepK * 32;
-    uint4 *dst = a.xw + (size_t)row * pieces;
+    const int pieces = (H + kStepK - 1) / kStepK * 32;
     for (int p = tid; p < pieces; p += blockDim.x) {
         const int k = (p >> 5) * kStepK + word_k(p & 3, (p >> 2) & 7);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (real && k < a.H) {
+        if (x && k < H) {
             float f[8];
             unpack8(__ldg(x + (k >> 3)), f);
             __half2 h[4];
@@ -232,6 +222,28 @@ ep_expert_pack_kernel(const ExpertArgs a) {
         }
         dst[p] = v;
     }
+    return __uint_as_float((unsigned)(e - 14) << 23);
+}
+
+// The row of x that a layout row takes, null for a row without a token.
+__device__ __forceinline__ const uint4 *source_row(const ExpertArgs &a, int src) {
+    const bool real = src >= 0 && src < (a.by_token ? a.T : a.R_max);
+    if (!real && src != -1) bounds_fail(a.status);
+    return real ? reinterpret_cast<const uint4 *>(a.x + (size_t)src * a.H) : nullptr;
+}
+
+// One CTA per row.
+__global__ void __launch_bounds__(kPackThreads)
+ep_expert_pack_kernel(const ExpertArgs a) {
+    pdl_begin();
+    const int row = blockIdx.x, tid = threadIdx.x;
+    if (row == 0 && tid == 0) *a.drawn = 0u;
+    const int R = a.row_offsets[a.G];                               // these three loads go out together
+    const int src = a.by_token ? a.src_info[2 * (size_t)row] : row;
+    if (cta_status(a.status) || row >= R) return;
+    const int pieces = (a.H + kStepK - 1) / kStepK * 32;
+    const float xs = pack_row(source_row(a, src), a.H, a.xw + (size_t)row * pieces);
+    if (tid == 0) a.xs[row] = xs;
 }
 
 // How a kernel is built: MT m16 tiles of weight rows per warp and NT blocks of 8 layout rows per pass, for THREADS threads
@@ -463,10 +475,88 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     }
 }
 
+// One token: every row is its expert's only one, so rows are items of their own and a layout of K (+1) rows needs no scan.  A
+// CTA packs the row for itself while its first weights are on their way, which saves the kernels above a launch and its
+// dependency.  Taken while one wave of CTAs covers the rows, with items of at most 8 steps or split ones (1 token, us against
+// the kernels above: top-8 of 128, 2048 -> 2 x 768 gated 6.7 against 8.2, 768 -> 2048 4.8 against 6.5; top-2 of 8, 14336 -> 4096
+// 27.4 against 31.6; 4096 -> 2 x 7168 gated 21.0 against 21.6, where KS = 2 just fits, and 4096 -> 2 x 14336, where it does not,
+// 36.5 against 30.8).
+constexpr int kRowThreads = 256, kRowWave = 304;
+
+template <int ALIGN>
+__global__ void __launch_bounds__(kRowThreads, 2)
+ep_expert_row_kernel(const ExpertArgs a, int one_wave) {
+    constexpr int MT = 2, kWarps = kRowThreads / 32;
+    extern __shared__ uint4 s_x[];                                  // [step][word][quad thread]
+    __shared__ float s_sum[kWarps][2 * MT][8];                      // of each warp's rows g and g + 8 of its tiles
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gl = lane >> 2, q = lane & 3;
+    const int row = blockIdx.y, KS = a.KS, kw = warp & (KS - 1), nw = warp / KS;
+    pdl_begin_if(one_wave);
+    const int R = a.row_offsets[a.G], g = a.expert_ids[row];        // these loads go out together
+    const int src = a.by_token ? a.src_info[2 * (size_t)row] : row;
+    if (cta_status(a.status) || row >= R) return;
+    if (g < 0 || g >= a.G) {
+        bounds_fail(a.status);
+        return;
+    }
+    const int n_out = a.swiglu ? a.N >> 1 : a.N, per_warp = a.swiglu ? 8 * MT : 16 * MT, rows_out = per_warp * (kWarps / KS);
+    const int steps = (a.H + kStepK - 1) / kStepK;
+    const uint8_t *const scales_end = a.scales + (size_t)a.G * a.N * (a.H >> 4);
+    unsigned w_row[2 * MT];                                         // as in the kernel above
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int n = blockIdx.x * rows_out + nw * per_warp + mt * (a.swiglu ? 8 : 16) + gl;
+        const unsigned base = (unsigned)g * (unsigned)a.N;
+        w_row[2 * mt] = base + (unsigned)min(n, n_out - 1);
+        w_row[2 * mt + 1] = base + (unsigned)(a.swiglu ? n_out + min(n, n_out - 1) : min(n + 8, n_out - 1));
+    }
+    Weights<MT, ALIGN> nxt;
+    load_weights<ALIGN, MT>(nxt, a.codes, a.scales, scales_end, w_row, kw, q, a.H);
+    const int n = blockIdx.x * rows_out + tid;                      // the output of this thread
+    const bool mine = tid < rows_out && n < n_out;
+    float rs = 0.0f, rs_up = 0.0f;
+    if (mine) {
+        rs = a.row_scale[(size_t)g * a.N + n];
+        if (a.swiglu) rs_up = a.row_scale[(size_t)g * a.N + n_out + n];
+    }
+    const float xs = pack_row(source_row(a, src), a.H, s_x);
+    __syncthreads();
+    float acc[MT][1][4] = {};
+    const int xo[1] = {0};
+    for (int st = kw; st < steps; st += KS) {
+        const Weights<MT, ALIGN> w = nxt;
+        // past the last step this loads it once more: no branch around the loads
+        load_weights<ALIGN, MT>(nxt, a.codes, a.scales, scales_end, w_row, st + KS < steps ? st + KS : st, q, a.H);
+        mma_step<1>(w, s_x + st * 32 + q, xo, acc);                 // all 8 columns are the row; the first is kept
+    }
+    if (q == 0) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            s_sum[warp][2 * mt][gl] = acc[mt][0][0];
+            s_sum[warp][2 * mt + 1][gl] = acc[mt][0][2];
+        }
+    }
+    __syncthreads();
+    if (!mine) return;
+    const int tw = tid / per_warp * KS, j = tid % per_warp;
+    float v = 0.0f, up = 0.0f;
+    for (int w = tw; w < tw + KS; ++w) {
+        if (a.swiglu) {
+            v += s_sum[w][j >> 3 << 1][j & 7];
+            up += s_sum[w][(j >> 3 << 1) + 1][j & 7];
+        } else {
+            v += s_sum[w][j >> 3][j & 7];
+        }
+    }
+    v *= xs * rs;
+    if (a.swiglu) v = v / (1.0f + expf(-v)) * (up * xs * rs_up);
+    a.out[(size_t)row * n_out + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
 // Up to 8 rows per expert: two steps of weights in 128 registers, 16 warps per SM, passes of 8 rows.  More: a pass serves 16
 // rows and 12 warps have 168 registers each, since spilled prefetches would be waited for.  8 experts, top-2, 4096 -> 2 x 2048
 // gated, with 4 / 6 / 8 / 10 rows per expert: 23 / 28 / 32 / 36 us with passes of 8 rows, 30 / 31 / 33 / 35 us with 16; 64
-// experts with 4 / 8: 105 / 156 against 119 / 161; 8 experts with 16 rows, 14336 -> 4096: 137 and 104 us.  Of the shapes for 16
+// experts with 4 / 8: 105 / 156 against 119 / 161; 8 experts with 16 rows, 14336 -> 4096: 137 and 100 us.  Of the shapes for 16
 // rows this one is best there: 10 % more with two CTAs of 6 warps, 18 % with 8 warps, 31 % with passes of 32 rows.
 using FewRows = Shape<2, 1, 256, 2, 8>;
 using MoreRows = Shape<2, 2, 384, 1, 8>;
@@ -480,7 +570,7 @@ using FewUnaligned = Shape<2, 1, 384, 1, 8>;
 // begin and end it, a little longer where sums are joined.  Passes of 8 rows are bound by HBM, so CTAs that work alone on an SM
 // are faster, and the last drawn items end within about 0.6 of an item's time of x; passes of 16 rows are bound by their own
 // instructions and take whole rounds.  KS 1 / 2 / 4: 16 tokens, top-8 of 256, 7168 -> 2 x 2048 gated 274 / 265 / 277 us; 64
-// tokens, top-4 of 64, 4096 -> 2 x 2048 106 / 114 / 128; 1 token, top-8 of 128, 2048 -> 2 x 768 11.4 / 8.4 / 8.2; 64 tokens,
+// tokens, top-4 of 64, 4096 -> 2 x 2048 106 / 114 / 128; 4 tokens, top-8 of 128, 2048 -> 2 x 768 20 / 17 / 18; 64 tokens,
 // top-2 of 8, 14336 -> 4096 103 / 111 / 126.
 template <typename S>
 int choose_split(const ExpertArgs &a, int steps, float chunks) {
@@ -516,6 +606,23 @@ int launch_expert_matvec(ExpertArgs a, float chunks, cudaStream_t st) {
     return launch_pdl(kern, dim3(grid), dim3(S::THREADS), S::SMEM, st, a);
 }
 
+// CTAs of the row kernel when KS of a CTA's warps share a tile.
+int row_blocks(const ExpertArgs &a, int KS) {
+    const int n_out = a.swiglu ? a.N / 2 : a.N, rows_out = FewRows::MT * (a.swiglu ? 8 : 16) * (kRowThreads / 32 / KS);
+    return (n_out + rows_out - 1) / rows_out;
+}
+
+template <int ALIGN>
+int launch_expert_row(ExpertArgs a, cudaStream_t st) {
+    constexpr auto kern = ep_expert_row_kernel<ALIGN>;
+    const int rc = allow_smem<kern>((size_t)pack_steps(kMaxH) * 512);
+    if (rc != EP_OK) return rc;
+    a.KS = 1;                                                       // the most that one wave of CTAs has room for
+    while (a.KS < 4 && 2 * a.KS <= pack_steps(a.H) && row_blocks(a, 2 * a.KS) * a.R_max <= kRowWave) a.KS *= 2;
+    const dim3 grid(row_blocks(a, a.KS), a.R_max);
+    return launch_pdl(kern, grid, dim3(kRowThreads), (size_t)pack_steps(a.H) * 512, st, a, one_wave(grid.x * grid.y));
+}
+
 }  // namespace
 }  // namespace ep
 
@@ -547,7 +654,7 @@ extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t
     a.x = x; a.codes = codes; a.scales = scales; a.row_scale = row_scale;
     a.H = H; a.N = N; a.by_token = x_by_token; a.swiglu = swiglu;
     a.T = L->T; a.G = L->E + L->fused_shared; a.R_max = layout_rows(L);
-    a.row_offsets = L->row_offsets; a.src_info = L->src_info; a.status = L->status;
+    a.row_offsets = L->row_offsets; a.expert_ids = L->expert_ids; a.src_info = L->src_info; a.status = L->status;
     const int steps = pack_steps(H);
     a.xw = (uint4 *)workspace;
     a.drawn = (unsigned *)(a.xw + (size_t)a.R_max * steps * 32);
@@ -561,6 +668,10 @@ extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t
     const float chunks = active * fmaxf(1.0f, per_expert / rows + 0.5f) + (L->fused_shared ? ceilf(L->T / rows) : 0.0f);
     cudaStream_t st = as_stream(stream);
     const bool by64 = H % 64 == 0 && (reinterpret_cast<uintptr_t>(codes) & 31u) == 0;
+    if (L->T == 1 && a.R_max <= L->K + 1 && row_blocks(a, steps > 8 ? 2 : 1) * a.R_max <= kRowWave) {
+        if (by64) return launch_expert_row<32>(a, st);
+        return H % 32 == 0 ? launch_expert_row<16>(a, st) : launch_expert_row<8>(a, st);
+    }
     if (few) {
         if (by64) return launch_expert_matvec<32, FewRows>(a, chunks, st);
         return H % 32 == 0 ? launch_expert_matvec<16, FewRows>(a, chunks, st) : launch_expert_matvec<8, FewUnaligned>(a, chunks, st);

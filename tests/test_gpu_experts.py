@@ -67,7 +67,8 @@ def check(ep, L, w, by_token, swiglu, seed, zero=()):
 CASES = [(1, 1, 1, 0, 16, 1), (1, 8, 16, 0, 2048, 96), (1, 2, 8, 1, 64, 34), (2, 2, 4, 0, 48, 5), (3, 2, 8, 0, 32, 17),
          (7, 1, 1, 0, 80, 33), (8, 1, 1, 1, 128, 64), (9, 1, 1, 0, 144, 40), (16, 2, 4, 0, 256, 130), (17, 1, 1, 0, 272, 31),
          (31, 4, 8, 1, 320, 66), (33, 2, 2, 0, 512, 20), (65, 3, 4, 0, 1040, 24), (130, 8, 8, 0, 96, 48), (40, 8, 64, 1, 384, 36),
-         (4, 2, 1000, 0, 64, 16), (5, 3, 6, 0, 7168, 18), (1500, 2, 3, 1, 128, 40), (12, 2, 8, 0, 14336, 22), (2, 2, 4, 0, 32768, 8)]
+         (4, 2, 1000, 0, 64, 16), (5, 3, 6, 0, 7168, 18), (1500, 2, 3, 1, 128, 40), (12, 2, 8, 0, 14336, 22), (2, 2, 4, 0, 32768, 8),
+         (1, 4, 6, 1, 1040, 70), (1, 8, 8, 0, 2080, 300), (1, 3, 5, 1, 32768, 20), (1, 2, 3, 0, 7168, 600), (1, 1, 2, 0, 272, 1001)]
 
 
 @pytest.mark.parametrize("T,K,E,S,H,N", CASES)
