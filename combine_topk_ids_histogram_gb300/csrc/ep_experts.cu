@@ -668,7 +668,7 @@ extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t
     const float chunks = active * fmaxf(1.0f, per_expert / rows + 0.5f) + (L->fused_shared ? ceilf(L->T / rows) : 0.0f);
     cudaStream_t st = as_stream(stream);
     const bool by64 = H % 64 == 0 && (reinterpret_cast<uintptr_t>(codes) & 31u) == 0;
-    if (L->T == 1 && a.R_max <= L->K + 1 && row_blocks(a, steps > 8 ? 2 : 1) * a.R_max <= kRowWave) {
+    if (L->T == 1 && a.R_max <= L->K + 1 && L->expert_ids && row_blocks(a, steps > 8 ? 2 : 1) * a.R_max <= kRowWave) {
         if (by64) return launch_expert_row<32>(a, st);
         return H % 32 == 0 ? launch_expert_row<16>(a, st) : launch_expert_row<8>(a, st);
     }

@@ -233,6 +233,26 @@ def test_rows_outside_the_layout_are_not_used():
     assert (buf[L.R_max:] == 7).all() and (buf[[3, 5]] == 0).all()
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("H,N", [(2048, 96), (784, 40), (96, 300)])
+def test_one_token_without_expert_ids_and_padded(H, N, swiglu):
+    """A layout's expert_ids may be absent: the general kernels give the same products within the bound; so do a padded
+    layout and one whose slots are partly unused."""
+    import combine_topk_ids_histogram_gb300 as ep
+    ids = routing(1, 4, 8, 3)
+    w = weights(8, N, H, 5)
+    L = ep.dispatch_layout(ids, 8)
+    check(ep, L, w, True, swiglu, 2)
+    kept, L.c.expert_ids = L.c.expert_ids, None
+    check(ep, L, w, True, swiglu, 2)
+    L.c.expert_ids = kept
+    ids[0, 1] = -1
+    check(ep, ep.dispatch_layout(ids, 8), w, True, swiglu, 2)
+    check(ep, ep.dispatch_layout(torch.full_like(ids, -1), 8), w, True, swiglu, 2)
+    for pad in (2, 16):
+        check(ep, ep.dispatch_layout_routed(8, topk_ids=ids[:, :1].contiguous(), pad_multiple=pad)[0], w, True, swiglu, 2)
+
+
 def test_no_tokens_and_refusals():
     import combine_topk_ids_histogram_gb300 as ep
     L = ep.dispatch_layout(torch.empty(0, 2, dtype=torch.int32, device="cuda"), 4)
