@@ -342,7 +342,10 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
         }
     };
     Cursor cur = {(int)blockIdx.x, 0, 0, 0};
-    if (cur.item >= items) return;
+    if (cur.item >= items) {                                        // this kernel must not end before the first one has
+        pdl_wait();
+        return;
+    }
     locate(cur);
     Cursor pf = cur;
     unsigned pf_row[2 * MT];

@@ -212,6 +212,27 @@ def test_status_repeat_and_streams():
     assert ep.read_status(over) == ep.STATUS_OVERFLOW and (out == 7).all()
 
 
+def test_calls_on_layouts_without_rows_stay_in_order():
+    """A call on a layout without rows, between calls that share its workspace and draw their items: nothing of it may
+    run beside the next one, whose counter of drawn items lies in that workspace."""
+    import combine_topk_ids_histogram_gb300 as ep
+    T, E, H, N = 64, 64, 512, 2600                                     # several items per CTA
+    ids = routing(T, 4, E, 7)
+    full, none = ep.dispatch_layout(ids, E), ep.dispatch_layout(torch.full_like(ids, -1), E)
+    w = weights(E, N, H, 4)
+    x = torch.randn(T, H, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    ws = torch.empty(ep.expert_matvec_workspace_bytes(full, H), dtype=torch.uint8, device="cuda")
+    want = ep.expert_matvec(x, *w, full, workspace=ws).clone()
+    outs = [torch.full_like(want, float("nan")) for _ in range(20)]
+    empty = torch.full((none.R_max, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    for out in outs:
+        ep.expert_matvec(x, *w, none, out=empty, workspace=ws)
+        ep.expert_matvec(x, *w, full, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    R = int(full.row_offsets[-1])
+    assert all(torch.equal(o[:R], want[:R]) for o in outs) and (empty == 7).all()
+
+
 def test_rows_outside_the_layout_are_not_used():
     """A src_info entry that names no token is a zero row, and row_offsets past R_max are cut there; the bounds-checked
     build reports such an entry and writes nothing."""
