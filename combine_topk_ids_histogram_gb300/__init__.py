@@ -223,7 +223,6 @@ class Layout:
             raise EPError(EP_ERR_INVALID_ARG, "layout sizes")
         self.workspace = torch.zeros(nb, dtype=torch.uint8, device=dev)
         self.capacity = T
-        self._scratch = {}                       # expert_matvec's workspaces by (stream, H): see scratch
         self.c = _Layout(
             row_offsets=self.row_offsets.data_ptr(), expert_ids=self.expert_ids.data_ptr(),
             src_info=self.src_info.data_ptr(), row_of=self.row_of.data_ptr(),
@@ -233,21 +232,6 @@ class Layout:
     @property
     def ref(self):
         return ctypes.byref(self.c)
-
-    def scratch(self, H: int, stream: int):
-        """expert_matvec's workspace for the current stream, whose handle `stream` is, as (pointer, bytes, tensor): calls on one stream run one
-        after another and share it, another stream gets its own, and a call that is captured into a graph gets one
-        of that graph's.  (Kept because a torch allocation between two launches adds 6 us to a call's host time.)"""
-        capturing = torch.cuda.is_current_stream_capturing()
-        key = (stream, H)
-        w = None if capturing else self._scratch.get(key)
-        if w is None:
-            n = expert_matvec_workspace_bytes(self, H)
-            t = torch.empty(n, dtype=torch.uint8, device=self.status.device)
-            w = (t.data_ptr(), n, t)
-            if not capturing:
-                self._scratch[key] = w
-        return w
 
     def shape_key(self):
         return (self.T, self.K, self.E, self.P, self.S, self.pad, self.row_capacity)
@@ -751,8 +735,8 @@ def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ro
     """ep_expert_matvec -> bf16 [R_max, N] (or [R_max, N/2] with swiglu): each row of the layout times
     its group's 4-bit weights, codes uint8 [G, N, H/2], scales uint8 [G, N, H/16] (E4M3) and row_scale
     fp32 [G, N].  x bf16 is [T, H] when by_token (rows take their token's vector), else [R_max, H].
-    ``workspace``: a uint8 buffer of ``expert_matvec_workspace_bytes`` to use; without one a call takes the
-    layout's for the current stream (``Layout.scratch``), or its own when a ``stream`` is given."""
+    ``workspace``: a uint8 buffer of ``expert_matvec_workspace_bytes`` to reuse, in calls that do not overlap on the
+    GPU nor are made from several host threads at once; without one a call allocates its own."""
     if codes.dim() != 3:
         raise ValueError(f"codes: expected [{L.G}, N, H/2], got {tuple(codes.shape)}")
     G, N, half = codes.shape
@@ -765,14 +749,10 @@ def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ro
     if out is None:
         out = torch.empty(max(L.R_max, 1), n_out, dtype=torch.bfloat16, device=x.device)
     po = _rows(out, L.R_max, n_out, "out")
-    handle = _stream(stream)
-    if workspace is None and stream is None:
-        pw, nw, _ = L.scratch(H, handle.value)
-    else:
-        if workspace is None:
-            workspace = _scratch(expert_matvec_workspace_bytes(L, H), x.device, stream)
-        pw, nw = _ptr(workspace), workspace.numel() * workspace.element_size()
-    rc = _lib.ep_expert_matvec(px, 1 if by_token else 0, pc, ps, pr, H, N, 1 if swiglu else 0, L.ref, po, pw, nw, handle)
+    if workspace is None:
+        workspace = _scratch(expert_matvec_workspace_bytes(L, H), x.device, stream)
+    rc = _lib.ep_expert_matvec(px, 1 if by_token else 0, pc, ps, pr, H, N, 1 if swiglu else 0, L.ref, po, _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc, "ep_expert_matvec")
     return out
 

@@ -436,7 +436,8 @@ size_t ep_layer_norm_bwd_workspace_bytes(int T, int hidden_size);
  *   grad_y [T, H] dtype, row stride grad_stride (e); x, weight, mean (NULL allowed when rms is 1) and
  *   rstd as in the forward call.
  *   workspace: ep_layer_norm_bwd_workspace_bytes(T, H) bytes, 16-byte aligned; needs no
- *   initialisation, and calls that share one must not overlap on the GPU.
+ *   initialisation.  Calls that share one must not overlap on the GPU, nor be made by several host
+ *   threads at once, on one stream either: a call is up to two launches, and another's may come between.
  * Sums are fp32 in an order fixed by the sizes and the GPU's SM count: results repeat bit for
  * bit.  T = 0 writes zero parameter gradients.
  */
@@ -499,8 +500,9 @@ size_t ep_expert_matvec_workspace_bytes(const ep_layout_t *L, int hidden_size);
  *   -> out     [R_max * N] bf16: out[r, n] = weight row n . x, or with swiglu [R_max * N/2] bf16:
  *              silu(gate) * up, silu(v) = v / (1 + exp(-v)); fp32 sums, rounded once.
  *   workspace  ep_expert_matvec_workspace_bytes(L, H) bytes (about 2H bytes per row of R_max), 16-byte
- *              aligned; needs no initialisation, and calls that share
- *              one must not overlap on the GPU.
+ *              aligned; needs no initialisation.  Calls that share one must not overlap on the GPU, nor be
+ *              made by several host threads at once, on one stream either: a call is up to two
+ *              launches, and another's may come between.
  * The rows [0, row_offsets[G]) are written; a padding row is the product of a zero row.  Nothing
  * is written while the layout's status word is non-zero.
  */
