@@ -7,7 +7,7 @@
 //             dw = sum over rows of g * xh, db = sum over rows of g
 //
 // Statistics and sums are fp32.  The variance is summed over (x - mean) in a second pass over
-// registers, so rows with a large mean lose nothing.  HBM is the floor of both passes: each row is
+// registers, which also corrects the mean, so rows with a large mean lose nothing.  HBM is the floor of both passes: each row is
 // read once and written once.  4096 x 7168 bf16 RMS forward: 22 us, 0.80 of the measured copy bandwidth with the launch;
 // 32768 x 7168 bf16 backward: 310 us, 0.68, where issue and the row sums at 14 warps per SM bound it; single rows: 1.9 us.
 //
@@ -221,6 +221,15 @@ template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("c
 // ---------------------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------------------
+// The mean that the first pass over a row gives is off by the rounding of its sum.  The second pass also sums d = x - mean,
+// whose own mean delta is what the first one missed: the mean, d and the variance are corrected by it.  A constant row has
+// d = delta exactly, and so y = bias.
+// The variance about the corrected mean from the mean square about the first one; NaN stays NaN.
+__device__ __forceinline__ float centred_var(float mean_square, float delta) {
+    const float v = fmaf(-delta, delta, mean_square);
+    return v < 0.0f ? 0.0f : v;
+}
+
 template <typename T, typename W, int LAY>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, const W *__restrict__ b,
@@ -229,7 +238,7 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
     constexpr int D = kFwdStages<T>;
     using U = Units<T, kFwdEpt, LAY>;
     extern __shared__ __align__(16) char smem[];                    // [copy][weight, bias], [group][stage]
-    __shared__ __align__(16) float s_red[2][32][4];                 // a group's values lie in whole rows of 4
+    __shared__ __align__(16) float s_red[2][32][4];                 // a group's values, or pairs of values, lie in whole rows
     const int G = blockDim.x, R = blockDim.y, tid = threadIdx.x, ty = threadIdx.y;
     if (ty * G + tid < 128) s_red[0][0][ty * G + tid] = s_red[1][0][ty * G + tid] = 0.0f;
     pdl_begin();
@@ -245,7 +254,7 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
         if (row + i * step < rows) src.copy(row + i * step, stages + i * bytes, tid, G);
         copies_commit();
     }
-    const float inv_h = 1.0f / (float)H;
+    const float h = (float)H;
     // the parameters, as far behind a 16-byte boundary as the group's rows (L1 is too small beside the stages to keep them)
     W *s_w = reinterpret_cast<W *>(smem + (LAY == kShifted ? ty : 0) * 2 * params), *s_b = s_w + params / sizeof(W);
 #pragma unroll 8
@@ -255,6 +264,7 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
     }
     const int red_rows = ((G >> 5) + 3) / 4;
     float *red0 = &s_red[0][ty * red_rows][0], *red1 = &s_red[1][ty * red_rows][0];
+    f32x2 *red2 = reinterpret_cast<f32x2 *>(&s_red[1][ty * (((G >> 5) + 1) / 2)][0]);   // red1's place, for a layer norm
     __syncthreads();
     for (int at = 0, buf = 0; row < rows; row += step, at = at + 1 == D ? 0 : at + 1, buf ^= 1) {
         copies_wait<D - 2>();
@@ -266,13 +276,13 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
         f32x2 d[U::N][U::E / 2];
 #pragma unroll
         for (int i = 0; i < U::N; ++i) un.load(s_row, i, d[i]);
-        float mean = 0.0f;
+        float mean = 0.0f, var;
         if (!rms) {
             f32x2 s = f2(0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < U::N; ++i) s = un.add(s, i, d[i]);
             const float2 p = f2_get(s);
-            mean = group_sum(p.x + p.y, red0, G, ty) * inv_h;
+            mean = group_sum(p.x + p.y, red0, G, ty) / h;
             const f32x2 neg = f2(-mean, -mean);
 #pragma unroll
             for (int i = 0; i < U::N; ++i)
@@ -288,7 +298,23 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
             q = un.add(q, i, sq);
         }
         const float2 p = f2_get(q);
-        const float rstd = rsqrtf(fmaf(group_sum(p.x + p.y, rms && buf ? red0 : red1, G, ty), inv_h, eps));
+        if (rms) {
+            var = group_sum(p.x + p.y, buf ? red0 : red1, G, ty) / h;
+        } else {
+            f32x2 s = f2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < U::N; ++i) s = un.add(s, i, d[i]);
+            const float2 r = f2_get(s), t = group_sum2(f2(r.x + r.y, p.x + p.y), red2, G, ty);
+            const float delta = t.x / h;
+            var = centred_var(t.y / h, delta);
+            mean += delta;
+            const f32x2 neg = f2(-delta, -delta);
+#pragma unroll
+            for (int i = 0; i < U::N; ++i)
+#pragma unroll
+                for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_add(d[i][j], neg);
+        }
+        const float rstd = rsqrtf(var + eps);
         if (tid == 0) {
             if (!rms) mean_out[row] = mean;
             rstd_out[row] = rstd;
@@ -317,8 +343,12 @@ __global__ void __launch_bounds__(1024, 1)
 ep_norm_row_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, const W *__restrict__ b,
                    int H, float eps, int rms, int one_wave, T *__restrict__ y, float *__restrict__ mean_out,
                    float *__restrict__ rstd_out) {
-    __shared__ __align__(16) float s_red[2][32];
-    if (threadIdx.x < 32) s_red[0][threadIdx.x] = s_red[1][threadIdx.x] = 0.0f;
+    __shared__ __align__(16) float s_red[32];
+    __shared__ __align__(16) f32x2 s_red2[32];
+    if (threadIdx.x < 32) {
+        s_red[threadIdx.x] = 0.0f;
+        s_red2[threadIdx.x] = f2(0.0f, 0.0f);
+    }
     __syncthreads();
     pdl_begin_if(one_wave);
     const int G = blockDim.x, tid = threadIdx.x, row = blockIdx.x, nv = H / VEC;
@@ -346,18 +376,30 @@ ep_norm_row_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) s += d[i][j];
-        mean = group_sum(s, s_red[0], G, 0) / (float)H;
+        mean = group_sum(s, s_red, G, 0) / (float)H;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) d[i][j] = tid + i * G < nv ? d[i][j] - mean : 0.0f;
     }
-    float q = 0.0f;
+    float q = 0.0f, sd = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) q = fmaf(d[i][j], d[i][j], q);
-    const float rstd = 1.0f / sqrtf(group_sum(q, s_red[1], G, 0) / (float)H + eps);
+        for (int j = 0; j < VEC; ++j) {
+            q = fmaf(d[i][j], d[i][j], q);
+            sd += d[i][j];
+        }
+    float var, delta = 0.0f;
+    if (rms) {
+        var = group_sum(q, s_red, G, 0) / (float)H;
+    } else {
+        const float2 t = group_sum2(f2(sd, q), s_red2, G, 0);
+        delta = t.x / (float)H;
+        var = centred_var(t.y / (float)H, delta);
+        mean += delta;
+    }
+    const float rstd = 1.0f / sqrtf(var + eps);
     if (tid == 0) {
         if (!rms) mean_out[row] = mean;
         rstd_out[row] = rstd;
@@ -371,7 +413,7 @@ ep_norm_row_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__
             if (NV > 1) w0 = ld_pack<W, VEC>(w + (size_t)v * VEC);
             w0.unpack(o);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) o[j] *= d[i][j] * rstd;
+            for (int j = 0; j < VEC; ++j) o[j] *= (d[i][j] - delta) * rstd;
             if (b) {
                 float c[VEC];
                 if (NV > 1) b0 = ld_pack<W, VEC>(b + (size_t)v * VEC);

@@ -1,5 +1,8 @@
 """Layer norm and RMS norm, forward and backward, against the 64-bit definition: every type, widths that no
 vector divides, strided rows, rows that are constant or hold infinities, one token and none."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -251,3 +254,125 @@ def test_refusals():
         ep.layer_norm_bwd(gy, x, w, mean, rstd, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ep.EPError):
         ep.layer_norm(torch.zeros(1, 40000, device="cuda"), torch.zeros(40000, device="cuda"))
+
+
+# ------------------------------------------------------------------------------- rows past the one-row kernel's border
+def resident_rows(H, dt, aligned=True):
+    """Rows up to which the forward pass takes the kernel with a CTA per row: read from the source, so that moving the border
+    there cannot move these tests' cases to the other side of it unnoticed."""
+    import combine_topk_ids_histogram_gb300 as ep
+    src = open(os.path.join(os.path.dirname(ep.__file__), "csrc", "ep_norm.cu")).read()
+    threads = eval(re.search(r"constexpr int kResidentThreads = ([0-9 *]+);", src).group(1))
+    vec = (4 if dt == torch.float32 else 8) if aligned else 1
+    per_row = H // vec if H // vec <= 1024 else (H // vec + 7) // 8
+    return threads // ((per_row + 31) // 32 * 32)
+
+
+MANY = [(9801, 256), (9803, 40), (4901, 1024), (1301, 2048), (703, 4096)]
+
+
+@pytest.mark.parametrize("dt,wdt", TYPES)
+@pytest.mark.parametrize("T,H", MANY)
+def test_many_aligned_rows(dt, wdt, T, H):
+    """The pipelined forward kernel at every shape of its groups: one warp (no named barrier, up to 21 groups) to four."""
+    import combine_topk_ids_histogram_gb300 as ep
+    assert T > resident_rows(H, dt)
+    x, w, b, gy = make(T, H, dt, wdt, T + H)
+    for bias in (b, None):
+        _, mean, rstd = check_forward(ep, x, w, bias, 1e-5, False)
+        _, _, rrstd = check_forward(ep, x, w, bias, 1e-5, True)
+    check_backward(ep, gy, x, w, mean, rstd, False)
+    check_backward(ep, gy, x, w, None, rrstd, True)
+
+
+@pytest.mark.parametrize("T,H", [(9801, 300), (9801, 301), (4901, 1024), (1201, 7168)])
+def test_many_rows_non_finite_and_repeated(T, H):
+    """Non-finite rows stay in their rows; an infinity under RMS leaves 0 or the bias in its row's finite places; a second call
+    gives the same bits."""
+    import combine_topk_ids_histogram_gb300 as ep
+    dt = torch.float32 if H < 1000 else torch.bfloat16
+    assert T > resident_rows(H, dt, aligned=H % 4 == 0)
+    x, w, b, gy = make(T, H, dt, dt, 5)
+    bad = x.clone()
+    bad[2, 7] = float("inf")
+    bad[5, H - 1] = float("nan")
+    rows = [r for r in range(T) if r not in (2, 5)]
+    for rms in (False, True):
+        clean, again = ep.layer_norm(x, w, b, rms=rms), ep.layer_norm(x, w, b, rms=rms)
+        assert torch.equal(clean[0], again[0]) and torch.equal(clean[2], again[2])
+        y, mean, rstd = ep.layer_norm(bad, w, b, rms=rms)
+        assert torch.equal(y[rows], clean[0][rows]) and torch.equal(rstd[rows], clean[2][rows])
+        assert torch.isnan(y[5]).all()
+        if rms:
+            others = [c for c in range(H) if c != 7]
+            assert torch.isnan(y[2, 7]) and torch.equal(y[2, others], b[others]) and rstd[2] == 0
+        else:
+            assert torch.isnan(y[2]).all()
+        dx, _, db = ep.layer_norm_bwd(gy, bad, w, mean, rstd, rms=rms, bias=True)
+        want = ep.layer_norm_bwd(gy, x, w, clean[1], clean[2], rms=rms, bias=True)
+        assert torch.equal(dx[rows], want[0][rows]) and torch.equal(db, want[2])
+
+
+@pytest.mark.parametrize("rms_case", ["few", "wide"])
+def test_an_infinity_under_rms(rms_case):
+    import combine_topk_ids_histogram_gb300 as ep
+    T, H = (4, 300) if rms_case == "few" else (3, 9000)
+    x, w, b, _ = make(T, H, torch.bfloat16, torch.bfloat16, 3)
+    x[1, 5] = float("-inf")
+    others = [c for c in range(H) if c != 5]
+    for bias in (b, None):
+        y, _, rstd = ep.layer_norm(x, w, bias, rms=True)
+        assert rstd[1] == 0 and torch.isnan(y[1, 5])
+        assert torch.equal(y[1, others].float(), (torch.zeros_like(b) if bias is None else b)[others].float())
+
+
+# 1/H is not exact at these widths; (T: in few rows, and in many)
+CONSTANT = [(7168, 4, 1500), (1111, 4, 2000), (5120, 4, 2000), (40, 4, 10000), (300, 4, 10000), (9000, 4, 2000)]
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H,few,many", CONSTANT)
+@pytest.mark.parametrize("shifted", [False, True])
+def test_constant_rows_of_any_width(H, few, many, dt, shifted):
+    """y = bias and mean = the constant, exactly: x - mean is then the same few units for all elements, their sum (below 2^24
+    units) and its H-th part are exact, and the correction by it leaves 0.  The variance is off by at most 2^-21 of the
+    square of that difference."""
+    import combine_topk_ids_histogram_gb300 as ep
+    consts = torch.tensor([0.0, 1.0, -3.0, 0.3, 100.0, 1000.0, -1001.0, 2000.0, 4099.0, 1.7e4, -4e4, 1e-3]).to(dt).cuda()
+    w, b = torch.linspace(-1.5, 1.5, H).to(dt).cuda(), torch.linspace(-2, 3, H).to(dt).cuda()
+    assert few <= resident_rows(H, dt, not shifted) < many
+    for T in (few, many):
+        c = consts[torch.arange(T, device="cuda") % len(consts)]
+        wide = torch.zeros(T, H + 13, dtype=dt, device="cuda")
+        x = wide[:, 3:3 + H] if shifted else torch.empty(T, H, dtype=dt, device="cuda")
+        x.copy_(c[:, None].expand(T, H))
+        y, mean, rstd = ep.layer_norm(x, w, b, eps=1e-5)
+        assert torch.equal(y, b.expand(T, H)), (y.float() - b.float()).abs().max()
+        assert torch.equal(mean, c.float())
+        want = 1e-5 ** -0.5
+        tol = want * (0.5 * 2.0 ** -21 * (ref.ROW * ref.d64(c).abs()) ** 2 / 1e-5 + 4 * ref.EPS24)
+        ref.assert_within(rstd, torch.full((T,), want, dtype=torch.float64), tol, "rstd")
+
+
+@pytest.mark.parametrize("T,H", [(3, 7168), (1500, 7168), (3, 1111), (2000, 1111), (4, 9000), (9900, 300)])
+@pytest.mark.parametrize("m", [30.0, 1000.0, -1e5])
+def test_large_means_lose_nothing(T, H, m):
+    """With d0 = the first pass's error of the mean, at most ROW * mean|x|: the corrected d is off by the rounding of
+    x - mean (of the order of |c| + d0) and by the error of its mean, ROW * mean|d|; y, mean and rstd follow."""
+    import combine_topk_ids_histogram_gb300 as ep
+    g = torch.Generator().manual_seed(T + H)
+    assert T < 10 or T > resident_rows(H, torch.float32, aligned=H % 4 == 0)
+    x = (m + torch.randn(T, H, generator=g)).cuda()
+    w, b = (1 + 0.2 * torch.randn(H, generator=g)).cuda(), torch.randn(H, generator=g).cuda()
+    y, mean, rstd = ep.layer_norm(x, w, b)
+    ry, rmean, rrstd = ref.norm(x, w, b, 1e-5, False)
+    c, wd, bd, r = ref.d64(x) - rmean[:, None], ref.d64(w).abs(), ref.d64(b).abs(), rrstd[:, None]
+    d0 = (ref.ROW * ref.d64(x).abs().mean(1))[:, None]
+    of_mean = (ref.ROW + 3 * ref.EPS24) * (c.abs().mean(1, keepdim=True) + d0)
+    dc = of_mean + 3 * ref.EPS24 * (c.abs() + d0)
+    drel = ref.ROW * (1 + (d0 * r) ** 2) + 8 * ref.EPS24
+    xh = c.abs() * r
+    ty = 1.01 * (r * dc * wd + xh * wd * (drel + 4 * ref.EPS24)) + 4 * ref.EPS24 * (xh * wd + bd) + ref.EPS24 * ry.abs()
+    ref.assert_within(y, ry, ty, "y")
+    ref.assert_within(rstd, rrstd, rrstd * drel[:, 0], "rstd")
+    ref.assert_within(mean, rmean, of_mean[:, 0] + 1.01 * ref.EPS24 * rmean.abs(), "mean")
