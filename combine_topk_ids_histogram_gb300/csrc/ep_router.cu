@@ -75,7 +75,7 @@ __device__ __forceinline__ float slot_prob(float l, bool used, const T *row, int
 #pragma unroll
     for (int i = 0; i < V; ++i) m = fmaxf(m, v[i]);
     m = warp_max(m);
-    if (m == neg_inf) return 0.0f;
+    if (m == neg_inf) m = 0.0f;                                     // all masked, or NaN (which the maximum passes over)
     float total = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) total += expf(v[i] - m);

@@ -120,6 +120,19 @@ def test_nan_shows_and_stays_in_its_row():
             assert torch.equal(p[t], clean[m][1][t])
 
 
+def test_nan_shows_beside_masked_experts():
+    """A NaN logit is selected first and its probability is NaN, where nothing but masked experts is beside it too."""
+    import combine_topk_ids_histogram_gb300 as ep
+    for E in (5, 32, 40, 256):
+        l = torch.full((3, E), float("-inf"), device="cuda")
+        l[0, E - 2] = float("nan")
+        l[1, 1], l[1, 3] = float("nan"), 0.5
+        for score, renorm in MODES:
+            ids, p = ep.router_topk(l, 4, score=score, renormalize=renorm)
+            assert ids.tolist() == [[E - 2, -1, -1, -1], [1, 3, -1, -1], [-1] * 4]
+            assert torch.isnan(p[0, 0]) and torch.isnan(p[1, 0]) and (p[0, 1:] == 0).all() and (p[2] == 0).all()
+
+
 def test_strided_logits():
     import combine_topk_ids_histogram_gb300 as ep
     for off, E, width in ((0, 64, 80), (3, 60, 77), (8, 128, 160)):
