@@ -39,7 +39,7 @@ struct ExpertArgs {
     int KS;                              // warps that share a tile and split its k: 1, 2 or 4
     const int32_t *row_offsets, *expert_ids, *src_info, *status;
     uint4 *xw;                           // [R_max][step][word][quad thread] x as fp16, 16-byte pieces
-    float *xs;                           // [R_max] what a row's sums are multiplied by
+    uint32_t *xs;                        // [R_max] what a row's sums are multiplied by: two powers of two as bf16
     int draw;                            // CTAs draw their items; needs two steps or more of every warp in an item
     unsigned *drawn;                     // items drawn beyond the first two of every CTA
     uint16_t *out;
@@ -187,9 +187,9 @@ __device__ __forceinline__ void mma_step(const Weights<MT, ALIGN> &d, const uint
     }
 }
 
-// A row of x (null: no token) as fp16 in the order that the products take, and what its sums are multiplied by: all
-// threads of a CTA together.
-__device__ __forceinline__ float pack_row(const uint4 *x, int H, uint4 *dst) {
+// A row of x (null: no token) as fp16 in the order that the products take, and what its sums are multiplied by, as a pair
+// of bf16: all threads of a CTA together.
+__device__ __forceinline__ uint32_t pack_row(const uint4 *x, int H, uint4 *dst) {
     __shared__ unsigned s_top[kPackThreads / 32];
     const int tid = threadIdx.x;
     unsigned top = 0u;                                              // largest finite magnitude, as bf16 bits
@@ -222,8 +222,13 @@ __device__ __forceinline__ float pack_row(const uint4 *x, int H, uint4 *dst) {
         }
         dst[p] = v;
     }
-    return __uint_as_float((unsigned)(e - 14) << 23);
+    const unsigned both = (unsigned)(e - 14) + 127u, half = both >> 1;          // 2^(e - 141) in biased exponents, and halved
+    return half << 23 | (both - half) << 7;
 }
+
+// A sum of products times the scales of its row of W and its row of x.  The latter, a power of two, is multiplied in two
+// halves around the former: no product on the way leaves fp32's range unless the result does (row scales of W of 2^-86 to 2^86).
+__device__ __forceinline__ float scaled(float sum, float rs, uint32_t xs) { return sum * bf16_hi(xs) * rs * bf16_lo(xs); }
 
 // The row of x that a layout row takes, null for a row without a token.
 __device__ __forceinline__ const uint4 *source_row(const ExpertArgs &a, int src) {
@@ -242,7 +247,7 @@ ep_expert_pack_kernel(const ExpertArgs a) {
     const int src = a.by_token ? a.src_info[2 * (size_t)row] : row;
     if (cta_status(a.status) || row >= R) return;
     const int pieces = (a.H + kStepK - 1) / kStepK * 32;
-    const float xs = pack_row(source_row(a, src), a.H, a.xw + (size_t)row * pieces);
+    const uint32_t xs = pack_row(source_row(a, src), a.H, a.xw + (size_t)row * pieces);
     if (tid == 0) a.xs[row] = xs;
 }
 
@@ -272,7 +277,8 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     constexpr int kExpertThreads = S::THREADS, kExpertWarps = S::WARPS, kTileRows = 16 * MT;
     extern __shared__ uint4 s_x[];                                  // [2][8 * NT][PITCH]
     __shared__ float s_red[kExpertWarps][4 * MT * NT][32];               // partial sums, [warp][register][lane]
-    __shared__ float s_xs[2][kChunkRows], s_rs[2][kExpertThreads];  // scales of an item's rows of x and of W (the up rows last)
+    __shared__ uint32_t s_xs[2][kChunkRows];                        // scales of an item's rows of x
+    __shared__ float s_rs[2][kExpertThreads];                       // and of W (the up rows last)
     __shared__ int s_first[kMaxE + 2];                              // chunks before each group
     __shared__ int s_row[kMaxE + 2];                                // first row of each group
     __shared__ int s_warp[kExpertWarps];
@@ -462,16 +468,17 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
                 }
             }
             const int at = nw * per_warp + mt * (a.swiglu ? 8 : 16) + gl, n = cur.block * rows_out + at;
-            const float xs = s_xs[parity][r], *rs = s_rs[parity] + at;
+            const uint32_t xs = s_xs[parity][r];
+            const float *rs = s_rs[parity] + at;
             uint16_t *out = a.out + (size_t)(row0 + r) * n_out;
             if (a.swiglu) {
                 if (n < n_out) {
-                    const float gate = v[0] * xs * rs[0], up = v[1] * xs * rs[rows_out];
+                    const float gate = scaled(v[0], rs[0], xs), up = scaled(v[1], rs[rows_out], xs);
                     out[n] = __bfloat16_as_ushort(__float2bfloat16_rn(gate / (1.0f + expf(-gate)) * up));
                 }
             } else {
-                if (n < n_out) out[n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0] * xs * rs[0]));
-                if (n + 8 < n_out) out[n + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(v[1] * xs * rs[8]));
+                if (n < n_out) out[n] = __bfloat16_as_ushort(__float2bfloat16_rn(scaled(v[0], rs[0], xs)));
+                if (n + 8 < n_out) out[n + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(scaled(v[1], rs[8], xs)));
             }
         }
         cur = nx;
@@ -522,7 +529,7 @@ ep_expert_row_kernel(const ExpertArgs a, int one_wave) {
         rs = a.row_scale[(size_t)g * a.N + n];
         if (a.swiglu) rs_up = a.row_scale[(size_t)g * a.N + n_out + n];
     }
-    const float xs = pack_row(source_row(a, src), a.H, s_x);
+    const uint32_t xs = pack_row(source_row(a, src), a.H, s_x);
     __syncthreads();
     float acc[MT][1][4] = {};
     const int xo[1] = {0};
@@ -551,8 +558,8 @@ ep_expert_row_kernel(const ExpertArgs a, int one_wave) {
             v += s_sum[w][j >> 3][j & 7];
         }
     }
-    v *= xs * rs;
-    if (a.swiglu) v = v / (1.0f + expf(-v)) * (up * xs * rs_up);
+    v = scaled(v, rs, xs);
+    if (a.swiglu) v = v / (1.0f + expf(-v)) * scaled(up, rs_up, xs);
     a.out[(size_t)row * n_out + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
@@ -634,7 +641,7 @@ using namespace ep;
 extern "C" size_t ep_expert_matvec_workspace_bytes(const ep_layout_t *L, int hidden_size) {
     if (!layout_ok(L) || !hidden_ok(hidden_size)) return 0;
     const size_t R = layout_rows(L);
-    return R * pack_steps(hidden_size) * 512 + 16 + R * sizeof(float);
+    return R * pack_steps(hidden_size) * 512 + 16 + R * sizeof(uint32_t);
 }
 
 extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t *codes, const uint8_t *scales,
@@ -661,7 +668,7 @@ extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t
     const int steps = pack_steps(H);
     a.xw = (uint4 *)workspace;
     a.drawn = (unsigned *)(a.xw + (size_t)a.R_max * steps * 32);
-    a.xs = (float *)(a.drawn + 4);
+    a.xs = (uint32_t *)(a.drawn + 4);
     a.out = out;
     const float per_expert = (float)L->T * L->K / L->E;
     const bool few = per_expert <= 8.0f;

@@ -192,6 +192,29 @@ def test_special_values():
     assert (ep.expert_matvec(big, codes, scales, row_scale, L) == float("inf")).all()
 
 
+# one token, few rows per expert, many
+TOKENS = [(1, 2, 4), (6, 1, 2), (40, 1, 2)]
+
+
+@pytest.mark.parametrize("T,K,E", TOKENS)
+@pytest.mark.parametrize("x_exp,row_scale", [(110, 2.0 ** -40), (-112, 1.37 * 2.0 ** -20), (120, -1.2 * 2.0 ** -100), (-60, 1.1 * 2.0 ** 100)])
+def test_large_and_small_values_times_their_scales(T, K, E, x_exp, row_scale):
+    """Sums that leave fp32's range before the row's scale brings them back."""
+    import combine_topk_ids_histogram_gb300 as ep
+    N, H = 70, 512
+    codes, scales, _ = weights(E, N, H, 3)
+    rs = torch.full((E, N), row_scale, device="cuda")
+    x = (torch.randn(T, H, generator=torch.Generator().manual_seed(8)).clamp(-2, 2) * 2.0 ** x_exp).to(torch.bfloat16).cuda()
+    L = ep.dispatch_layout(routing(T, K, E, 5), E)
+    got = ep.expert_matvec(x, codes, scales, rs, L)
+    off, src = L.row_offsets.cpu().numpy(), L.src_info.cpu().numpy()
+    for g in range(E):
+        a, b = off[g], off[g + 1]
+        wm = ref.weights(codes[g].cpu().numpy(), scales[g].cpu().numpy(), rs[g].cpu().numpy())
+        want, tol = ref.experts(x.double().cpu().numpy()[src[a:b, 0]], wm, False)
+        ref.assert_within(got[a:b], want, tol, f"group {g}")
+
+
 def test_status_repeat_and_streams():
     import combine_topk_ids_histogram_gb300 as ep
     ids = routing(20, 4, 16, 5)
