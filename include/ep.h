@@ -498,7 +498,9 @@ size_t ep_expert_matvec_workspace_bytes(const ep_layout_t *L, int hidden_size);
  *              gives this format, with row_scale = its inverse scales widened to fp32.
  *   N          out_rows, 1 <= N <= 65536; with swiglu 1 even: N/2 gate rows, then N/2 up rows.
  *   -> out     [R_max * N] bf16: out[r, n] = weight row n . x, or with swiglu [R_max * N/2] bf16:
- *              silu(gate) * up, silu(v) = v / (1 + exp(-v)); fp32 sums, rounded once.
+ *              silu(gate) * up, silu(v) = v / (1 + exp(-v)); rounded once.  Sums are fp32: the tensor
+ *              cores, whose adder truncates, add over at most 2048 elements of k, and fp32 additions join
+ *              those.  A value of x below 2^-32 of the largest of its row loses its last bits.
  *   workspace  ep_expert_matvec_workspace_bytes(L, H) bytes (about 2H bytes per row of R_max), 16-byte
  *              aligned; needs no initialisation.  Calls that share one must not overlap on the GPU, nor be
  *              made by several host threads at once, on one stream either: a call is up to two

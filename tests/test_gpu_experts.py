@@ -215,6 +215,27 @@ def test_large_and_small_values_times_their_scales(T, K, E, x_exp, row_scale):
         ref.assert_within(got[a:b], want, tol, f"group {g}")
 
 
+@pytest.mark.parametrize("T,K,E,N", [(1, 2, 4, 64), (6, 1, 2, 64), (16, 2, 8, 4096), (64, 2, 8, 4096)])
+def test_long_sums_keep_their_last_bits(T, K, E, N):
+    """1 - 1 and thousands of terms far below them.  The products are added on the tensor cores over at most 2048 k, 128 steps
+    that are each off by at most 2^-22 of what they add, and those sums in fp32: within (128 + 8 + 16) * 2^-22 * sum|w x|
+    whatever the width.  (All of these terms together are more than that.)"""
+    import combine_topk_ids_histogram_gb300 as ep
+    H, small = 14336, 0.8984375 * 2.0 ** -27
+    codes = torch.full((E, N, H // 2), 0x22, dtype=torch.uint8, device="cuda")
+    scales = torch.full((E, N, H // 16), 0x38, dtype=torch.uint8, device="cuda")
+    rs = torch.ones(E, N, device="cuda")
+    x = torch.full((T, H), small, device="cuda")
+    x[:, 0], x[:, -1] = 1.0, -1.0
+    L = ep.dispatch_layout(routing(T, K, E, 5), E)
+    got = ep.expert_matvec(x.bfloat16(), codes, scales, rs, L)
+    want = (H - 2) * small
+    tol = 152 * 2.0 ** -22 * (2 + want) + 2.0 ** -8 * want
+    assert tol < want
+    err = (got.double() - want).abs().max().item()
+    assert err <= tol, (err, tol, want)
+
+
 def test_status_repeat_and_streams():
     import combine_topk_ids_histogram_gb300 as ep
     ids = routing(20, 4, 16, 5)
