@@ -59,13 +59,18 @@ __device__ __forceinline__ float group_sum(float a, float *red, int G, int ty) {
     return s;
 }
 __device__ __forceinline__ float2 group_sum2(f32x2 a, f32x2 *red, int G, int ty) {
+    // the lower half of a warp adds up the first values, the upper half the second ones
+    const int lane = threadIdx.x & 31, upper = lane >> 4;
+    const float2 p = f2_get(a);
+    float v = upper ? p.y : p.x;
+    v += __shfl_xor_sync(kFullMask, upper ? p.x : p.y, 16);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float2 v = f2_get(a);
-        a = f2_add(a, f2(__shfl_xor_sync(kFullMask, v.x, o), __shfl_xor_sync(kFullMask, v.y, o)));
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    if (G == 32) {
+        const float other = __shfl_xor_sync(kFullMask, v, 16);
+        return upper ? make_float2(other, v) : make_float2(v, other);
     }
-    if (G == 32) return f2_get(a);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    if ((lane & 15) == 0) reinterpret_cast<float *>(red + (threadIdx.x >> 5))[upper] = v;
     group_barrier(G, ty);
     f32x2 s = f2(0.0f, 0.0f);
     for (int i = 0; i < (G >> 5); i += 2) {
@@ -137,6 +142,28 @@ template <typename T, int EPT, int LAY> struct Units {
             if (has(i, 2 * j)) row[col(i, 2 * j)] = p.x;
             if (has(i, 2 * j + 1)) row[col(i, 2 * j + 1)] = p.y;
         }
+    }
+    // sum + the squares of the unit's values that are in the row
+    __device__ __forceinline__ f32x2 add_squares(f32x2 sum, int i, const f32x2 (&v)[E / 2]) const {
+        bool done = false;
+        if constexpr (LAY != kAny) {
+            done = whole(i);
+            if (done) {
+                f32x2 s = f2_mul(v[0], v[0]);
+#pragma unroll
+                for (int j = 1; j < E / 2; ++j) s = f2_fma(v[j], v[j], s);
+                sum = f2_add(sum, s);
+            }
+        }
+        if constexpr (LAY != kAligned) {
+            if (!done)
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j) {
+                    const float2 p = f2_get(f2_mul(v[j], v[j]));
+                    sum = f2_add(sum, f2(has(i, 2 * j) ? p.x : 0.0f, has(i, 2 * j + 1) ? p.y : 0.0f));
+                }
+        }
+        return sum;
     }
     // sum + the unit's values that are in the row
     __device__ __forceinline__ f32x2 add(f32x2 sum, int i, const f32x2 (&v)[E / 2]) const {
@@ -221,9 +248,12 @@ template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("c
 // ---------------------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------------------
-// The mean that the first pass over a row gives is off by the rounding of its sum.  The second pass also sums d = x - mean,
-// whose own mean delta is what the first one missed: the mean, d and the variance are corrected by it.  A constant row has
-// d = delta exactly, and so y = bias.
+// The mean that the first pass over a row gives is off by the rounding of its sum and of 1/H.  The second pass also sums
+// d = x - mean, whose own mean delta is what the first one missed: the mean and the variance are corrected by it, and d too
+// unless delta is below kMeanSlack standard deviations, a quarter of the last bit of a d of one standard deviation.  A constant
+// row has d = delta exactly, and so y = bias.
+constexpr float kMeanSlack = 0x1p-26f;
+
 // The variance about the corrected mean from the mean square about the first one; NaN stays NaN.
 __device__ __forceinline__ float centred_var(float mean_square, float delta) {
     const float v = fmaf(-delta, delta, mean_square);
@@ -254,7 +284,7 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
         if (row + i * step < rows) src.copy(row + i * step, stages + i * bytes, tid, G);
         copies_commit();
     }
-    const float h = (float)H;
+    const float h = (float)H, inv_h = 1.0f / h;
     // the parameters, as far behind a 16-byte boundary as the group's rows (L1 is too small beside the stages to keep them)
     W *s_w = reinterpret_cast<W *>(smem + (LAY == kShifted ? ty : 0) * 2 * params), *s_b = s_w + params / sizeof(W);
 #pragma unroll 8
@@ -276,13 +306,13 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
         f32x2 d[U::N][U::E / 2];
 #pragma unroll
         for (int i = 0; i < U::N; ++i) un.load(s_row, i, d[i]);
-        float mean = 0.0f, var;
+        float mean = 0.0f, rstd;
         if (!rms) {
             f32x2 s = f2(0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < U::N; ++i) s = un.add(s, i, d[i]);
             const float2 p = f2_get(s);
-            mean = group_sum(p.x + p.y, red0, G, ty) / h;
+            mean = group_sum(p.x + p.y, red0, G, ty) * inv_h;
             const f32x2 neg = f2(-mean, -mean);
 #pragma unroll
             for (int i = 0; i < U::N; ++i)
@@ -291,30 +321,27 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
         }
         f32x2 q = f2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < U::N; ++i) {
-            f32x2 sq[U::E / 2];
-#pragma unroll
-            for (int j = 0; j < U::E / 2; ++j) sq[j] = f2_mul(d[i][j], d[i][j]);
-            q = un.add(q, i, sq);
-        }
+        for (int i = 0; i < U::N; ++i) q = un.add_squares(q, i, d[i]);
         const float2 p = f2_get(q);
         if (rms) {
-            var = group_sum(p.x + p.y, buf ? red0 : red1, G, ty) / h;
+            rstd = __frsqrt_rn(group_sum(p.x + p.y, buf ? red0 : red1, G, ty) / h + eps);
         } else {
             f32x2 s = f2(0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < U::N; ++i) s = un.add(s, i, d[i]);
             const float2 r = f2_get(s), t = group_sum2(f2(r.x + r.y, p.x + p.y), red2, G, ty);
-            const float delta = t.x / h;
-            var = centred_var(t.y / h, delta);
+            float delta = t.x * inv_h;
+            rstd = __frsqrt_rn(centred_var(t.y / h, delta) + eps);
+            if (fabsf(delta) * rstd > kMeanSlack) {
+                delta = t.x / h;
+                const f32x2 neg = f2(-delta, -delta);
+#pragma unroll
+                for (int i = 0; i < U::N; ++i)
+#pragma unroll
+                    for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_add(d[i][j], neg);
+            }
             mean += delta;
-            const f32x2 neg = f2(-delta, -delta);
-#pragma unroll
-            for (int i = 0; i < U::N; ++i)
-#pragma unroll
-                for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_add(d[i][j], neg);
         }
-        const float rstd = rsqrtf(var + eps);
         if (tid == 0) {
             if (!rms) mean_out[row] = mean;
             rstd_out[row] = rstd;
@@ -326,11 +353,15 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
             f32x2 u[U::E / 2];
             un.load(s_w, i, u);
 #pragma unroll
-            for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_mul(f2_mul(d[i][j], r2), u[j]);
+            for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_mul(d[i][j], r2);
             if (b) {
-                un.load(s_b, i, u);
+                f32x2 c[U::E / 2];
+                un.load(s_b, i, c);
 #pragma unroll
-                for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_add(d[i][j], u[j]);
+                for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_fma(d[i][j], u[j], c[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_mul(d[i][j], u[j]);
             }
             un.store(yr, i, d[i]);
         }
@@ -352,6 +383,7 @@ ep_norm_row_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__
     __syncthreads();
     pdl_begin_if(one_wave);
     const int G = blockDim.x, tid = threadIdx.x, row = blockIdx.x, nv = H / VEC;
+    const float h = (float)H, inv_h = 1.0f / h;
     const T *xr = x + (size_t)row * ldx;
     float d[NV][VEC];
 #pragma unroll
@@ -376,7 +408,7 @@ ep_norm_row_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) s += d[i][j];
-        mean = group_sum(s, s_red, G, 0) / (float)H;
+        mean = group_sum(s, s_red, G, 0) * inv_h;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -390,16 +422,16 @@ ep_norm_row_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__
             q = fmaf(d[i][j], d[i][j], q);
             sd += d[i][j];
         }
-    float var, delta = 0.0f;
+    float rstd, delta = 0.0f;
     if (rms) {
-        var = group_sum(q, s_red, G, 0) / (float)H;
+        rstd = __frsqrt_rn(group_sum(q, s_red, G, 0) / h + eps);
     } else {
         const float2 t = group_sum2(f2(sd, q), s_red2, G, 0);
-        delta = t.x / (float)H;
-        var = centred_var(t.y / (float)H, delta);
+        delta = t.x * inv_h;
+        rstd = __frsqrt_rn(centred_var(t.y / h, delta) + eps);
+        if (fabsf(delta) * rstd > kMeanSlack) delta = t.x / h;
         mean += delta;
     }
-    const float rstd = 1.0f / sqrtf(var + eps);
     if (tid == 0) {
         if (!rms) mean_out[row] = mean;
         rstd_out[row] = rstd;
@@ -412,14 +444,15 @@ ep_norm_row_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__
             float o[VEC];
             if (NV > 1) w0 = ld_pack<W, VEC>(w + (size_t)v * VEC);
             w0.unpack(o);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) o[j] *= (d[i][j] - delta) * rstd;
+            float c[VEC];
             if (b) {
-                float c[VEC];
                 if (NV > 1) b0 = ld_pack<W, VEC>(b + (size_t)v * VEC);
                 b0.unpack(c);
+            }
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) o[j] += c[j];
+            for (int j = 0; j < VEC; ++j) {
+                const float n = (d[i][j] - delta) * rstd;
+                o[j] = b ? fmaf(n, o[j], c[j]) : n * o[j];
             }
             st_pack_stream<T, VEC>(yr + (size_t)v * VEC, o);
         }

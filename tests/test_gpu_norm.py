@@ -376,3 +376,21 @@ def test_large_means_lose_nothing(T, H, m):
     ref.assert_within(y, ry, ty, "y")
     ref.assert_within(rstd, rrstd, rrstd * drel[:, 0], "rstd")
     ref.assert_within(mean, rmean, of_mean[:, 0] + 1.01 * ref.EPS24 * rmean.abs(), "mean")
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H,many", [(7168, 1500), (1110, 2000), (300, 10000)])
+@pytest.mark.parametrize("rms", [False, True])
+def test_statistics_do_not_depend_on_the_number_of_rows(H, many, dt, rms):
+    """Rows of whole numbers and their negatives: their sum is 0 and that of their squares exact in any order, so that
+    rstd is the same bits in few rows and in many."""
+    import combine_topk_ids_histogram_gb300 as ep
+    g = torch.Generator().manual_seed(H)
+    half = torch.randint(-8, 9, (many, H // 2), generator=g) + torch.randint(-4, 5, (many, 1), generator=g)
+    x = torch.cat([half, -half], 1).to(dt).cuda()
+    w = torch.ones(H, dtype=dt, device="cuda")
+    assert many > resident_rows(H, dt, H % 8 == 0)
+    y, _, rstd = ep.layer_norm(x, w, rms=rms)
+    for at in range(0, 200, 4):
+        y4, _, rstd4 = ep.layer_norm(x[at:at + 4].contiguous(), w, rms=rms)
+        assert torch.equal(rstd4, rstd[at:at + 4]) and torch.equal(y4, y[at:at + 4])
