@@ -500,7 +500,7 @@ ep_norm_bwd_kernel(const T *__restrict__ g, long long ldg, const T *__restrict__
     for (int i = 0; i < U::N; ++i)
 #pragma unroll
         for (int j = 0; j < U::E / 2; ++j) dw[i][j] = db[i][j] = f2(0.0f, 0.0f);
-    const float inv_h = 1.0f / (float)H;
+    const float h = (float)H;
     float next_mean = 0.0f, next_rstd = 0.0f;                       // a row ahead
     if (row < rows) {
         if (!rms) next_mean = mean_in[row];
@@ -546,7 +546,7 @@ ep_norm_bwd_kernel(const T *__restrict__ g, long long ldg, const T *__restrict__
         }
         const float2 pa = f2_get(sa), px = f2_get(sax);
         const float2 s = group_sum2(f2(pa.x + pa.y, px.x + px.y), red[buf], G, ty);
-        const float ma = rms ? 0.0f : s.x * inv_h, max_ = s.y * inv_h;
+        const float ma = rms ? 0.0f : s.x / h, max_ = s.y / h;
         const f32x2 neg_ma = f2(-ma, -ma), neg_max = f2(-max_, -max_);
         T *out = dx + (size_t)row * H;
 #pragma unroll
@@ -618,7 +618,7 @@ ep_norm_bwd_few_kernel(const T *__restrict__ g, long long ldg, const T *__restri
         }
         __syncthreads();
         const float2 s = group_sum2(f2(sa, sax), s_red, kFewThreads, 0);
-        const float inv_h = 1.0f / (float)H, ma = rms ? 0.0f : s.x * inv_h, max_ = s.y * inv_h;
+        const float ma = rms ? 0.0f : s.x / (float)H, max_ = s.y / (float)H;
         for (int c = tid * VEC; c < H; c += kFewThreads * VEC) {
             float xf[VEC], gf[VEC], wf[VEC], o[VEC];
             ld_pack<T, VEC>(xr + c).unpack(xf);

@@ -394,3 +394,18 @@ def test_statistics_do_not_depend_on_the_number_of_rows(H, many, dt, rms):
     for at in range(0, 200, 4):
         y4, _, rstd4 = ep.layer_norm(x[at:at + 4].contiguous(), w, rms=rms)
         assert torch.equal(rstd4, rstd[at:at + 4]) and torch.equal(y4, y[at:at + 4])
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,H", [(4, 7168), (1000, 7168), (4, 1110), (2000, 1110), (4, 300), (3000, 300), (900, 9000)])
+def test_gradient_of_a_row_of_equal_gradients_is_zero(T, H, dt):
+    """With weight 1, grad_y = c and xh summing to 0, a - mean(a) and the sum of a * xh are exactly 0."""
+    import combine_topk_ids_histogram_gb300 as ep
+    g = torch.Generator().manual_seed(H)
+    half = torch.randint(-8, 9, (T, H // 2), generator=g)
+    x = torch.cat([half, -half], 1).to(dt).cuda()
+    gy = ((torch.arange(T) % 7 - 3)[:, None] * torch.ones(1, H)).to(dt).cuda()
+    w = torch.ones(H, dtype=dt, device="cuda")
+    rstd = torch.full((T,), 0.125, device="cuda")                       # a * xh: whole eighths, exact in any order
+    dx, _, _ = ep.layer_norm_bwd(gy, x, w, torch.zeros(T, device="cuda"), rstd)
+    assert (dx == 0).all()
