@@ -59,7 +59,7 @@ __device__ __forceinline__ float slot_prob(float l, bool used, const T *row, int
         const float m = fminf(warp_max(used ? l : neg_inf), 0.0f);
         // exp(l - m) / (1 + exp(l)) below 0 and 1 / (1 + exp(-l)) from there on (then m = 0)
         const float e = expf(-fabsf(l)), top = l >= 0.0f ? 1.0f : m == 0.0f ? e : expf(l - m);
-        const float s = used ? __fdividef(top, 1.0f + e) : 0.0f;        // 1 <= 1 + e <= 2: good to 2 ulp
+        const float s = used ? top / (1.0f + e) : 0.0f;
         const float total = warp_sum(s);
         return used ? sc.scale * (s / total) : 0.0f;
     }
