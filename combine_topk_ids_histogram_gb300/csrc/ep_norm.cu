@@ -28,9 +28,11 @@ template <typename T> constexpr int kFwdStages = sizeof(T) == 4 ? 3 : 4;
 constexpr int kSharedBytes = 226 * 1024; // shared memory for stages and parameters
 constexpr int kBwdMaxH = 8192;
 constexpr int kPartials = 304;           // rows of partial column sums a workspace has room for
-// Few rows.  Forward: one CTA per row while all of them are resident at once (bf16, us against the pipelined kernel: H = 2048,
+// Few rows.  Forward: one CTA per row while the rows have at most 2048 threads per SM (at 36 to 64 registers per thread they
+// then run in one or two waves).  us against the pipelined kernel, bf16: H = 2048,
 // T = 1000 4.2 against 4.7, T = 2000 6.5 against 6.4; H = 7168, T = 304 5.1 against 5.4, T = 600 9.5 against 7.6; H = 256,
-// T = 8000 5.7 against 6.8).  Backward: one launch that reads x and g twice, up to few_bwd_rows rows (us against the pipelined
+// T = 8000 5.7 against 6.8; H = 16384, four vectors per thread, T = 300 5.6 against 7.7, T = 600 12.2 against 14.4 (eight,
+// which spill: 9.1 and 14.5).  Backward: one launch that reads x and g twice, up to few_bwd_rows rows (us against the pipelined
 // kernel, bf16: H = 256, T = 400 5.5 against 6.0, T = 600 7.5 against 6.2; H = 2048, T = 200 4.2 against 10.8, T = 800 11.3
 // against 11.7, T = 1000 13.5 against 11.8; H = 8192, T = 800 22.0 against 26.6, T = 1500 38.4 against 33.6.  fp32: H = 2048,
 // T = 400 8.6 against 8.2; H = 8192, T = 400 20.2 against 25.4, T = 600 29.4 against 29.2).
@@ -762,14 +764,15 @@ constexpr int laid(int H, int lay, int vec) { return lay == kShifted ? H + 2 * (
 template <typename T, typename W, int LAY>
 int launch_fwd(const NormArgs &a) {
     constexpr int VEC = 16 / sizeof(T), RV = LAY == kAligned ? VEC : 1;   // the one-row kernel's vectors
+    constexpr int NV = RV == 8 ? 4 : 8;                                  // of them per thread in rows of more than 1024
     const int nv = a.H / RV;
-    if ((long long)a.rows * round_up(nv <= 1024 ? nv : (nv + 7) / 8, 32) <= kResidentThreads) {
+    if ((long long)a.rows * round_up(nv <= 1024 ? nv : (nv + NV - 1) / NV, 32) <= kResidentThreads) {
         if (nv <= 1024) return launch_fwd_rows<T, W, RV, 1>(a);
-        if (nv <= 8192) return launch_fwd_rows<T, W, RV, 8>(a);
+        if (nv <= 1024 * NV) return launch_fwd_rows<T, W, RV, NV>(a);
     }
     const int row_bytes = kFwdStages<T> * RowSource<T, kFwdEpt, LAY>::stage_bytes(a.H), params = 2 * param_bytes<W>(a.H + 2 * VEC);
     const dim3 block = group_shape(laid(a.H, LAY, VEC), kFwdEpt, kFwdThreads, LAY, params, row_bytes);
-    if (block.y < 1) return launch_fwd_rows<T, W, RV, (RV == 1 ? 32 : 8)>(a);
+    if (block.y < 1) return launch_fwd_rows<T, W, RV, (RV == 1 ? 32 : NV)>(a);
     constexpr auto kern = ep_norm_kernel<T, W, LAY>;
     const int rc = allow_smem<kern>(kSharedBytes);
     if (rc != EP_OK) return rc;
