@@ -350,7 +350,8 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
     const int per_warp = a.swiglu ? kTileRows / 2 : kTileRows;
     const int rows_out = per_warp * NS;                             // output columns of an item
     const int blocks = (n_out + rows_out - 1) / rows_out;
-    const int items = s_first[a.G] * blocks;                        // the output holds 128 elements per item: fits an int
+    // fits an int: an item has 32 columns or more, a chunk 8 rows but for a group's last, and the output fits the device
+    const int items = s_first[a.G] * blocks;
     const int steps = (a.H + kStepK - 1) / kStepK;
 
     struct Cursor {
@@ -525,10 +526,10 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
 // the kernels above: top-8 of 128, 2048 -> 2 x 768 gated 6.7 against 8.2, 768 -> 2048 4.8 against 6.5; top-2 of 8, 14336 -> 4096
 // 27.4 against 31.6; 4096 -> 2 x 7168 gated 21.0 against 21.6, where KS = 2 just fits, and 4096 -> 2 x 14336, where it does not,
 // 36.5 against 30.8).
-constexpr int kRowThreads = 256, kRowWave = 304;
+constexpr int kRowThreads = 256, kRowCtas = 2;                      // per SM
 
 template <int ALIGN>
-__global__ void __launch_bounds__(kRowThreads, 2)
+__global__ void __launch_bounds__(kRowThreads, kRowCtas)
 ep_expert_row_kernel(const ExpertArgs a, int one_wave) {
     constexpr int MT = 2, kWarps = kRowThreads / 32;
     extern __shared__ uint4 s_x[];                                  // [step][word][quad thread]
@@ -621,10 +622,11 @@ int choose_split(const ExpertArgs &a, int steps, float chunks) {
     const int n_out = a.swiglu ? a.N / 2 : a.N, per_warp = S::MT * (a.swiglu ? 8 : 16);
     int best = 1;
     float best_time = 0.0f;
+    const float sms = (float)std::max(device_sm_count(), 1);
     for (int ks = 1; ks <= 4 && ks <= steps; ks *= 2) {
         const int rows = per_warp * (S::WARPS / ks);
         const float items = chunks * (float)((n_out + rows - 1) / rows);
-        const float x = items / (152.0f * S::CTAS);
+        const float x = items / (sms * S::CTAS);
         const float begin_end = ks == 1 ? 1.0f : ks == 2 ? 1.25f : 1.4f;
         const float time = (S::NT > 1 ? ceilf(x) : fmaxf(x, 1.0f) + 0.6f) * ((float)((steps + ks - 1) / ks) + begin_end);
         if (ks == 1 || time < best_time) {
@@ -656,13 +658,16 @@ int row_blocks(const ExpertArgs &a, int KS) {
     return (n_out + rows_out - 1) / rows_out;
 }
 
+// And how many of them are resident at once.
+int row_wave() { return kRowCtas * device_sm_count(); }
+
 template <int ALIGN>
 int launch_expert_row(ExpertArgs a, cudaStream_t st) {
     constexpr auto kern = ep_expert_row_kernel<ALIGN>;
     const int rc = allow_smem<kern>((size_t)pack_steps(kMaxH) * 512);
     if (rc != EP_OK) return rc;
     a.KS = 1;                                                       // the most that one wave of CTAs has room for
-    while (a.KS < 4 && 2 * a.KS <= pack_steps(a.H) && row_blocks(a, 2 * a.KS) * a.R_max <= kRowWave) a.KS *= 2;
+    while (a.KS < 4 && 2 * a.KS <= pack_steps(a.H) && row_blocks(a, 2 * a.KS) * a.R_max <= row_wave()) a.KS *= 2;
     const dim3 grid(row_blocks(a, a.KS), a.R_max);
     return launch_pdl(kern, grid, dim3(kRowThreads), (size_t)pack_steps(a.H) * 512, st, a, one_wave(grid.x * grid.y));
 }
@@ -712,7 +717,7 @@ extern "C" int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t
     const float chunks = active * fmaxf(1.0f, per_expert / rows + 0.5f) + (L->fused_shared ? ceilf(L->T / rows) : 0.0f);
     cudaStream_t st = as_stream(stream);
     const bool by64 = H % 64 == 0 && (reinterpret_cast<uintptr_t>(codes) & 31u) == 0;
-    if (L->T == 1 && a.R_max <= L->K + 1 && L->expert_ids && row_blocks(a, steps > 8 ? 2 : 1) * a.R_max <= kRowWave) {
+    if (L->T == 1 && a.R_max <= L->K + 1 && L->expert_ids && row_blocks(a, steps > 8 ? 2 : 1) * a.R_max <= row_wave()) {
         if (by64) return launch_expert_row<32>(a, st);
         return H % 32 == 0 ? launch_expert_row<16>(a, st) : launch_expert_row<8>(a, st);
     }

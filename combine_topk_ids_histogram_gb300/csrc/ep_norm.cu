@@ -28,7 +28,7 @@ template <typename T> constexpr int kFwdStages = sizeof(T) == 4 ? 3 : 4;
 constexpr int kSharedBytes = 226 * 1024; // shared memory for stages and parameters
 constexpr int kBwdMaxH = 8192;
 constexpr int kPartials = 304;           // rows of partial column sums a workspace has room for
-// Few rows.  Forward: one CTA per row while the rows have at most 2048 threads per SM (at 36 to 64 registers per thread they
+// Few rows.  Forward: one CTA per row while the rows have at most kResidentPerSm threads per SM (at 36 to 64 registers per thread they
 // then run in one or two waves).  us against the pipelined kernel, bf16: H = 2048,
 // T = 1000 4.2 against 4.7, T = 2000 6.5 against 6.4; H = 7168, T = 304 5.1 against 5.4, T = 600 9.5 against 7.6; H = 256,
 // T = 8000 5.7 against 6.8; H = 16384, four vectors per thread, T = 300 5.6 against 7.7, T = 600 12.2 against 14.4 (eight,
@@ -36,7 +36,7 @@ constexpr int kPartials = 304;           // rows of partial column sums a worksp
 // kernel, bf16: H = 256, T = 400 5.5 against 6.0, T = 600 7.5 against 6.2; H = 2048, T = 200 4.2 against 10.8, T = 800 11.3
 // against 11.7, T = 1000 13.5 against 11.8; H = 8192, T = 800 22.0 against 26.6, T = 1500 38.4 against 33.6.  fp32: H = 2048,
 // T = 400 8.6 against 8.2; H = 8192, T = 400 20.2 against 25.4, T = 600 29.4 against 29.2).
-constexpr int kResidentThreads = 152 * 2048;
+constexpr int kResidentPerSm = 2048;
 constexpr int few_bwd_rows(int H, int element) { return element == 2 && H > 256 ? 800 : 456; }
 
 constexpr int round_up(int n, int to) { return (n + to - 1) / to * to; }
@@ -766,7 +766,7 @@ int launch_fwd(const NormArgs &a) {
     constexpr int VEC = 16 / sizeof(T), RV = LAY == kAligned ? VEC : 1;   // the one-row kernel's vectors
     constexpr int NV = RV == 8 ? 4 : 8;                                  // of them per thread in rows of more than 1024
     const int nv = a.H / RV;
-    if ((long long)a.rows * round_up(nv <= 1024 ? nv : (nv + NV - 1) / NV, 32) <= kResidentThreads) {
+    if ((long long)a.rows * round_up(nv <= 1024 ? nv : (nv + NV - 1) / NV, 32) <= (long long)device_sm_count() * kResidentPerSm) {
         if (nv <= 1024) return launch_fwd_rows<T, W, RV, 1>(a);
         if (nv <= 1024 * NV) return launch_fwd_rows<T, W, RV, NV>(a);
     }

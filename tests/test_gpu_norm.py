@@ -262,7 +262,8 @@ def resident_rows(H, dt, aligned=True):
     there cannot move these tests' cases to the other side of it unnoticed."""
     import combine_topk_ids_histogram_gb300 as ep
     src = open(os.path.join(os.path.dirname(ep.__file__), "csrc", "ep_norm.cu")).read()
-    threads = eval(re.search(r"constexpr int kResidentThreads = ([0-9 *]+);", src).group(1))
+    threads = int(re.search(r"constexpr int kResidentPerSm = (\d+);", src).group(1))
+    threads *= torch.cuda.get_device_properties(0).multi_processor_count
     vec = (4 if dt == torch.float32 else 8) if aligned else 1
     per_row = H // vec if H // vec <= 1024 else (H // vec + 7) // 8
     return threads // ((per_row + 31) // 32 * 32)
