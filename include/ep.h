@@ -417,8 +417,11 @@ typedef enum { EP_BF16 = 0, EP_F16 = 1, EP_F32 = 2 } ep_dtype_t;
  *   -> rstd [T] fp32 = 1/sqrt(sum((x - mean)^2)/H + eps), mean [T] fp32 (e): what the backward
  *      pass takes;
  *   -> y    [T*H] dtype, dense (e) = (x - mean) * rstd * weight + bias.
- * All arithmetic is fp32, rounded once into y; the variance is summed over x - mean.  eps >= 0 (with
- * eps = 0 a constant row gives NaN).  A NaN or infinity in a row makes that row NaN and no other.
+ * All arithmetic is fp32, rounded once into y; the variance is summed over x - mean, which also
+ * corrects the mean, so a constant row gives y = bias (eps > 0).  eps >= 0; with eps = 0 a row of variance 0 has
+ * no defined result.  A NaN in a row makes that row NaN and no other, and so does an infinity
+ * when rms is 0.  With rms 1 an infinity makes its row's rstd 0, so that infinite elements give NaN and finite
+ * ones 0 (or bias).  A sum of squares beyond fp32 counts as infinite.
  */
 int ep_layer_norm(const void *x, long long x_stride, int dtype, const void *weight, const void *bias,
                   int param_dtype, int T, int hidden_size, float eps, int rms, void *y, float *mean,
