@@ -698,7 +698,9 @@ def router_topk(logits: torch.Tensor, K: int, bias: torch.Tensor | None = None, 
                 renormalize: bool = True, scale: float = 1.0, out=None, stream=None):
     """ep_router_topk -> (topk_ids int32 [T, K], probs fp32 [T, K]) from logits [T, E] bf16 / fp16 /
     fp32 (rows may have a stride): the K largest of logit + bias (fp32 [E]), ties to the lower id; -1
-    with probability 0 where only -inf is left."""
+    with probability 0 where only -inf is left.  The bias is added to the logit.  Where a router adds it to the
+    score instead, ``ids, _ = router_topk(torch.sigmoid(logits.float()) + bias, K)`` selects, the probabilities
+    are those of ``logits`` at these ids, and ``router_topk_bwd`` takes ``logits`` and these ids."""
     pl, T, E, ld, dt = _matrix(logits, "logits")
     if out is None:
         out = (torch.empty(T, K, dtype=torch.int32, device=logits.device),

@@ -459,7 +459,12 @@ int ep_layer_norm_bwd(const void *grad_y, long long grad_stride, const void *x, 
  * topk_ids the layout calls take and the probs ep_combine takes.
  *   logits [T, E] of type dtype, row stride `stride` (e); bias [E] fp32 or NULL (e).
  *   Selection: the K experts with the largest fp32 logit + bias, in descending order, ties to the
- *   lower id (K <= E, K <= 32).  An expert whose sum is -inf is not selectable; slots for
+ *   lower id (K <= E, K <= 32).  The bias is added to the LOGIT, not to the score: routers that add
+ *   a balancing bias to sigmoid(l) order experts differently.  For those, take the ids of
+ *   this call on sigmoid(l) + bias as fp32 logits without bias, and the probabilities of the ids
+ *   from the logits l; ep_router_topk_bwd takes such ids as they are.  Selection limited to groups
+ *   of experts is not offered (mask the other groups' experts with -inf).
+ *   An expert whose sum is -inf is not selectable; slots for
  *   which no expert is left get id -1 and probability 0, so a fully masked row routes nowhere.
  *   Any finite value, the type's lowest among them, is selectable.  A NaN sorts above every
  *   number, so that it shows in the outputs.

@@ -178,6 +178,29 @@ def test_gradient_against_differences(score, renorm):
         assert (np.abs(dl[:, e] - diff) <= tol).all()
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,K", [(1, 16, 4), (33, 64, 6), (500, 256, 8)])
+def test_a_bias_on_the_score_takes_two_steps(T, E, K, renorm):
+    """The call's bias is added to the logit.  A router that adds it to sigmoid(logit) takes its ids from a call on those
+    sums, its probabilities from the logits at these ids, and its gradient from the backward call with these ids."""
+    import combine_topk_ids_histogram_gb300 as ep
+    g = torch.Generator().manual_seed(E)
+    l, bias = make(T, E, torch.float32, E), torch.randn(E, generator=g).cuda()
+    s = torch.sigmoid(l) + bias
+    ids, _ = ep.router_topk(s, K)
+    want = ref.select(s, None, K)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    assert T == 1 or not np.array_equal(want, ref.select(l, bias, K))          # another order than the call's own bias gives
+    p = torch.sigmoid(l).gather(1, ids.long())
+    p = 2.5 * (p / p.sum(1, keepdim=True) if renorm else p)
+    rp, _ = ref.probs(l, want, "sigmoid", renorm, 2.5)
+    ref.assert_within(p, rp, ref.probs_rel(l, want) * rp, "probs")
+    gp = torch.randn(T, K, generator=g).cuda()
+    dl = ep.router_topk_bwd(gp, l, ids, score="sigmoid", renormalize=renorm, scale=2.5)
+    rd, td = ref.router_bwd(gp, l, want, "sigmoid", renorm, 2.5)
+    ref.assert_within(dl, rd, 1.01 * ref.U[l.dtype] * np.abs(rd) + td + 2.0 ** -120, "grad_logits")
+
+
 def test_no_tokens_and_refusals():
     import combine_topk_ids_histogram_gb300 as ep
     l = torch.empty(0, 16, device="cuda")
