@@ -8,8 +8,9 @@
 //
 // Statistics and sums are fp32.  The variance is summed over (x - mean) in a second pass over
 // registers, which also corrects the mean, so rows with a large mean lose nothing.  HBM is the floor of both passes: each row is
-// read once and written once.  4096 x 7168 bf16 RMS forward: 22 us, 0.80 of the measured copy bandwidth with the launch;
-// 32768 x 7168 bf16 backward: 310 us, 0.68, where issue and the row sums at 14 warps per SM bound it; single rows: 1.9 us.
+// read once and written once.  4096 x 7168 bf16 forward: RMS 21.5 us, 0.82 of the measured copy bandwidth with the launch, layer
+// norm 28.5 us, 0.62 (the corrected mean is another pass over registers and a second sum);
+// 32768 x 7168 bf16 backward: 292 us, 0.72, where issue and the row sums at 14 warps per SM bound it; single rows: 1.9 us.
 //
 // Many rows: one CTA per SM whose threads form groups, a group holding 32 elements of a row per thread, and
 // looping over rows.  Rows arrive in a ring of shared-memory stages by asynchronous copies, so that the
@@ -28,16 +29,19 @@ template <typename T> constexpr int kFwdStages = sizeof(T) == 4 ? 3 : 4;
 constexpr int kSharedBytes = 226 * 1024; // shared memory for stages and parameters
 constexpr int kBwdMaxH = 8192;
 constexpr int kPartials = 304;           // rows of partial column sums a workspace has room for
-// Few rows.  Forward: one CTA per row while the rows have at most kResidentPerSm threads per SM (at 36 to 64 registers per thread they
-// then run in one or two waves).  us against the pipelined kernel, bf16: H = 2048,
-// T = 1000 4.2 against 4.7, T = 2000 6.5 against 6.4; H = 7168, T = 304 5.1 against 5.4, T = 600 9.5 against 7.6; H = 256,
-// T = 8000 5.7 against 6.8; H = 16384, four vectors per thread, T = 300 5.6 against 7.7, T = 600 12.2 against 14.4 (eight,
-// which spill: 9.1 and 14.5).  Backward: one launch that reads x and g twice, up to few_bwd_rows rows (us against the pipelined
-// kernel, bf16: H = 256, T = 400 5.5 against 6.0, T = 600 7.5 against 6.2; H = 2048, T = 200 4.2 against 10.8, T = 800 11.3
-// against 11.7, T = 1000 13.5 against 11.8; H = 8192, T = 800 22.0 against 26.6, T = 1500 38.4 against 33.6.  fp32: H = 2048,
-// T = 400 8.6 against 8.2; H = 8192, T = 400 20.2 against 25.4, T = 600 29.4 against 29.2).
-constexpr int kResidentPerSm = 2048;
-constexpr int few_bwd_rows(int H, int element) { return element == 2 && H > 256 ? 800 : 456; }
+// Few rows.  Forward: one CTA per row while the rows have at most kResidentPerSm threads per SM.  us against the pipelined
+// kernel, bf16, layer norm / RMS: H = 256, T = 8000 5.9 / 5.7 against 7.7 / 5.6, T = 9500 6.5 / 6.5 against 7.7 / 5.7; H = 2048,
+// T = 1000 4.6 / 3.4 against 5.0 / 4.3, T = 1216 5.3 / 3.8 against 4.9 / 4.3; H = 7168, T = 152 3.5 / 2.4 against 5.3 / 4.4,
+// T = 304 6.2 / 4.1 against 5.5 / 4.4, T = 347 8.2 / 5.5 against 5.5 / 4.5; H = 16384, four vectors per thread, T = 300
+// 5.6 / 4.3 against 7.7 / 5.9 (eight, which spill: 9.1 / 6.7).
+// Backward: one launch that reads x and g twice, up to few_bwd_rows rows.  us against the pipelined kernel, bf16: H = 256, T = 400
+// 5.6 against 6.2, T = 456 6.8 against 6.2; H = 2048, T = 800 11.3 against 11.6, T = 1000 13.7 against 11.7; H = 8192, T = 800
+// 21.4 against 25.2, T = 1500 37.4 against 31.5.  fp32: H = 2048, T = 300 6.8 against 7.8, T = 400 8.8 against 7.9; H = 4096,
+// T = 456 12.4 against 13.4; H = 8192, T = 456 22.6 against 24.6, T = 600 28.2 against 27.2.
+constexpr int kResidentPerSm = 1696;
+constexpr int few_bwd_rows(int H, int element) {
+    return element == 2 ? (H > 256 ? 800 : 400) : (H >= 4096 ? 456 : 340);
+}
 
 constexpr int round_up(int n, int to) { return (n + to - 1) / to * to; }
 
