@@ -5,9 +5,9 @@
 //
 // Weights are in the format the NVFP4 dispatch writes.  A group's weights are read from HBM once for
 // all of its rows, so HBM bounds the call while an expert has few rows: 9/16 byte per weight.  16 tokens, top-8 of 256 and a
-// shared expert, 7168 -> 2 x 2048 gated: 265 us, 0.80 of the measured copy bandwidth (0.94 while all SMs work); 1 token, top-8 of
-// 128, 2048 -> 2 x 768: 6.7 us.  From about 16 rows per expert on the conversion and the products bound it: 64 tokens, top-2 of
-// 8, 14336 -> 4096: 100 us.
+// shared expert, 7168 -> 2 x 2048 gated: 268 us, 0.80 of the measured copy bandwidth (0.94 while all SMs work); 1 token, top-8 of
+// 128, 2048 -> 2 x 768: 6.4 us.  From about 16 rows per expert on the conversion and the products bound it: 64 tokens, top-2 of
+// 8, 14336 -> 4096: 102 us.
 //
 // The products run on mma.sync.m16n8k16 with weight rows as M and layout rows as N: at 8 rows
 // or fewer per expert the tensor cores are far from their rate, and operands that a thread builds in
@@ -523,9 +523,9 @@ ep_expert_matvec_kernel(const ExpertArgs a) {
 // One token: every row is its expert's only one, so rows are items of their own and a layout of K (+1) rows needs no scan.  A
 // CTA packs the row for itself while its first weights are on their way, which saves the kernels above a launch and its
 // dependency.  Taken while one wave of CTAs covers the rows, with items of at most 8 steps or split ones (1 token, us against
-// the kernels above: top-8 of 128, 2048 -> 2 x 768 gated 6.7 against 8.2, 768 -> 2048 4.8 against 6.5; top-2 of 8, 14336 -> 4096
-// 27.4 against 31.6; 4096 -> 2 x 7168 gated 21.0 against 21.6, where KS = 2 just fits, and 4096 -> 2 x 14336, where it does not,
-// 36.5 against 30.8).
+// the kernels above: top-8 of 128, 2048 -> 2 x 768 gated 6.4 against 8.2, 768 -> 2048 4.3 against 6.7; top-2 of 8, 14336 -> 4096
+// 24.0 against 32.6; 4096 -> 2 x 7168 gated 18.7 against 22.1, where KS = 2 just fits, and 4096 -> 2 x 14336, where it does not,
+// 31.3 by both).
 constexpr int kRowThreads = 256, kRowCtas = 2;                      // per SM
 
 template <int ALIGN>
@@ -600,23 +600,23 @@ ep_expert_row_kernel(const ExpertArgs a, int one_wave) {
 
 // Up to 8 rows per expert: two steps of weights in 128 registers, 16 warps per SM, passes of 8 rows.  More: a pass serves 16
 // rows and 12 warps have 168 registers each, since spilled prefetches would be waited for.  8 experts, top-2, 4096 -> 2 x 2048
-// gated, with 4 / 6 / 8 / 10 rows per expert: 23 / 28 / 32 / 36 us with passes of 8 rows, 30 / 31 / 33 / 35 us with 16; 64
-// experts with 4 / 8: 105 / 156 against 119 / 161; 8 experts with 16 rows, 14336 -> 4096: 137 and 100 us.  Of the shapes for 16
+// gated, with 4 / 6 / 8 / 10 rows per expert: 23 / 28 / 33 / 37 us with passes of 8 rows, 31 / 32 / 34 / 36 us with 16; 64
+// experts with 4 / 8: 106 / 157 against 116 / 159; 8 experts with 16 rows, 14336 -> 4096: 141 and 102 us.  Of the shapes for 16
 // rows this one is best there: 10 % more with two CTAs of 6 warps, 18 % with 8 warps, 31 % with passes of 32 rows.
 using FewRows = Shape<2, 1, 256, 2, 8>;
 using MoreRows = Shape<2, 2, 384, 1, 8>;
 
 // Rows on 8-byte boundaries only need more registers for their scales.  16 tokens, 64 experts, top-4, 2064 -> 2 x 2048 gated /
-// 7184 -> the same: 58 / 164 us with FewRows, which spills, 54 / 156 us with this.  On 16-byte boundaries FewRows holds: 53 us
+// 7184 -> the same: 58 / 164 us with FewRows, which spills, 55 / 155 us with this.  On 16-byte boundaries FewRows holds: 53 us
 // at 2080, 60 with this.  (2048 takes 37 us: its rows fill whole steps of 256 k and one load brings each thread's 64 codes.)
 using FewUnaligned = Shape<2, 1, 384, 1, 8>;
 
 // KS: the split that ends soonest.  x is the number of items per CTA, and an item lasts its warps' steps and about one more to
 // begin and end it, a little longer where sums are joined.  Passes of 8 rows are bound by HBM, so CTAs that work alone on an SM
 // are faster, and the last drawn items end within about 0.6 of an item's time of x; passes of 16 rows are bound by their own
-// instructions and take whole rounds.  KS 1 / 2 / 4: 16 tokens, top-8 of 256, 7168 -> 2 x 2048 gated 274 / 265 / 277 us; 64
-// tokens, top-4 of 64, 4096 -> 2 x 2048 106 / 114 / 128; 4 tokens, top-8 of 128, 2048 -> 2 x 768 20 / 17 / 18; 64 tokens,
-// top-2 of 8, 14336 -> 4096 103 / 111 / 126.
+// instructions and take whole rounds.  KS 1 / 2 / 4: 16 tokens, top-8 of 256, 7168 -> 2 x 2048 gated 269 / 266 / 283 us; 64
+// tokens, top-4 of 64, 4096 -> 2 x 2048 106 / 117 / 132; 4 tokens, top-8 of 128, 2048 -> 2 x 768 20 / 17 / 18; 64 tokens,
+// top-2 of 8, 14336 -> 4096 102 / 112 / 131.
 template <typename S>
 int choose_split(const ExpertArgs &a, int steps, float chunks) {
     const int n_out = a.swiglu ? a.N / 2 : a.N, per_warp = S::MT * (a.swiglu ? 8 : 16);

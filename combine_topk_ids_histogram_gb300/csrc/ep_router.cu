@@ -6,8 +6,8 @@
 // of the lanes' largest keys bounds the K-th largest key from below; the few keys at or above it (about K + 2 for
 // independent scores) are gathered and ranked against one another.  Against K rounds of finding and
 // striking out the largest of all keys this takes half of the instructions, whose issue bounds the call: 32768 tokens of 256
-// fp32 sigmoid scores with a bias, top-8, take 15.0 us (32.6 with rounds) at 418 instructions per token, issue slots 79 % busy;
-// 16 tokens of 128 take 2.3 us.
+// fp32 sigmoid scores with a bias, top-8, take 15.2 us (32.6 with rounds) at 425 instructions per token, issue slots 74 % busy;
+// 16 tokens of 128 take 2.1 us.
 #include "ep_host.h"
 #include "ep_types.cuh"
 
