@@ -9,8 +9,8 @@
 // Statistics and sums are fp32.  The variance is summed over (x - mean) in a second pass over
 // registers, which also corrects the mean, so rows with a large mean lose nothing.  HBM is the floor of both passes: each row is
 // read once and written once.  4096 x 7168 bf16 forward: RMS 21.5 us, 0.82 of the measured copy bandwidth with the launch, layer
-// norm 28.5 us, 0.62 (the corrected mean is another pass over registers and a second sum);
-// 32768 x 7168 bf16 backward: 292 us, 0.72, where issue and the row sums at 14 warps per SM bound it; single rows: 1.9 us.
+// norm 28.1 us, 0.63 (the corrected mean is another pass over registers and a second sum);
+// 32768 x 7168 bf16 backward: 292 us, 0.72, where issue and the row sums at 14 warps per SM bound it; single rows: 2.0 us.
 //
 // Many rows: one CTA per SM whose threads form groups, a group holding 32 elements of a row per thread, and
 // looping over rows.  Rows arrive in a ring of shared-memory stages by asynchronous copies, so that the
@@ -254,11 +254,11 @@ template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("c
 // ---------------------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------------------
-// The mean that the first pass over a row gives is off by the rounding of its sum and of 1/H.  The second pass also sums
-// d = x - mean, whose own mean delta is what the first one missed: the mean and the variance are corrected by it, and d too
-// unless delta is below kMeanSlack standard deviations, a quarter of the last bit of a d of one standard deviation.  A constant
-// row has d = delta exactly, and so y = bias.
-constexpr float kMeanSlack = 0x1p-26f;
+// The mean that the first pass over a row gives is off by the rounding of its sum.  The second pass also sums d = x - mean,
+// whose own mean delta is what the first one missed, and the roundings of the d's, up to 2^-24 of their mean magnitude (all
+// to one side where x has few digits).  The variance is corrected by it; the mean and d are too where delta is more than those
+// can be, twice that of the root mean square of d.  A constant row has d = delta exactly, and so y = bias.
+__device__ __forceinline__ bool mean_missed(float delta, float mean_square) { return delta * delta > 0x1p-46f * mean_square; }
 
 // The variance about the corrected mean from the mean square about the first one; NaN stays NaN.
 __device__ __forceinline__ float centred_var(float mean_square, float delta) {
@@ -318,7 +318,7 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
 #pragma unroll
             for (int i = 0; i < U::N; ++i) s = un.add(s, i, d[i]);
             const float2 p = f2_get(s);
-            mean = group_sum(p.x + p.y, red0, G, ty) * inv_h;
+            mean = group_sum(p.x + p.y, red0, G, ty) / h;
             const f32x2 neg = f2(-mean, -mean);
 #pragma unroll
             for (int i = 0; i < U::N; ++i)
@@ -337,16 +337,17 @@ ep_norm_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__ w, 
             for (int i = 0; i < U::N; ++i) s = un.add(s, i, d[i]);
             const float2 r = f2_get(s), t = group_sum2(f2(r.x + r.y, p.x + p.y), red2, G, ty);
             float delta = t.x * inv_h;
-            rstd = __frsqrt_rn(centred_var(t.y / h, delta) + eps);
-            if (fabsf(delta) * rstd > kMeanSlack) {
+            const float mean_square = t.y / h;
+            rstd = __frsqrt_rn(centred_var(mean_square, delta) + eps);
+            if (mean_missed(delta, mean_square)) {
                 delta = t.x / h;
                 const f32x2 neg = f2(-delta, -delta);
 #pragma unroll
                 for (int i = 0; i < U::N; ++i)
 #pragma unroll
                     for (int j = 0; j < U::E / 2; ++j) d[i][j] = f2_add(d[i][j], neg);
+                mean += delta;
             }
-            mean += delta;
         }
         if (tid == 0) {
             if (!rms) mean_out[row] = mean;
@@ -414,7 +415,7 @@ ep_norm_row_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) s += d[i][j];
-        mean = group_sum(s, s_red, G, 0) * inv_h;
+        mean = group_sum(s, s_red, G, 0) / h;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -434,8 +435,9 @@ ep_norm_row_kernel(const T *__restrict__ x, long long ldx, const W *__restrict__
     } else {
         const float2 t = group_sum2(f2(sd, q), s_red2, G, 0);
         delta = t.x * inv_h;
-        rstd = __frsqrt_rn(centred_var(t.y / h, delta) + eps);
-        if (fabsf(delta) * rstd > kMeanSlack) delta = t.x / h;
+        const float mean_square = t.y / h;
+        rstd = __frsqrt_rn(centred_var(mean_square, delta) + eps);
+        delta = mean_missed(delta, mean_square) ? t.x / h : 0.0f;
         mean += delta;
     }
     if (tid == 0) {

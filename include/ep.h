@@ -418,7 +418,7 @@ typedef enum { EP_BF16 = 0, EP_F16 = 1, EP_F32 = 2 } ep_dtype_t;
  *      pass takes;
  *   -> y    [T*H] dtype, dense (e) = (x - mean) * rstd * weight + bias.
  * All arithmetic is fp32, rounded once into y; the variance is summed over x - mean, which also
- * corrects the mean, so a constant row gives y = bias, to 2^-26 of weight (eps > 0).  eps >= 0; with
+ * corrects the mean, so a constant row gives y = bias (eps > 0).  eps >= 0; with
  * eps = 0 a row of variance 0 has no defined result.  A NaN in a row makes that row NaN and no other, and so does an infinity
  * when rms is 0.  With rms 1 an infinity makes its row's rstd 0, so that infinite elements give NaN and finite
  * ones 0 (or bias).  A sum of squares beyond fp32 counts as infinite.

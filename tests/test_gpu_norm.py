@@ -410,3 +410,19 @@ def test_gradient_of_a_row_of_equal_gradients_is_zero(T, H, dt):
     rstd = torch.full((T,), 0.125, device="cuda")                       # a * xh: whole eighths, exact in any order
     dx, _, _ = ep.layer_norm_bwd(gy, x, w, torch.zeros(T, device="cuda"), rstd)
     assert (dx == 0).all()
+
+
+@pytest.mark.parametrize("T,H", [(1, 2048), (3, 7168), (1500, 7168), (9801, 256), (2000, 1111)])
+def test_mean_near_zero_keeps_its_digits(T, H):
+    """Values that are whole sixteenths below 8: their sum is exact in fp32 in any order, so that the mean is its H-th part, rounded
+    once, however near 0 it is."""
+    import combine_topk_ids_histogram_gb300 as ep
+    g = torch.Generator().manual_seed(T)
+    half = torch.randint(-127, 128, (T, H // 2), generator=g)
+    x = torch.cat([half, -half, torch.zeros(T, H % 2, dtype=half.dtype)], 1)
+    x[:, 0] += torch.arange(T) % 3 - 1                                  # the sum is -1, 0 or 1 sixteenth
+    x = (x.clamp(-127, 127).double() / 16)
+    w = torch.ones(H, device="cuda").bfloat16()
+    _, mean, _ = ep.layer_norm(x.bfloat16().cuda(), w)
+    want = x.sum(1) / H
+    assert torch.equal(mean.cpu(), want.float())
