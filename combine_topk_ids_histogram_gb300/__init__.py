@@ -10,7 +10,7 @@ Entry points (same names as the C ABI, without the ``ep_`` prefix):
 ``dispatch_layout_nvfp4``, ``dispatch_layout_padded_nvfp4``, ``dispatch_bf16``, ``dispatch_fp8``, ``combine``, ``combine_bwd``,
 ``dispatch_bwd``, ``routing_map_to_topk``, ``indices_to_multihot``, ``rows_max``,
 ``read_status``, ``cvt_e2m1``, ``cvt_e4m3``; around the dispatch: ``layer_norm``, ``layer_norm_bwd``,
-``router_topk``, ``router_topk_bwd`` and ``expert_matvec``.
+``router_topk``, ``router_topk_bwd``, ``expert_matvec``, ``expert_linear`` and ``expert_linear_bwd``.
 """
 from __future__ import annotations
 
@@ -32,10 +32,12 @@ EP_ERR_BAD_EXPERT = 3
 EP_ERR_CUDA = 5
 EP_ERR_TOO_LARGE = 6
 EP_ERR_BOUNDS = 7
+EP_ERR_TIMEOUT = 8
 NOALLOC_WORKSPACE_BYTES = 1 << 20
 STATUS_OVERFLOW = 1
 STATUS_BAD_EXPERT = 2
 STATUS_BOUNDS = 8
+STATUS_TIMEOUT = 16
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # ep_dtype_t
 SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -96,6 +98,8 @@ SIGNATURES = {
     "ep_router_topk_bwd": (_I, [_P, _P, _LL, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P]),
     "ep_expert_matvec_workspace_bytes": (_Z, [_LP, _I]),
     "ep_expert_matvec": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _LP, _P, _P, _Z, _P]),
+    "ep_expert_linear": (_I, [_P, _LL, _P, _I, _I, _I, _I, _LP, _P, _P, _P]),
+    "ep_expert_linear_bwd": (_I, [_P, _LL, _P, _LL, _P, _I, _I, _I, _P, _LP, _P, _P, _I, _I, _P]),
     "ep_read_status": (_I, [_LP, _P, ctypes.POINTER(ctypes.c_int32)]),
     "ep_strerror": (ctypes.c_char_p, [_I]),
     "ep_cvt_e2m1": (_I, [_P, _P, _L, _P]),
@@ -773,6 +777,93 @@ def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ro
             _free(pw)
     _check(rc, "ep_expert_matvec")
     return out
+
+
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _layout_rows(t: torch.Tensor, L: Layout, cols: int, dtype, what: str):
+    """Pointer and row stride of a 2-D tensor with a row for each row of the layout's buffers."""
+    p, rows, n, stride, _ = _matrix(t, what)
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if n != cols or rows < L.R_max:
+        raise ValueError(f"{what}: needs at least {L.R_max} rows of {cols}, got {tuple(t.shape)}")
+    return p, stride
+
+
+def _out_rows(t: torch.Tensor, L: Layout, cols: int, dtype, what: str) -> int:
+    """Pointer of a contiguous tensor of at least the layout's rows."""
+    if t.dim() != 2 or t.shape[0] < L.R_max:
+        raise ValueError(f"{what}: needs at least {L.R_max} rows of {cols}, got {tuple(t.shape)}")
+    return _buffer(t, (t.shape[0], cols), (dtype,), what)
+
+
+def _weights(w: torch.Tensor, L: Layout):
+    if w.dim() != 3:
+        raise ValueError(f"w: expected [{L.G}, N, K], got {tuple(w.shape)}")
+    return _buffer(w, (L.G, w.shape[1], w.shape[2]), _HALF, "w")
+
+
+def expert_linear(x: torch.Tensor, w: torch.Tensor, L: Layout, swiglu: bool = False, save: bool = False, out=None, stream=None):
+    """ep_expert_linear: each row of the layout times its group's weights, for any number of rows.  x [R_max, K] in row
+    order (what ``dispatch_bf16`` returns; rows may have a stride, a multiple of 8), w [G, N, K], both bf16 or both fp16 ->
+    out [R_max, N].  With ``swiglu`` w holds N/2 gate rows, then N/2 up rows, and out [R_max, N/2] is silu(gate) * up; with
+    ``save`` too the call returns (out, gate_up [R_max, N]) for ``expert_linear_bwd``.  ``out``: the buffer, or both."""
+    pw = _weights(w, L)
+    G, N, K = w.shape
+    px, ld = _layout_rows(x, L, K, w.dtype, "x")
+    if save and not swiglu:
+        raise ValueError("save keeps the gate and up values of swiglu")
+    n_out = N // 2 if swiglu else N
+    if out is None:
+        new = lambda n: torch.empty(max(L.R_max, 1), n, dtype=w.dtype, device=x.device)
+        out = (new(n_out), new(N)) if save else new(n_out)
+    y, gu = out if save else (out, None)
+    rc = _lib.ep_expert_linear(px, ld, pw, K, N, DTYPES[w.dtype], 1 if swiglu else 0, L.ref, _out_rows(y, L, n_out, w.dtype, "out"),
+                               _out_rows(gu, L, N, w.dtype, "gate_up") if save else None, _stream(stream))
+    _check(rc, "ep_expert_linear")
+    return out
+
+
+def expert_linear_bwd(grad: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor, L: Layout, gate_up: torch.Tensor | None = None,
+                      need=(True, True), grad_w_dtype=None, accumulate: bool = False, out=None, stream=None):
+    """ep_expert_linear_bwd -> (grad_x [R_max, K], grad_w [G, N, K]) of ``expert_linear(x, w, L)`` from grad [R_max, N].
+    With ``gate_up`` [R_max, 2K], saved by the ``swiglu`` call that made x, the first is the gradient of gate_up [R_max, 2K]
+    instead, which is ``grad`` for that call's weights.  ``need``: which of the two to compute (None for the other).
+    grad_w is in w's dtype or ``grad_w_dtype`` = torch.float32, and with ``accumulate`` (fp32, with ``out``) it is added to what
+    is there.  ``out``: the two buffers."""
+    pw = _weights(w, L)
+    G, N, K = w.shape
+    pg, ldg = _layout_rows(grad, L, N, w.dtype, "grad")
+    need_x, need_w = need
+    gx, gw = out if out is not None else (None, None)
+    cols = K if gate_up is None else 2 * K
+    px = pgx = pgu = pgw = None
+    ldx, wdt = K, w.dtype
+    if need_x:
+        if gx is None:
+            gx = torch.empty(max(L.R_max, 1), cols, dtype=w.dtype, device=grad.device)
+        pgx = _out_rows(gx, L, cols, w.dtype, "grad_x")
+        pgu = None if gate_up is None else _out_rows(gate_up, L, cols, w.dtype, "gate_up")
+    elif gate_up is not None:
+        raise ValueError("gate_up is for the gradient of the rows")
+    if need_w:
+        if x is None:
+            raise ValueError("the gradient of the weights needs x")
+        px, ldx = _layout_rows(x, L, K, w.dtype, "x")
+        if gw is None:
+            if accumulate:
+                raise ValueError("accumulate adds to a buffer: pass out=")
+            gw = torch.empty(G, N, K, dtype=grad_w_dtype or w.dtype, device=grad.device)
+        wdt = gw.dtype
+        if wdt not in (w.dtype, torch.float32) or (grad_w_dtype is not None and grad_w_dtype != wdt):
+            raise TypeError(f"grad_w: dtype {wdt}")
+        pgw = _buffer(gw, (G, N, K), (wdt,), "grad_w")
+    rc = _lib.ep_expert_linear_bwd(pg, ldg, px, ldx, pw, K, N, DTYPES[w.dtype], pgu, L.ref, pgx, pgw, DTYPES[wdt],
+                                   1 if accumulate else 0, _stream(stream))
+    _check(rc, "ep_expert_linear_bwd")
+    return gx if need_x else None, gw if need_w else None
 
 
 def read_status(L: Layout, stream=None) -> int:

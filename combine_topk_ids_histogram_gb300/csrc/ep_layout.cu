@@ -1046,6 +1046,7 @@ extern "C" int ep_read_status(const ep_layout_t *L, void *stream, int32_t *host_
     if (cudaStreamSynchronize(st) != cudaSuccess) return EP_ERR_CUDA;
     *host_status = v;
     if (v & EP_STATUS_BOUNDS) return EP_ERR_BOUNDS;
+    if (v & EP_STATUS_TIMEOUT) return EP_ERR_TIMEOUT;
     if (v & EP_STATUS_OVERFLOW) return EP_ERR_OVERFLOW;
     if (v & EP_STATUS_BAD_EXPERT) return EP_ERR_BAD_EXPERT;
     return EP_OK;
@@ -1063,6 +1064,7 @@ extern "C" const char *ep_strerror(int code) {
         case EP_ERR_TOO_LARGE: return "the sizes need more scratch than the fixed no-allocation array holds";
         case EP_ERR_BOUNDS:
             return "an index fell outside its buffer and the access was skipped (bounds-checked build)";
+        case EP_ERR_TIMEOUT: return "a wait between the warps of a kernel ran out";
         default: return "unknown error";
     }
 }

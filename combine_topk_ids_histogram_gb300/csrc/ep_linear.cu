@@ -1,0 +1,664 @@
+// ep_linear.cu -- grouped products of the rows of a dispatch layout with their group's 16-bit weights, optionally with the gated
+// activation silu(gate) * up, and their gradients.
+//
+//   forward     out[r, n] = sum over k of x[r, k] w[g, n, k]                 (gated: w holds F gate rows, then F up rows)
+//   grad_x      out[r, k] = sum over n of grad[r, n] w[g, n, k]              (or, through the gate, that of gate and up)
+//   grad_w      out[g, n, k] = sum over the rows r of g of grad[r, n] x[r, k]
+//
+// One persistent kernel, templated on the form.  The weights' rows (or columns) are M of the tensor cores' product and the layout's
+// rows are N, in steps of 32: a group of any number of rows then costs about what its rows cost, and weights, which have
+// hundreds of rows or more, fill M.  A pair of CTAs shares a product of 256 x 256: each loads 128 of M and half of N by TMA and
+// keeps the sums of its 128 of M in tensor memory, twice, so that one tile's results leave while the next one's
+// are added up.  Warp 0 loads, warp 1 of the first CTA issues the products, warps 4 to 7 take results out; warp 2 (grad_w)
+// clears the rows behind a group's last one in shared memory, since there they are summed over.
+#include <math.h>
+
+#include <algorithm>
+
+#include "ep_async.cuh"
+#include "ep_host.h"
+#include "ep_tensor.cuh"
+#include "ep_types.cuh"
+
+namespace ep {
+namespace {
+
+enum Form { kPlain, kGlu, kGradX, kGradGate, kGradW };
+
+constexpr int kThreads = 256;
+constexpr int kBlockK = 64;                  // of the summed dimension in a stage: 128 bytes, one swizzle row
+constexpr int kStages = 5;
+constexpr int kTileA = 128 * kBlockK * 2;    // bytes a CTA loads of each operand per stage
+constexpr int kTileB = 128 * kBlockK * 2;
+constexpr int kStageBytes = kTileA + kTileB;
+constexpr int kStaging = 32768;
+constexpr int kCols = 256;                   // columns of tensor memory per tile's sums
+constexpr int kMaxGroups = kMaxE + 1;
+// The tensor cores' sums in fp32 truncate, by up to 2^-23 of the sum per 16 products; an fp32 gradient leaves them every 2048 rows.
+constexpr int kChunkRows = 2048;
+
+struct Control {
+    uint64_t full[kStages], empty[kStages], landed[kStages];
+    uint64_t sums_full[2], sums_empty[2];
+    uint32_t tmem, skip;
+    int part[kThreads / 32];
+    int off[kMaxGroups + 1];                 // first row of each group
+    int start[kMaxGroups + 1];               // first tile of each group
+};
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kStaging + sizeof(Control);
+static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+
+struct LinearArgs {
+    const int32_t *row_offsets;
+    int32_t *status;
+    int G, R_max;
+    int M;                                   // of the output: features of a row (gated: F), rows of a weight gradient
+    int sum;                                 // length of the sums (forms that sum over rows: columns of the output)
+    int f16, wide, add;                      // operands fp16; grad_w: fp32 output, added to what is there
+    uint16_t *out, *gate_up;                 // gate_up: saved by kGlu, read by kGradGate
+};
+
+// A tile: rows or features, and what is summed over.
+struct Work {
+    int g, m, row, n;                        // group; first of M of the pair; first row; valid of N
+    int col;                                 // grad_w: first column
+    int kb, last;                            // blocks of 64 to sum over, and the valid of the last
+    bool first;                              // grad_w: not a later chunk of the same tile
+};
+
+// The tiles of a CTA pair in turn.  Every role walks them for itself.
+template <int FORM, int CG> struct Walk {
+    static constexpr int kM = FORM == kGlu ? 64 * CG : 128 * CG, kN = 128 * CG;
+    static constexpr int kUnit = 16 * CG;    // of N in a product
+    const LinearArgs &a;
+    const Control &c;
+    int tile, step, tiles, m_tiles, g, chunk;
+
+    __device__ Walk(const LinearArgs &a_, const Control &c_, int first, int step_)
+        : a(a_), c(c_), tile(first - step_), step(step_), m_tiles((a_.M + kM - 1) / kM), g(0), chunk(0) {
+        tiles = FORM == kGradW ? a.G * m_tiles * ((a.sum + kN - 1) / kN) : c.start[a.G];
+    }
+    __device__ bool next(Work &w) {
+        if constexpr (FORM == kGradW) {
+            const int rows = tile < 0 ? 0 : c.off[w.g + 1] - c.off[w.g];
+            if (a.wide && tile >= 0 && (chunk + 1) * kChunkRows < rows) {
+                ++chunk;
+            } else {
+                chunk = 0;
+                tile += step;
+                if (tile >= tiles) return false;
+                const int n_tiles = (a.sum + kN - 1) / kN, in = tile % (m_tiles * n_tiles);
+                w.g = tile / (m_tiles * n_tiles);
+                w.m = in % m_tiles * kM;
+                w.col = in / m_tiles * kN;
+                w.n = min(kN, a.sum - w.col);
+            }
+            w.first = chunk == 0;
+            w.row = c.off[w.g] + chunk * kChunkRows;
+            int left = max(c.off[w.g + 1] - w.row, 0);
+            if (a.wide) left = min(left, kChunkRows);
+            w.kb = (left + kBlockK - 1) / kBlockK;
+            w.last = left - (w.kb - 1) * kBlockK;
+        } else {
+            tile += step;
+            if (tile >= tiles) return false;
+            int hi = a.G;                    // the last group that begins at or before the tile
+            while (hi - g > 1) {
+                const int mid = (g + hi) >> 1;
+                if (c.start[mid] <= tile) g = mid;
+                else hi = mid;
+            }
+            const int rows = c.off[g + 1] - c.off[g], parts = (rows + kN - 1) / kN, in = tile - c.start[g];
+            // the group's rows in equal parts: a part of few rows would load the weights for little work
+            const int part = ((rows + parts - 1) / parts + kUnit - 1) / kUnit * kUnit, at = in % parts * part;
+            w.g = g;
+            w.m = in / parts * kM;
+            w.row = c.off[g] + at;
+            w.n = min(part, rows - at);
+            w.kb = (a.sum + kBlockK - 1) / kBlockK;
+            w.last = a.sum - (w.kb - 1) * kBlockK;
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int f16) {
+    return f16 ? f32_to_word(lo, hi, __half()) : f32_to_word(lo, hi, __nv_bfloat16());
+}
+__device__ __forceinline__ float wide16(uint16_t v, int f16) {
+    return f16 ? __half2float(__ushort_as_half(v)) : __uint_as_float((uint32_t)v << 16);
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+// And whether `v` holds for all of them.
+__device__ __forceinline__ bool bar_all(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(id), "r"(threads), "r"((uint32_t)v) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void cp_async16(void *smem, const void *gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+
+// s = 1 / (1 + exp(-v)): the fast exponential and division are off by under 2^-16 of s, a hundredth of the outputs' rounding.
+__device__ __forceinline__ float sigmoid_fast(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+template <int FORM, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ CUtensorMap map_out, const LinearArgs a) {
+    constexpr bool kAmn = FORM == kGradX || FORM == kGradGate || FORM == kGradW, kBmn = FORM == kGradW;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *const smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    uint8_t *const staging = smem + kStages * kStageBytes;
+    Control &c = *reinterpret_cast<Control *>(staging + kStaging);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const int pair = blockIdx.x / CG, pairs = gridDim.x / CG;
+
+    if (CG == 2) cluster_arrive();
+    if (tid == 0) {
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&c.full[s]), CG);         // each CTA's loader (or its clearing warp)
+            mbar_init(smem_u32(&c.empty[s]), 1);
+            mbar_init(smem_u32(&c.landed[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&c.sums_full[b]), 1);
+            mbar_init(smem_u32(&c.sums_empty[b]), 4 * CG);
+        }
+        mbar_init_done();
+    }
+    if (warp == 2) tmem_alloc<CG>(smem_u32(&c.tmem), 2 * kCols);
+    pdl_begin();
+    // Groups' rows, kept inside the buffers whatever the layout says, and a running count of their tiles.
+    constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
+    const int per = (a.G + kThreads - 1) / kThreads, g0 = tid * per;
+    int mine[kPer], sum = 0;
+    for (int i = tid; i <= a.G; i += kThreads) {
+        const int v = a.row_offsets[i];
+        if (v < 0 || v > a.R_max) bounds_fail(a.status);
+        c.off[i] = min(max(v, 0), a.R_max);
+    }
+    if (CG == 2) cluster_wait();                         // the other CTA has begun
+    if (tid == 0 && rank == 0) {                         // the pair acts on one reading of the status
+        const uint32_t st = (uint32_t)load_status(a.status);
+        c.skip = st;
+        if (CG == 2) st_cluster(at_rank(smem_u32(&c.skip), 1), st);
+    }
+    __syncthreads();
+    if (FORM != kGradW) {
+        const int m_tiles = (a.M + Walk<FORM, CG>::kM - 1) / Walk<FORM, CG>::kM;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            mine[i] = 0;
+            if (i < per && g0 + i < a.G)
+                mine[i] = (max(c.off[g0 + i + 1] - c.off[g0 + i], 0) + 128 * CG - 1) / (128 * CG) * m_tiles;
+            sum += mine[i];
+        }
+        int run = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(kFullMask, run, o);
+            if (lane >= o) run += up;
+        }
+        if (lane == 31) c.part[warp] = run;
+        __syncthreads();
+        run -= sum;
+        for (int w = 0; w < warp; ++w) run += c.part[w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (i < per && g0 + i < a.G) c.start[g0 + i] = run;
+            run += mine[i];
+        }
+        if (tid == kThreads - 1) c.start[a.G] = run;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = c.tmem;
+    bool ok = true;                                      // false: a wait ran out
+    if (c.skip == 0) {
+        Walk<FORM, CG> walk(a, c, pair, pairs);
+        Work w = {};
+        if (warp == 0) {                                 // ------------------------------------------------ loads
+            if (lane == 0) {
+                int s = 0, used = 0;
+                uint32_t round = 0;
+                while (ok && walk.next(w)) {
+                    const int half = (w.n + Walk<FORM, CG>::kUnit - 1) / Walk<FORM, CG>::kUnit * 16, boxes = (half + 31) >> 5;
+                    const int m = w.m + (int)rank * (Walk<FORM, CG>::kM / CG), n = (FORM == kGradW ? w.col : w.row) + (int)rank * half;
+                    const uint32_t bytes = kTileA + (FORM == kGradW ? kTileB : boxes * 4096);
+                    for (int b = 0; b < w.kb; ++b) {
+                        if (used == kStages && !(ok = mbar_wait(smem_u32(&c.empty[s]), (round & 1) ^ 1))) break;
+                        const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kTileA;
+                        // a block that ends inside 16 rows lands here first and is cleared behind its end
+                        const bool clear = FORM == kGradW && b == w.kb - 1 && (w.last & 15) != 0;
+                        const uint32_t bar = clear ? smem_u32(&c.landed[s]) : at_rank(smem_u32(&c.full[s]), 0);
+                        mbar_arrive_expect(clear ? at_rank(bar, rank) : bar, bytes);
+                        const int k = b * kBlockK;
+                        if constexpr (FORM == kGradW) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                tma_load_2d<CG>(sa + i * 8192, &map_a, m + 64 * i, w.row + k, bar);
+                                tma_load_2d<CG>(sb + i * 8192, &map_b, n + 64 * i, w.row + k, bar);
+                            }
+                        } else {
+                            if constexpr (FORM == kGlu) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    tma_load_3d<CG>(sa + i * 4096, &map_a, k, (i & 1) * a.M + m + (i >> 1) * 32, w.g, bar);
+                            } else if constexpr (FORM == kPlain) {
+                                tma_load_3d<CG>(sa, &map_a, k, m, w.g, bar);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) tma_load_3d<CG>(sa + i * 8192, &map_a, m + 64 * i, k, w.g, bar);
+                            }
+                            for (int i = 0; i < boxes; ++i) tma_load_2d<CG>(sb + i * 4096, &map_b, k, n + 32 * i, bar);
+                        }
+                        if (++s == kStages) s = 0, ++round;
+                        used = min(used + 1, kStages);
+                    }
+                }
+                // Nothing of the pair may still be on its way to this CTA when it ends.
+                for (int i = 0; ok && i < used; ++i) {
+                    s = s == 0 ? kStages - 1 : s - 1;
+                    if (s == kStages - 1) --round;
+                    ok = mbar_wait(smem_u32(&c.empty[s]), round & 1);
+                }
+                if (!ok) {
+                    const unsigned long long t = global_ns();
+                    while (global_ns() - t < 1000000ull) {}
+                }
+            }
+        } else if (warp == 1) {                          // ------------------------------------------------ products
+            if (lane == 0 && rank == 0) {
+                int s = 0, buf = 0;
+                uint32_t round = 0, tiles = 0;
+                const uint32_t idesc = mma_desc(a.f16 != 0, 128 * CG, 0, kAmn, kBmn);
+                while (ok && walk.next(w)) {
+                    if (w.kb == 0) continue;
+                    if (!(ok = mbar_wait(smem_u32(&c.sums_empty[buf]), ((tiles >> 1) & 1) ^ 1))) break;
+                    tc_fence_after();
+                    const uint32_t id = idesc | (uint32_t)((w.n + Walk<FORM, CG>::kUnit - 1) / Walk<FORM, CG>::kUnit * CG) << 18;
+                    const uint32_t d = tmem + buf * kCols;
+                    for (int b = 0; b < w.kb; ++b) {
+                        if (!(ok = mbar_wait(smem_u32(&c.full[s]), round & 1))) break;
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + s * kStageBytes);
+                        const uint64_t da = smem_desc(sa, 8192), db = smem_desc(sa + kTileA, 8192);
+                        const int steps = b == w.kb - 1 ? (w.last + 15) >> 4 : kBlockK / 16;
+                        for (int i = 0; i < steps; ++i)
+                            tc_mma<CG>(d, da + i * (kAmn ? 128 : 2), db + i * (kBmn ? 128 : 2), id, b > 0 || i > 0);
+                        tc_commit<CG>(smem_u32(&c.empty[s]));
+                        if (++s == kStages) s = 0, ++round;
+                    }
+                    if (!ok) break;
+                    tc_commit<CG>(smem_u32(&c.sums_full[buf]));
+                    buf ^= 1;
+                    ++tiles;
+                }
+            }
+        } else if (warp == 2) {                          // ------------------------------------------------ rows to clear
+            if constexpr (FORM == kGradW) {
+                int s = 0;
+                uint32_t seen = 0;                       // parity of landed[s]
+                while (ok && walk.next(w)) {
+                    s = (s + max(w.kb - 1, 0)) % kStages;
+                    if (w.kb == 0) continue;
+                    if (w.last & 15) {
+                        if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.landed[s]), seen >> s & 1)))) break;
+                        seen ^= 1u << s;
+                        // rows last to the next multiple of 16, of two blocks of 64 columns of each operand
+                        uint8_t *const st = smem + s * kStageBytes + w.last * 128;
+                        const int rows = 16 - (w.last & 15);
+                        for (int i = lane; i < 4 * rows * 8; i += 32)
+                            *reinterpret_cast<uint4 *>(st + i / (rows * 8) * 8192 + i % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(at_rank(smem_u32(&c.full[s]), 0));
+                    }
+                    if (++s == kStages) s = 0;
+                }
+            }
+        } else if (warp >= 4) {                          // ------------------------------------------------ results
+            const int q = warp - 4, et = tid - 128;
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+            int buf = 0;
+            uint32_t tiles = 0;
+            uint16_t *const st16 = reinterpret_cast<uint16_t *>(staging);
+            while (ok && walk.next(w)) {
+                const int m0 = w.m + (int)rank * (Walk<FORM, CG>::kM / CG);          // first feature of this CTA
+                const uint32_t sums = lanes + buf * kCols;
+                const int chunks = (w.n + 31) >> 5;
+                if constexpr (FORM == kGradW) {
+                    if (w.kb > 0) {
+                        if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_full[buf]), (tiles >> 1) & 1)))) break;
+                        tc_fence_after();
+                    }
+                    // 32 rows of 128 bytes per warp at a time: 32 columns of fp32 or 64 of 16 bits, swizzled as TMA reads them
+                    const int cols = a.wide ? 32 : 64;
+                    int at = 0;
+                    if (!w.first && lane == 0) bulk_wait_all();      // the chunk before, added up
+                    for (int col = 0; col < w.n; col += cols, at ^= 1) {
+                        uint8_t *const line = staging + (q * 2 + at) * 4096 + lane * 128;
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        __syncwarp();
+                        float v[32] = {};
+                        if (a.wide) {
+                            if (w.kb > 0) {
+                                tmem_ld32(sums + col, v);
+                                tmem_wait_ld();
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<float4 *>(line + ((i ^ (lane & 7)) << 4)) =
+                                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (w.kb > 0) {
+                                    tmem_ld32(sums + col + 32 * h, v);
+                                    tmem_wait_ld();
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    *reinterpret_cast<uint4 *>(line + (((4 * h + i) ^ (lane & 7)) << 4)) =
+                                        make_uint4(pack16(v[8 * i], v[8 * i + 1], a.f16), pack16(v[8 * i + 2], v[8 * i + 3], a.f16),
+                                                   pack16(v[8 * i + 4], v[8 * i + 5], a.f16), pack16(v[8 * i + 6], v[8 * i + 7], a.f16));
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && m0 + q * 32 < a.M) {
+                            const uint32_t src = smem_u32(staging + (q * 2 + at) * 4096);
+                            if (a.wide && (a.add || !w.first)) tma_add_3d(&map_out, src, w.col + col, m0 + q * 32, w.g);
+                            else tma_store_3d(&map_out, src, w.col + col, m0 + q * 32, w.g);
+                        }
+                        if (lane == 0) bulk_commit();
+                    }
+                    if (w.kb == 0) continue;
+                } else {
+                    const int F = a.M;
+                    auto prefetch = [&](int ch) {        // the saved gate and up of 32 rows
+                        for (int i = et; i < 512; i += 128) {
+                            const int t = ch * 32 + (i >> 4), f = m0 + (i & 15) * 8;
+                            if (t < w.n && f < F) {
+                                const uint16_t *src = a.gate_up + (size_t)(w.row + t) * 2 * F + f;
+                                cp_async16(st16 + (ch & 1) * 8192 + i * 8, src);
+                                cp_async16(st16 + (ch & 1) * 8192 + 4096 + i * 8, src + F);
+                            }
+                        }
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                    };
+                    bar_sync(1, 128);                    // the last tile has left the staging buffers
+                    if constexpr (FORM == kGradGate) prefetch(0);
+                    if (!(ok = bar_all(1, 128, mbar_wait(smem_u32(&c.sums_full[buf]), (tiles >> 1) & 1)))) break;
+                    tc_fence_after();
+                    for (int ch = 0; ch < chunks; ++ch) {
+                        float v[32];
+                        tmem_ld32(sums + ch * 32, v);
+                        tmem_wait_ld();
+                        const size_t row0 = (size_t)w.row + ch * 32;
+                        const int rows = min(32, w.n - ch * 32);
+                        if constexpr (FORM == kPlain || FORM == kGradX) {
+                            uint16_t *const st = st16 + (ch & 1) * 4096;
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                const uint32_t p = pack16(v[j], v[j + 1], a.f16);
+                                st[j * 128 + et] = (uint16_t)p;
+                                st[(j + 1) * 128 + et] = (uint16_t)(p >> 16);
+                            }
+                            bar_sync(1, 128);
+                            for (int i = et; i < rows * 16; i += 128) {
+                                const int f = m0 + (i & 15) * 8;
+                                if (f < F) *reinterpret_cast<uint4 *>(a.out + (row0 + (i >> 4)) * F + f) = *reinterpret_cast<const uint4 *>(st + i * 8);
+                            }
+                        } else if constexpr (FORM == kGradGate) {
+                            asm volatile("cp.async.wait_group 0;" ::: "memory");
+                            bar_sync(1, 128);            // everyone's pieces of this chunk; the other buffer is free
+                            if (ch + 1 < chunks) prefetch(ch + 1);
+                            uint16_t *const st = st16 + (ch & 1) * 8192;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float gate = wide16(st[j * 128 + et], a.f16), up = wide16(st[4096 + j * 128 + et], a.f16);
+                                const float s = sigmoid_fast(gate), ds = v[j] * s;
+                                const uint32_t p = pack16(ds * up * (1.0f + gate * (1.0f - s)), ds * gate, a.f16);
+                                st[j * 128 + et] = (uint16_t)p;
+                                st[4096 + j * 128 + et] = (uint16_t)(p >> 16);
+                            }
+                            bar_sync(1, 128);
+                            for (int i = et; i < rows * 16; i += 128) {
+                                const int f = m0 + (i & 15) * 8;
+                                if (f < F) {
+                                    uint16_t *const dst = a.out + (row0 + (i >> 4)) * 2 * F + f;
+                                    *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(st + i * 8);
+                                    *reinterpret_cast<uint4 *>(dst + F) = *reinterpret_cast<const uint4 *>(st + 4096 + i * 8);
+                                }
+                            }
+                        } else {
+                            // Even warps hold gates, odd warps the ups of the same 32 features: each takes half of the rows.
+                            const int up = q & 1, f = (q >> 1) * 32 + lane;
+                            float *const swap = reinterpret_cast<float *>(staging);
+                            uint16_t *const act = st16 + 4096 + (ch & 1) * 2048, *const gu = st16 + 8192 + (ch & 1) * 4096;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) swap[(q * 16 + j) * 32 + lane] = up ? v[j] : v[16 + j];
+                            if (a.gate_up) {
+#pragma unroll
+                                for (int j = 0; j < 32; j += 2) {
+                                    const uint32_t p = pack16(v[j], v[j + 1], a.f16);
+                                    gu[j * 128 + up * 64 + f] = (uint16_t)p;
+                                    gu[(j + 1) * 128 + up * 64 + f] = (uint16_t)(p >> 16);
+                                }
+                            }
+                            bar_sync(2 + (q >> 1), 64);
+#pragma unroll
+                            for (int j = 0; j < 16; j += 2) {
+                                float y[2];
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const float other = swap[((q ^ 1) * 16 + j + i) * 32 + lane], own = up ? v[16 + j + i] : v[j + i];
+                                    const float gate = up ? other : own;
+                                    y[i] = gate * sigmoid_fast(gate) * (up ? own : other);
+                                }
+                                const uint32_t p = pack16(y[0], y[1], a.f16);
+                                act[(up * 16 + j) * 64 + f] = (uint16_t)p;
+                                act[(up * 16 + j + 1) * 64 + f] = (uint16_t)(p >> 16);
+                            }
+                            bar_sync(1, 128);
+                            for (int i = et; i < rows * 8; i += 128) {
+                                const int f8 = m0 + (i & 7) * 8;
+                                if (f8 < F) *reinterpret_cast<uint4 *>(a.out + (row0 + (i >> 3)) * F + f8) = *reinterpret_cast<const uint4 *>(act + i * 8);
+                            }
+                            if (a.gate_up) {
+                                for (int i = et; i < rows * 16; i += 128) {
+                                    const int f8 = m0 + (i & 7) * 8;
+                                    if (f8 < F) *reinterpret_cast<uint4 *>(a.gate_up + (row0 + (i >> 4)) * 2 * F + (i & 8 ? F : 0) + f8) =
+                                                    *reinterpret_cast<const uint4 *>(gu + i * 8);
+                                }
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(at_rank(smem_u32(&c.sums_empty[buf]), 0));
+                buf ^= 1;
+                ++tiles;
+            }
+            if (FORM == kGradW && lane == 0) bulk_wait_all();
+        }
+    }
+    if (!ok) atomicOr(a.status, EP_STATUS_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();
+    tc_fence_after();
+    if (warp == 2) tmem_free<CG>(tmem, 2 * kCols);
+}
+
+// ------------------------------------------------------------------------------------------------------------ host
+using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                            const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder() {
+    static const Encode fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<Encode>(p);
+    }();
+    return fn;
+}
+
+// A map over [d2][d1][d0] elements (d0 contiguous, rows `ld` elements apart) with boxes of [1][b1][b0], 128 bytes wide.
+bool encode(CUtensorMap *m, const void *p, int bytes, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t ld, uint32_t b0, uint32_t b1) {
+    const Encode fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {d0, d1, d2 ? d2 : 1}, strides[2] = {ld * bytes, ld * bytes * d1};
+    const cuuint32_t box[3] = {b0, b1, 1}, one[3] = {1, 1, 1};
+    return fn(m, bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, d2 ? 3 : 2, const_cast<void *>(p), dims,
+              strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTA groups of `kernel` that the device holds at once; cached per device.
+template <auto kernel, int CG> int resident_groups() {
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> cached[kMaxDev];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const bool cacheable = dev >= 0 && dev < kMaxDev;
+    if (cacheable && (n = cached[dev].load(std::memory_order_relaxed)) > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CG);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
+    if (cacheable) cached[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <int FORM, int CG>
+int launch_form(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const LinearArgs &a, cudaStream_t st) {
+    constexpr auto kern = ep_linear_kernel<FORM, CG>;
+    const int rc = allow_smem<kern>(kSmem);
+    if (rc != EP_OK) return rc;
+    const int groups = resident_groups<kern, CG>();
+    if (groups <= 0) return EP_ERR_CUDA;
+    constexpr int kM = Walk<FORM, CG>::kM, kN = Walk<FORM, CG>::kN;
+    const long long m_tiles = (a.M + kM - 1) / kM;
+    const long long tiles = m_tiles * (FORM == kGradW ? (long long)a.G * ((a.sum + kN - 1) / kN) : (long long)a.R_max / kN + std::min(a.G, a.R_max));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::max(1ll, std::min<long long>(groups, tiles)) * CG);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return launch_result(cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, a));
+}
+
+// Sizes and pointers common to both calls.
+bool linear_ok(const ep_layout_t *L, int K, int N, int dtype) {
+    return layout_ok(L) && hidden_ok(K) && N >= 16 && N <= kMaxN && N % 16 == 0 && (dtype == EP_BF16 || dtype == EP_F16);
+}
+bool stride_ok(long long ld, int cols) { return ld >= cols && ld % 8 == 0 && ld < (1ll << 31); }
+
+LinearArgs linear_args(const ep_layout_t *L, int dtype) {
+    LinearArgs a = {};
+    a.row_offsets = L->row_offsets;
+    a.status = L->status;
+    a.G = L->E + L->fused_shared;
+    a.R_max = layout_rows(L);
+    a.f16 = dtype == EP_F16;
+    return a;
+}
+
+}  // namespace
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_expert_linear(const void *x, long long x_stride, const void *w, int in_features, int out_rows, int dtype, int swiglu,
+                                const ep_layout_t *L, void *out, void *gate_up, void *stream) {
+    EP_NVTX_RANGE("ep_expert_linear");
+    const int K = in_features, N = out_rows;
+    if (!linear_ok(L, K, N, dtype) || !stride_ok(x_stride, K) || (swiglu != 0 && swiglu != 1)) return EP_ERR_INVALID_ARG;
+    if (swiglu ? N % 32 != 0 : gate_up != nullptr) return EP_ERR_INVALID_ARG;
+    for (const void *p : {x, w, (const void *)out, (const void *)gate_up})
+        if (!aligned16(p)) return EP_ERR_INVALID_ARG;
+    if (L->T == 0) return EP_OK;
+    if (!x || !w || !out) return EP_ERR_INVALID_ARG;
+    LinearArgs a = linear_args(L, dtype);
+    a.M = swiglu ? N / 2 : N;
+    a.sum = K;
+    a.out = (uint16_t *)out;
+    a.gate_up = (uint16_t *)gate_up;
+    CUtensorMap ma, mb;
+    if (!encode(&ma, w, 2, K, N, a.G, K, kBlockK, swiglu ? 32 : 128) || !encode(&mb, x, 2, K, a.R_max, 0, x_stride, kBlockK, 32))
+        return EP_ERR_CUDA;
+    cudaStream_t st = as_stream(stream);
+    return swiglu ? launch_form<kGlu, 2>(ma, mb, mb, a, st) : launch_form<kPlain, 2>(ma, mb, mb, a, st);
+}
+
+extern "C" int ep_expert_linear_bwd(const void *grad, long long grad_stride, const void *x, long long x_stride, const void *w,
+                                    int in_features, int out_rows, int dtype, const void *gate_up, const ep_layout_t *L, void *grad_x,
+                                    void *grad_w, int grad_w_dtype, int accumulate, void *stream) {
+    EP_NVTX_RANGE("ep_expert_linear_bwd");
+    const int K = in_features, N = out_rows;
+    if (!linear_ok(L, K, N, dtype) || !stride_ok(grad_stride, N) || (!grad_x && !grad_w)) return EP_ERR_INVALID_ARG;
+    if (gate_up && !grad_x) return EP_ERR_INVALID_ARG;
+    if (grad_w) {
+        if (!stride_ok(x_stride, K) || (accumulate != 0 && accumulate != 1)) return EP_ERR_INVALID_ARG;
+        if (grad_w_dtype != dtype && grad_w_dtype != EP_F32) return EP_ERR_INVALID_ARG;
+        if (accumulate && grad_w_dtype != EP_F32) return EP_ERR_INVALID_ARG;
+    }
+    for (const void *p : {grad, x, w, gate_up, (const void *)grad_x, (const void *)grad_w})
+        if (!aligned16(p)) return EP_ERR_INVALID_ARG;
+    if (L->T > 0 && (!grad || (grad_x && !w) || (grad_w && !x))) return EP_ERR_INVALID_ARG;
+    LinearArgs a = linear_args(L, dtype);
+    cudaStream_t st = as_stream(stream);
+    CUtensorMap ma, mb, mo;
+    if (grad_x && L->T > 0) {
+        a.M = K;
+        a.sum = N;
+        a.out = (uint16_t *)grad_x;
+        a.gate_up = (uint16_t *)const_cast<void *>(gate_up);
+        if (!encode(&ma, w, 2, K, N, a.G, K, 64, kBlockK) || !encode(&mb, grad, 2, N, a.R_max, 0, grad_stride, kBlockK, 32))
+            return EP_ERR_CUDA;
+        const int rc = gate_up ? launch_form<kGradGate, 2>(ma, mb, mb, a, st) : launch_form<kGradX, 2>(ma, mb, mb, a, st);
+        if (rc != EP_OK) return rc;
+    }
+    if (!grad_w) return EP_OK;
+    a.M = N;
+    a.sum = K;
+    a.wide = grad_w_dtype == EP_F32;
+    a.add = accumulate;
+    // without a token there is nothing to load, and the maps only need a valid address
+    const bool none = L->T == 0;
+    const uint64_t rows = none ? 1 : a.R_max;
+    if (!encode(&ma, none ? grad_w : grad, 2, N, rows, 0, none ? N : grad_stride, 64, kBlockK) ||
+        !encode(&mb, none ? grad_w : x, 2, K, rows, 0, none ? K : x_stride, 64, kBlockK) ||
+        !encode(&mo, grad_w, a.wide ? 4 : 2, K, N, a.G, K, a.wide ? 32 : 64, 32))
+        return EP_ERR_CUDA;
+    return launch_form<kGradW, 2>(ma, mb, mo, a, st);
+}

@@ -59,8 +59,9 @@ typedef enum {
     EP_ERR_CUDA = 5,          /* a CUDA call failed (launch error, or the sync in read_status) */
     EP_ERR_TOO_LARGE = 6,     /* ep_dispatch_layout_noalloc: the sizes need more scratch than
                                  its fixed array holds (EP_NOALLOC_WORKSPACE_BYTES)            */
-    EP_ERR_BOUNDS = 7         /* ep_read_status, bounds-checked build only: an index fell
+    EP_ERR_BOUNDS = 7,        /* ep_read_status, bounds-checked build only: an index fell
                                  outside its buffer and the access was skipped                */
+    EP_ERR_TIMEOUT = 8        /* ep_read_status: a wait between the warps of a kernel ran out  */
 } ep_status_t;
 
 /* Bits of the device status word written by ep_dispatch_layout. */
@@ -75,6 +76,11 @@ typedef enum {
  * The default build skips rows outside [0, R_max) in the same way but records nothing.
  */
 #define EP_STATUS_BOUNDS     8
+/*
+ * Set by ep_expert_linear and ep_expert_linear_bwd when a wait between the warps of their kernel has
+ * lasted two seconds, which means a fault in the kernel: it ends then, its outputs incomplete.
+ */
+#define EP_STATUS_TIMEOUT   16
 
 /*
  * The dispatch layout: caller-allocated device buffers, filled by ep_dispatch_layout and read
@@ -520,6 +526,48 @@ int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t *codes, co
                      const float *row_scale, int hidden_size, int out_rows, int swiglu,
                      const ep_layout_t *L, uint16_t *out, void *workspace,
                      size_t workspace_bytes, void *stream);
+
+/*
+ * ep_expert_linear -- the experts' products with 16-bit weights, for any number of rows: every row of
+ * a layout times the weights of its group, on the tensor cores.
+ *   x          [R_max, K] in row order (what ep_dispatch_bf16 writes), rows x_stride elements apart: at
+ *              least K, a multiple of 8.  K = in_features, a multiple of 16, at most 32768.
+ *   w          [G * N * K] for the G = E + S groups.  N = out_rows, a multiple of 16, at most 65536.
+ *   dtype      EP_BF16 or EP_F16, of x, w and every output.
+ *   swiglu     0: out [R_max * N], out[r, n] = sum over k of x[r, k] w[g, n, k].
+ *              1: w holds N/2 gate rows, then N/2 up rows (N a multiple of 32), and out [R_max * N/2] is
+ *              silu(gate) * up, silu(v) = v / (1 + exp(-v)).
+ *   gate_up    with swiglu [R_max * N] or NULL: gate and up of every row, for the backward pass.
+ * Sums are fp32 on the tensor cores, whose adder truncates (by up to 2^-23 of the sum every 16
+ * products); every output is rounded once.  The rows [0, row_offsets[G]) are written; padding rows are
+ * rows like others, and zero where x is.  No row takes part in another's result, whatever it holds.
+ * Nothing is written while the layout's status word is non-zero.  No workspace, no atomics: the
+ * same call gives the same bits.
+ */
+int ep_expert_linear(const void *x, long long x_stride, const void *w, int in_features, int out_rows,
+                     int dtype, int swiglu, const ep_layout_t *L, void *out, void *gate_up,
+                     void *stream);
+
+/*
+ * ep_expert_linear_bwd -- gradients of ep_expert_linear without swiglu, and through it.
+ *   grad       [R_max, N], rows grad_stride elements apart; x, w, K, N, dtype as in the forward call.
+ *   gate_up    NULL, or [R_max * 2K] saved by the call with swiglu that made x.
+ *   -> grad_x  NULL, or [R_max * K]: grad_x[r, k] = sum over n of grad[r, n] w[g, n, k].  With gate_up
+ *              [R_max * 2K] instead: the gradient of gate and up, which is `grad` of the call for those
+ *              products.  With d the sum above (not rounded) and s = 1/(1 + exp(-gate)):
+ *              d * up * s * (1 + gate * (1 - s)), and d * gate * s.
+ *   -> grad_w  NULL, or [G * N * K] in grad_w_dtype (dtype or EP_F32): grad_w[g, n, k] = sum over the rows
+ *              of g of grad[r, n] x[r, k]; zeros for a group without rows.  accumulate 1 (EP_F32 only)
+ *              adds to what is there.  Sums of EP_F32 leave the tensor cores every 2048 rows.
+ * Rows as in the forward call; padding rows take part in grad_w, so x or grad has to be zero there (and
+ * neither infinite nor NaN): ep_dispatch_bf16 and ep_combine_bwd write zeros.  Rows outside a group, or behind the last one, take no part
+ * in its grad_w.  grad_x and grad_w may not both be NULL; w is not read without grad_x nor x without
+ * grad_w, and they may be NULL then.
+ */
+int ep_expert_linear_bwd(const void *grad, long long grad_stride, const void *x, long long x_stride,
+                         const void *w, int in_features, int out_rows, int dtype,
+                         const void *gate_up, const ep_layout_t *L, void *grad_x, void *grad_w,
+                         int grad_w_dtype, int accumulate, void *stream);
 
 /* Human-readable name of a return code. */
 const char *ep_strerror(int code);
