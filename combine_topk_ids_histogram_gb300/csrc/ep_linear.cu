@@ -286,7 +286,9 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                     const uint32_t id = idesc | (uint32_t)((w.n + Walk<FORM, CG>::kUnit - 1) / Walk<FORM, CG>::kUnit * CG) << 18;
                     const uint32_t d = tmem + buf * kCols;
                     for (int b = 0; b < w.kb; ++b) {
-                        if (!(ok = mbar_wait(smem_u32(&c.full[s]), round & 1))) break;
+                        const bool cleared = FORM == kGradW && b == w.kb - 1 && (w.last & 15) != 0;
+                        const uint32_t full = smem_u32(&c.full[s]);
+                        if (!(ok = cleared ? mbar_wait<true>(full, round & 1) : mbar_wait(full, round & 1))) break;
                         tc_fence_after();
                         const uint32_t sa = smem_u32(smem + s * kStageBytes);
                         const uint64_t da = smem_desc(sa, 8192), db = smem_desc(sa + kTileA, 8192);
@@ -319,7 +321,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                             *reinterpret_cast<uint4 *>(st + i / (rows * 8) * 8192 + i % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
                         asm volatile("fence.proxy.async;" ::: "memory");
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(at_rank(smem_u32(&c.full[s]), 0));
+                        if (lane == 0) mbar_arrive_release(at_rank(smem_u32(&c.full[s]), 0));
                     }
                     if (++s == kStages) s = 0;
                 }

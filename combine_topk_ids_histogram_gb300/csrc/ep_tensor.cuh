@@ -42,19 +42,32 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 __device__ __forceinline__ void mbar_init_done() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
-// One arrival, and `bytes` that copies will still bring; `bar` lies in the cluster's window.
-__device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
+// Arrivals; `bar` lies in the cluster's window, and may be the other CTA's.  What they order is in tensor memory or written by
+// copies, which have fences and counts of their own, so these have the default scope, the CTA's: at cluster scope each of them is a memory
+// barrier of the whole SM (a product's block of k took 1750 cycles instead of 550 with them).
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// One arrival, and `bytes` that copies will still bring.
+__device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// An arrival behind this thread's stores to shared memory, for a wait with `kCluster`.
+__device__ __forceinline__ void mbar_arrive_release(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+template <bool kCluster> __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    if constexpr (kCluster)
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
 __device__ __forceinline__ unsigned long long global_ns() {
@@ -65,11 +78,11 @@ __device__ __forceinline__ unsigned long long global_ns() {
 // Waits for the end of the phase of that parity, two seconds at most.  Everything that a role waits for is work of its own
 // CTA pair, of microseconds; a wait that runs out means a lost arrival, and the caller ends its loop.
 constexpr unsigned long long kWaitNs = 2000000000ull;
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    if (mbar_try(bar, parity)) return true;
+template <bool kCluster = false> __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+    if (mbar_try<kCluster>(bar, parity)) return true;
     unsigned long long begin = 0;
     for (unsigned i = 1;; ++i) {
-        if (mbar_try(bar, parity)) return true;
+        if (mbar_try<kCluster>(bar, parity)) return true;
         if ((i & 255u) == 0) {
             const unsigned long long now = global_ns();
             if (begin == 0) begin = now;
