@@ -10,7 +10,8 @@ Entry points (same names as the C ABI, without the ``ep_`` prefix):
 ``dispatch_layout_nvfp4``, ``dispatch_layout_padded_nvfp4``, ``dispatch_bf16``, ``dispatch_fp8``, ``combine``, ``combine_bwd``,
 ``dispatch_bwd``, ``routing_map_to_topk``, ``indices_to_multihot``, ``rows_max``,
 ``read_status``, ``cvt_e2m1``, ``cvt_e4m3``; around the dispatch: ``layer_norm``, ``layer_norm_bwd``,
-``router_topk``, ``router_topk_bwd``, ``expert_matvec``, ``expert_linear`` and ``expert_linear_bwd``.
+``router_topk``, ``router_topk_bwd``, ``expert_matvec``, ``expert_linear``,
+``expert_linear_bwd`` and ``lora_add``.
 """
 from __future__ import annotations
 
@@ -100,6 +101,7 @@ SIGNATURES = {
     "ep_expert_matvec": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _LP, _P, _P, _Z, _P]),
     "ep_expert_linear": (_I, [_P, _LL, _P, _I, _I, _I, _I, _LP, _P, _P, _P]),
     "ep_expert_linear_bwd": (_I, [_P, _LL, _P, _LL, _P, _I, _I, _I, _P, _LP, _P, _P, _I, _I, _P]),
+    "ep_lora_add": (_I, [_P, _LL, _P, _LL, _P, _P, _P, _I, _I, _I, _I, _I, _LP, _P, _LL, _P]),
     "ep_read_status": (_I, [_LP, _P, ctypes.POINTER(ctypes.c_int32)]),
     "ep_strerror": (ctypes.c_char_p, [_I]),
     "ep_cvt_e2m1": (_I, [_P, _P, _L, _P]),
@@ -864,6 +866,37 @@ def expert_linear_bwd(grad: torch.Tensor, x: torch.Tensor | None, w: torch.Tenso
                                    1 if accumulate else 0, _stream(stream))
     _check(rc, "ep_expert_linear_bwd")
     return gx if need_x else None, gw if need_w else None
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, L: Layout, scale: torch.Tensor | None = None,
+             by_token: bool = True, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """ep_lora_add: out[t] = y[t] + scale[g] * b[g] (a[g] x[t]) for the adapter g of each token, from a layout of adapter ids
+    [T, 1] (``dispatch_layout(ids, n_adapters)``); out[t] = y[t] where the id is -1.  y [T, N] and x [T, H] (rows may have a
+    stride, a multiple of 8), a [G, r, H] and b [G, N, r], all bf16 or all fp16; scale fp32 [G], None for 1.  Without
+    ``by_token`` y, x and out are in the layout's row order [R_max, *], for any layout (adapters of experts).  ``out`` may be
+    y, which is then added to in place."""
+    pa, pb = _buffer(a, tuple(a.shape), _HALF, "a"), _buffer(b, tuple(b.shape), (a.dtype,), "b")
+    if a.dim() != 3 or a.shape[0] != L.G or b.dim() != 3 or b.shape[0] != L.G or b.shape[2] != a.shape[1]:
+        raise ValueError(f"expected a [{L.G}, r, H] and b [{L.G}, N, r], got {tuple(a.shape)} and {tuple(b.shape)}")
+    r, H, N, dt = a.shape[1], a.shape[2], b.shape[1], a.dtype
+
+    def rows(t, cols, what):
+        p, n, m, ld, _ = _matrix(t, what)
+        if t.dtype != dt:
+            raise TypeError(f"{what}: dtype {t.dtype}, expected {dt}")
+        if m != cols or (n != L.T if by_token else n < L.R_max):
+            raise ValueError(f"{what}: expected {L.T if by_token else L.R_max} rows of {cols}, got {tuple(t.shape)}")
+        return p, ld
+
+    py, ldy = rows(y, N, "y")
+    px, ldx = rows(x, H, "x")
+    if out is None:
+        out = torch.empty(y.shape, dtype=dt, device=y.device)
+    po, ldo = rows(out, N, "out")
+    rc = _lib.ep_lora_add(py, ldy, px, ldx, pa, pb, None if scale is None else _buffer(scale, (L.G,), _F32, "scale"), H, N, r, DTYPES[dt],
+                          1 if by_token else 0, L.ref, po, ldo, _stream(stream))
+    _check(rc, "ep_lora_add")
+    return out
 
 
 def read_status(L: Layout, stream=None) -> int:

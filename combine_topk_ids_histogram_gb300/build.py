@@ -24,7 +24,7 @@ LIB = os.path.join(BUILD, "libep_gb300.so")
 LIB_CHECKED = os.path.join(BUILD, "libep_gb300_checked.so")
 
 SOURCES = ["ep_layout.cu", "ep_dispatch.cu", "ep_combine.cu", "ep_routing.cu", "ep_norm.cu", "ep_router.cu",
-           "ep_experts.cu", "ep_linear.cu"]
+           "ep_experts.cu", "ep_linear.cu", "ep_lora.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -569,6 +569,29 @@ int ep_expert_linear_bwd(const void *grad, long long grad_stride, const void *x,
                          const void *gate_up, const ep_layout_t *L, void *grad_x, void *grad_w,
                          int grad_w_dtype, int accumulate, void *stream);
 
+/*
+ * ep_lora_add -- low-rank adapters of many requests at once, beside a projection y that they share: the
+ * layout groups the rows by adapter, as it groups them by expert.
+ *   a          [G * r * H], b [G * N * r] for the G = E + S groups, dtype; r = rank, a multiple of 8 from 8
+ *              to 128 (adapters of a lower rank are filled up with zeros); H = in_features and N =
+ *              out_features as K and N of ep_expert_linear.
+ *   scale      [G] fp32, or NULL for 1.
+ *   by_token   1: y, out [T, N] and x [T, H]; the layout is one of adapter ids [T, 1] (K = 1, no shared
+ *              expert): out[t] = y[t] + scale[g] * b[g] (a[g] x[t]), and out[t] = y[t] where the id is -1.
+ *              0: y, out [R_max, N] and x [R_max, H] in row order (adapters of experts): the rows
+ *              [0, row_offsets[G]) are written.
+ *   y, x, out  rows y_stride, x_stride, out_stride elements apart, multiples of 8.  out may be y (with the
+ *              same stride: added in place, rows without an adapter untouched), and overlaps nothing else.
+ *   dtype      EP_BF16 or EP_F16, of y, x, a, b and out.
+ * Both sums are fp32.  a[g] x goes into the second one as the sum of two 16-bit numbers (16 bits of it
+ * with EP_BF16, 22 with EP_F16); out is rounded once.  Nothing is written while the layout's status word is
+ * non-zero.  No workspace, no atomics: the same call gives the same bits.
+ */
+int ep_lora_add(const void *y, long long y_stride, const void *x, long long x_stride, const void *a,
+                const void *b, const float *scale, int in_features, int out_features, int rank,
+                int dtype, int by_token, const ep_layout_t *L, void *out, long long out_stride,
+                void *stream);
+
 /* Human-readable name of a return code. */
 const char *ep_strerror(int code);
 
