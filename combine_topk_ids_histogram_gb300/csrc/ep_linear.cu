@@ -140,8 +140,16 @@ __device__ __forceinline__ void cp_async16(void *smem, const void *gmem) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
 }
 
-// s = 1 / (1 + exp(-v)): the fast exponential and division are off by under 2^-16 of s, a hundredth of the outputs' rounding.
-__device__ __forceinline__ float sigmoid_fast(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+// s = 1 / (1 + exp(-v)), and 1 - s without cancellation, from e = exp(-|v|): no exponential overflows, small ones keep their digits
+// down to the subnormal numbers, and the divisor lies in [1, 2], where the fast division is within 2 ulp.
+struct Sigmoid {
+    float s, rest;
+    __device__ explicit Sigmoid(float v) {
+        const float e = expf(-fabsf(v)), r = __fdividef(1.0f, 1.0f + e);
+        s = v < 0.0f ? e * r : r;
+        rest = v < 0.0f ? r : e * r;
+    }
+};
 
 template <int FORM, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -427,8 +435,8 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 #pragma unroll
                             for (int j = 0; j < 32; ++j) {
                                 const float gate = wide16(st[j * 128 + et], a.f16), up = wide16(st[4096 + j * 128 + et], a.f16);
-                                const float s = sigmoid_fast(gate), ds = v[j] * s;
-                                const uint32_t p = pack16(ds * up * (1.0f + gate * (1.0f - s)), ds * gate, a.f16);
+                                const Sigmoid sig(gate);
+                                const uint32_t p = pack16(v[j] * up * (sig.s * (1.0f + gate * sig.rest)), v[j] * (gate * sig.s), a.f16);
                                 st[j * 128 + et] = (uint16_t)p;
                                 st[4096 + j * 128 + et] = (uint16_t)(p >> 16);
                             }
@@ -464,7 +472,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                                 for (int i = 0; i < 2; ++i) {
                                     const float other = swap[((q ^ 1) * 16 + j + i) * 32 + lane], own = up ? v[16 + j + i] : v[j + i];
                                     const float gate = up ? other : own;
-                                    y[i] = gate * sigmoid_fast(gate) * (up ? own : other);
+                                    y[i] = gate * Sigmoid(gate).s * (up ? own : other);
                                 }
                                 const uint32_t p = pack16(y[0], y[1], a.f16);
                                 act[(up * 16 + j) * 64 + f] = (uint16_t)p;
