@@ -160,7 +160,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     uint8_t *const smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     uint8_t *const staging = smem + kStages * kStageBytes;
     Control &c = *reinterpret_cast<Control *>(staging + kStaging);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
     const int pair = blockIdx.x / CG, pairs = gridDim.x / CG;
 
@@ -233,7 +233,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         Walk<FORM, CG> walk(a, c, pair, pairs);
         Work w = {};
         if (warp == 0) {                                 // ------------------------------------------------ loads
-            if (lane == 0) {
+            if (elect_one()) {
                 int s = 0, used = 0;
                 uint32_t round = 0;
                 while (ok && walk.next(w)) {
@@ -283,31 +283,34 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 }
             }
         } else if (warp == 1) {                          // ------------------------------------------------ products
-            if (lane == 0 && rank == 0) {
+            if (rank == 0) {                             // the whole warp keeps step, one lane issues
                 int s = 0, buf = 0;
                 uint32_t round = 0, tiles = 0;
                 const uint32_t idesc = mma_desc(a.f16 != 0, 128 * CG, 0, kAmn, kBmn);
+                const uint64_t desc = smem_desc(smem_u32(smem), 8192);
                 while (ok && walk.next(w)) {
                     if (w.kb == 0) continue;
-                    if (!(ok = mbar_wait(smem_u32(&c.sums_empty[buf]), ((tiles >> 1) & 1) ^ 1))) break;
+                    if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_empty[buf]), ((tiles >> 1) & 1) ^ 1)))) break;
                     tc_fence_after();
                     const uint32_t id = idesc | (uint32_t)((w.n + Walk<FORM, CG>::kUnit - 1) / Walk<FORM, CG>::kUnit * CG) << 18;
                     const uint32_t d = tmem + buf * kCols;
                     for (int b = 0; b < w.kb; ++b) {
-                        const bool cleared = FORM == kGradW && b == w.kb - 1 && (w.last & 15) != 0;
+                        const bool last = b == w.kb - 1, cleared = FORM == kGradW && last && (w.last & 15) != 0;
                         const uint32_t full = smem_u32(&c.full[s]);
-                        if (!(ok = cleared ? mbar_wait<true>(full, round & 1) : mbar_wait(full, round & 1))) break;
+                        if (!(ok = __all_sync(kFullMask, cleared ? mbar_wait<true>(full, round & 1) : mbar_wait(full, round & 1)))) break;
                         tc_fence_after();
-                        const uint32_t sa = smem_u32(smem + s * kStageBytes);
-                        const uint64_t da = smem_desc(sa, 8192), db = smem_desc(sa + kTileA, 8192);
-                        const int steps = b == w.kb - 1 ? (w.last + 15) >> 4 : kBlockK / 16;
-                        for (int i = 0; i < steps; ++i)
-                            tc_mma<CG>(d, da + i * (kAmn ? 128 : 2), db + i * (kBmn ? 128 : 2), id, b > 0 || i > 0);
-                        tc_commit<CG>(smem_u32(&c.empty[s]));
+                        const uint64_t da = desc + s * (kStageBytes >> 4), db = da + (kTileA >> 4);
+                        if (elect_one()) {
+                            const int steps = last ? (w.last + 15) >> 4 : kBlockK / 16;
+#pragma unroll
+                            for (int i = 0; i < kBlockK / 16; ++i)
+                                if (i < steps) tc_mma<CG>(d, da + i * (kAmn ? 128 : 2), db + i * (kBmn ? 128 : 2), id, b > 0 || i > 0);
+                            tc_commit<CG>(smem_u32(&c.empty[s]));
+                            if (last) tc_commit<CG>(smem_u32(&c.sums_full[buf]));
+                        }
+                        __syncwarp();
                         if (++s == kStages) s = 0, ++round;
                     }
-                    if (!ok) break;
-                    tc_commit<CG>(smem_u32(&c.sums_full[buf]));
                     buf ^= 1;
                     ++tiles;
                 }

@@ -11,6 +11,14 @@ namespace ep {
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
+// One lane of a whole warp, the same every time.  The compiler takes the branch behind it for uniform, so that the operands of
+// TMA and tensor-core instructions stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // ---------------------------------------------------------------------------------------
 // Clusters
 // ---------------------------------------------------------------------------------------
