@@ -9,8 +9,8 @@
 // rows are N, in steps of 32: a group of any number of rows then costs about what its rows cost, and weights, which have
 // hundreds of rows or more, fill M.  A pair of CTAs shares a product of 256 x 256: each loads 128 of M and half of N by TMA and
 // keeps the sums of its 128 of M in tensor memory, twice, so that one tile's results leave while the next one's
-// are added up.  Warp 0 loads, warp 1 of the first CTA issues the products, warps 4 to 7 take results out; warp 2 (grad_w)
-// clears the rows behind a group's last one in shared memory, since there they are summed over.
+// are added up.  Warp 0 loads, warp 1 of the first CTA issues the products, warps 4 to 11 take results out, four at a time 32
+// columns; warp 2 (grad_w) clears the rows behind a group's last one in shared memory, since there they are summed over.
 #include <math.h>
 
 #include <algorithm>
@@ -25,28 +25,32 @@ namespace {
 
 enum Form { kPlain, kGlu, kGradX, kGradGate, kGradW };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kOutGroups = 2;                // of four warps that take results out
 constexpr int kBlockK = 64;                  // of the summed dimension in a stage: 128 bytes, one swizzle row
-constexpr int kStages = 5;
 constexpr int kTileA = 128 * kBlockK * 2;    // bytes a CTA loads of each operand per stage
 constexpr int kTileB = 128 * kBlockK * 2;
 constexpr int kStageBytes = kTileA + kTileB;
-constexpr int kStaging = 32768;
 constexpr int kCols = 256;                   // columns of tensor memory per tile's sums
 constexpr int kMaxGroups = kMaxE + 1;
+constexpr int kMaxStages = 5;
+// Bytes in which a group of four warps turns its results into rows, and the stages that there is room for.
+__host__ __device__ constexpr int staging_bytes(Form f) { return f == kPlain || f == kGradX ? 16384 : 32768; }
+__host__ __device__ constexpr int stages_of(Form f) { return f == kPlain || f == kGradX ? 5 : 4; }
+constexpr int kSuper = 8;                    // grad_w: tiles of N that go through all of K before the next
 // The tensor cores' sums in fp32 truncate, by up to 2^-23 of the sum per 16 products; an fp32 gradient leaves them every 2048 rows.
 constexpr int kChunkRows = 2048;
 
 struct Control {
-    uint64_t full[kStages], empty[kStages], landed[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages];
     uint64_t sums_full[2], sums_empty[2];
     uint32_t tmem, skip;
     int part[kThreads / 32];
     int off[kMaxGroups + 1];                 // first row of each group
     int start[kMaxGroups + 1];               // first tile of each group
 };
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kStaging + sizeof(Control);
-static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+constexpr size_t smem_bytes(Form f) { return 1024 + stages_of(f) * kStageBytes + kOutGroups * staging_bytes(f) + sizeof(Control); }
+static_assert(smem_bytes(kPlain) <= 227 * 1024 && smem_bytes(kGradW) <= 227 * 1024, "shared memory of a CTA");
 
 struct LinearArgs {
     const int32_t *row_offsets;
@@ -55,6 +59,7 @@ struct LinearArgs {
     int M;                                   // of the output: features of a row (gated: F), rows of a weight gradient
     int sum;                                 // length of the sums (forms that sum over rows: columns of the output)
     int f16, wide, add;                      // operands fp16; grad_w: fp32 output, added to what is there
+    int whole_a, whole_b;                    // whether the operand's map has the blocks of 64 (kGlu: the 32 gates and ups) as dimensions
     uint16_t *out, *gate_up;                 // gate_up: saved by kGlu, read by kGradGate
 };
 
@@ -67,7 +72,7 @@ struct Work {
 };
 
 // The tiles of a CTA pair in turn.  Every role walks them for itself.
-template <int FORM, int CG> struct Walk {
+template <Form FORM, int CG> struct Walk {
     static constexpr int kM = FORM == kGlu ? 64 * CG : 128 * CG, kN = 128 * CG;
     static constexpr int kUnit = 16 * CG;    // of N in a product
     const LinearArgs &a;
@@ -77,6 +82,11 @@ template <int FORM, int CG> struct Walk {
     __device__ Walk(const LinearArgs &a_, const Control &c_, int first, int step_)
         : a(a_), c(c_), tile(first - step_), step(step_), m_tiles((a_.M + kM - 1) / kM), g(0), chunk(0) {
         tiles = FORM == kGradW ? a.G * m_tiles * ((a.sum + kN - 1) / kN) : c.start[a.G];
+    }
+    // Of N, what each CTA loads: whole blocks of 64 where one copy brings them.
+    __device__ int half(const Work &w) const {
+        const int unit = FORM == kGradW && a.whole_b ? 64 : kUnit / CG;
+        return (w.n + unit * CG - 1) / (unit * CG) * unit;
     }
     __device__ bool next(Work &w) {
         if constexpr (FORM == kGradW) {
@@ -89,8 +99,9 @@ template <int FORM, int CG> struct Walk {
                 if (tile >= tiles) return false;
                 const int n_tiles = (a.sum + kN - 1) / kN, in = tile % (m_tiles * n_tiles);
                 w.g = tile / (m_tiles * n_tiles);
-                w.m = in % m_tiles * kM;
-                w.col = in / m_tiles * kN;
+                const int first = in / (kSuper * n_tiles) * kSuper, wide = min(kSuper, m_tiles - first), at = in - first * n_tiles;
+                w.m = (first + at % wide) * kM;
+                w.col = at / wide * kN;
                 w.n = min(kN, a.sum - w.col);
             }
             w.first = chunk == 0;
@@ -151,15 +162,16 @@ struct Sigmoid {
     }
 };
 
-template <int FORM, int CG>
+template <Form FORM, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                 const __grid_constant__ CUtensorMap map_out, const LinearArgs a) {
+                 const __grid_constant__ CUtensorMap map_c, const LinearArgs a) {
+    constexpr int kStages = stages_of(FORM), kStaging = staging_bytes(FORM);
     constexpr bool kAmn = FORM == kGradX || FORM == kGradGate || FORM == kGradW, kBmn = FORM == kGradW;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     uint8_t *const staging = smem + kStages * kStageBytes;
-    Control &c = *reinterpret_cast<Control *>(staging + kStaging);
+    Control &c = *reinterpret_cast<Control *>(staging + kOutGroups * kStaging);
     const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
     const int pair = blockIdx.x / CG, pairs = gridDim.x / CG;
@@ -175,7 +187,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&c.sums_full[b]), 1);
-            mbar_init(smem_u32(&c.sums_empty[b]), 4 * CG);
+            mbar_init(smem_u32(&c.sums_empty[b]), 4 * kOutGroups * CG);
         }
         mbar_init_done();
     }
@@ -236,40 +248,61 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             if (elect_one()) {
                 int s = 0, used = 0;
                 uint32_t round = 0;
-                while (ok && walk.next(w)) {
-                    const int half = (w.n + Walk<FORM, CG>::kUnit - 1) / Walk<FORM, CG>::kUnit * 16, boxes = (half + 31) >> 5;
-                    const int m = w.m + (int)rank * (Walk<FORM, CG>::kM / CG), n = (FORM == kGradW ? w.col : w.row) + (int)rank * half;
-                    const uint32_t bytes = kTileA + (FORM == kGradW ? kTileB : boxes * 4096);
+                bool more = walk.next(w);
+                while (ok && more) {
+                    Work then = w;                       // the next tile, looked up while this one's loads are on their way
+                    const int half = walk.half(w), m = w.m + (int)rank * (Walk<FORM, CG>::kM / CG);
+                    const int n = (FORM == kGradW ? w.col : w.row) + (int)rank * half;
+                    const uint32_t bytes = kTileA + (FORM == kGradW || half > 96 ? kTileB : ((half + 31) >> 5) * 4096);
                     for (int b = 0; b < w.kb; ++b) {
                         if (used == kStages && !(ok = mbar_wait(smem_u32(&c.empty[s]), (round & 1) ^ 1))) break;
-                        const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kTileA;
                         // a block that ends inside 16 rows lands here first and is cleared behind its end
                         const bool clear = FORM == kGradW && b == w.kb - 1 && (w.last & 15) != 0;
                         const uint32_t bar = clear ? smem_u32(&c.landed[s]) : at_rank(smem_u32(&c.full[s]), 0);
                         mbar_arrive_expect(clear ? at_rank(bar, rank) : bar, bytes);
+                        // One copy for an operand where its map allows it: each copy takes this thread some 50 cycles, of the 512 that
+                        // the products of a block last.
+                        const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kTileA;
                         const int k = b * kBlockK;
                         if constexpr (FORM == kGradW) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                tma_load_2d<CG>(sa + i * 8192, &map_a, m + 64 * i, w.row + k, bar);
-                                tma_load_2d<CG>(sb + i * 8192, &map_b, n + 64 * i, w.row + k, bar);
+                            if (a.whole_a) {
+                                tma_load<CG, 3>(sa, &map_a, {0, w.row + k, m >> 6}, bar);
+                            } else {
+                                tma_load<CG, 2>(sa, &map_a, {m, w.row + k}, bar);
+                                tma_load<CG, 2>(sa + 8192, &map_a, {m + 64, w.row + k}, bar);
+                            }
+                            if (a.whole_b) {
+                                tma_load<CG, 3>(sb, &map_b, {0, w.row + k, n >> 6}, bar);
+                            } else {
+                                tma_load<CG, 2>(sb, &map_b, {n, w.row + k}, bar);
+                                tma_load<CG, 2>(sb + 8192, &map_b, {n + 64, w.row + k}, bar);
                             }
                         } else {
-                            if constexpr (FORM == kGlu) {
+                            if constexpr (FORM == kPlain) {
+                                tma_load<CG, 3>(sa, &map_a, {k, m, w.g}, bar);
+                            } else if constexpr (FORM == kGlu) {
+                                if (a.whole_a) {
+                                    tma_load<CG, 5>(sa, &map_a, {k, 0, 0, m >> 5, w.g}, bar);
+                                } else {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    tma_load_3d<CG>(sa + i * 4096, &map_a, k, (i & 1) * a.M + m + (i >> 1) * 32, w.g, bar);
-                            } else if constexpr (FORM == kPlain) {
-                                tma_load_3d<CG>(sa, &map_a, k, m, w.g, bar);
+                                    for (int i = 0; i < 4; ++i) tma_load<CG, 3>(sa + i * 4096, &map_a, {k, (i & 1) * a.M + m + (i >> 1) * 32, w.g}, bar);
+                                }
+                            } else if (a.whole_a) {
+                                tma_load<CG, 4>(sa, &map_a, {0, k, m >> 6, w.g}, bar);
                             } else {
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) tma_load_3d<CG>(sa + i * 8192, &map_a, m + 64 * i, k, w.g, bar);
+                                tma_load<CG, 3>(sa, &map_a, {m, k, w.g}, bar);
+                                tma_load<CG, 3>(sa + 8192, &map_a, {m + 64, k, w.g}, bar);
                             }
-                            for (int i = 0; i < boxes; ++i) tma_load_2d<CG>(sb + i * 4096, &map_b, k, n + 32 * i, bar);
+                            if (half > 96) tma_load<CG, 2>(sb, &map_b, {k, n}, bar);
+                            else
+                                for (int i = 0; i < half; i += 32) tma_load<CG, 2>(sb + i * 128, &map_c, {k, n + i}, bar);
                         }
                         if (++s == kStages) s = 0, ++round;
                         used = min(used + 1, kStages);
+                        if (b == 0) more = walk.next(then);
                     }
+                    if (w.kb == 0) more = walk.next(then);
+                    w = then;
                 }
                 // Nothing of the pair may still be on its way to this CTA when it ends.
                 for (int i = 0; ok && i < used; ++i) {
@@ -288,11 +321,16 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 uint32_t round = 0, tiles = 0;
                 const uint32_t idesc = mma_desc(a.f16 != 0, 128 * CG, 0, kAmn, kBmn);
                 const uint64_t desc = smem_desc(smem_u32(smem), 8192);
-                while (ok && walk.next(w)) {
-                    if (w.kb == 0) continue;
+                bool more = walk.next(w);
+                while (ok && more) {
+                    Work then = w;
+                    if (w.kb == 0) {
+                        more = walk.next(w);
+                        continue;
+                    }
                     if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_empty[buf]), ((tiles >> 1) & 1) ^ 1)))) break;
                     tc_fence_after();
-                    const uint32_t id = idesc | (uint32_t)((w.n + Walk<FORM, CG>::kUnit - 1) / Walk<FORM, CG>::kUnit * CG) << 18;
+                    const uint32_t id = idesc | (uint32_t)(walk.half(w) * CG >> 4) << 18;
                     const uint32_t d = tmem + buf * kCols;
                     for (int b = 0; b < w.kb; ++b) {
                         const bool last = b == w.kb - 1, cleared = FORM == kGradW && last && (w.last & 15) != 0;
@@ -310,7 +348,9 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         }
                         __syncwarp();
                         if (++s == kStages) s = 0, ++round;
+                        if (b == 0) more = walk.next(then);
                     }
+                    w = then;
                     buf ^= 1;
                     ++tiles;
                 }
@@ -338,11 +378,12 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 }
             }
         } else if (warp >= 4) {                          // ------------------------------------------------ results
-            const int q = warp - 4, et = tid - 128;
+            const int q = warp & 3, part = (warp - 4) >> 2, et = tid & 127, bar = 1 + 3 * part;
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
             int buf = 0;
             uint32_t tiles = 0;
-            uint16_t *const st16 = reinterpret_cast<uint16_t *>(staging);
+            uint8_t *const own = staging + part * kStaging;
+            uint16_t *const st16 = reinterpret_cast<uint16_t *>(own);
             while (ok && walk.next(w)) {
                 const int m0 = w.m + (int)rank * (Walk<FORM, CG>::kM / CG);          // first feature of this CTA
                 const uint32_t sums = lanes + buf * kCols;
@@ -356,8 +397,8 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                     const int cols = a.wide ? 32 : 64;
                     int at = 0;
                     if (!w.first && lane == 0) bulk_wait_all();      // the chunk before, added up
-                    for (int col = 0; col < w.n; col += cols, at ^= 1) {
-                        uint8_t *const line = staging + (q * 2 + at) * 4096 + lane * 128;
+                    for (int col = part * cols; col < w.n; col += kOutGroups * cols, at ^= 1) {
+                        uint8_t *const line = own + (q * 2 + at) * 4096 + lane * 128;
                         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                         __syncwarp();
                         float v[32] = {};
@@ -387,9 +428,9 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0 && m0 + q * 32 < a.M) {
-                            const uint32_t src = smem_u32(staging + (q * 2 + at) * 4096);
-                            if (a.wide && (a.add || !w.first)) tma_add_3d(&map_out, src, w.col + col, m0 + q * 32, w.g);
-                            else tma_store_3d(&map_out, src, w.col + col, m0 + q * 32, w.g);
+                            const uint32_t src = smem_u32(own + (q * 2 + at) * 4096);
+                            if (a.wide && (a.add || !w.first)) tma_add_3d(&map_c, src, w.col + col, m0 + q * 32, w.g);
+                            else tma_store_3d(&map_c, src, w.col + col, m0 + q * 32, w.g);
                         }
                         if (lane == 0) bulk_commit();
                     }
@@ -401,40 +442,41 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                             const int t = ch * 32 + (i >> 4), f = m0 + (i & 15) * 8;
                             if (t < w.n && f < F) {
                                 const uint16_t *src = a.gate_up + (size_t)(w.row + t) * 2 * F + f;
-                                cp_async16(st16 + (ch & 1) * 8192 + i * 8, src);
-                                cp_async16(st16 + (ch & 1) * 8192 + 4096 + i * 8, src + F);
+                                cp_async16(st16 + (ch / kOutGroups & 1) * 8192 + i * 8, src);
+                                cp_async16(st16 + (ch / kOutGroups & 1) * 8192 + 4096 + i * 8, src + F);
                             }
                         }
                         asm volatile("cp.async.commit_group;" ::: "memory");
                     };
-                    bar_sync(1, 128);                    // the last tile has left the staging buffers
-                    if constexpr (FORM == kGradGate) prefetch(0);
-                    if (!(ok = bar_all(1, 128, mbar_wait(smem_u32(&c.sums_full[buf]), (tiles >> 1) & 1)))) break;
+                    bar_sync(bar, 128);                    // the last tile has left the staging buffers
+                    if constexpr (FORM == kGradGate) prefetch(part);
+                    if (!(ok = bar_all(bar, 128, mbar_wait(smem_u32(&c.sums_full[buf]), (tiles >> 1) & 1)))) break;
                     tc_fence_after();
-                    for (int ch = 0; ch < chunks; ++ch) {
+                    for (int ch = part; ch < chunks; ch += kOutGroups) {
+                        const int at = ch / kOutGroups & 1;  // of the two staging buffers
                         float v[32];
                         tmem_ld32(sums + ch * 32, v);
                         tmem_wait_ld();
                         const size_t row0 = (size_t)w.row + ch * 32;
                         const int rows = min(32, w.n - ch * 32);
                         if constexpr (FORM == kPlain || FORM == kGradX) {
-                            uint16_t *const st = st16 + (ch & 1) * 4096;
+                            uint16_t *const st = st16 + at * 4096;
 #pragma unroll
                             for (int j = 0; j < 32; j += 2) {
                                 const uint32_t p = pack16(v[j], v[j + 1], a.f16);
                                 st[j * 128 + et] = (uint16_t)p;
                                 st[(j + 1) * 128 + et] = (uint16_t)(p >> 16);
                             }
-                            bar_sync(1, 128);
+                            bar_sync(bar, 128);
                             for (int i = et; i < rows * 16; i += 128) {
                                 const int f = m0 + (i & 15) * 8;
                                 if (f < F) *reinterpret_cast<uint4 *>(a.out + (row0 + (i >> 4)) * F + f) = *reinterpret_cast<const uint4 *>(st + i * 8);
                             }
                         } else if constexpr (FORM == kGradGate) {
                             asm volatile("cp.async.wait_group 0;" ::: "memory");
-                            bar_sync(1, 128);            // everyone's pieces of this chunk; the other buffer is free
-                            if (ch + 1 < chunks) prefetch(ch + 1);
-                            uint16_t *const st = st16 + (ch & 1) * 8192;
+                            bar_sync(bar, 128);            // everyone's pieces of this chunk; the other buffer is free
+                            if (ch + kOutGroups < chunks) prefetch(ch + kOutGroups);
+                            uint16_t *const st = st16 + at * 8192;
 #pragma unroll
                             for (int j = 0; j < 32; ++j) {
                                 const float gate = wide16(st[j * 128 + et], a.f16), up = wide16(st[4096 + j * 128 + et], a.f16);
@@ -443,7 +485,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                                 st[j * 128 + et] = (uint16_t)p;
                                 st[4096 + j * 128 + et] = (uint16_t)(p >> 16);
                             }
-                            bar_sync(1, 128);
+                            bar_sync(bar, 128);
                             for (int i = et; i < rows * 16; i += 128) {
                                 const int f = m0 + (i & 15) * 8;
                                 if (f < F) {
@@ -455,8 +497,8 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         } else {
                             // Even warps hold gates, odd warps the ups of the same 32 features: each takes half of the rows.
                             const int up = q & 1, f = (q >> 1) * 32 + lane;
-                            float *const swap = reinterpret_cast<float *>(staging);
-                            uint16_t *const act = st16 + 4096 + (ch & 1) * 2048, *const gu = st16 + 8192 + (ch & 1) * 4096;
+                            float *const swap = reinterpret_cast<float *>(own);
+                            uint16_t *const act = st16 + 4096 + at * 2048, *const gu = st16 + 8192 + at * 4096;
 #pragma unroll
                             for (int j = 0; j < 16; ++j) swap[(q * 16 + j) * 32 + lane] = up ? v[j] : v[16 + j];
                             if (a.gate_up) {
@@ -467,7 +509,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                                     gu[(j + 1) * 128 + up * 64 + f] = (uint16_t)(p >> 16);
                                 }
                             }
-                            bar_sync(2 + (q >> 1), 64);
+                            bar_sync(bar + 1 + (q >> 1), 64);
 #pragma unroll
                             for (int j = 0; j < 16; j += 2) {
                                 float y[2];
@@ -481,7 +523,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                                 act[(up * 16 + j) * 64 + f] = (uint16_t)p;
                                 act[(up * 16 + j + 1) * 64 + f] = (uint16_t)(p >> 16);
                             }
-                            bar_sync(1, 128);
+                            bar_sync(bar, 128);
                             for (int i = et; i < rows * 8; i += 128) {
                                 const int f8 = m0 + (i & 7) * 8;
                                 if (f8 < F) *reinterpret_cast<uint4 *>(a.out + (row0 + (i >> 3)) * F + f8) = *reinterpret_cast<const uint4 *>(act + i * 8);
@@ -530,19 +572,37 @@ Encode encoder() {
     return fn;
 }
 
-// A map over [d2][d1][d0] elements (d0 contiguous, rows `ld` elements apart) with boxes of [1][b1][b0], 128 bytes wide.
-bool encode(CUtensorMap *m, const void *p, int bytes, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t ld, uint32_t b0, uint32_t b1) {
+struct Dim {
+    uint64_t size, stride;                       // elements
+    uint32_t box;
+};
+// A map over these dimensions, the innermost first (stride 1), in boxes that are 128 bytes wide.
+template <int N> bool encode(CUtensorMap *m, const void *p, int bytes, const Dim (&d)[N]) {
     const Encode fn = encoder();
     if (!fn) return false;
-    const cuuint64_t dims[3] = {d0, d1, d2 ? d2 : 1}, strides[2] = {ld * bytes, ld * bytes * d1};
-    const cuuint32_t box[3] = {b0, b1, 1}, one[3] = {1, 1, 1};
-    return fn(m, bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, d2 ? 3 : 2, const_cast<void *>(p), dims,
-              strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    cuuint64_t sizes[N], strides[N];
+    cuuint32_t box[N], one[N];
+    for (int i = 0; i < N; ++i) {
+        sizes[i] = d[i].size;
+        if (i) strides[i - 1] = d[i].stride * bytes;
+        box[i] = d[i].box;
+        one[i] = 1;
+    }
+    return fn(m, bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, N, const_cast<void *>(p), sizes, strides,
+              box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Rows of `cols`, of which the sums run along a row (boxes of `box` rows), or down the rows (two blocks of 64 columns by 64
+// rows; one box where blocks are whole, which a last one that is not would read beyond the matrix).
+bool encode_rows(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box) {
+    return encode(m, p, 2, {{cols, 1, kBlockK}, {rows, ld, box}});
+}
+bool encode_columns(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows, uint64_t ld, bool whole) {
+    return whole ? encode(m, p, 2, {{64, 1, 64}, {rows, ld, kBlockK}, {cols / 64, 64, 2}}) : encode(m, p, 2, {{cols, 1, 64}, {rows, ld, kBlockK}});
 }
 
 // CTA groups of `kernel` that the device holds at once; cached per device.
-template <auto kernel, int CG> int resident_groups() {
+template <auto kernel, int CG> int resident_groups(size_t smem) {
     constexpr int kMaxDev = 64;
     static std::atomic<int> cached[kMaxDev];
     int dev = 0, n = 0;
@@ -552,7 +612,7 @@ template <auto kernel, int CG> int resident_groups() {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CG);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CG;
@@ -564,12 +624,13 @@ template <auto kernel, int CG> int resident_groups() {
     return n;
 }
 
-template <int FORM, int CG>
-int launch_form(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const LinearArgs &a, cudaStream_t st) {
+template <Form FORM, int CG>
+int launch_form(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const LinearArgs &a, cudaStream_t st) {
     constexpr auto kern = ep_linear_kernel<FORM, CG>;
+    constexpr size_t kSmem = smem_bytes(FORM);
     const int rc = allow_smem<kern>(kSmem);
     if (rc != EP_OK) return rc;
-    const int groups = resident_groups<kern, CG>();
+    const int groups = resident_groups<kern, CG>(kSmem);
     if (groups <= 0) return EP_ERR_CUDA;
     constexpr int kM = Walk<FORM, CG>::kM, kN = Walk<FORM, CG>::kN;
     const long long m_tiles = (a.M + kM - 1) / kM;
@@ -587,7 +648,7 @@ int launch_form(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return launch_result(cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, a));
+    return launch_result(cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, a));
 }
 
 // Sizes and pointers common to both calls.
@@ -626,11 +687,16 @@ extern "C" int ep_expert_linear(const void *x, long long x_stride, const void *w
     a.sum = K;
     a.out = (uint16_t *)out;
     a.gate_up = (uint16_t *)gate_up;
-    CUtensorMap ma, mb;
-    if (!encode(&ma, w, 2, K, N, a.G, K, kBlockK, swiglu ? 32 : 128) || !encode(&mb, x, 2, K, a.R_max, 0, x_stride, kBlockK, 32))
-        return EP_ERR_CUDA;
+    const uint64_t k = K, f = a.M, g = a.G, each = (uint64_t)N * K;
+    a.whole_a = swiglu && f % 32 == 0;
+    CUtensorMap ma, mb, mc;
+    bool ok = encode_rows(&mb, x, K, a.R_max, x_stride, 128) && encode_rows(&mc, x, K, a.R_max, x_stride, 32);
+    if (!swiglu) ok = ok && encode(&ma, w, 2, {{k, 1, kBlockK}, {(uint64_t)N, k, 128}, {g, each, 1}});
+    else if (!a.whole_a) ok = ok && encode(&ma, w, 2, {{k, 1, kBlockK}, {2 * f, k, 32}, {g, each, 1}});
+    else ok = ok && encode(&ma, w, 2, {{k, 1, kBlockK}, {32, k, 32}, {2, f * k, 2}, {f / 32, 32 * k, 2}, {g, each, 1}});
+    if (!ok) return EP_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    return swiglu ? launch_form<kGlu, 2>(ma, mb, mb, a, st) : launch_form<kPlain, 2>(ma, mb, mb, a, st);
+    return swiglu ? launch_form<kGlu, 2>(ma, mb, mc, a, st) : launch_form<kPlain, 2>(ma, mb, mc, a, st);
 }
 
 extern "C" int ep_expert_linear_bwd(const void *grad, long long grad_stride, const void *x, long long x_stride, const void *w,
@@ -650,15 +716,18 @@ extern "C" int ep_expert_linear_bwd(const void *grad, long long grad_stride, con
     if (L->T > 0 && (!grad || (grad_x && !w) || (grad_w && !x))) return EP_ERR_INVALID_ARG;
     LinearArgs a = linear_args(L, dtype);
     cudaStream_t st = as_stream(stream);
-    CUtensorMap ma, mb, mo;
+    CUtensorMap ma, mb, mc;
+    const uint64_t k = K, n = N, g = a.G, each = n * k;
     if (grad_x && L->T > 0) {
         a.M = K;
         a.sum = N;
         a.out = (uint16_t *)grad_x;
         a.gate_up = (uint16_t *)const_cast<void *>(gate_up);
-        if (!encode(&ma, w, 2, K, N, a.G, K, 64, kBlockK) || !encode(&mb, grad, 2, N, a.R_max, 0, grad_stride, kBlockK, 32))
-            return EP_ERR_CUDA;
-        const int rc = gate_up ? launch_form<kGradGate, 2>(ma, mb, mb, a, st) : launch_form<kGradX, 2>(ma, mb, mb, a, st);
+        a.whole_a = K % 64 == 0;
+        const bool ok = a.whole_a ? encode(&ma, w, 2, {{64, 1, 64}, {n, k, kBlockK}, {k / 64, 64, 2}, {g, each, 1}})
+                                  : encode(&ma, w, 2, {{k, 1, 64}, {n, k, kBlockK}, {g, each, 1}});
+        if (!ok || !encode_rows(&mb, grad, N, a.R_max, grad_stride, 128) || !encode_rows(&mc, grad, N, a.R_max, grad_stride, 32)) return EP_ERR_CUDA;
+        const int rc = gate_up ? launch_form<kGradGate, 2>(ma, mb, mc, a, st) : launch_form<kGradX, 2>(ma, mb, mc, a, st);
         if (rc != EP_OK) return rc;
     }
     if (!grad_w) return EP_OK;
@@ -666,12 +735,14 @@ extern "C" int ep_expert_linear_bwd(const void *grad, long long grad_stride, con
     a.sum = K;
     a.wide = grad_w_dtype == EP_F32;
     a.add = accumulate;
+    a.whole_a = N % 64 == 0;
+    a.whole_b = K % 64 == 0;
     // without a token there is nothing to load, and the maps only need a valid address
     const bool none = L->T == 0;
     const uint64_t rows = none ? 1 : a.R_max;
-    if (!encode(&ma, none ? grad_w : grad, 2, N, rows, 0, none ? N : grad_stride, 64, kBlockK) ||
-        !encode(&mb, none ? grad_w : x, 2, K, rows, 0, none ? K : x_stride, 64, kBlockK) ||
-        !encode(&mo, grad_w, a.wide ? 4 : 2, K, N, a.G, K, a.wide ? 32 : 64, 32))
+    if (!encode_columns(&ma, none ? grad_w : grad, n, rows, none ? n : grad_stride, a.whole_a) ||
+        !encode_columns(&mb, none ? grad_w : x, k, rows, none ? k : x_stride, a.whole_b) ||
+        !encode(&mc, grad_w, a.wide ? 4 : 2, {{k, 1, a.wide ? 32u : 64u}, {n, k, 32}, {g, each, 1}}))
         return EP_ERR_CUDA;
-    return launch_form<kGradW, 2>(ma, mb, mo, a, st);
+    return launch_form<kGradW, 2>(ma, mb, mc, a, st);
 }

@@ -105,24 +105,31 @@ template <bool kCluster = false> __device__ __forceinline__ bool mbar_wait(uint3
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
-// Into this CTA's shared memory; `bar` may be the barrier of the pair's other CTA when CG is 2.
-template <int CG>
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar) {
-    if constexpr (CG == 2)
-        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                     "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(bar) : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                     "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(bar) : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar) {
-    if constexpr (CG == 2)
-        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                     "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                     "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
+// DIMS coordinates from c[0], the innermost.  Into this CTA's shared memory; `bar` may be the barrier of the pair's other CTA when
+// CG is 2.
+template <int CG, int DIMS>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *m, const int (&c)[DIMS], uint32_t bar) {
+#define EP_TMA_LOAD(group)                                                                                                        \
+    if constexpr (DIMS == 2)                                                                                                      \
+        asm volatile("cp.async.bulk.tensor.2d" group ".shared::cluster.global.tile.mbarrier::complete_tx::bytes "                 \
+                     "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(m), "r"(c[0]), "r"(c[1]), "r"(bar) : "memory");                \
+    else if constexpr (DIMS == 3)                                                                                                 \
+        asm volatile("cp.async.bulk.tensor.3d" group ".shared::cluster.global.tile.mbarrier::complete_tx::bytes "                 \
+                     "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(m), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(bar) : "memory"); \
+    else if constexpr (DIMS == 4)                                                                                                 \
+        asm volatile("cp.async.bulk.tensor.4d" group ".shared::cluster.global.tile.mbarrier::complete_tx::bytes "                 \
+                     "[%0], [%1, {%2, %3, %4, %5}], [%6];"                                                                        \
+                     ::"r"(dst), "l"(m), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]), "r"(bar) : "memory");                        \
+    else                                                                                                                          \
+        asm volatile("cp.async.bulk.tensor.5d" group ".shared::cluster.global.tile.mbarrier::complete_tx::bytes "                 \
+                     "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];"                                                                    \
+                     ::"r"(dst), "l"(m), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]), "r"(c[4]), "r"(bar) : "memory");
+    if constexpr (CG == 2) {
+        EP_TMA_LOAD(".cta_group::2")
+    } else {
+        EP_TMA_LOAD("")
+    }
+#undef EP_TMA_LOAD
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, uint32_t src, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
