@@ -162,6 +162,60 @@ struct Sigmoid {
     }
 };
 
+// Into a stage in shared memory.
+template <int CG> struct Load {
+    uint32_t stage, bar;
+    template <int DIMS> __device__ void operator()(int at, const CUtensorMap &m, const int (&c)[DIMS]) const { tma_load<CG, DIMS>(stage + at, &m, c, bar); }
+};
+
+// The copies of block b of a tile, whose m and n begin at these for the CTA.  One for an operand where its map allows it: each takes
+// the issuing thread some 50 cycles of the 512 that the products of a block last.
+template <Form FORM, int CG> struct Copies {
+    const CUtensorMap &map_a, &map_b, &map_c;
+    const LinearArgs &a;
+    template <typename To> __device__ __forceinline__ void block(const Work &w, int b, int m, int n, int half, const To &to, bool take_a, bool take_b) const {
+        const int k = b * kBlockK;
+        if (take_a) {
+            if constexpr (FORM == kGradW) {
+                if (a.whole_a) {
+                    to(0, map_a, {0, w.row + k, m >> 6});
+                } else {
+                    to(0, map_a, {m, w.row + k});
+                    to(8192, map_a, {m + 64, w.row + k});
+                }
+            } else if constexpr (FORM == kPlain) {
+                to(0, map_a, {k, m, w.g});
+            } else if constexpr (FORM == kGlu) {
+                if (a.whole_a) {
+                    to(0, map_a, {k, 0, 0, m >> 5, w.g});
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) to(i * 4096, map_a, {k, (i & 1) * a.M + m + (i >> 1) * 32, w.g});
+                }
+            } else if (a.whole_a) {
+                to(0, map_a, {0, k, m >> 6, w.g});
+            } else {
+                to(0, map_a, {m, k, w.g});
+                to(8192, map_a, {m + 64, k, w.g});
+            }
+        }
+        if (take_b) {
+            if constexpr (FORM == kGradW) {
+                if (a.whole_b) {
+                    to(kTileA, map_b, {0, w.row + k, n >> 6});
+                } else {
+                    to(kTileA, map_b, {n, w.row + k});
+                    to(kTileA + 8192, map_b, {n + 64, w.row + k});
+                }
+            } else if (half > 96) {
+                to(kTileA, map_b, {k, n});
+            } else {
+                for (int i = 0; i < half; i += 32) to(kTileA + i * 128, map_c, {k, n + i});
+            }
+        }
+    }
+};
+
 template <Form FORM, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -260,43 +314,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         const bool clear = FORM == kGradW && b == w.kb - 1 && (w.last & 15) != 0;
                         const uint32_t bar = clear ? smem_u32(&c.landed[s]) : at_rank(smem_u32(&c.full[s]), 0);
                         mbar_arrive_expect(clear ? at_rank(bar, rank) : bar, bytes);
-                        // One copy for an operand where its map allows it: each copy takes this thread some 50 cycles, of the 512 that
-                        // the products of a block last.
-                        const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kTileA;
-                        const int k = b * kBlockK;
-                        if constexpr (FORM == kGradW) {
-                            if (a.whole_a) {
-                                tma_load<CG, 3>(sa, &map_a, {0, w.row + k, m >> 6}, bar);
-                            } else {
-                                tma_load<CG, 2>(sa, &map_a, {m, w.row + k}, bar);
-                                tma_load<CG, 2>(sa + 8192, &map_a, {m + 64, w.row + k}, bar);
-                            }
-                            if (a.whole_b) {
-                                tma_load<CG, 3>(sb, &map_b, {0, w.row + k, n >> 6}, bar);
-                            } else {
-                                tma_load<CG, 2>(sb, &map_b, {n, w.row + k}, bar);
-                                tma_load<CG, 2>(sb + 8192, &map_b, {n + 64, w.row + k}, bar);
-                            }
-                        } else {
-                            if constexpr (FORM == kPlain) {
-                                tma_load<CG, 3>(sa, &map_a, {k, m, w.g}, bar);
-                            } else if constexpr (FORM == kGlu) {
-                                if (a.whole_a) {
-                                    tma_load<CG, 5>(sa, &map_a, {k, 0, 0, m >> 5, w.g}, bar);
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) tma_load<CG, 3>(sa + i * 4096, &map_a, {k, (i & 1) * a.M + m + (i >> 1) * 32, w.g}, bar);
-                                }
-                            } else if (a.whole_a) {
-                                tma_load<CG, 4>(sa, &map_a, {0, k, m >> 6, w.g}, bar);
-                            } else {
-                                tma_load<CG, 3>(sa, &map_a, {m, k, w.g}, bar);
-                                tma_load<CG, 3>(sa + 8192, &map_a, {m + 64, k, w.g}, bar);
-                            }
-                            if (half > 96) tma_load<CG, 2>(sb, &map_b, {k, n}, bar);
-                            else
-                                for (int i = 0; i < half; i += 32) tma_load<CG, 2>(sb + i * 128, &map_c, {k, n + i}, bar);
-                        }
+                        Copies<FORM, CG>{map_a, map_b, map_c, a}.block(w, b, m, n, half, Load<CG>{smem_u32(smem + s * kStageBytes), bar}, true, true);
                         if (++s == kStages) s = 0, ++round;
                         used = min(used + 1, kStages);
                         if (b == 0) more = walk.next(then);
