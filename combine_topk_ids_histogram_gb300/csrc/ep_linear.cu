@@ -41,9 +41,21 @@ constexpr int kSuper = 8;                    // grad_w: tiles of N that go throu
 // The tensor cores' sums in fp32 truncate, by up to 2^-23 of the sum per 16 products; an fp32 gradient leaves them every 2048 rows.
 constexpr int kChunkRows = 2048;
 
+// A tile: rows or features, and what is summed over.
+struct Work {
+    int g, m, row, n;                        // group (-1: no more tiles); first of M of the pair; first row; valid of N
+    int col;                                 // grad_w: first column
+    int kb, last;                            // blocks of 64 to sum over, and the valid of the last
+    int half;                                // of N, what each CTA loads
+    int first;                               // grad_w: not a later chunk of the same tile
+};
+
+constexpr int kSlots = 8;                    // tiles that the roles may be apart
+
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages];
-    uint64_t sums_full[2], sums_empty[2];
+    uint64_t sums_full[2], sums_empty[2], work_full[kSlots], work_empty[kSlots];
+    Work work[kSlots];
     uint32_t tmem, skip;
     int part[kThreads / 32];
     int off[kMaxGroups + 1];                 // first row of each group
@@ -63,15 +75,7 @@ struct LinearArgs {
     uint16_t *out, *gate_up;                 // gate_up: saved by kGlu, read by kGradGate
 };
 
-// A tile: rows or features, and what is summed over.
-struct Work {
-    int g, m, row, n;                        // group; first of M of the pair; first row; valid of N
-    int col;                                 // grad_w: first column
-    int kb, last;                            // blocks of 64 to sum over, and the valid of the last
-    bool first;                              // grad_w: not a later chunk of the same tile
-};
-
-// The tiles of a CTA pair in turn.  Every role walks them for itself.
+// The tiles of a CTA pair in turn.
 template <Form FORM, int CG> struct Walk {
     static constexpr int kM = FORM == kGlu ? 64 * CG : 128 * CG, kN = 128 * CG;
     static constexpr int kUnit = 16 * CG;    // of N in a product
@@ -82,11 +86,6 @@ template <Form FORM, int CG> struct Walk {
     __device__ Walk(const LinearArgs &a_, const Control &c_, int first, int step_)
         : a(a_), c(c_), tile(first - step_), step(step_), m_tiles((a_.M + kM - 1) / kM), g(0), chunk(0) {
         tiles = FORM == kGradW ? a.G * m_tiles * ((a.sum + kN - 1) / kN) : c.start[a.G];
-    }
-    // Of N, what each CTA loads: whole blocks of 64 where one copy brings them.
-    __device__ int half(const Work &w) const {
-        const int unit = FORM == kGradW && a.whole_b ? 64 : kUnit / CG;
-        return (w.n + unit * CG - 1) / (unit * CG) * unit;
     }
     __device__ bool next(Work &w) {
         if constexpr (FORM == kGradW) {
@@ -129,7 +128,29 @@ template <Form FORM, int CG> struct Walk {
             w.kb = (a.sum + kBlockK - 1) / kBlockK;
             w.last = a.sum - (w.kb - 1) * kBlockK;
         }
+        // whole blocks of 64 where one copy brings them
+        const int unit = FORM == kGradW && a.whole_b ? 64 : kUnit / CG;
+        w.half = (w.n + unit * CG - 1) / (unit * CG) * unit;
         return true;
+    }
+};
+
+// A role's view of them: one warp looks tiles up ahead of the others and hands them over in shared memory, since the look-up takes
+// some 700 cycles, in which no copy or product would be issued.
+struct Feed {
+    Control &c;
+    int i;
+    // Called by a whole warp, or by one lane alone.
+    template <bool kWarp> __device__ bool next(Work &w, uint32_t rank, bool &ok) {
+        const int s = i % kSlots;
+        ok = mbar_wait(smem_u32(&c.work_full[s]), i / kSlots & 1);
+        if constexpr (kWarp) ok = __all_sync(kFullMask, ok);
+        if (!ok) return false;
+        w = c.work[s];
+        ++i;
+        if constexpr (kWarp) __syncwarp();
+        if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(at_rank(smem_u32(&c.work_empty[s]), rank));
+        return w.g >= 0;
     }
 };
 
@@ -243,6 +264,11 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             mbar_init(smem_u32(&c.sums_full[b]), 1);
             mbar_init(smem_u32(&c.sums_empty[b]), 4 * kOutGroups * CG);
         }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(smem_u32(&c.work_full[s]), 1);
+            // loads, results, products in the first CTA, rows to clear
+            mbar_init(smem_u32(&c.work_empty[s]), 1 + 4 * kOutGroups + (rank == 0) + (FORM == kGradW));
+        }
         mbar_init_done();
     }
     if (warp == 2) tmem_alloc<CG>(smem_u32(&c.tmem), 2 * kCols);
@@ -296,16 +322,14 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     const uint32_t tmem = c.tmem;
     bool ok = true;                                      // false: a wait ran out
     if (c.skip == 0) {
-        Walk<FORM, CG> walk(a, c, pair, pairs);
+        Feed feed{c, 0};
         Work w = {};
         if (warp == 0) {                                 // ------------------------------------------------ loads
             if (elect_one()) {
                 int s = 0, used = 0;
                 uint32_t round = 0;
-                bool more = walk.next(w);
-                while (ok && more) {
-                    Work then = w;                       // the next tile, looked up while this one's loads are on their way
-                    const int half = walk.half(w), m = w.m + (int)rank * (Walk<FORM, CG>::kM / CG);
+                while (ok && feed.next<false>(w, rank, ok)) {
+                    const int half = w.half, m = w.m + (int)rank * (Walk<FORM, CG>::kM / CG);
                     const int n = (FORM == kGradW ? w.col : w.row) + (int)rank * half;
                     const uint32_t bytes = kTileA + (FORM == kGradW || half > 96 ? kTileB : ((half + 31) >> 5) * 4096);
                     for (int b = 0; b < w.kb; ++b) {
@@ -317,10 +341,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         Copies<FORM, CG>{map_a, map_b, map_c, a}.block(w, b, m, n, half, Load<CG>{smem_u32(smem + s * kStageBytes), bar}, true, true);
                         if (++s == kStages) s = 0, ++round;
                         used = min(used + 1, kStages);
-                        if (b == 0) more = walk.next(then);
                     }
-                    if (w.kb == 0) more = walk.next(then);
-                    w = then;
                 }
                 // Nothing of the pair may still be on its way to this CTA when it ends.
                 for (int i = 0; ok && i < used; ++i) {
@@ -339,16 +360,11 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 uint32_t round = 0, tiles = 0;
                 const uint32_t idesc = mma_desc(a.f16 != 0, 128 * CG, 0, kAmn, kBmn);
                 const uint64_t desc = smem_desc(smem_u32(smem), 8192);
-                bool more = walk.next(w);
-                while (ok && more) {
-                    Work then = w;
-                    if (w.kb == 0) {
-                        more = walk.next(w);
-                        continue;
-                    }
+                while (ok && feed.next<true>(w, rank, ok)) {
+                    if (w.kb == 0) continue;
                     if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_empty[buf]), ((tiles >> 1) & 1) ^ 1)))) break;
                     tc_fence_after();
-                    const uint32_t id = idesc | (uint32_t)(walk.half(w) * CG >> 4) << 18;
+                    const uint32_t id = idesc | (uint32_t)(w.half * CG >> 4) << 18;
                     const uint32_t d = tmem + buf * kCols;
                     for (int b = 0; b < w.kb; ++b) {
                         const bool last = b == w.kb - 1, cleared = FORM == kGradW && last && (w.last & 15) != 0;
@@ -366,9 +382,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         }
                         __syncwarp();
                         if (++s == kStages) s = 0, ++round;
-                        if (b == 0) more = walk.next(then);
                     }
-                    w = then;
                     buf ^= 1;
                     ++tiles;
                 }
@@ -377,7 +391,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             if constexpr (FORM == kGradW) {
                 int s = 0;
                 uint32_t seen = 0;                       // parity of landed[s]
-                while (ok && walk.next(w)) {
+                while (ok && feed.next<true>(w, rank, ok)) {
                     s = (s + max(w.kb - 1, 0)) % kStages;
                     if (w.kb == 0) continue;
                     if (w.last & 15) {
@@ -395,6 +409,17 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                     if (++s == kStages) s = 0;
                 }
             }
+        } else if (warp == 3) {                          // ------------------------------------------------ tiles
+            if (elect_one()) {
+                Walk<FORM, CG> walk(a, c, pair, pairs);
+                for (int i = 0; ok && w.g >= 0; ++i) {
+                    if (!walk.next(w)) w.g = -1;
+                    const int s = i % kSlots;
+                    if (i >= kSlots && !(ok = mbar_wait(smem_u32(&c.work_empty[s]), (i / kSlots & 1) ^ 1))) break;
+                    c.work[s] = w;
+                    mbar_arrive(at_rank(smem_u32(&c.work_full[s]), rank));
+                }
+            }
         } else if (warp >= 4) {                          // ------------------------------------------------ results
             const int q = warp & 3, part = (warp - 4) >> 2, et = tid & 127, bar = 1 + 3 * part;
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
@@ -402,7 +427,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             uint32_t tiles = 0;
             uint8_t *const own = staging + part * kStaging;
             uint16_t *const st16 = reinterpret_cast<uint16_t *>(own);
-            while (ok && walk.next(w)) {
+            while (ok && feed.next<true>(w, rank, ok)) {
                 const int m0 = w.m + (int)rank * (Walk<FORM, CG>::kM / CG);          // first feature of this CTA
                 const uint32_t sums = lanes + buf * kCols;
                 const int chunks = (w.n + 31) >> 5;
