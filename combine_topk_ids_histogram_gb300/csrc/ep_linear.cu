@@ -11,6 +11,7 @@
 // keeps the sums of its 128 of M in tensor memory, twice, so that one tile's results leave while the next one's
 // are added up.  Warp 0 loads, warp 1 of the first CTA issues the products, warps 4 to 11 take results out, four at a time 32
 // columns; warp 2 (grad_w) clears the rows behind a group's last one in shared memory, since there they are summed over.
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -50,11 +51,13 @@ struct Work {
     int first;                               // grad_w: not a later chunk of the same tile
 };
 
-constexpr int kSlots = 8;                    // tiles that the roles may be apart
+constexpr int kSlots = 3;                    // tiles that the roles may be apart, and be taken ahead
 
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages];
     uint64_t sums_full[2], sums_empty[2], work_full[kSlots], work_empty[kSlots];
+    uint64_t drawn, read;                    // the answer to a request for the next tile: arrived, and read by both CTAs
+    uint4 answer;
     Work work[kSlots];
     uint32_t tmem, skip;
     int part[kThreads / 32];
@@ -75,44 +78,30 @@ struct LinearArgs {
     uint16_t *out, *gate_up;                 // gate_up: saved by kGlu, read by kGradGate
 };
 
-// The tiles of a CTA pair in turn.
-template <Form FORM, int CG> struct Walk {
+// What tile number `tile` is.
+template <Form FORM, int CG> struct Tiles {
     static constexpr int kM = FORM == kGlu ? 64 * CG : 128 * CG, kN = 128 * CG;
     static constexpr int kUnit = 16 * CG;    // of N in a product
     const LinearArgs &a;
     const Control &c;
-    int tile, step, tiles, m_tiles, g, chunk;
 
-    __device__ Walk(const LinearArgs &a_, const Control &c_, int first, int step_)
-        : a(a_), c(c_), tile(first - step_), step(step_), m_tiles((a_.M + kM - 1) / kM), g(0), chunk(0) {
-        tiles = FORM == kGradW ? a.G * m_tiles * ((a.sum + kN - 1) / kN) : c.start[a.G];
-    }
-    __device__ bool next(Work &w) {
+    // False behind the last one.
+    __device__ bool look_up(int tile, Work &w) {
+        const int m_tiles = (a.M + kM - 1) / kM;
         if constexpr (FORM == kGradW) {
-            const int rows = tile < 0 ? 0 : c.off[w.g + 1] - c.off[w.g];
-            if (a.wide && tile >= 0 && (chunk + 1) * kChunkRows < rows) {
-                ++chunk;
-            } else {
-                chunk = 0;
-                tile += step;
-                if (tile >= tiles) return false;
-                const int n_tiles = (a.sum + kN - 1) / kN, in = tile % (m_tiles * n_tiles);
-                w.g = tile / (m_tiles * n_tiles);
-                const int first = in / (kSuper * n_tiles) * kSuper, wide = min(kSuper, m_tiles - first), at = in - first * n_tiles;
-                w.m = (first + at % wide) * kM;
-                w.col = at / wide * kN;
-                w.n = min(kN, a.sum - w.col);
-            }
-            w.first = chunk == 0;
-            w.row = c.off[w.g] + chunk * kChunkRows;
-            int left = max(c.off[w.g + 1] - w.row, 0);
-            if (a.wide) left = min(left, kChunkRows);
-            w.kb = (left + kBlockK - 1) / kBlockK;
-            w.last = left - (w.kb - 1) * kBlockK;
+            const int n_tiles = (a.sum + kN - 1) / kN, in = tile % (m_tiles * n_tiles);
+            w.g = tile / (m_tiles * n_tiles);
+            if (w.g >= a.G) return false;
+            const int first = in / (kSuper * n_tiles) * kSuper, wide = min(kSuper, m_tiles - first), at = in - first * n_tiles;
+            w.m = (first + at % wide) * kM;
+            w.col = at / wide * kN;
+            w.n = min(kN, a.sum - w.col);
+            w.row = c.off[w.g];
+            w.first = 1;
+            blocks(w);
         } else {
-            tile += step;
-            if (tile >= tiles) return false;
-            int hi = a.G;                    // the last group that begins at or before the tile
+            if (tile >= c.start[a.G]) return false;
+            int g = 0, hi = a.G;             // the last group that begins at or before the tile
             while (hi - g > 1) {
                 const int mid = (g + hi) >> 1;
                 if (c.start[mid] <= tile) g = mid;
@@ -132,6 +121,20 @@ template <Form FORM, int CG> struct Walk {
         const int unit = FORM == kGradW && a.whole_b ? 64 : kUnit / CG;
         w.half = (w.n + unit * CG - 1) / (unit * CG) * unit;
         return true;
+    }
+    // grad_w: the next chunk of the same tile.
+    __device__ bool next_chunk(Work &w) {
+        if (FORM != kGradW || !a.wide || w.row + kChunkRows >= c.off[w.g + 1]) return false;
+        w.row += kChunkRows;
+        w.first = 0;
+        blocks(w);
+        return true;
+    }
+    __device__ void blocks(Work &w) {
+        int left = max(c.off[w.g + 1] - w.row, 0);
+        if (a.wide) left = min(left, kChunkRows);
+        w.kb = (left + kBlockK - 1) / kBlockK;
+        w.last = left - (w.kb - 1) * kBlockK;
     }
 };
 
@@ -249,7 +252,6 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     Control &c = *reinterpret_cast<Control *>(staging + kOutGroups * kStaging);
     const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-    const int pair = blockIdx.x / CG, pairs = gridDim.x / CG;
 
     if (CG == 2) cluster_arrive();
     if (tid == 0) {
@@ -264,6 +266,8 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             mbar_init(smem_u32(&c.sums_full[b]), 1);
             mbar_init(smem_u32(&c.sums_empty[b]), 4 * kOutGroups * CG);
         }
+        mbar_init(smem_u32(&c.drawn), 1);
+        mbar_init(smem_u32(&c.read), CG);
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(smem_u32(&c.work_full[s]), 1);
             // loads, results, products in the first CTA, rows to clear
@@ -290,7 +294,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     }
     __syncthreads();
     if (FORM != kGradW) {
-        const int m_tiles = (a.M + Walk<FORM, CG>::kM - 1) / Walk<FORM, CG>::kM;
+        const int m_tiles = (a.M + Tiles<FORM, CG>::kM - 1) / Tiles<FORM, CG>::kM;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             mine[i] = 0;
@@ -329,7 +333,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 int s = 0, used = 0;
                 uint32_t round = 0;
                 while (ok && feed.next<false>(w, rank, ok)) {
-                    const int half = w.half, m = w.m + (int)rank * (Walk<FORM, CG>::kM / CG);
+                    const int half = w.half, m = w.m + (int)rank * (Tiles<FORM, CG>::kM / CG);
                     const int n = (FORM == kGradW ? w.col : w.row) + (int)rank * half;
                     const uint32_t bytes = kTileA + (FORM == kGradW || half > 96 ? kTileB : ((half + 31) >> 5) * 4096);
                     for (int b = 0; b < w.kb; ++b) {
@@ -411,14 +415,38 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             }
         } else if (warp == 3) {                          // ------------------------------------------------ tiles
             if (elect_one()) {
-                Walk<FORM, CG> walk(a, c, pair, pairs);
-                for (int i = 0; ok && w.g >= 0; ++i) {
-                    if (!walk.next(w)) w.g = -1;
-                    const int s = i % kSlots;
-                    if (i >= kSlots && !(ok = mbar_wait(smem_u32(&c.work_empty[s]), (i / kSlots & 1) ^ 1))) break;
-                    c.work[s] = w;
-                    mbar_arrive(at_rank(smem_u32(&c.work_full[s]), rank));
+                Tiles<FORM, CG> tiles{a, c};
+                const uint32_t read = at_rank(smem_u32(&c.read), 0);
+                int tile = blockIdx.x / CG, slot = 0;
+                uint32_t round = 0;
+                auto hand_over = [&]() {
+                    if (round > 0 && !(ok = mbar_wait(smem_u32(&c.work_empty[slot]), (round & 1) ^ 1))) return;
+                    c.work[slot] = w;
+                    mbar_arrive(at_rank(smem_u32(&c.work_full[slot]), rank));
+                    if (++slot == kSlots) slot = 0, ++round;
+                };
+                for (uint32_t i = 0; ok; ++i) {
+                    const bool some = tile >= 0 && tiles.look_up(tile, w);
+                    if (tile >= 0) {                     // ask for the next one, once both CTAs have read the last answer
+                        mbar_arrive_expect(at_rank(smem_u32(&c.drawn), rank), 16);
+                        if (rank == 0) {
+                            if (i > 0 && !(ok = mbar_wait(smem_u32(&c.read), (i & 1) ^ 1))) break;
+                            next_cluster_request(smem_u32(&c.answer), smem_u32(&c.drawn));
+                        }
+                    }
+                    if (some) {
+                        hand_over();
+                        while (ok && tiles.next_chunk(w)) hand_over();
+                    }
+                    if (!ok || tile < 0) break;
+                    if (!(ok = mbar_wait(smem_u32(&c.drawn), i & 1))) break;
+                    tile = next_cluster_block(smem_u32(&c.answer));
+                    if (tile >= 0) tile /= CG;
+                    fence_proxy_async_smem();
+                    mbar_arrive(read);
                 }
+                w.g = -1;
+                if (ok) hand_over();
             }
         } else if (warp >= 4) {                          // ------------------------------------------------ results
             const int q = warp & 3, part = (warp - 4) >> 2, et = tid & 127, bar = 1 + 3 * part;
@@ -428,7 +456,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             uint8_t *const own = staging + part * kStaging;
             uint16_t *const st16 = reinterpret_cast<uint16_t *>(own);
             while (ok && feed.next<true>(w, rank, ok)) {
-                const int m0 = w.m + (int)rank * (Walk<FORM, CG>::kM / CG);          // first feature of this CTA
+                const int m0 = w.m + (int)rank * (Tiles<FORM, CG>::kM / CG);          // first feature of this CTA
                 const uint32_t sums = lanes + buf * kCols;
                 const int chunks = (w.n + 31) >> 5;
                 if constexpr (FORM == kGradW) {
@@ -644,42 +672,18 @@ bool encode_columns(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows,
     return whole ? encode(m, p, 2, {{64, 1, 64}, {rows, ld, kBlockK}, {cols / 64, 64, 2}}) : encode(m, p, 2, {{cols, 1, 64}, {rows, ld, kBlockK}});
 }
 
-// CTA groups of `kernel` that the device holds at once; cached per device.
-template <auto kernel, int CG> int resident_groups(size_t smem) {
-    constexpr int kMaxDev = 64;
-    static std::atomic<int> cached[kMaxDev];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    const bool cacheable = dev >= 0 && dev < kMaxDev;
-    if (cacheable && (n = cached[dev].load(std::memory_order_relaxed)) > 0) return n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CG);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
-    if (cacheable) cached[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 template <Form FORM, int CG>
 int launch_form(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const LinearArgs &a, cudaStream_t st) {
     constexpr auto kern = ep_linear_kernel<FORM, CG>;
     constexpr size_t kSmem = smem_bytes(FORM);
     const int rc = allow_smem<kern>(kSmem);
     if (rc != EP_OK) return rc;
-    const int groups = resident_groups<kern, CG>(kSmem);
-    if (groups <= 0) return EP_ERR_CUDA;
-    constexpr int kM = Walk<FORM, CG>::kM, kN = Walk<FORM, CG>::kN;
+    constexpr int kM = Tiles<FORM, CG>::kM, kN = Tiles<FORM, CG>::kN;
     const long long m_tiles = (a.M + kM - 1) / kM;
     const long long tiles = m_tiles * (FORM == kGradW ? (long long)a.G * ((a.sum + kN - 1) / kN) : (long long)a.R_max / kN + std::min(a.G, a.R_max));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::max(1ll, std::min<long long>(groups, tiles)) * CG);
+    if (tiles > INT_MAX / CG) return EP_ERR_INVALID_ARG;
+    cfg.gridDim = dim3((unsigned)std::max(1ll, tiles) * CG);        // the most there can be; clusters that run take them in turn
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;

@@ -100,6 +100,25 @@ template <bool kCluster = false> __device__ __forceinline__ bool mbar_wait(uint3
 }
 
 // ---------------------------------------------------------------------------------------
+// Work of clusters that have not begun: a running cluster takes the place of one of its own grid, which is then never
+// launched.  The answer (16 bytes, 16-byte aligned) and its count on `bar` go to the same addresses in every CTA of the cluster.
+// After an answer without a cluster no further request may be made.
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ void next_cluster_request(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], [%1];"
+                 ::"r"(answer), "r"(bar) : "memory");
+}
+// The first block of the cluster that this one replaces, or -1.
+__device__ __forceinline__ int next_cluster_block(uint32_t answer) {
+    int x;
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%1];\n\tmov.b32 %0, -1;\n\t"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+                 : "=r"(x) : "r"(answer) : "memory");
+    return x;
+}
+
+// ---------------------------------------------------------------------------------------
 // Tiled TMA copies.  c0 (the innermost coordinate) times the element size is a multiple of 16 bytes everywhere.
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *m) {
