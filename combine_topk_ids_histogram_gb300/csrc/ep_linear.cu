@@ -34,10 +34,10 @@ constexpr int kTileB = 128 * kBlockK * 2;
 constexpr int kStageBytes = kTileA + kTileB;
 constexpr int kCols = 256;                   // columns of tensor memory per tile's sums
 constexpr int kMaxGroups = kMaxE + 1;
-constexpr int kMaxStages = 5;
-// Bytes in which a group of four warps turns its results into rows, and the stages that there is room for.
-__host__ __device__ constexpr int staging_bytes(Form f) { return f == kPlain || f == kGradX ? 16384 : 32768; }
-__host__ __device__ constexpr int stages_of(Form f) { return f == kPlain || f == kGradX ? 5 : 4; }
+// As many stages as fit.  What they hide is the way from L2: with 3 / 4 / 5 of them the gated products of 8192 tokens, top-8 of 128,
+// 2048 -> 2 x 768 took 327 / 294 / 272 us, the down products 188 / 172 / 156.
+constexpr int kStages = 6;
+constexpr int kStaging = 16384;              // bytes in which a group of four warps turns its results into rows
 constexpr int kSuper = 8;                    // grad_w: tiles of N that go through all of K before the next
 // The tensor cores' sums in fp32 truncate, by up to 2^-23 of the sum per 16 products; an fp32 gradient leaves them every 2048 rows.
 constexpr int kChunkRows = 2048;
@@ -45,7 +45,7 @@ constexpr int kChunkRows = 2048;
 // A tile: rows or features, and what is summed over.
 struct Work {
     int g, m, row, n;                        // group (-1: no more tiles); first of M of the pair; first row; valid of N
-    int col;                                 // grad_w: first column
+    int col, end;                            // grad_w: first column; row behind the group's last
     int kb, last;                            // blocks of 64 to sum over, and the valid of the last
     int half;                                // of N, what each CTA loads
     int first;                               // grad_w: not a later chunk of the same tile
@@ -54,18 +54,17 @@ struct Work {
 constexpr int kSlots = 3;                    // tiles that the roles may be apart, and be taken ahead
 
 struct Control {
-    uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages];
+    uint64_t full[kStages], empty[kStages], landed[kStages];
     uint64_t sums_full[2], sums_empty[2], work_full[kSlots], work_empty[kSlots];
     uint64_t drawn, read;                    // the answer to a request for the next tile: arrived, and read by both CTAs
     uint4 answer;
     Work work[kSlots];
     uint32_t tmem, skip;
     int part[kThreads / 32];
-    int off[kMaxGroups + 1];                 // first row of each group
-    int start[kMaxGroups + 1];               // first tile of each group
+    int start[(kMaxGroups + 1) / 2 + 1];     // first tile of every other group
 };
-constexpr size_t smem_bytes(Form f) { return 1024 + stages_of(f) * kStageBytes + kOutGroups * staging_bytes(f) + sizeof(Control); }
-static_assert(smem_bytes(kPlain) <= 227 * 1024 && smem_bytes(kGradW) <= 227 * 1024, "shared memory of a CTA");
+constexpr size_t kSmem = (size_t)kStages * kStageBytes + kOutGroups * kStaging + sizeof(Control);
+static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 
 struct LinearArgs {
     const int32_t *row_offsets;
@@ -74,7 +73,7 @@ struct LinearArgs {
     int M;                                   // of the output: features of a row (gated: F), rows of a weight gradient
     int sum;                                 // length of the sums (forms that sum over rows: columns of the output)
     int f16, wide, add;                      // operands fp16; grad_w: fp32 output, added to what is there
-    int whole_a, whole_b;                    // whether the operand's map has the blocks of 64 (kGlu: the 32 gates and ups) as dimensions
+    int whole_a, whole_b;                    // whether the operand's map has the blocks of 64 as a dimension
     uint16_t *out, *gate_up;                 // gate_up: saved by kGlu, read by kGradGate
 };
 
@@ -85,8 +84,11 @@ template <Form FORM, int CG> struct Tiles {
     const LinearArgs &a;
     const Control &c;
 
+    // A group's first row, inside the buffers whatever the layout says.
+    __device__ int off(int g) const { return min(max(a.row_offsets[g], 0), a.R_max); }
+    __device__ int parts(int rows) const { return (max(rows, 0) + kN - 1) / kN; }
     // False behind the last one.
-    __device__ bool look_up(int tile, Work &w) {
+    __device__ bool look_up(int tile, Work &w) const {
         const int m_tiles = (a.M + kM - 1) / kM;
         if constexpr (FORM == kGradW) {
             const int n_tiles = (a.sum + kN - 1) / kN, in = tile % (m_tiles * n_tiles);
@@ -96,23 +98,31 @@ template <Form FORM, int CG> struct Tiles {
             w.m = (first + at % wide) * kM;
             w.col = at / wide * kN;
             w.n = min(kN, a.sum - w.col);
-            w.row = c.off[w.g];
+            w.row = off(w.g);
+            w.end = off(w.g + 1);
             w.first = 1;
             blocks(w);
         } else {
-            if (tile >= c.start[a.G]) return false;
-            int g = 0, hi = a.G;             // the last group that begins at or before the tile
-            while (hi - g > 1) {
-                const int mid = (g + hi) >> 1;
-                if (c.start[mid] <= tile) g = mid;
+            int p = 0, hi = (a.G + 1) / 2;   // the last two groups that begin at or before the tile
+            if (tile >= c.start[hi]) return false;
+            while (hi - p > 1) {
+                const int mid = (p + hi) >> 1;
+                if (c.start[mid] <= tile) p = mid;
                 else hi = mid;
             }
-            const int rows = c.off[g + 1] - c.off[g], parts = (rows + kN - 1) / kN, in = tile - c.start[g];
+            int g = 2 * p, begin = off(g), end = off(g + 1), in = tile - c.start[p];
+            const int behind = off(min(g + 2, a.G)), tiles = parts(end - begin) * m_tiles;
+            if (in >= tiles) {
+                in -= tiles;
+                begin = end;
+                end = behind;
+                ++g;
+            }
             // the group's rows in equal parts: a part of few rows would load the weights for little work
-            const int part = ((rows + parts - 1) / parts + kUnit - 1) / kUnit * kUnit, at = in % parts * part;
+            const int rows = end - begin, n = parts(rows), part = ((rows + n - 1) / n + kUnit - 1) / kUnit * kUnit, at = in % n * part;
             w.g = g;
-            w.m = in / parts * kM;
-            w.row = c.off[g] + at;
+            w.m = in / n * kM;
+            w.row = begin + at;
             w.n = min(part, rows - at);
             w.kb = (a.sum + kBlockK - 1) / kBlockK;
             w.last = a.sum - (w.kb - 1) * kBlockK;
@@ -123,15 +133,15 @@ template <Form FORM, int CG> struct Tiles {
         return true;
     }
     // grad_w: the next chunk of the same tile.
-    __device__ bool next_chunk(Work &w) {
-        if (FORM != kGradW || !a.wide || w.row + kChunkRows >= c.off[w.g + 1]) return false;
+    __device__ bool next_chunk(Work &w) const {
+        if (FORM != kGradW || !a.wide || w.row + kChunkRows >= w.end) return false;
         w.row += kChunkRows;
         w.first = 0;
         blocks(w);
         return true;
     }
-    __device__ void blocks(Work &w) {
-        int left = max(c.off[w.g + 1] - w.row, 0);
+    __device__ void blocks(Work &w) const {
+        int left = max(w.end - w.row, 0);
         if (a.wide) left = min(left, kChunkRows);
         w.kb = (left + kBlockK - 1) / kBlockK;
         w.last = left - (w.kb - 1) * kBlockK;
@@ -210,12 +220,7 @@ template <Form FORM, int CG> struct Copies {
             } else if constexpr (FORM == kPlain) {
                 to(0, map_a, {k, m, w.g});
             } else if constexpr (FORM == kGlu) {
-                if (a.whole_a) {
-                    to(0, map_a, {k, 0, 0, m >> 5, w.g});
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) to(i * 4096, map_a, {k, (i & 1) * a.M + m + (i >> 1) * 32, w.g});
-                }
+                to(0, map_a, {k, 0, 0, m >> 4, w.g});
             } else if (a.whole_a) {
                 to(0, map_a, {0, k, m >> 6, w.g});
             } else {
@@ -244,10 +249,8 @@ template <Form FORM, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ CUtensorMap map_c, const LinearArgs a) {
-    constexpr int kStages = stages_of(FORM), kStaging = staging_bytes(FORM);
     constexpr bool kAmn = FORM == kGradX || FORM == kGradGate || FORM == kGradW, kBmn = FORM == kGradW;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *const smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    extern __shared__ __align__(1024) uint8_t smem[];    // nothing else is in shared memory, so that it begins on such a boundary
     uint8_t *const staging = smem + kStages * kStageBytes;
     Control &c = *reinterpret_cast<Control *>(staging + kOutGroups * kStaging);
     const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
@@ -277,29 +280,29 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     }
     if (warp == 2) tmem_alloc<CG>(smem_u32(&c.tmem), 2 * kCols);
     pdl_begin();
-    // Groups' rows, kept inside the buffers whatever the layout says, and a running count of their tiles.
-    constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
-    const int per = (a.G + kThreads - 1) / kThreads, g0 = tid * per;
-    int mine[kPer], sum = 0;
-    for (int i = tid; i <= a.G; i += kThreads) {
-        const int v = a.row_offsets[i];
-        if (v < 0 || v > a.R_max) bounds_fail(a.status);
-        c.off[i] = min(max(v, 0), a.R_max);
-    }
     if (CG == 2) cluster_wait();                         // the other CTA has begun
     if (tid == 0 && rank == 0) {                         // the pair acts on one reading of the status
         const uint32_t st = (uint32_t)load_status(a.status);
         c.skip = st;
         if (CG == 2) st_cluster(at_rank(smem_u32(&c.skip), 1), st);
     }
-    __syncthreads();
-    if (FORM != kGradW) {
-        const int m_tiles = (a.M + Tiles<FORM, CG>::kM - 1) / Tiles<FORM, CG>::kM;
+    const Tiles<FORM, CG> tiles{a, c};
+    if (kBoundsCheck) {
+        for (int i = tid; i <= a.G; i += kThreads)
+            if (a.row_offsets[i] != tiles.off(i)) bounds_fail(a.status);
+    }
+    if (FORM != kGradW) {                                // a running count of the groups' tiles
+        constexpr int kPer = ((kMaxGroups + 1) / 2 + kThreads - 1) / kThreads;
+        const int m_tiles = (a.M + tiles.kM - 1) / tiles.kM, n = (a.G + 1) / 2, per = (n + kThreads - 1) / kThreads;
+        int mine[kPer], sum = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             mine[i] = 0;
-            if (i < per && g0 + i < a.G)
-                mine[i] = (max(c.off[g0 + i + 1] - c.off[g0 + i], 0) + 128 * CG - 1) / (128 * CG) * m_tiles;
+            const int g = 2 * (tid * per + i);
+            if (i < per && g < a.G) {
+                const int b0 = tiles.off(g), b1 = tiles.off(g + 1), b2 = tiles.off(min(g + 2, a.G));
+                mine[i] = (tiles.parts(b1 - b0) + tiles.parts(b2 - b1)) * m_tiles;
+            }
             sum += mine[i];
         }
         int run = sum;
@@ -314,10 +317,10 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         for (int w = 0; w < warp; ++w) run += c.part[w];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            if (i < per && g0 + i < a.G) c.start[g0 + i] = run;
+            if (i < per && tid * per + i < n) c.start[tid * per + i] = run;
             run += mine[i];
         }
-        if (tid == kThreads - 1) c.start[a.G] = run;
+        if (tid == kThreads - 1) c.start[n] = run;
     }
     tc_fence_before();
     __syncthreads();
@@ -361,12 +364,12 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         } else if (warp == 1) {                          // ------------------------------------------------ products
             if (rank == 0) {                             // the whole warp keeps step, one lane issues
                 int s = 0, buf = 0;
-                uint32_t round = 0, tiles = 0;
+                uint32_t round = 0, done = 0;
                 const uint32_t idesc = mma_desc(a.f16 != 0, 128 * CG, 0, kAmn, kBmn);
                 const uint64_t desc = smem_desc(smem_u32(smem), 8192);
                 while (ok && feed.next<true>(w, rank, ok)) {
                     if (w.kb == 0) continue;
-                    if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_empty[buf]), ((tiles >> 1) & 1) ^ 1)))) break;
+                    if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_empty[buf]), ((done >> 1) & 1) ^ 1)))) break;
                     tc_fence_after();
                     const uint32_t id = idesc | (uint32_t)(w.half * CG >> 4) << 18;
                     const uint32_t d = tmem + buf * kCols;
@@ -388,7 +391,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         if (++s == kStages) s = 0, ++round;
                     }
                     buf ^= 1;
-                    ++tiles;
+                    ++done;
                 }
             }
         } else if (warp == 2) {                          // ------------------------------------------------ rows to clear
@@ -415,7 +418,6 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             }
         } else if (warp == 3) {                          // ------------------------------------------------ tiles
             if (elect_one()) {
-                Tiles<FORM, CG> tiles{a, c};
                 const uint32_t read = at_rank(smem_u32(&c.read), 0);
                 int tile = blockIdx.x / CG, slot = 0;
                 uint32_t round = 0;
@@ -449,28 +451,26 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 if (ok) hand_over();
             }
         } else if (warp >= 4) {                          // ------------------------------------------------ results
-            const int q = warp & 3, part = (warp - 4) >> 2, et = tid & 127, bar = 1 + 3 * part;
+            const int q = warp & 3, part = (warp - 4) >> 2, et = tid & 127, bar = 1 + part;
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
             int buf = 0;
-            uint32_t tiles = 0;
+            uint32_t done = 0;
             uint8_t *const own = staging + part * kStaging;
             uint16_t *const st16 = reinterpret_cast<uint16_t *>(own);
             while (ok && feed.next<true>(w, rank, ok)) {
                 const int m0 = w.m + (int)rank * (Tiles<FORM, CG>::kM / CG);          // first feature of this CTA
                 const uint32_t sums = lanes + buf * kCols;
-                const int chunks = (w.n + 31) >> 5;
                 if constexpr (FORM == kGradW) {
                     if (w.kb > 0) {
-                        if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_full[buf]), (tiles >> 1) & 1)))) break;
+                        if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_full[buf]), (done >> 1) & 1)))) break;
                         tc_fence_after();
                     }
                     // 32 rows of 128 bytes per warp at a time: 32 columns of fp32 or 64 of 16 bits, swizzled as TMA reads them
                     const int cols = a.wide ? 32 : 64;
-                    int at = 0;
                     if (!w.first && lane == 0) bulk_wait_all();      // the chunk before, added up
-                    for (int col = part * cols; col < w.n; col += kOutGroups * cols, at ^= 1) {
-                        uint8_t *const line = own + (q * 2 + at) * 4096 + lane * 128;
-                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    for (int col = part * cols; col < w.n; col += kOutGroups * cols) {
+                        uint8_t *const line = own + q * 4096 + lane * 128;
+                        if (lane == 0) bulk_wait_read_all();
                         __syncwarp();
                         float v[32] = {};
                         if (a.wide) {
@@ -499,7 +499,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0 && m0 + q * 32 < a.M) {
-                            const uint32_t src = smem_u32(own + (q * 2 + at) * 4096);
+                            const uint32_t src = smem_u32(own + q * 4096);
                             if (a.wide && (a.add || !w.first)) tma_add_3d(&map_c, src, w.col + col, m0 + q * 32, w.g);
                             else tma_store_3d(&map_c, src, w.col + col, m0 + q * 32, w.g);
                         }
@@ -508,28 +508,32 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                     if (w.kb == 0) continue;
                 } else {
                     const int F = a.M;
-                    auto prefetch = [&](int ch) {        // the saved gate and up of 32 rows
-                        for (int i = et; i < 512; i += 128) {
-                            const int t = ch * 32 + (i >> 4), f = m0 + (i & 15) * 8;
+                    constexpr int kRows = FORM == kGradGate ? 16 : 32;          // of the output at a time
+                    const int chunks = (w.n + kRows - 1) / kRows;
+                    auto prefetch = [&](int ch) {        // the saved gate and up of 16 rows
+                        uint16_t *const st = st16 + (ch / kOutGroups & 1) * 4096;
+                        for (int i = et; i < 256; i += 128) {
+                            const int t = ch * kRows + (i >> 4), f = m0 + (i & 15) * 8;
                             if (t < w.n && f < F) {
                                 const uint16_t *src = a.gate_up + (size_t)(w.row + t) * 2 * F + f;
-                                cp_async16(st16 + (ch / kOutGroups & 1) * 8192 + i * 8, src);
-                                cp_async16(st16 + (ch / kOutGroups & 1) * 8192 + 4096 + i * 8, src + F);
+                                cp_async16(st + i * 8, src);
+                                cp_async16(st + 2048 + i * 8, src + F);
                             }
                         }
                         asm volatile("cp.async.commit_group;" ::: "memory");
                     };
                     bar_sync(bar, 128);                    // the last tile has left the staging buffers
                     if constexpr (FORM == kGradGate) prefetch(part);
-                    if (!(ok = bar_all(bar, 128, mbar_wait(smem_u32(&c.sums_full[buf]), (tiles >> 1) & 1)))) break;
+                    if (!(ok = bar_all(bar, 128, mbar_wait(smem_u32(&c.sums_full[buf]), (done >> 1) & 1)))) break;
                     tc_fence_after();
                     for (int ch = part; ch < chunks; ch += kOutGroups) {
                         const int at = ch / kOutGroups & 1;  // of the two staging buffers
-                        float v[32];
-                        tmem_ld32(sums + ch * 32, v);
+                        float v[kRows];
+                        if constexpr (kRows == 16) tmem_ld16(sums + ch * kRows, v);
+                        else tmem_ld32(sums + ch * kRows, v);
                         tmem_wait_ld();
-                        const size_t row0 = (size_t)w.row + ch * 32;
-                        const int rows = min(32, w.n - ch * 32);
+                        const size_t row0 = (size_t)w.row + ch * kRows;
+                        const int rows = min(kRows, w.n - ch * kRows);
                         if constexpr (FORM == kPlain || FORM == kGradX) {
                             uint16_t *const st = st16 + at * 4096;
 #pragma unroll
@@ -547,14 +551,14 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                             asm volatile("cp.async.wait_group 0;" ::: "memory");
                             bar_sync(bar, 128);            // everyone's pieces of this chunk; the other buffer is free
                             if (ch + kOutGroups < chunks) prefetch(ch + kOutGroups);
-                            uint16_t *const st = st16 + at * 8192;
+                            uint16_t *const st = st16 + at * 4096;
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float gate = wide16(st[j * 128 + et], a.f16), up = wide16(st[4096 + j * 128 + et], a.f16);
+                            for (int j = 0; j < kRows; ++j) {
+                                const float gate = wide16(st[j * 128 + et], a.f16), up = wide16(st[2048 + j * 128 + et], a.f16);
                                 const Sigmoid sig(gate);
                                 const uint32_t p = pack16(v[j] * up * (sig.s * (1.0f + gate * sig.rest)), v[j] * (gate * sig.s), a.f16);
                                 st[j * 128 + et] = (uint16_t)p;
-                                st[4096 + j * 128 + et] = (uint16_t)(p >> 16);
+                                st[2048 + j * 128 + et] = (uint16_t)(p >> 16);
                             }
                             bar_sync(bar, 128);
                             for (int i = et; i < rows * 16; i += 128) {
@@ -562,17 +566,16 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                                 if (f < F) {
                                     uint16_t *const dst = a.out + (row0 + (i >> 4)) * 2 * F + f;
                                     *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(st + i * 8);
-                                    *reinterpret_cast<uint4 *>(dst + F) = *reinterpret_cast<const uint4 *>(st + 4096 + i * 8);
+                                    *reinterpret_cast<uint4 *>(dst + F) = *reinterpret_cast<const uint4 *>(st + 2048 + i * 8);
                                 }
                             }
                         } else {
-                            // Even warps hold gates, odd warps the ups of the same 32 features: each takes half of the rows.
-                            const int up = q & 1, f = (q >> 1) * 32 + lane;
-                            float *const swap = reinterpret_cast<float *>(own);
-                            uint16_t *const act = st16 + 4096 + at * 2048, *const gu = st16 + 8192 + at * 4096;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) swap[(q * 16 + j) * 32 + lane] = up ? v[j] : v[16 + j];
+                            // The lower 16 lanes hold gates, the upper ones the ups of the same features: each takes half of the rows.
+                            const bool up = lane >= 16;
+                            const int f = q * 16 + (lane & 15);
+                            uint16_t *const act = st16 + at * 2048, *const gu = st16 + 4096;
                             if (a.gate_up) {
+                                if (ch != part) bar_sync(bar, 128);      // the rows before have left
 #pragma unroll
                                 for (int j = 0; j < 32; j += 2) {
                                     const uint32_t p = pack16(v[j], v[j + 1], a.f16);
@@ -580,13 +583,12 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                                     gu[(j + 1) * 128 + up * 64 + f] = (uint16_t)(p >> 16);
                                 }
                             }
-                            bar_sync(bar + 1 + (q >> 1), 64);
 #pragma unroll
                             for (int j = 0; j < 16; j += 2) {
                                 float y[2];
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
-                                    const float other = swap[((q ^ 1) * 16 + j + i) * 32 + lane], own = up ? v[16 + j + i] : v[j + i];
+                                    const float other = __shfl_xor_sync(kFullMask, up ? v[j + i] : v[16 + j + i], 16), own = up ? v[16 + j + i] : v[j + i];
                                     const float gate = up ? other : own;
                                     y[i] = gate * Sigmoid(gate).s * (up ? own : other);
                                 }
@@ -613,7 +615,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(at_rank(smem_u32(&c.sums_empty[buf]), 0));
                 buf ^= 1;
-                ++tiles;
+                ++done;
             }
             if (FORM == kGradW && lane == 0) bulk_wait_all();
         }
@@ -675,7 +677,6 @@ bool encode_columns(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows,
 template <Form FORM, int CG>
 int launch_form(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const LinearArgs &a, cudaStream_t st) {
     constexpr auto kern = ep_linear_kernel<FORM, CG>;
-    constexpr size_t kSmem = smem_bytes(FORM);
     const int rc = allow_smem<kern>(kSmem);
     if (rc != EP_OK) return rc;
     constexpr int kM = Tiles<FORM, CG>::kM, kN = Tiles<FORM, CG>::kN;
@@ -735,12 +736,10 @@ extern "C" int ep_expert_linear(const void *x, long long x_stride, const void *w
     a.out = (uint16_t *)out;
     a.gate_up = (uint16_t *)gate_up;
     const uint64_t k = K, f = a.M, g = a.G, each = (uint64_t)N * K;
-    a.whole_a = swiglu && f % 32 == 0;
     CUtensorMap ma, mb, mc;
     bool ok = encode_rows(&mb, x, K, a.R_max, x_stride, 128) && encode_rows(&mc, x, K, a.R_max, x_stride, 32);
     if (!swiglu) ok = ok && encode(&ma, w, 2, {{k, 1, kBlockK}, {(uint64_t)N, k, 128}, {g, each, 1}});
-    else if (!a.whole_a) ok = ok && encode(&ma, w, 2, {{k, 1, kBlockK}, {2 * f, k, 32}, {g, each, 1}});
-    else ok = ok && encode(&ma, w, 2, {{k, 1, kBlockK}, {32, k, 32}, {2, f * k, 2}, {f / 32, 32 * k, 2}, {g, each, 1}});
+    else ok = ok && encode(&ma, w, 2, {{k, 1, kBlockK}, {16, k, 16}, {2, f * k, 2}, {f / 16, 16 * k, 4}, {g, each, 1}});     // 16 gates, their 16 ups
     if (!ok) return EP_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
     return swiglu ? launch_form<kGlu, 2>(ma, mb, mc, a, st) : launch_form<kPlain, 2>(ma, mb, mc, a, st);
