@@ -875,25 +875,19 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     stride, a multiple of 8), a [G, r, H] and b [G, N, r], all bf16 or all fp16; scale fp32 [G], None for 1.  Without
     ``by_token`` y, x and out are in the layout's row order [R_max, *], for any layout (adapters of experts).  ``out`` may be
     y, which is then added to in place."""
-    pa, pb = _buffer(a, tuple(a.shape), _HALF, "a"), _buffer(b, tuple(b.shape), (a.dtype,), "b")
-    if a.dim() != 3 or a.shape[0] != L.G or b.dim() != 3 or b.shape[0] != L.G or b.shape[2] != a.shape[1]:
+    if a.dim() != 3 or b.dim() != 3:
         raise ValueError(f"expected a [{L.G}, r, H] and b [{L.G}, N, r], got {tuple(a.shape)} and {tuple(b.shape)}")
-    r, H, N, dt = a.shape[1], a.shape[2], b.shape[1], a.dtype
-
-    def rows(t, cols, what):
-        p, n, m, ld, _ = _matrix(t, what)
-        if t.dtype != dt:
-            raise TypeError(f"{what}: dtype {t.dtype}, expected {dt}")
-        if m != cols or (n != L.T if by_token else n < L.R_max):
-            raise ValueError(f"{what}: expected {L.T if by_token else L.R_max} rows of {cols}, got {tuple(t.shape)}")
-        return p, ld
-
-    py, ldy = rows(y, N, "y")
-    px, ldx = rows(x, H, "x")
+    (_, r, H), N, dt = a.shape, b.shape[1], a.dtype
+    pa, pb = _buffer(a, (L.G, r, H), _HALF, "a"), _buffer(b, (L.G, N, r), (dt,), "b")
+    n = L.T if by_token else L.R_max
     if out is None:
         out = torch.empty(y.shape, dtype=dt, device=y.device)
-    po, ldo = rows(out, N, "out")
-    rc = _lib.ep_lora_add(py, ldy, px, ldx, pa, pb, None if scale is None else _buffer(scale, (L.G,), _F32, "scale"), H, N, r, DTYPES[dt],
+    (py, ly, wy, ldy, ty), (px, lx, wx, ldx, tx), (po, lo, wo, ldo, to) = _matrix(y, "y"), _matrix(x, "x"), _matrix(out, "out")
+    if ty != tx or ty != to or y.dtype != dt:
+        raise TypeError(f"y {y.dtype}, x {x.dtype} and out {out.dtype}: expected {dt}")
+    if wy != N or wx != H or wo != N or min(ly, lx, lo) < n or (by_token and max(ly, lx, lo) != n):
+        raise ValueError(f"expected {n} rows: y and out of {N}, x of {H}; got {tuple(y.shape)}, {tuple(out.shape)}, {tuple(x.shape)}")
+    rc = _lib.ep_lora_add(py, ldy, px, ldx, pa, pb, None if scale is None else _buffer(scale, (L.G,), _F32, "scale"), H, N, r, ty,
                           1 if by_token else 0, L.ref, po, ldo, _stream(stream))
     _check(rc, "ep_lora_add")
     return out
