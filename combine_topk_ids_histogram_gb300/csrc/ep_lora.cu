@@ -280,9 +280,10 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
 
 // ------------------------------------------------------------------------------------------------------------ many rows
 // The same for tiles of 64 rows, where the bytes of x, y and out are what counts: both products stream through a ring in shared
-// memory that cp.async fills three stages ahead, 64 columns of x with 64 of A, then 64 of y with 64 rows of B, and four warps'
+// memory that cp.async fills ahead of them, 64 columns of x with 64 of A, then 64 of y with 64 rows of B, and four warps'
 // 16 rows share each of them.
-constexpr int kTileRows = 64, kRing = 4;
+constexpr int kTileRows = 64;
+constexpr int ring_stages(int RN) { return RN == 16 ? 4 : RN == 8 ? 6 : 8; }     // in up to 96 KB, for two CTAs to an SM
 
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gmem, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(valid ? 16 : 0) : "memory");
@@ -304,7 +305,7 @@ template <int RN> struct Ring {
 
 template <typename T, int RN>
 __global__ void __launch_bounds__(kThreads, 2) ep_lora_rows_kernel(const LoraArgs a, int one_wave) {
-    constexpr int kR = 8 * RN, kCells = kTileRows * kR, kK = RN / 2;
+    constexpr int kR = 8 * RN, kCells = kTileRows * kR, kK = RN / 2, kRing = RN == 16 ? 4 : RN == 8 ? 6 : 8;
     extern __shared__ __align__(16) uint8_t s_raw[];
     Ring<RN> *const ring = reinterpret_cast<Ring<RN> *>(s_raw);
     float *const s_part = reinterpret_cast<float *>(s_raw), *const s_mine = s_part + 2 * kCells, *const s_all = s_part;
@@ -349,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_rows_kernel(const LoraArg
     const bool right = RN >= 4 || tid < 128;
     const int piece = tid & 7, at0 = s_at[tid >> 3], at1 = s_at[32 + (tid >> 3)];
     const uint32_t base = smem_u32(s_raw), to0 = base + piece_at<8>(tid >> 3, piece) * 16, to1 = to0 + 32 * 8 * 16;
-    auto fill = [&](int i, int col, int cols, const uint16_t *p0, const uint16_t *p1, const uint16_t *const (&pr)[kMine], size_t step,
+    auto fill = [&](int slot, int col, int cols, const uint16_t *p0, const uint16_t *p1, const uint16_t *const (&pr)[kMine], size_t step,
                     const uint32_t (&tor)[kMine], const bool (&okr)[kMine]) {
         if (col < cols) {
-            const uint32_t st = (i & (kRing - 1)) * (uint32_t)sizeof(Ring<RN>);
+            const uint32_t st = slot * (uint32_t)sizeof(Ring<RN>);
             const bool in = col + 8 * piece < cols;
             cp_async16_or_zero(to0 + st, in ? p0 + col : a.x, in && at0 >= 0);
             cp_async16_or_zero(to1 + st, in ? p1 + col : a.x, in && at1 >= 0);
@@ -373,21 +374,22 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_rows_kernel(const LoraArg
         pr[j] = a.a + ((size_t)g * a.r + (okr[j] ? r : 0)) * a.H + 8 * piece;
         tor[j] = base + (uint32_t)(offsetof(Ring<RN>, right) + piece_at<8>(r, piece) * 16);
     }
-    auto fill_first = [&](int i) {                           // stage i of this CTA
+    auto fill_first = [&](int i, int slot) {                 // stage i of this CTA
         const int col = (rank + i * a.C) * 64;
         const bool in = col + 8 * piece < a.H;
         bool ok[kMine];
 #pragma unroll
         for (int j = 0; j < kMine; ++j) ok[j] = okr[j] && in;
-        fill(i, col, a.H, p0, p1, pr, 1, tor, ok);
+        fill(slot, col, a.H, p0, p1, pr, 1, tor, ok);
     };
-    for (int i = 0; i < kRing - 1; ++i) fill_first(i);
-    for (int i = 0; (rank + i * a.C) * 64 < a.H; ++i) {
+    for (int i = 0; i < kRing - 1; ++i) fill_first(i, i);
+    int now = 0, then = kRing - 1;                           // the slot in use, and the one to fill
+    for (int i = 0; (rank + i * a.C) * 64 < a.H; ++i, now = now == kRing - 1 ? 0 : now + 1, then = then == kRing - 1 ? 0 : then + 1) {
         cp_async_wait<kRing - 2>();
         __syncthreads();
-        fill_first(i + kRing - 1);
+        fill_first(i + kRing - 1, then);
         if (!busy) continue;
-        const Ring<RN> &st = ring[i % kRing];
+        const Ring<RN> &st = ring[now];
         const uint4 x0 = st.left[piece_at<8>(16 * rg + c, 4 * split + q)], x1 = st.left[piece_at<8>(16 * rg + c + 8, 4 * split + q)];
 #pragma unroll
         for (int j = 0; j < RN; ++j) {
@@ -454,21 +456,23 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_rows_kernel(const LoraArg
         pr[j] = a.b + ((size_t)g * a.N + n) * a.r + (okr[j] ? 8 * k : 0);
         tor[j] = base + (uint32_t)(offsetof(Ring<RN>, right) + piece_at<RN>(n, k) * 16);
     }
-    auto fill_second = [&](int i) {
+    auto fill_second = [&](int i, int slot) {
         const int col = (rank + i * a.C) * 64;
         bool ok[kMine];
 #pragma unroll
         for (int j = 0; j < kMine; ++j) ok[j] = okr[j] && col + rows_b[j] < a.N;
-        fill(i, col, a.N, p0, p1, pr, a.r, tor, ok);
+        fill(slot, col, a.N, p0, p1, pr, a.r, tor, ok);
     };
-    for (int i = 0; i < kRing - 1; ++i) fill_second(i);
-    for (int i = 0; (rank + i * a.C) * 64 < a.N; ++i) {
+    for (int i = 0; i < kRing - 1; ++i) fill_second(i, i);
+    now = 0;
+    then = kRing - 1;
+    for (int i = 0; (rank + i * a.C) * 64 < a.N; ++i, now = now == kRing - 1 ? 0 : now + 1, then = then == kRing - 1 ? 0 : then + 1) {
         cp_async_wait<kRing - 2>();
         __syncthreads();
-        fill_second(i + kRing - 1);
+        fill_second(i + kRing - 1, then);
         const int n = (rank + i * a.C) * 64 + 32 * split + 8 * q;
         if (!busy || n - 8 * q >= a.N) continue;
-        const Ring<RN> &st = ring[i % kRing];
+        const Ring<RN> &st = ring[now];
         float sum[4][4] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -525,7 +529,7 @@ template <auto kern> int launch_lora(const LoraArgs &a, size_t smem, int copy, c
 }
 
 template <typename T, int RN> int launch_rank(const LoraArgs &a, int copy, cudaStream_t st) {
-    if (a.rows == kTileRows) return launch_lora<ep_lora_rows_kernel<T, RN>>(a, sizeof(Ring<RN>) * kRing, copy, st);
+    if (a.rows == kTileRows) return launch_lora<ep_lora_rows_kernel<T, RN>>(a, sizeof(Ring<RN>) * ring_stages(RN), copy, st);
     return launch_lora<ep_lora_kernel<T, RN>>(a, (size_t)(kWarps + 2) * 16 * 8 * RN * sizeof(float), copy, st);
 }
 template <typename T> int launch_type(const LoraArgs &a, int copy, cudaStream_t st) {
