@@ -39,8 +39,11 @@ constexpr int kMaxGroups = kMaxE + 1;
 constexpr int kStages = 6;
 constexpr int kStaging = 16384;              // bytes in which a group of four warps turns its results into rows
 constexpr int kSuper = 8;                    // grad_w: tiles of N that go through all of K before the next
-// The tensor cores' sums in fp32 truncate, by up to 2^-23 of the sum per 16 products; an fp32 gradient leaves them every 2048 rows.
-constexpr int kChunkRows = 2048;
+// The tensor cores' adder truncates, by up to 2^-23 of the sum per 16 products, all to one side: sums of an fp32 gradient leave them
+// every 512 rows and are added up in registers, rounded to nearest.  Normal operands lose 4.7e-7 of the sums' norm then (of one sign
+// 9e-7) whatever the number of rows; with 256 / 1024 / 2048 rows 2.3e-7 / 1.0e-6 / 1.9e-6, and 8 x 28672 x 4096 gradients of 8192
+// rows took 1520 / 1390 / 1340 us where these take 1430.
+constexpr int kChunkRows = 512;
 
 // A tile: rows or features, and what is summed over.
 struct Work {
@@ -48,7 +51,7 @@ struct Work {
     int col, end;                            // grad_w: first column; row behind the group's last
     int kb, last;                            // blocks of 64 to sum over, and the valid of the last
     int half;                                // of N, what each CTA loads
-    int first;                               // grad_w: not a later chunk of the same tile
+    int first, final;                        // grad_w: whether it is the first chunk of the tile's rows, and the last
 };
 
 constexpr int kSlots = 3;                    // tiles that the roles may be apart, and be taken ahead
@@ -145,6 +148,7 @@ template <Form FORM, int CG> struct Tiles {
         if (a.wide) left = min(left, kChunkRows);
         w.kb = (left + kBlockK - 1) / kBlockK;
         w.last = left - (w.kb - 1) * kBlockK;
+        w.final = !a.wide || w.row + kChunkRows >= w.end;
     }
 };
 
@@ -457,6 +461,8 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             uint32_t done = 0;
             uint8_t *const own = staging + part * kStaging;
             uint16_t *const st16 = reinterpret_cast<uint16_t *>(own);
+            constexpr int kWide = FORM == kGradW ? kCols / 32 / kOutGroups : 1;
+            float total[kWide][32];                      // an fp32 gradient's sums over the chunks so far
             while (ok && feed.next<true>(w, rank, ok)) {
                 const int m0 = w.m + (int)rank * (Tiles<FORM, CG>::kM / CG);          // first feature of this CTA
                 const uint32_t sums = lanes + buf * kCols;
@@ -465,26 +471,53 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_full[buf]), (done >> 1) & 1)))) break;
                         tc_fence_after();
                     }
-                    // 32 rows of 128 bytes per warp at a time: 32 columns of fp32 or 64 of 16 bits, swizzled as TMA reads them
-                    const int cols = a.wide ? 32 : 64;
-                    if (!w.first && lane == 0) bulk_wait_all();      // the chunk before, added up
-                    for (int col = part * cols; col < w.n; col += kOutGroups * cols) {
-                        uint8_t *const line = own + q * 4096 + lane * 128;
+                    // 32 rows of 128 bytes per warp at a time, swizzled as TMA reads them: 32 columns of fp32 or 64 of 16 bits
+                    uint8_t *const line = own + q * 4096 + lane * 128;
+                    auto store = [&](int col) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && m0 + q * 32 < a.M) {
+                            const uint32_t src = smem_u32(own + q * 4096);
+                            if (a.wide && a.add) tma_add_3d(&map_c, src, w.col + col, m0 + q * 32, w.g);
+                            else tma_store_3d(&map_c, src, w.col + col, m0 + q * 32, w.g);
+                        }
+                        if (lane == 0) bulk_commit();
+                    };
+                    auto left = [&]() {                  // the rows before have been read
                         if (lane == 0) bulk_wait_read_all();
                         __syncwarp();
-                        float v[32] = {};
-                        if (a.wide) {
-                            if (w.kb > 0) {
+                    };
+                    if (a.wide) {
+#pragma unroll
+                        for (int i = 0; i < kWide; ++i) {
+                            const int col = (i * kOutGroups + part) * 32;
+                            if (col >= w.n) continue;
+                            if (w.first) {
+                                if (w.kb > 0) tmem_ld32(sums + col, total[i]);
+                                else
+                                    for (int j = 0; j < 32; ++j) total[i][j] = 0.0f;
+                                tmem_wait_ld();
+                            } else {
+                                float v[32];
                                 tmem_ld32(sums + col, v);
                                 tmem_wait_ld();
-                            }
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<float4 *>(line + ((i ^ (lane & 7)) << 4)) =
-                                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                        } else {
+                                for (int j = 0; j < 32; ++j) total[i][j] += v[j];
+                            }
+                            if (!w.final) continue;
+                            left();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                *reinterpret_cast<float4 *>(line + ((j ^ (lane & 7)) << 4)) =
+                                    make_float4(total[i][4 * j], total[i][4 * j + 1], total[i][4 * j + 2], total[i][4 * j + 3]);
+                            store(col);
+                        }
+                    } else {
+                        for (int col = part * 64; col < w.n; col += kOutGroups * 64) {
+                            left();
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
+                                float v[32] = {};
                                 if (w.kb > 0) {
                                     tmem_ld32(sums + col + 32 * h, v);
                                     tmem_wait_ld();
@@ -495,15 +528,8 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                                         make_uint4(pack16(v[8 * i], v[8 * i + 1], a.f16), pack16(v[8 * i + 2], v[8 * i + 3], a.f16),
                                                    pack16(v[8 * i + 4], v[8 * i + 5], a.f16), pack16(v[8 * i + 6], v[8 * i + 7], a.f16));
                             }
+                            store(col);
                         }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0 && m0 + q * 32 < a.M) {
-                            const uint32_t src = smem_u32(own + q * 4096);
-                            if (a.wide && (a.add || !w.first)) tma_add_3d(&map_c, src, w.col + col, m0 + q * 32, w.g);
-                            else tma_store_3d(&map_c, src, w.col + col, m0 + q * 32, w.g);
-                        }
-                        if (lane == 0) bulk_commit();
                     }
                     if (w.kb == 0) continue;
                 } else {

@@ -558,7 +558,7 @@ int ep_expert_linear(const void *x, long long x_stride, const void *w, int in_fe
  *              d * up * s * (1 + gate * (1 - s)), and d * gate * s.
  *   -> grad_w  NULL, or [G * N * K] in grad_w_dtype (dtype or EP_F32): grad_w[g, n, k] = sum over the rows
  *              of g of grad[r, n] x[r, k]; zeros for a group without rows.  accumulate 1 (EP_F32 only)
- *              adds to what is there.  Sums of EP_F32 leave the tensor cores every 2048 rows.
+ *              adds to what is there.  Sums of EP_F32 leave the tensor cores every 512 rows (about 1e-6 of them is lost).
  * Rows as in the forward call; padding rows take part in grad_w, so x or grad has to be zero there (and
  * neither infinite nor NaN): ep_dispatch_bf16 and ep_combine_bwd write zeros.  Rows outside a group, or behind the last one, take no part
  * in its grad_w.  grad_x and grad_w may not both be NULL; w is not read without grad_x nor x without
