@@ -51,6 +51,18 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// The power of two that brings a largest magnitude to [2^14, 2^15), in fp16's range: from its exponent (1 for 0, infinities and NaN).
+__device__ __forceinline__ float fp16_scale(float most) {
+    const int e = (int)(__float_as_uint(most) >> 23) - 127;
+    return most > 0.0f && e < 128 ? __uint_as_float((uint32_t)(min(14 - e, 126) + 127) << 23) : 1.0f;
+}
+
 // A sum v of A x as two 16-bit numbers, hi + lo: their products with B are exact in fp32, and v keeps 16 bits (bf16) or 22 (fp16).
 template <typename T> __device__ __forceinline__ void split2(float v0, float v1, uint32_t &hi, uint32_t &lo) {
     hi = f32_to_word(v0, v1, T());
@@ -225,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
             float v = 0.0f;
             for (int k = lane; k < kR; k += 32) v = fmaxf(v, fabsf(s_all[i * kR + k]));
             v = warp_max(v);
-            if (lane == 0) s_scale[i] = v > 0.0f && v < 3.4e38f ? exp2f((float)min(14 - ilogbf(v), 126)) : 1.0f;
+            if (lane == 0) s_scale[i] = fp16_scale(v);
         }
         __syncthreads();
     }
@@ -305,11 +317,15 @@ template <int RN> struct Ring {
 
 template <typename T, int RN>
 __global__ void __launch_bounds__(kThreads, 2) ep_lora_rows_kernel(const LoraArgs a, int one_wave) {
-    constexpr int kR = 8 * RN, kCells = kTileRows * kR, kK = RN / 2, kRing = RN == 16 ? 4 : RN == 8 ? 6 : 8;
+    constexpr int kR = 8 * RN, kK = RN / 2, kRing = RN == 16 ? 4 : RN == 8 ? 6 : 8;
+    // Sums of A x: two warps' parts, in rows that begin 8 banks apart, then all of them in the second's place, 2 banks apart, which is
+    // what their writers and readers meet least in.  They lie in the ring's first kHeld slots.
+    constexpr int kPitch = kR + 8, kPart = kTileRows * kPitch, kPitchAll = kR + 2;
+    constexpr int kHeld = (2 * kPart * (int)sizeof(float) + (int)sizeof(Ring<RN>) - 1) / (int)sizeof(Ring<RN>);
+    static_assert(kHeld < kRing, "room for the sums");
     extern __shared__ __align__(16) uint8_t s_raw[];
     Ring<RN> *const ring = reinterpret_cast<Ring<RN> *>(s_raw);
-    float *const s_part = reinterpret_cast<float *>(s_raw), *const s_mine = s_part + 2 * kCells, *const s_all = s_part;
-    static_assert(sizeof(Ring<RN>) * kRing >= 3 * kCells * sizeof(float), "the sums take the place of the ring");
+    float *const s_part = reinterpret_cast<float *>(s_raw), *const s_all = s_part + kPart;
     __shared__ float s_scale[kTileRows];
     __shared__ int s_at[kTileRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane >> 2, q = lane & 3, rg = warp & 3, split = warp >> 2;
@@ -400,51 +416,6 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_rows_kernel(const LoraArg
     }
     cp_async_wait<0>();
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < RN; ++j) {
-        float *const p = s_part + split * kCells + (16 * rg + c) * kR + 8 * j + 2 * q;
-        *reinterpret_cast<float2 *>(p) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2 *>(p + 8 * kR) = make_float2(acc[j][2], acc[j][3]);
-    }
-    __syncthreads();
-    for (int i = tid; i < kCells; i += kThreads) s_mine[i] = s_part[i] + s_part[kCells + i];
-    cluster_sync_all();                                  // (a barrier of the CTA where it is alone)
-    for (int i = tid; i < kCells; i += kThreads) {
-        float v = 0.0f;
-        for (int k = 0; k < a.C; ++k) v += ld_cluster_f32(at_rank(smem_u32(s_mine + i), k));
-        s_all[i] = v;
-    }
-    __syncthreads();
-    if constexpr (std::is_same_v<T, __half>) {           // a power of two per row keeps the sums in fp16's range
-        for (int i = warp; i < kTileRows; i += kWarps) {
-            float v = 0.0f;
-            for (int k = lane; k < kR; k += 32) v = fmaxf(v, fabsf(s_all[i * kR + k]));
-            v = warp_max(v);
-            if (lane == 0) s_scale[i] = v > 0.0f && v < 3.4e38f ? exp2f((float)min(14 - ilogbf(v), 126)) : 1.0f;
-        }
-        __syncthreads();
-    }
-    uint32_t hi[kK][4], lo[kK][4];
-    float back[2];                                       // adapter's scale, over the row's
-    int at[2];
-    const float scale = a.scale ? a.scale[g] : 1.0f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int j = 16 * rg + c + 8 * i;
-        at[i] = s_at[j];
-        float f = 1.0f;
-        if constexpr (std::is_same_v<T, __half>) f = s_scale[j];
-        back[i] = scale / f;
-#pragma unroll
-        for (int s = 0; s < kK; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = RN == 2 ? 4 * q + 2 * h : s / 2 * 32 + 8 * q + s % 2 * 4 + 2 * h;
-                const float2 v = *reinterpret_cast<const float2 *>(s_all + j * kR + k);
-                split2<T>(v.x * f, v.y * f, hi[s][i + 2 * h], lo[s][i + 2 * h]);
-            }
-    }
-    cluster_sync_all();                                  // the sums have been read everywhere: the ring may have their place
     p0 = a.y + (at0 >= 0 ? at0 * a.ldy : 0) + 8 * piece;
     p1 = a.y + (at1 >= 0 ? at1 * a.ldy : 0) + 8 * piece;
     int rows_b[kMine];
@@ -463,9 +434,63 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_rows_kernel(const LoraArg
         for (int j = 0; j < kMine; ++j) ok[j] = okr[j] && col + rows_b[j] < a.N;
         fill(slot, col, a.N, p0, p1, pr, a.r, tor, ok);
     };
-    for (int i = 0; i < kRing - 1; ++i) fill_second(i, i);
-    now = 0;
-    then = kRing - 1;
+    for (int i = 0; i < kRing - kHeld; ++i) fill_second(i, kHeld + i);          // what the sums leave room for comes meanwhile
+#pragma unroll
+    for (int j = 0; j < RN; ++j) {
+        float *const p = s_part + split * kPart + (16 * rg + c) * kPitch + 8 * j + 2 * q;
+        *reinterpret_cast<float2 *>(p) = make_float2(acc[j][0], acc[j][1]);
+        *reinterpret_cast<float2 *>(p + 8 * kPitch) = make_float2(acc[j][2], acc[j][3]);
+    }
+    __syncthreads();
+    for (int i = tid; i < kTileRows * kR / 4; i += kThreads) {
+        float4 *const p = reinterpret_cast<float4 *>(s_part + i / (kR / 4) * kPitch + i % (kR / 4) * 4);
+        const float4 u = p[0], v = p[kPart / 4];
+        p[0] = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+    }
+    cluster_sync_all();                                      // (a barrier of the CTA where it is alone)
+    for (int i = tid; i < kTileRows * kR / 4; i += kThreads) {
+        const int r = i / (kR / 4), k4 = i % (kR / 4) * 4;
+        const uint32_t at = smem_u32(s_part + r * kPitch + k4);
+        float4 v = ld_cluster_f32x4(at_rank(at, 0));
+        for (int k = 1; k < a.C; ++k) {
+            const float4 u = ld_cluster_f32x4(at_rank(at, k));
+            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+        }
+        float2 *const to = reinterpret_cast<float2 *>(s_all + r * kPitchAll + k4);
+        to[0] = make_float2(v.x, v.y);
+        to[1] = make_float2(v.z, v.w);
+        if constexpr (std::is_same_v<T, __half>) {           // kR / 4 lanes hold a row
+            float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+#pragma unroll
+            for (int o = kR / 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+            if (k4 == 0) s_scale[r] = fp16_scale(m);
+        }
+    }
+    __syncthreads();
+    uint32_t hi[kK][4], lo[kK][4];
+    float back[2];                                           // adapter's scale, over the row's
+    int at[2];
+    const float scale = a.scale ? a.scale[g] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int j = 16 * rg + c + 8 * i;
+        at[i] = s_at[j];
+        float f = 1.0f;
+        if constexpr (std::is_same_v<T, __half>) f = s_scale[j];
+        back[i] = scale / f;
+#pragma unroll
+        for (int s = 0; s < kK; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = RN == 2 ? 4 * q + 2 * h : s / 2 * 32 + 8 * q + s % 2 * 4 + 2 * h;
+                const float2 v = *reinterpret_cast<const float2 *>(s_all + j * kPitchAll + k);
+                split2<T>(v.x * f, v.y * f, hi[s][i + 2 * h], lo[s][i + 2 * h]);
+            }
+    }
+    cluster_sync_all();                                      // the sums have been read everywhere: the ring has their place again
+    for (int i = kRing - kHeld; i < kRing - 1; ++i) fill_second(i, i - (kRing - kHeld));
+    now = kHeld;
+    then = kHeld - 1;
     for (int i = 0; (rank + i * a.C) * 64 < a.N; ++i, now = now == kRing - 1 ? 0 : now + 1, then = then == kRing - 1 ? 0 : then + 1) {
         cp_async_wait<kRing - 2>();
         __syncthreads();
@@ -474,21 +499,27 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_rows_kernel(const LoraArg
         if (!busy || n - 8 * q >= a.N) continue;
         const Ring<RN> &st = ring[now];
         float sum[4][4] = {};
+        const int nb = 32 * split + 8 * (c >> 1) + (c & 1);  // + 2j
+        if constexpr (RN == 2) {
+            uint2 w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int nb = 32 * split + 8 * (c >> 1) + 2 * j + (c & 1);
-            if constexpr (RN == 2) {
-                const uint2 w = *(reinterpret_cast<const uint2 *>(st.right + nb * 2) + q);
-                mma16<T>(sum[j], lo[0][0], lo[0][1], lo[0][2], lo[0][3], w.x, w.y);
-                mma16<T>(sum[j], hi[0][0], hi[0][1], hi[0][2], hi[0][3], w.x, w.y);
-            } else {
+            for (int j = 0; j < 4; ++j) w[j] = *(reinterpret_cast<const uint2 *>(st.right + (nb + 2 * j) * 2) + q);
 #pragma unroll
-                for (int s = 0; s < RN / 4; ++s) {
-                    const uint4 w = st.right[piece_at<RN>(nb, 4 * s + q)];
-                    mma16<T>(sum[j], lo[2 * s][0], lo[2 * s][1], lo[2 * s][2], lo[2 * s][3], w.x, w.y);
-                    mma16<T>(sum[j], hi[2 * s][0], hi[2 * s][1], hi[2 * s][2], hi[2 * s][3], w.x, w.y);
-                    mma16<T>(sum[j], lo[2 * s + 1][0], lo[2 * s + 1][1], lo[2 * s + 1][2], lo[2 * s + 1][3], w.z, w.w);
-                    mma16<T>(sum[j], hi[2 * s + 1][0], hi[2 * s + 1][1], hi[2 * s + 1][2], hi[2 * s + 1][3], w.z, w.w);
+            for (int j = 0; j < 4; ++j) mma16<T>(sum[j], lo[0][0], lo[0][1], lo[0][2], lo[0][3], w[j].x, w[j].y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma16<T>(sum[j], hi[0][0], hi[0][1], hi[0][2], hi[0][3], w[j].x, w[j].y);
+        } else {
+#pragma unroll
+            for (int s = 0; s < RN / 4; ++s) {               // four sums side by side: each product waits for the one before in its sum
+                uint4 w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = st.right[piece_at<RN>(nb + 2 * j, 4 * s + q)];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t *const f = h & 1 ? hi[2 * s + (h >> 1)] : lo[2 * s + (h >> 1)];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma16<T>(sum[j], f[0], f[1], f[2], f[3], h < 2 ? w[j].x : w[j].z, h < 2 ? w[j].y : w[j].w);
                 }
             }
         }
