@@ -2,9 +2,11 @@
 
 decode_step   norm -> router logits -> experts and probabilities -> layout -> 4-bit gate/up and down products on the
               layout's rows -> combine -> residual.  Nothing is dispatched: the products take each row's token.
+              With adapters, each token's request adds its low-rank adapter beside the block.
 train_step    the same block with bf16 expert weights, forward and backward: norm, router, layout, BF16 dispatch, the
-              experts (a loop of library GEMMs stands in for a grouped GEMM), combine; then the gradients of x and
-              of every weight, with combine_bwd's probability gradients going back through the router.
+              experts' grouped products (gate, up and activation in one call, then the down product), combine; then the
+              gradients of x and of every weight, with combine_bwd's probability gradients going back through the router.
+              No row extent is read by the host.
 
     python examples/moe_block.py [--tokens 16] [--hidden 2048] [--width 768] [--experts 128] [--topk 8]
 """
@@ -38,47 +40,35 @@ def make_weights(H: int, F: int, E: int, device="cuda", seed: int = 0) -> dict:
                 w13=(normal(E, 2 * F, H) / H ** 0.5).bfloat16(), w2=(normal(E, H, F) / F ** 0.5).bfloat16())
 
 
-def decode_step(x: torch.Tensor, p: dict, w13, w2, K: int) -> torch.Tensor:
-    """x [T, H] bf16 -> [T, H]; w13 and w2 are quantised."""
+def decode_step(x: torch.Tensor, p: dict, w13, w2, K: int, adapters=None) -> torch.Tensor:
+    """x [T, H] bf16 -> [T, H]; w13 and w2 are quantised.  adapters: (ids int32 [T, 1], -1 for none; a [n, r, H]; b [n, H, r];
+    scale [n])."""
     h, _, _ = ep.layer_norm(x, p["norm"], rms=True)
     ids, probs = ep.router_topk(h @ p["router"].t(), K, bias=p["bias"], score="sigmoid", scale=SCALE)
     L = ep.dispatch_layout(ids, p["router"].shape[0])
     a = ep.expert_matvec(h, *w13, L, by_token=True, swiglu=True)
     y = ep.expert_matvec(a, *w2, L, by_token=False)
-    return x + ep.combine(y, probs, L)
+    out = x + ep.combine(y, probs, L)
+    if adapters is not None:
+        ids, a, b, scale = adapters
+        ep.lora_add(out, h, a, b, ep.dispatch_layout(ids, a.shape[0]), scale=scale, out=out)
+    return out
 
 
 def train_step(x: torch.Tensor, grad_out: torch.Tensor, p: dict, K: int):
     """Forward and backward of the block's MoE branch (without the residual): (out, ids, grads of x, norm, router, w13, w2)."""
-    E, F = p["router"].shape[0], p["w2"].shape[2]
     h, _, rstd = ep.layer_norm(x, p["norm"], rms=True)
     logits = h @ p["router"].t()
     ids, probs = ep.router_topk(logits, K, bias=p["bias"], score="sigmoid", scale=SCALE)
-    L = ep.dispatch_layout(ids, E)
+    L = ep.dispatch_layout(ids, p["router"].shape[0])
     rows = ep.dispatch_bf16(h, L)
-    y = torch.empty_like(rows)
-    off = L.row_offsets.tolist()                                   # a grouped GEMM would read the extents on the device
-    saved = {}
-    for e in range(E):
-        a, b = off[e], off[e + 1]
-        if a < b:
-            gate, up = (rows[a:b] @ p["w13"][e].t()).float().chunk(2, 1)
-            act = (torch.nn.functional.silu(gate) * up).bfloat16()
-            saved[e] = gate, up, act
-            torch.matmul(act, p["w2"][e].t(), out=y[a:b])
+    act, gate_up = ep.expert_linear(rows, p["w13"], L, swiglu=True, save=True)
+    y = ep.expert_linear(act, p["w2"], L)
     out = ep.combine(y, probs, L)
 
     grad_y, grad_probs = ep.combine_bwd(grad_out, y, probs, L)
-    grad_rows = torch.empty_like(rows)
-    gw13, gw2 = torch.zeros_like(p["w13"]), torch.zeros_like(p["w2"])
-    for e, (gate, up, act) in saved.items():
-        a, b = off[e], off[e + 1]
-        gw2[e] = grad_y[a:b].t() @ act
-        ga = (grad_y[a:b] @ p["w2"][e]).float()
-        s = torch.sigmoid(gate)
-        g13 = torch.cat([ga * up * s * (1 + gate * (1 - s)), ga * gate * s], 1).bfloat16()
-        gw13[e] = g13.t() @ rows[a:b]
-        torch.matmul(g13, p["w13"][e], out=grad_rows[a:b])
+    grad_gate_up, gw2 = ep.expert_linear_bwd(grad_y, act, p["w2"], L, gate_up=gate_up)
+    grad_rows, gw13 = ep.expert_linear_bwd(grad_gate_up, rows, p["w13"], L)
     grad_logits = ep.router_topk_bwd(grad_probs, logits, ids, score="sigmoid", scale=SCALE)
     grad_h = ep.dispatch_bwd(grad_rows, L) + grad_logits @ p["router"]
     grad_x, grad_norm, _ = ep.layer_norm_bwd(grad_h, x, p["norm"], None, rstd, rms=True)

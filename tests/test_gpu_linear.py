@@ -1,4 +1,7 @@
 """The grouped 16-bit products and their gradients against the 64-bit definition."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -323,3 +326,35 @@ def test_offsets_beyond_32_bits():
         parts = [ref.grad_gate(*ref.linear(out[i:i + 1], w[0 if i < R - 300 else 1].t()), gu[i:i + 1]) for i in range(R)[rows]]
         d, err = (torch.cat(v) for v in zip(*parts))
         ref.assert_within(gx[rows], d, ref.rounded(d, err, BF16), str(rows))
+
+
+def test_offsets_outside_the_buffers():
+    """A layout whose extents a caller has overwritten: nothing behind the buffers' rows is written or taken into a sum, and the
+    bounds-checked build reports it."""
+    import combine_topk_ids_histogram_gb300 as ep
+    L = ref.layout_of(ep, [10, 20, 30])
+    L.row_offsets.copy_(torch.tensor([-7, 10, 30, 1 << 30], dtype=torch.int32))
+    x, w, g = normal(1, 60, 64), normal(2, 3, 96, 64), normal(3, 60, 96)
+    buf, out = guarded(60, 96, BF16)
+    ep.expert_linear(x, w, L, out=out)
+    got = [out.clone(), None, None]
+    L.status.zero_()
+    got[1:] = ep.expert_linear_bwd(g, x, w, L)
+    torch.cuda.synchronize()
+    assert (buf[60 * 96:] == 7).all()
+    assert (L.status[0].item() & ep.STATUS_BOUNDS != 0) == bool(ep.CHECKED)
+    L = ref.layout_of(ep, [10, 20, 30])
+    want = [ep.expert_linear(x, w, L), *ep.expert_linear_bwd(g, x, w, L)]
+    if not ep.CHECKED:                                   # (there the second kernel of a call may see the first one's report)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_on_the_bounds_checked_build():
+    if os.environ.get("EP_GB300_CHECKED", "0") == "1":
+        pytest.skip("this process runs on it already")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu and not slow", "tests/test_gpu_linear.py", "tests/test_gpu_lora.py",
+                        "-k", "not bounds_checked"], cwd=root, env=dict(os.environ, EP_GB300_CHECKED="1"), capture_output=True, text=True,
+                       timeout=900)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]
+    assert " passed" in r.stdout

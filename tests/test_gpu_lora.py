@@ -169,3 +169,26 @@ def test_status_graph_and_streams():
         out = ep.lora_add(y, x, a, b, L, scale=scale, stream=s)
     s.synchronize()
     assert torch.equal(out, want)
+
+
+def test_decode_step_with_adapters():
+    """The example's block with an adapter per request, in and out of a CUDA graph."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import combine_topk_ids_histogram_gb300 as ep
+    import moe_block as M
+    T, H, F, E, K = 20, 256, 96, 8, 2
+    p = M.make_weights(H, F, E)
+    q13, q2 = M.quantise(p["w13"]), M.quantise(p["w2"])
+    ids, x, _, a, b, scale = make(T, 3, 16, H, H, BF16, 4)
+    without = M.decode_step(x, p, q13, q2, K)
+    out = M.decode_step(x, p, q13, q2, K, (ids, a, b, scale))
+    h, _, _ = ep.layer_norm(x, p["norm"], rms=True)
+    want, tol = expected(without, h, a, b, scale, [(ids[:, 0] == g).nonzero()[:, 0] for g in range(3)])
+    ref.assert_within(out, want, tol, "out")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = M.decode_step(x, p, q13, q2, K, (ids, a, b, scale))
+    graph.replay()
+    assert torch.equal(held, out)
