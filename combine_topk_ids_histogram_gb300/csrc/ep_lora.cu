@@ -291,11 +291,12 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
 }
 
 // ------------------------------------------------------------------------------------------------------------ many rows
-// The same for tiles of 64 rows, where the bytes of x, y and out are what counts: both products stream through a ring in shared
-// memory that cp.async fills ahead of them, 64 columns of x with 64 of A, then 64 of y with 64 rows of B, and four warps'
-// 16 rows share each of them.
-constexpr int kTileRows = 64;
-constexpr int ring_stages(int RN) { return RN == 16 ? 4 : RN == 8 ? 6 : 8; }     // in up to 96 KB, for two CTAs to an SM
+// The same for tiles of 128 rows on tcgen05, where the bytes of x, y and out are what counts.  The rows are M; both products stream
+// through a ring in shared memory that cp.async fills ahead: 64 columns of x with 64 of A (N is r), then 64 of y with 64 rows of B
+// (K is r).  The CTAs of a cluster split H, add up A x through each other's shared memory, and split N.  (With mma.sync from
+// shared memory the tensor cores and the shared memory's bandwidth bound it: 71 us where this takes TCUS, 8192 tokens, 5 adapters of rank 64,
+// 4096 -> 4096.)
+constexpr int kTileRows = 128, kRing = 3;
 
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gmem, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(valid ? 16 : 0) : "memory");
@@ -303,32 +304,29 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gm
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Rows of `pitch` 16-byte pieces.  A quarter of a warp reads four pieces of two neighbouring rows: with 8 pieces or more to a row the
-// odd ones are exchanged in fours, so that the two do not meet in the same banks.
-template <int PITCH> __device__ __forceinline__ int piece_at(int row, int piece) {
-    return row * PITCH + (PITCH >= 8 ? piece ^ ((row & 1) << 2) : piece);
-}
+// Where 16-byte piece p (of 8) of a row is in a tile of 128-byte rows, in the swizzle that tcgen05.mma reads.
+__device__ __forceinline__ uint32_t swizzled(int row, int p) { return row * 128 + ((p ^ (row & 7)) << 4); }
 
-template <int RN> struct Ring {
-    static constexpr int kRank = 8 * RN;                     // rows of A, and columns of B
-    uint4 left[kTileRows * 8];                               // 64 rows x 64 columns of x, then of y
-    uint4 right[kRank * 8];                                  // rank x 64 columns of A, then 64 rows x rank of B
+// RB: blocks of 64 that r fills at most (1: r <= 64, 2: r <= 128).
+template <int RB> struct TileSmem {
+    static constexpr int kPitch = 64 * RB + 4;               // of the exchanged sums, in fp32: 16 bytes of each row in banks of their own
+    static constexpr int kLeft = kTileRows * 128, kRight = RB * 8192, kStage = kLeft + kRight;
+    static constexpr int kLow = RB * kTileRows * 128;        // A x as 16-bit operand: high parts, then low parts
+    static constexpr int kBytes = kRing * kStage + 2 * kLow + 1024;
+    static_assert(kTileRows * kPitch * 4 <= kRing * kStage, "the exchanged sums take the place of the ring");
 };
 
-template <typename T, int RN>
-__global__ void __launch_bounds__(kThreads, 2) ep_lora_rows_kernel(const LoraArgs a, int one_wave) {
-    constexpr int kR = 8 * RN, kK = RN / 2, kRing = RN == 16 ? 4 : RN == 8 ? 6 : 8;
-    // Sums of A x: two warps' parts, in rows that begin 8 banks apart, then all of them in the second's place, 2 banks apart, which is
-    // what their writers and readers meet least in.  They lie in the ring's first kHeld slots.
-    constexpr int kPitch = kR + 8, kPart = kTileRows * kPitch, kPitchAll = kR + 2;
-    constexpr int kHeld = (2 * kPart * (int)sizeof(float) + (int)sizeof(Ring<RN>) - 1) / (int)sizeof(Ring<RN>);
-    static_assert(kHeld < kRing, "room for the sums");
+template <typename T, int RB>
+__global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a, int one_wave) {
+    using S = TileSmem<RB>;
+    constexpr uint32_t kTmem = 128;                          // columns: the sums of A x, then of 64 outputs
     extern __shared__ __align__(16) uint8_t s_raw[];
-    Ring<RN> *const ring = reinterpret_cast<Ring<RN> *>(s_raw);
-    float *const s_part = reinterpret_cast<float *>(s_raw), *const s_all = s_part + kPart;
-    __shared__ float s_scale[kTileRows];
+    uint8_t *const smem = s_raw + (1024 - (smem_u32(s_raw) & 1023)) % 1024;
+    __shared__ __align__(8) uint64_t s_done[kRing + 1];
+    __shared__ uint32_t s_tmem;
+    __shared__ float s_most[2][kTileRows];
     __shared__ int s_at[kTileRows];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane >> 2, q = lane & 3, rg = warp & 3, split = warp >> 2;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
     pdl_begin_if(one_wave);
     const int tile = blockIdx.x / a.C, rank = blockIdx.x % a.C;
     const bool copies = tile >= a.tiles + a.heads;
@@ -359,185 +357,213 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_rows_kernel(const LoraArg
         }
         s_at[tid] = at;
     }
+    if (warp == 4) tmem_alloc<1>(smem_u32(&s_tmem), kTmem);
+    if (tid == 0) {
+        for (int i = 0; i <= kRing; ++i) mbar_init(smem_u32(&s_done[i]), 1);
+        mbar_init_done();
+    }
+    tc_fence_before();
     __syncthreads();
-    const bool busy = rows.first + 16 * rg < rows.end;
-    // What this thread copies: a 16-byte piece of rows tid / 8 and 32 + tid / 8 of x or y, and of kMine rows of A or B.
-    constexpr int kMine = RN >= 4 ? RN / 4 : 1;
-    const bool right = RN >= 4 || tid < 128;
-    const int piece = tid & 7, at0 = s_at[tid >> 3], at1 = s_at[32 + (tid >> 3)];
-    const uint32_t base = smem_u32(s_raw), to0 = base + piece_at<8>(tid >> 3, piece) * 16, to1 = to0 + 32 * 8 * 16;
-    auto fill = [&](int slot, int col, int cols, const uint16_t *p0, const uint16_t *p1, const uint16_t *const (&pr)[kMine], size_t step,
-                    const uint32_t (&tor)[kMine], const bool (&okr)[kMine]) {
-        if (col < cols) {
-            const uint32_t st = slot * (uint32_t)sizeof(Ring<RN>);
-            const bool in = col + 8 * piece < cols;
-            cp_async16_or_zero(to0 + st, in ? p0 + col : a.x, in && at0 >= 0);
-            cp_async16_or_zero(to1 + st, in ? p1 + col : a.x, in && at1 >= 0);
+    tc_fence_after();
+    const uint32_t tmem = s_tmem, ring = smem_u32(smem), low = ring + kRing * S::kStage;
+    const bool f16 = std::is_same_v<T, __half>;
+    const int n1 = (a.r + 15) & ~15;                         // r in steps of the tensor cores
+    bool ok = true;                                          // false: a wait ran out, and no other is begun
+    // This thread copies a 16-byte piece of rows tid / 8 + 32 i of both tiles.
+    const int piece = tid & 7, r0 = tid >> 3;
+    const uint32_t to = swizzled(r0, piece);
+    const uint16_t *left[4];
+    bool has[4];
 #pragma unroll
-            for (int j = 0; j < kMine; ++j)
-                if (right) cp_async16_or_zero(tor[j] + st, okr[j] ? pr[j] + col * step : a.a, okr[j]);
+    for (int i = 0; i < 4; ++i) {
+        const int at = s_at[r0 + 32 * i];
+        has[i] = at >= 0;
+        left[i] = a.x + (has[i] ? at * a.ldx : 0) + 8 * piece;
+    }
+    const uint16_t *right = a.a + (size_t)g * a.r * a.H + 8 * piece;
+    auto fill_first = [&](int i, int slot) {
+        const int col = (rank + i * a.C) * 64;
+        if (col < a.H) {
+            const uint32_t st = ring + slot * S::kStage + to;
+            const bool in = col + 8 * piece < a.H;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cp_async16_or_zero(st + j * 4096, in ? left[j] + col : a.x, in && has[j]);
+#pragma unroll
+            for (int j = 0; j < 2 * RB; ++j) {
+                const int r = r0 + 32 * j;
+                const bool valid = in && r < a.r;
+                if (r < n1) cp_async16_or_zero(st + S::kLeft + j * 4096, valid ? right + (size_t)r * a.H + col : a.a, valid);
+            }
         }
         cp_async_commit();
     };
-    float acc[RN][4] = {};
-    const uint16_t *p0 = a.x + (at0 >= 0 ? at0 * a.ldx : 0) + 8 * piece, *p1 = a.x + (at1 >= 0 ? at1 * a.ldx : 0) + 8 * piece, *pr[kMine];
-    uint32_t tor[kMine];
-    bool okr[kMine];
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const int r = 32 * j + (tid >> 3);
-        okr[j] = r < a.r;
-        pr[j] = a.a + ((size_t)g * a.r + (okr[j] ? r : 0)) * a.H + 8 * piece;
-        tor[j] = base + (uint32_t)(offsetof(Ring<RN>, right) + piece_at<8>(r, piece) * 16);
-    }
-    auto fill_first = [&](int i, int slot) {                 // stage i of this CTA
-        const int col = (rank + i * a.C) * 64;
-        const bool in = col + 8 * piece < a.H;
-        bool ok[kMine];
-#pragma unroll
-        for (int j = 0; j < kMine; ++j) ok[j] = okr[j] && in;
-        fill(slot, col, a.H, p0, p1, pr, 1, tor, ok);
+    // ---- A x: every CTA sums its stages of H
+    int now = 0, then = kRing - 1;                           // the slot in use, and the one to fill
+    uint32_t phase = 0;                                      // of s_done, a bit each
+    auto done = [&](int i) {
+        if (ok) ok = mbar_wait(smem_u32(&s_done[i]), phase >> i & 1);
+        phase ^= 1u << i;
     };
     for (int i = 0; i < kRing - 1; ++i) fill_first(i, i);
-    int now = 0, then = kRing - 1;                           // the slot in use, and the one to fill
-    for (int i = 0; (rank + i * a.C) * 64 < a.H; ++i, now = now == kRing - 1 ? 0 : now + 1, then = then == kRing - 1 ? 0 : then + 1) {
+    const uint32_t id1 = mma_desc(f16, 128, n1, false, false);
+    for (int i = 0; (rank + i * a.C) * 64 < a.H; ++i) {
         cp_async_wait<kRing - 2>();
+        asm volatile("fence.proxy.async;" ::: "memory");
         __syncthreads();
-        fill_first(i + kRing - 1, then);
-        if (!busy) continue;
-        const Ring<RN> &st = ring[now];
-        const uint4 x0 = st.left[piece_at<8>(16 * rg + c, 4 * split + q)], x1 = st.left[piece_at<8>(16 * rg + c + 8, 4 * split + q)];
-#pragma unroll
-        for (int j = 0; j < RN; ++j) {
-            const uint4 w = st.right[piece_at<8>(8 * j + c, 4 * split + q)];
-            mma16<T>(acc[j], x0.x, x1.x, x0.y, x1.y, w.x, w.y);
-            mma16<T>(acc[j], x0.z, x1.z, x0.w, x1.w, w.z, w.w);
+        if (warp == 0 && elect_one()) {
+            tc_fence_after();
+            const uint64_t da = smem_desc(ring + now * S::kStage, 0), db = smem_desc(ring + now * S::kStage + S::kLeft, 0);
+            const int steps = min(4, (a.H - (rank + i * a.C) * 64 + 15) / 16);
+            for (int k = 0; k < steps; ++k) tc_mma<1>(tmem, da + 2 * k, db + 2 * k, id1, i > 0 || k > 0);
+            tc_commit<1>(smem_u32(&s_done[now]));
         }
+        __syncwarp();
+        if (i > 0) done(then);                               // the products of the stage before have read their slot
+        fill_first(i + kRing - 1, then);
+        then = now;
+        now = now == kRing - 1 ? 0 : now + 1;
     }
+    const bool any = rank * 64 < a.H;                        // (a CTA without a stage of H has zeros)
+    if (any) done(then);
     cp_async_wait<0>();
+    tc_fence_after();
     __syncthreads();
-    p0 = a.y + (at0 >= 0 ? at0 * a.ldy : 0) + 8 * piece;
-    p1 = a.y + (at1 >= 0 ? at1 * a.ldy : 0) + 8 * piece;
-    int rows_b[kMine];
+    // ---- the cluster's sums, as 16-bit operand
+    const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    float *const mine = reinterpret_cast<float *>(smem) + row * S::kPitch;
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const int p = j * kThreads + tid, n = p / RN, k = p % RN;
-        rows_b[j] = n;
-        okr[j] = 8 * k < a.r;
-        pr[j] = a.b + ((size_t)g * a.N + n) * a.r + (okr[j] ? 8 * k : 0);
-        tor[j] = base + (uint32_t)(offsetof(Ring<RN>, right) + piece_at<RN>(n, k) * 16);
-    }
-    auto fill_second = [&](int i, int slot) {
-        const int col = (rank + i * a.C) * 64;
-        bool ok[kMine];
+    for (int b = 0; b < RB; ++b) {
+        const int k0 = (half * RB + b) * 32;
+        if (k0 >= n1) continue;
+        float v[32] = {};
+        if (any) {
+            tmem_ld32(lanes + k0, v);
+            tmem_wait_ld();
+        }
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) ok[j] = okr[j] && col + rows_b[j] < a.N;
-        fill(slot, col, a.N, p0, p1, pr, a.r, tor, ok);
-    };
-    for (int i = 0; i < kRing - kHeld; ++i) fill_second(i, kHeld + i);          // what the sums leave room for comes meanwhile
-#pragma unroll
-    for (int j = 0; j < RN; ++j) {
-        float *const p = s_part + split * kPart + (16 * rg + c) * kPitch + 8 * j + 2 * q;
-        *reinterpret_cast<float2 *>(p) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2 *>(p + 8 * kPitch) = make_float2(acc[j][2], acc[j][3]);
-    }
-    __syncthreads();
-    for (int i = tid; i < kTileRows * kR / 4; i += kThreads) {
-        float4 *const p = reinterpret_cast<float4 *>(s_part + i / (kR / 4) * kPitch + i % (kR / 4) * 4);
-        const float4 u = p[0], v = p[kPart / 4];
-        p[0] = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+        for (int j = 0; j < 8; ++j) *reinterpret_cast<float4 *>(mine + k0 + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     }
     cluster_sync_all();                                      // (a barrier of the CTA where it is alone)
-    for (int i = tid; i < kTileRows * kR / 4; i += kThreads) {
-        const int r = i / (kR / 4), k4 = i % (kR / 4) * 4;
-        const uint32_t at = smem_u32(s_part + r * kPitch + k4);
-        float4 v = ld_cluster_f32x4(at_rank(at, 0));
-        for (int k = 1; k < a.C; ++k) {
-            const float4 u = ld_cluster_f32x4(at_rank(at, k));
-            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
-        }
-        float2 *const to = reinterpret_cast<float2 *>(s_all + r * kPitchAll + k4);
-        to[0] = make_float2(v.x, v.y);
-        to[1] = make_float2(v.z, v.w);
-        if constexpr (std::is_same_v<T, __half>) {           // kR / 4 lanes hold a row
-            float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+    float t[RB][32], most = 0.0f;
 #pragma unroll
-            for (int o = kR / 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-            if (k4 == 0) s_scale[r] = fp16_scale(m);
+    for (int b = 0; b < RB; ++b) {
+        const int k0 = (half * RB + b) * 32;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k0 + 4 * j < n1)
+                for (int k = 0; k < a.C; ++k) {
+                    const float4 u = ld_cluster_f32x4(at_rank(smem_u32(mine + k0 + 4 * j), k));
+                    v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+                }
+            t[b][4 * j] = v.x;
+            t[b][4 * j + 1] = v.y;
+            t[b][4 * j + 2] = v.z;
+            t[b][4 * j + 3] = v.w;
+            most = fmaxf(most, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
         }
     }
-    __syncthreads();
-    uint32_t hi[kK][4], lo[kK][4];
-    float back[2];                                           // adapter's scale, over the row's
-    int at[2];
-    const float scale = a.scale ? a.scale[g] : 1.0f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int j = 16 * rg + c + 8 * i;
-        at[i] = s_at[j];
-        float f = 1.0f;
-        if constexpr (std::is_same_v<T, __half>) f = s_scale[j];
-        back[i] = scale / f;
-#pragma unroll
-        for (int s = 0; s < kK; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = RN == 2 ? 4 * q + 2 * h : s / 2 * 32 + 8 * q + s % 2 * 4 + 2 * h;
-                const float2 v = *reinterpret_cast<const float2 *>(s_all + j * kPitchAll + k);
-                split2<T>(v.x * f, v.y * f, hi[s][i + 2 * h], lo[s][i + 2 * h]);
-            }
-    }
-    cluster_sync_all();                                      // the sums have been read everywhere: the ring has their place again
-    for (int i = kRing - kHeld; i < kRing - 1; ++i) fill_second(i, i - (kRing - kHeld));
-    now = kHeld;
-    then = kHeld - 1;
-    for (int i = 0; (rank + i * a.C) * 64 < a.N; ++i, now = now == kRing - 1 ? 0 : now + 1, then = then == kRing - 1 ? 0 : then + 1) {
-        cp_async_wait<kRing - 2>();
+    float f = 1.0f;                                          // a power of two per row keeps the sums in fp16's range
+    if (f16) {
+        s_most[half][row] = most;
         __syncthreads();
-        fill_second(i + kRing - 1, then);
-        const int n = (rank + i * a.C) * 64 + 32 * split + 8 * q;
-        if (!busy || n - 8 * q >= a.N) continue;
-        const Ring<RN> &st = ring[now];
-        float sum[4][4] = {};
-        const int nb = 32 * split + 8 * (c >> 1) + (c & 1);  // + 2j
-        if constexpr (RN == 2) {
-            uint2 w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = *(reinterpret_cast<const uint2 *>(st.right + (nb + 2 * j) * 2) + q);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma16<T>(sum[j], lo[0][0], lo[0][1], lo[0][2], lo[0][3], w[j].x, w[j].y);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma16<T>(sum[j], hi[0][0], hi[0][1], hi[0][2], hi[0][3], w[j].x, w[j].y);
-        } else {
-#pragma unroll
-            for (int s = 0; s < RN / 4; ++s) {               // four sums side by side: each product waits for the one before in its sum
-                uint4 w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = st.right[piece_at<RN>(nb + 2 * j, 4 * s + q)];
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const uint32_t *const f = h & 1 ? hi[2 * s + (h >> 1)] : lo[2 * s + (h >> 1)];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma16<T>(sum[j], f[0], f[1], f[2], f[3], h < 2 ? w[j].x : w[j].z, h < 2 ? w[j].y : w[j].w);
-                }
-            }
-        }
-        if (n >= a.N) continue;
-#pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2)
-            if (at[i2] >= 0) {
-                const uint4 y = st.left[piece_at<8>(16 * rg + c + 8 * i2, 4 * split + q)];
-                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 v = word_to_f32(w[j], T());
-                    o[j] = f32_to_word(fmaf(back[i2], sum[j][2 * i2], v.x), fmaf(back[i2], sum[j][2 * i2 + 1], v.y), T());
-                }
-                *reinterpret_cast<uint4 *>(a.out + at[i2] * a.ldo + n) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+        f = fp16_scale(fmaxf(most, s_most[half ^ 1][row]));
     }
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        const int k0 = (half * RB + b) * 32;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split2<T>(t[b][8 * j + 2 * i] * f, t[b][8 * j + 2 * i + 1] * f, hi[i], lo[i]);
+            uint8_t *const p = smem + kRing * S::kStage + (k0 / 64) * kTileRows * 128 + swizzled(row, k0 % 64 / 8 + j);
+            *reinterpret_cast<uint4 *>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(p + S::kLow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+    const float back = (a.scale ? a.scale[g] : 1.0f) / f;
+    cluster_sync_all();                                      // the sums have been read everywhere: the ring has their place again
+    // ---- out = y + B (A x): every CTA its stages of N
+#pragma unroll
+    for (int i = 0; i < 4; ++i) left[i] = a.y + (has[i] ? s_at[r0 + 32 * i] * a.ldy : 0) + 8 * piece;
+    right = a.b + (size_t)g * a.N * a.r + 8 * piece;
+    auto fill_second = [&](int i, int slot) {
+        const int col = (rank + i * a.C) * 64;
+        if (col < a.N) {
+            const uint32_t st = ring + slot * S::kStage + to;
+            const bool in = col + 8 * piece < a.N;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cp_async16_or_zero(st + j * 4096, in ? left[j] + col : a.y, in && has[j]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    const int n = col + r0 + 32 * j;
+                    const bool valid = n < a.N && 64 * b + 8 * piece < a.r;
+                    if (64 * b + 8 * piece < n1)
+                        cp_async16_or_zero(st + S::kLeft + b * 8192 + j * 4096, valid ? right + (size_t)n * a.r + 64 * b : a.b, valid);
+                }
+        }
+        cp_async_commit();
+    };
+    for (int i = 0; i < kRing - 1; ++i) fill_second(i, i);
+    now = 0;
+    then = kRing - 1;
+    const uint32_t id2 = mma_desc(f16, 128, 64, false, false);
+    for (int i = 0; (rank + i * a.C) * 64 < a.N; ++i) {
+        const int col = (rank + i * a.C) * 64;
+        cp_async_wait<kRing - 2>();
+        asm volatile("fence.proxy.async;" ::: "memory");
+        tc_fence_before();                                   // the sums before have been read
+        __syncthreads();
+        if (warp == 0 && elect_one()) {
+            tc_fence_after();
+            const uint64_t da = smem_desc(low, 0), db = smem_desc(ring + now * S::kStage + S::kLeft, 0);
+            for (int k = 0; k < n1 / 16; ++k) {
+                const uint64_t ka = (k >> 2) * (kTileRows * 128 / 16) + 2 * (k & 3), kb = (k >> 2) * (8192 / 16) + 2 * (k & 3);
+                tc_mma<1>(tmem, da + S::kLow / 16 + ka, db + kb, id2, k > 0);
+                tc_mma<1>(tmem, da + ka, db + kb, id2, true);
+            }
+            tc_commit<1>(smem_u32(&s_done[kRing]));
+        }
+        __syncwarp();
+        fill_second(i + kRing - 1, then);                    // the slot before was read before the barrier
+        done(kRing);
+        tc_fence_after();
+        uint8_t *const st = smem + now * S::kStage;
+        float v[32];
+        tmem_ld32(lanes + half * 32, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4 *const p = reinterpret_cast<uint4 *>(st + swizzled(row, half * 4 + j));
+            const uint4 y = *p;
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 yv = word_to_f32(w[k], T());
+                o[k] = f32_to_word(fmaf(back, v[8 * j + 2 * k], yv.x), fmaf(back, v[8 * j + 2 * k + 1], yv.y), T());
+            }
+            *p = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        __syncthreads();
+        if (col + 8 * piece < a.N) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (has[j]) *reinterpret_cast<uint4 *>(a.out + s_at[r0 + 32 * j] * a.ldo + col + 8 * piece) = *reinterpret_cast<const uint4 *>(st + to + j * 4096);
+        }
+        then = now;
+        now = now == kRing - 1 ? 0 : now + 1;
+    }
+    cp_async_wait<0>();
+    if (!ok) atomicOr(const_cast<int32_t *>(a.status), EP_STATUS_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 4) tmem_free<1>(tmem, kTmem);
 }
 
 template <auto kern> int launch_lora(const LoraArgs &a, size_t smem, int copy, cudaStream_t st) {
@@ -559,14 +585,14 @@ template <auto kern> int launch_lora(const LoraArgs &a, size_t smem, int copy, c
     return launch_result(cudaLaunchKernelEx(&cfg, kern, a, one_wave((int)cfg.gridDim.x)));
 }
 
-template <typename T, int RN> int launch_rank(const LoraArgs &a, int copy, cudaStream_t st) {
-    if (a.rows == kTileRows) return launch_lora<ep_lora_rows_kernel<T, RN>>(a, sizeof(Ring<RN>) * ring_stages(RN), copy, st);
-    return launch_lora<ep_lora_kernel<T, RN>>(a, (size_t)(kWarps + 2) * 16 * 8 * RN * sizeof(float), copy, st);
-}
 template <typename T> int launch_type(const LoraArgs &a, int copy, cudaStream_t st) {
-    if (a.r <= 16) return launch_rank<T, 2>(a, copy, st);
-    if (a.r <= 32) return launch_rank<T, 4>(a, copy, st);
-    return a.r <= 64 ? launch_rank<T, 8>(a, copy, st) : launch_rank<T, 16>(a, copy, st);
+    if (a.rows == kTileRows)
+        return a.r <= 64 ? launch_lora<ep_lora_tile_kernel<T, 1>>(a, TileSmem<1>::kBytes, copy, st)
+                         : launch_lora<ep_lora_tile_kernel<T, 2>>(a, TileSmem<2>::kBytes, copy, st);
+    const auto smem = [](int RN) { return (size_t)(kWarps + 2) * 16 * 8 * RN * sizeof(float); };
+    if (a.r <= 16) return launch_lora<ep_lora_kernel<T, 2>>(a, smem(2), copy, st);
+    if (a.r <= 32) return launch_lora<ep_lora_kernel<T, 4>>(a, smem(4), copy, st);
+    return a.r <= 64 ? launch_lora<ep_lora_kernel<T, 8>>(a, smem(8), copy, st) : launch_lora<ep_lora_kernel<T, 16>>(a, smem(16), copy, st);
 }
 
 bool lora_stride_ok(long long ld, int cols) { return ld >= cols && ld % 8 == 0; }
@@ -604,11 +630,11 @@ extern "C" int ep_lora_add(const void *y, long long y_stride, const void *x, lon
     const int sms = std::max(device_sm_count(), 1);
     p.rows = 1;
     while (p.rows < 16 && p.rows < per) p.rows *= 2;
-    if (per >= kTileRows) p.rows = kTileRows;
+    if (per >= 64) p.rows = kTileRows;
     p.tiles = (p.R_max + p.rows - 1) / p.rows;
     p.heads = p.rows > 1 ? p.G : 0;
-    p.C = 1;
-    while (p.C < kMaxCluster && ((long long)p.tiles + p.heads) * p.C * 2 <= 2 * sms && p.C * kWarps * 32 < std::max(H, N)) p.C *= 2;
+    const long long groups = (long long)p.tiles + p.heads, stages = (std::max(H, N) + 63) / 64;
+    p.C = (int)std::max(1ll, std::min({(long long)kMaxCluster, 2 * sms / groups, p.rows == kTileRows ? stages : (stages + 3) / 4}));
     int copy = by_token && out != y ? std::min((L->T + kWarps - 1) / kWarps, 2 * sms) : 0;
     copy = (copy + p.C - 1) / p.C * p.C;
     cudaStream_t st = as_stream(stream);
