@@ -3,17 +3,21 @@
 //
 //   out[t, :] = y[t, :] + scale[g] * B[g] (A[g] x[t, :])         for the adapter g of token t,
 //
-// out[t] = y[t] for a token without one.  A [G, r, H] and B [G, N, r] are read once per tile of rows, x and y once: HBM bounds
-// prompts, latency decode steps, so both products are one kernel.  A cluster of C CTAs takes a tile of rows.  Its warps split H
-// and add up A x with mma.sync (rows as M, r as N; the tensor cores are far from their rate at r <= 128), the partial sums are
-// added in a fixed order, first a CTA's warps through shared memory, then the CTAs through each other's, and the warps then
-// split N for the second product, which takes y along.  The contraction may take its k in any order as long as both
-// operands take the same one: a thread reads 8 consecutive elements of a row, and columns of the second product
-// are permuted so that a thread's sums are 8 consecutive outputs.
+// out[t] = y[t] for a token without one.  A [G, r, H] and B [G, N, r] are read once per tile of rows, x and y once.  A cluster of
+// C CTAs takes a tile of rows, all of one adapter, and both products of it, so that the r sums per row never leave the SMs:
+//   few rows    up to 16, on mma.sync (rows as M, r as N).  The warps of the cluster split H, add the sums up in a fixed order, first a
+//               CTA's through shared memory, then the CTAs' through each other's, and split N for the second product,
+//               which takes y along.  The contraction may take its k in any order as long as both operands take the same one: a thread reads
+//               8 consecutive elements of a row, and the second product's columns are permuted so that a thread's sums are
+//               8 consecutive outputs.  One token, rank 16, 2048 -> 2048: 4.0 us; 64 tokens, 48 adapters of rank 32, 7168 -> 4096:
+//               10.2 us (floor 3.9).  Latency bounds it: the ids, A and x, the exchange, B, one after another.
+//   many rows   128, on tcgen05.  8192 tokens, 5 adapters of rank 64, 4096 -> 4096: 60 us (floor 29).  HBM bounds the second half
+//               (5 TB/s), the exchange of the sums between the CTAs (a sixth of the time) and the copies' latency the first.
 #include <stddef.h>
 
 #include <algorithm>
 
+#include "ep_async.cuh"
 #include "ep_host.h"
 #include "ep_tensor.cuh"
 #include "ep_types.cuh"
@@ -32,6 +36,7 @@ struct LoraArgs {
     int H, N, r, T, G, R_max, by_token;
     int rows;                            // of the layout in a tile
     int tiles, heads, C;                 // tiles of rows; adapters' first rows apart (0 or G); CTAs on each
+    int copy;                            // whether rows without an adapter have to be copied
     const int32_t *row_offsets, *expert_ids, *src_info, *row_of, *status;
     uint16_t *out;
 };
@@ -95,13 +100,21 @@ struct Rows {
     }
 };
 
-// Rows without an adapter, to another buffer.
-__device__ void copy_rows(const LoraArgs &a, int cta, int ctas) {
-    for (int t = cta * kWarps + (threadIdx.x >> 5); t < a.T; t += ctas * kWarps) {
+// Rows without an adapter, to another buffer: the first eight warps of every CTA take some, eight 16-byte pieces per lane at a time.
+__device__ __forceinline__ void copy_rows(const LoraArgs &a) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int t = blockIdx.x * kWarps + warp; warp < kWarps && t < a.T; t += gridDim.x * kWarps) {
         const int row = a.row_of[t];
         if (row >= 0 && row < a.R_max) continue;
-        for (int n = (threadIdx.x & 31) * 8; n < a.N; n += 256)
-            *reinterpret_cast<uint4 *>(a.out + t * a.ldo + n) = *reinterpret_cast<const uint4 *>(a.y + t * a.ldy + n);
+        for (int n0 = lane * 8; n0 < a.N; n0 += 8 * 256) {
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (n0 + i * 256 < a.N) v[i] = *reinterpret_cast<const uint4 *>(a.y + t * a.ldy + n0 + i * 256);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (n0 + i * 256 < a.N) *reinterpret_cast<uint4 *>(a.out + t * a.ldo + n0 + i * 256) = v[i];
+        }
     }
 }
 
@@ -150,8 +163,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane >> 2, q = lane & 3;
     pdl_begin_if(one_wave);
     const int tile = blockIdx.x / a.C, rank = blockIdx.x % a.C, part = rank * kWarps + warp, parts = a.C * kWarps;
-    const bool copies = tile >= a.tiles + a.heads;
-    const Rows rows(a, copies ? 0 : tile);
+    const Rows rows(a, tile);
     if constexpr (kBoundsCheck) {                            // another CTA may set a bit meanwhile: the cluster acts on one reading
         __shared__ int s_status;
         if (tid == 0) s_status = load_status(a.status);
@@ -163,11 +175,10 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     } else if (load_status(a.status)) {
         return;
     }
-    if (copies) {
-        copy_rows(a, blockIdx.x - (a.tiles + a.heads) * a.C, gridDim.x - (a.tiles + a.heads) * a.C);
+    if (rows.end <= rows.first) {
+        if (a.copy) copy_rows(a);
         return;
     }
-    if (rows.end <= rows.first) return;
     const int g = rows.g;
     int at[2];                                           // the row of x, y and out; -1: none
 #pragma unroll
@@ -287,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
                 *reinterpret_cast<uint4 *>(a.out + at[i] * a.ldo + n) = make_uint4(o[0], o[1], o[2], o[3]);
             }
     }
+    if (a.copy) copy_rows(a);
     if (a.C > 1) cluster_sync_all();                         // the sums have been read everywhere
 }
 
@@ -294,15 +306,16 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
 // The same for tiles of 128 rows on tcgen05, where the bytes of x, y and out are what counts.  The rows are M; both products stream
 // through a ring in shared memory that cp.async fills ahead: 64 columns of x with 64 of A (N is r), then 64 of y with 64 rows of B
 // (K is r).  The CTAs of a cluster split H, add up A x through each other's shared memory, and split N.  (With mma.sync from
-// shared memory the tensor cores and the shared memory's bandwidth bound it: 71 us where this takes TCUS, 8192 tokens, 5 adapters of rank 64,
-// 4096 -> 4096.)
-constexpr int kTileRows = 128, kRing = 3;
+// shared memory its products took half of the time: 71 us with 8192 tokens, 5 adapters of rank 64, 4096 -> 4096, where this takes 60.)
+constexpr int kTileRows = 128, kRing = 3, kTileThreads = kThreads + 32;           // the last warp issues the products
 
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gmem, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(valid ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// An arrival once this thread's copies so far have landed (counted in the barrier's total).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 // Where 16-byte piece p (of 8) of a row is in a tile of 128-byte rows, in the swizzle that tcgen05.mma reads.
 __device__ __forceinline__ uint32_t swizzled(int row, int p) { return row * 128 + ((p ^ (row & 7)) << 4); }
@@ -316,21 +329,22 @@ template <int RB> struct TileSmem {
     static_assert(kTileRows * kPitch * 4 <= kRing * kStage, "the exchanged sums take the place of the ring");
 };
 
+// Eight warps copy, add up and write; the ninth waits for what they copied and issues the products.  It fences as well: the
+// fence between copies and tensor cores waits for all copies of the thread that issues it, those of later stages too.
 template <typename T, int RB>
-__global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a, int one_wave) {
+__global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraArgs a, int one_wave) {
     using S = TileSmem<RB>;
     constexpr uint32_t kTmem = 128;                          // columns: the sums of A x, then of 64 outputs
     extern __shared__ __align__(16) uint8_t s_raw[];
     uint8_t *const smem = s_raw + (1024 - (smem_u32(s_raw) & 1023)) % 1024;
-    __shared__ __align__(8) uint64_t s_done[kRing + 1];
+    __shared__ __align__(8) uint64_t s_full[kRing], s_free[kRing], s_done[2];
     __shared__ uint32_t s_tmem;
     __shared__ float s_most[2][kTileRows];
     __shared__ int s_at[kTileRows];
     const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
     pdl_begin_if(one_wave);
     const int tile = blockIdx.x / a.C, rank = blockIdx.x % a.C;
-    const bool copies = tile >= a.tiles + a.heads;
-    const Rows rows(a, copies ? 0 : tile);
+    const Rows rows(a, tile);
     if constexpr (kBoundsCheck) {
         __shared__ int s_status;
         if (tid == 0) s_status = load_status(a.status);
@@ -342,11 +356,10 @@ __global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a
     } else if (load_status(a.status)) {
         return;
     }
-    if (copies) {
-        copy_rows(a, blockIdx.x - (a.tiles + a.heads) * a.C, gridDim.x - (a.tiles + a.heads) * a.C);
+    if (rows.end <= rows.first) {
+        if (a.copy) copy_rows(a);
         return;
     }
-    if (rows.end <= rows.first) return;
     const int g = rows.g;
     if (tid < kTileRows) {
         const int row = rows.first + tid;
@@ -359,7 +372,12 @@ __global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a
     }
     if (warp == 4) tmem_alloc<1>(smem_u32(&s_tmem), kTmem);
     if (tid == 0) {
-        for (int i = 0; i <= kRing; ++i) mbar_init(smem_u32(&s_done[i]), 1);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(smem_u32(&s_full[i]), kThreads);
+            mbar_init(smem_u32(&s_free[i]), kWarps);
+        }
+        mbar_init(smem_u32(&s_done[0]), 1);
+        mbar_init(smem_u32(&s_done[1]), 1);
         mbar_init_done();
     }
     tc_fence_before();
@@ -370,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a
     const int n1 = (a.r + 15) & ~15;                         // r in steps of the tensor cores
     bool ok = true;                                          // false: a wait ran out, and no other is begun
     // This thread copies a 16-byte piece of rows tid / 8 + 32 i of both tiles.
-    const int piece = tid & 7, r0 = tid >> 3;
+    const int piece = tid & 7, r0 = (tid & (kThreads - 1)) >> 3;
     const uint32_t to = swizzled(r0, piece);
     const uint16_t *left[4];
     bool has[4];
@@ -381,8 +399,9 @@ __global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a
         left[i] = a.x + (has[i] ? at * a.ldx : 0) + 8 * piece;
     }
     const uint16_t *right = a.a + (size_t)g * a.r * a.H + 8 * piece;
+    const int first1 = (a.H + 63) / 64 * rank / a.C;
     auto fill_first = [&](int i, int slot) {
-        const int col = (rank + i * a.C) * 64;
+        const int col = (first1 + i) * 64;
         if (col < a.H) {
             const uint32_t st = ring + slot * S::kStage + to;
             const bool in = col + 8 * piece < a.H;
@@ -395,49 +414,50 @@ __global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a
                 if (r < n1) cp_async16_or_zero(st + S::kLeft + j * 4096, valid ? right + (size_t)r * a.H + col : a.a, valid);
             }
         }
-        cp_async_commit();
+        cp_async_arrive(smem_u32(&s_full[slot]));
     };
-    // ---- A x: every CTA sums its stages of H
-    int now = 0, then = kRing - 1;                           // the slot in use, and the one to fill
-    uint32_t phase = 0;                                      // of s_done, a bit each
-    auto done = [&](int i) {
-        if (ok) ok = mbar_wait(smem_u32(&s_done[i]), phase >> i & 1);
-        phase ^= 1u << i;
+    // ---- A x: every CTA sums its stages of H.  Stage i is in slot i % kRing; barriers' phases count on through both parts.
+    const int first2 = (a.N + 63) / 64 * rank / a.C, stages1 = (a.H + 63) / 64 * (rank + 1) / a.C - first1, stages2 = (a.N + 63) / 64 * (rank + 1) / a.C - first2;
+    auto wait = [&](uint64_t &bar, int phase) {
+        if (ok) ok = mbar_wait(smem_u32(&bar), phase & 1);
     };
-    for (int i = 0; i < kRing - 1; ++i) fill_first(i, i);
-    const uint32_t id1 = mma_desc(f16, 128, n1, false, false);
-    for (int i = 0; (rank + i * a.C) * 64 < a.H; ++i) {
-        cp_async_wait<kRing - 2>();
-        asm volatile("fence.proxy.async;" ::: "memory");
-        __syncthreads();
-        if (warp == 0 && elect_one()) {
-            tc_fence_after();
-            const uint64_t da = smem_desc(ring + now * S::kStage, 0), db = smem_desc(ring + now * S::kStage + S::kLeft, 0);
-            const int steps = min(4, (a.H - (rank + i * a.C) * 64 + 15) / 16);
-            for (int k = 0; k < steps; ++k) tc_mma<1>(tmem, da + 2 * k, db + 2 * k, id1, i > 0 || k > 0);
-            tc_commit<1>(smem_u32(&s_done[now]));
+    const bool issuer = warp == kWarps;
+    if (issuer) {
+        const uint32_t id1 = mma_desc(f16, 128, n1, false, false);
+        for (int i = 0; i < stages1; ++i) {
+            const int slot = i % kRing;
+            wait(s_full[slot], i / kRing);
+            fence_proxy_async_smem();
+            if (elect_one()) {
+                tc_fence_after();
+                const uint64_t da = smem_desc(ring + slot * S::kStage, 0), db = smem_desc(ring + slot * S::kStage + S::kLeft, 0);
+                const int steps = min(4, (a.H - (first1 + i) * 64 + 15) / 16);
+                for (int k = 0; k < steps; ++k) tc_mma<1>(tmem, da + 2 * k, db + 2 * k, id1, i > 0 || k > 0);
+                tc_commit<1>(smem_u32(&s_done[i & 1]));
+            }
+            __syncwarp();
         }
-        __syncwarp();
-        if (i > 0) done(then);                               // the products of the stage before have read their slot
-        fill_first(i + kRing - 1, then);
-        then = now;
-        now = now == kRing - 1 ? 0 : now + 1;
+    } else {
+        for (int i = 0; i < kRing - 1 && i < stages1; ++i) fill_first(i, i);
+        if (a.copy) copy_rows(a);                            // while they are on their way
+        for (int i = 0; i < stages1; ++i) {
+            if (i > 0) wait(s_done[(i - 1) & 1], (i - 1) >> 1);          // the products of stage i - 1 have read its slot
+            if (i + kRing - 1 < stages1) fill_first(i + kRing - 1, (i + kRing - 1) % kRing);
+        }
+        if (stages1 > 0) wait(s_done[(stages1 - 1) & 1], (stages1 - 1) >> 1);
     }
-    const bool any = rank * 64 < a.H;                        // (a CTA without a stage of H has zeros)
-    if (any) done(then);
-    cp_async_wait<0>();
     tc_fence_after();
     __syncthreads();
     // ---- the cluster's sums, as 16-bit operand
-    const int q = warp & 3, half = warp >> 2, row = q * 32 + lane;
+    const int q = warp & 3, half = (warp >> 2) & 1, row = q * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     float *const mine = reinterpret_cast<float *>(smem) + row * S::kPitch;
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
         const int k0 = (half * RB + b) * 32;
-        if (k0 >= n1) continue;
+        if (issuer || k0 >= n1) continue;
         float v[32] = {};
-        if (any) {
+        if (stages1 > 0) {
             tmem_ld32(lanes + k0, v);
             tmem_wait_ld();
         }
@@ -445,28 +465,55 @@ __global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a
         for (int j = 0; j < 8; ++j) *reinterpret_cast<float4 *>(mine + k0 + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     }
     cluster_sync_all();                                      // (a barrier of the CTA where it is alone)
+    // Lanes side by side read a row side by side: 16-byte reads of 32 rows of another CTA's took 60,000 cycles for what takes
+    // 4,000 so.  The sums pass through the operand's place, a row's pieces exchanged so that a thread reads its row without conflicts.
+    float4 *const all = reinterpret_cast<float4 *>(smem + kRing * S::kStage);
+    const int pieces = n1 / 4;
+    constexpr int kBatch = 4;                                // loads on their way together: each takes some 700 cycles
+    for (int i0 = tid; i0 < kTileRows * pieces; i0 += kBatch * kTileThreads) {
+        uint32_t from[kBatch];
+        float4 v[kBatch] = {};
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = min(i0 + j * kTileThreads, kTileRows * pieces - 1);
+            from[j] = smem_u32(reinterpret_cast<float *>(smem) + i / pieces * S::kPitch + i % pieces * 4);
+        }
+        for (int o = 0; o < a.C; o += 2) {
+            float4 u[2][kBatch];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) u[h][j] = ld_cluster_f32x4(at_rank(from[j], min(o + h, a.C - 1)));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    if (o + h < a.C) v[j] = make_float4(v[j].x + u[h][j].x, v[j].y + u[h][j].y, v[j].z + u[h][j].z, v[j].w + u[h][j].w);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * kTileThreads, r = i / pieces, k = i % pieces;
+            if (i < kTileRows * pieces) all[r * 16 * RB + (k ^ (r & 15))] = v[j];
+        }
+    }
+    __syncthreads();
     float t[RB][32], most = 0.0f;
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-        const int k0 = (half * RB + b) * 32;
+    for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (k0 + 4 * j < n1)
-                for (int k = 0; k < a.C; ++k) {
-                    const float4 u = ld_cluster_f32x4(at_rank(smem_u32(mine + k0 + 4 * j), k));
-                    v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
-                }
+            const int k = (half * RB + b) * 8 + j;
+            const float4 v = k < pieces ? all[row * 16 * RB + (k ^ (row & 15))] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             t[b][4 * j] = v.x;
             t[b][4 * j + 1] = v.y;
             t[b][4 * j + 2] = v.z;
             t[b][4 * j + 3] = v.w;
             most = fmaxf(most, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
         }
-    }
+    __syncthreads();
     float f = 1.0f;                                          // a power of two per row keeps the sums in fp16's range
     if (f16) {
-        s_most[half][row] = most;
+        if (!issuer) s_most[half][row] = most;
         __syncthreads();
         f = fp16_scale(fmaxf(most, s_most[half ^ 1][row]));
     }
@@ -479,18 +526,21 @@ __global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a
 #pragma unroll
             for (int i = 0; i < 4; ++i) split2<T>(t[b][8 * j + 2 * i] * f, t[b][8 * j + 2 * i + 1] * f, hi[i], lo[i]);
             uint8_t *const p = smem + kRing * S::kStage + (k0 / 64) * kTileRows * 128 + swizzled(row, k0 % 64 / 8 + j);
+            if (issuer) continue;
             *reinterpret_cast<uint4 *>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(p + S::kLow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
     const float back = (a.scale ? a.scale[g] : 1.0f) / f;
+    fence_proxy_async_smem();
+    tc_fence_before();
     cluster_sync_all();                                      // the sums have been read everywhere: the ring has their place again
     // ---- out = y + B (A x): every CTA its stages of N
 #pragma unroll
     for (int i = 0; i < 4; ++i) left[i] = a.y + (has[i] ? s_at[r0 + 32 * i] * a.ldy : 0) + 8 * piece;
     right = a.b + (size_t)g * a.N * a.r + 8 * piece;
     auto fill_second = [&](int i, int slot) {
-        const int col = (rank + i * a.C) * 64;
+        const int col = (first2 + i) * 64;
         if (col < a.N) {
             const uint32_t st = ring + slot * S::kStage + to;
             const bool in = col + 8 * piece < a.N;
@@ -506,59 +556,72 @@ __global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a
                         cp_async16_or_zero(st + S::kLeft + b * 8192 + j * 4096, valid ? right + (size_t)n * a.r + 64 * b : a.b, valid);
                 }
         }
-        cp_async_commit();
+        cp_async_arrive(smem_u32(&s_full[slot]));
     };
-    for (int i = 0; i < kRing - 1; ++i) fill_second(i, i);
-    now = 0;
-    then = kRing - 1;
-    const uint32_t id2 = mma_desc(f16, 128, 64, false, false);
-    for (int i = 0; (rank + i * a.C) * 64 < a.N; ++i) {
-        const int col = (rank + i * a.C) * 64;
-        cp_async_wait<kRing - 2>();
-        asm volatile("fence.proxy.async;" ::: "memory");
-        tc_fence_before();                                   // the sums before have been read
-        __syncthreads();
-        if (warp == 0 && elect_one()) {
+    tc_fence_after();
+    // Barriers have gone through these many phases: s_full by slot, s_done by parity.
+    auto full_phase = [&](int i) { return (stages1 - i % kRing + kRing - 1) / kRing + i / kRing; };
+    auto done_phase = [&](int i) { return (stages1 + 1 - (i & 1)) / 2 + (i >> 1); };
+    if (issuer) {
+        const uint32_t id2 = mma_desc(f16, 128, 64, false, false);
+        for (int i = 0; i < stages2; ++i) {
+            const int slot = i % kRing;
+            wait(s_full[slot], full_phase(i));
+            // (twice 64 columns of sums: those of stage i - 2 have been read when its slot's successor is filled)
+            if (i >= 2) wait(s_free[(i - 2) % kRing], (i - 2) / kRing);
+            fence_proxy_async_smem();
+            if (elect_one()) {
+                tc_fence_after();
+                const uint64_t da = smem_desc(low, 0), db = smem_desc(ring + slot * S::kStage + S::kLeft, 0);
+                for (int k = 0; k < n1 / 16; ++k) {
+                    const uint64_t ka = (k >> 2) * (kTileRows * 128 / 16) + 2 * (k & 3), kb = (k >> 2) * (8192 / 16) + 2 * (k & 3);
+                    tc_mma<1>(tmem + (i & 1) * 64, da + S::kLow / 16 + ka, db + kb, id2, k > 0);
+                    tc_mma<1>(tmem + (i & 1) * 64, da + ka, db + kb, id2, true);
+                }
+                tc_commit<1>(smem_u32(&s_done[i & 1]));
+            }
+            __syncwarp();
+        }
+    } else {
+        for (int i = 0; i < kRing - 1 && i < stages2; ++i) fill_second(i, i);
+        for (int i = 0; i < stages2; ++i) {
+            const int slot = i % kRing, col = (first2 + i) * 64;
+            if (i > 0) wait(s_free[(i - 1) % kRing], (i - 1) / kRing);   // every warp has written stage i - 1
+            if (i + kRing - 1 < stages2) fill_second(i + kRing - 1, (i + kRing - 1) % kRing);
+            wait(s_full[slot], full_phase(i));
+            wait(s_done[i & 1], done_phase(i));
+            __syncwarp();
             tc_fence_after();
-            const uint64_t da = smem_desc(low, 0), db = smem_desc(ring + now * S::kStage + S::kLeft, 0);
-            for (int k = 0; k < n1 / 16; ++k) {
-                const uint64_t ka = (k >> 2) * (kTileRows * 128 / 16) + 2 * (k & 3), kb = (k >> 2) * (8192 / 16) + 2 * (k & 3);
-                tc_mma<1>(tmem, da + S::kLow / 16 + ka, db + kb, id2, k > 0);
-                tc_mma<1>(tmem, da + ka, db + kb, id2, true);
+            uint8_t *const st = smem + slot * S::kStage;
+            float v[32];
+            tmem_ld32(lanes + (i & 1) * 64 + half * 32, v);
+            tmem_wait_ld();
+            tc_fence_before();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint4 *const p = reinterpret_cast<uint4 *>(st + swizzled(row, half * 4 + j));
+                const uint4 y = *p;
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 yv = word_to_f32(w[k], T());
+                    o[k] = f32_to_word(fmaf(back, v[8 * j + 2 * k], yv.x), fmaf(back, v[8 * j + 2 * k + 1], yv.y), T());
+                }
+                *p = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            tc_commit<1>(smem_u32(&s_done[kRing]));
-        }
-        __syncwarp();
-        fill_second(i + kRing - 1, then);                    // the slot before was read before the barrier
-        done(kRing);
-        tc_fence_after();
-        uint8_t *const st = smem + now * S::kStage;
-        float v[32];
-        tmem_ld32(lanes + half * 32, v);
-        tmem_wait_ld();
+            __syncwarp();
+            // this warp's 32 rows and 32 columns, four lanes to a row
+            const int n = col + half * 32 + (lane & 3) * 8;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint4 *const p = reinterpret_cast<uint4 *>(st + swizzled(row, half * 4 + j));
-            const uint4 y = *p;
-            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 yv = word_to_f32(w[k], T());
-                o[k] = f32_to_word(fmaf(back, v[8 * j + 2 * k], yv.x), fmaf(back, v[8 * j + 2 * k + 1], yv.y), T());
+            for (int j = 0; j < 4; ++j) {
+                const int r = q * 32 + j * 8 + (lane >> 2), at = s_at[r];
+                if (at >= 0 && n < a.N) *reinterpret_cast<uint4 *>(a.out + at * a.ldo + n) = *reinterpret_cast<const uint4 *>(st + swizzled(r, half * 4 + (lane & 3)));
             }
-            *p = make_uint4(o[0], o[1], o[2], o[3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(at_rank(smem_u32(&s_free[slot]), cluster_rank()));
         }
-        __syncthreads();
-        if (col + 8 * piece < a.N) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (has[j]) *reinterpret_cast<uint4 *>(a.out + s_at[r0 + 32 * j] * a.ldo + col + 8 * piece) = *reinterpret_cast<const uint4 *>(st + to + j * 4096);
-        }
-        then = now;
-        now = now == kRing - 1 ? 0 : now + 1;
     }
-    cp_async_wait<0>();
     if (!ok) atomicOr(const_cast<int32_t *>(a.status), EP_STATUS_TIMEOUT);
     tc_fence_before();
     __syncthreads();
@@ -566,12 +629,12 @@ __global__ void __launch_bounds__(kThreads) ep_lora_tile_kernel(const LoraArgs a
     if (warp == 4) tmem_free<1>(tmem, kTmem);
 }
 
-template <auto kern> int launch_lora(const LoraArgs &a, size_t smem, int copy, cudaStream_t st) {
+template <auto kern> int launch_lora(const LoraArgs &a, int threads, size_t smem, cudaStream_t st) {
     const int rc = allow_smem<kern>(smem);
     if (rc != EP_OK) return rc;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.tiles + a.heads) * a.C + copy));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)((a.tiles + a.heads) * a.C));
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -585,15 +648,21 @@ template <auto kern> int launch_lora(const LoraArgs &a, size_t smem, int copy, c
     return launch_result(cudaLaunchKernelEx(&cfg, kern, a, one_wave((int)cfg.gridDim.x)));
 }
 
-template <typename T> int launch_type(const LoraArgs &a, int copy, cudaStream_t st) {
+template <typename T> int launch_type(const LoraArgs &a, cudaStream_t st) {
     if (a.rows == kTileRows)
-        return a.r <= 64 ? launch_lora<ep_lora_tile_kernel<T, 1>>(a, TileSmem<1>::kBytes, copy, st)
-                         : launch_lora<ep_lora_tile_kernel<T, 2>>(a, TileSmem<2>::kBytes, copy, st);
+        return a.r <= 64 ? launch_lora<ep_lora_tile_kernel<T, 1>>(a, kTileThreads, TileSmem<1>::kBytes, st)
+                         : launch_lora<ep_lora_tile_kernel<T, 2>>(a, kTileThreads, TileSmem<2>::kBytes, st);
     const auto smem = [](int RN) { return (size_t)(kWarps + 2) * 16 * 8 * RN * sizeof(float); };
-    if (a.r <= 16) return launch_lora<ep_lora_kernel<T, 2>>(a, smem(2), copy, st);
-    if (a.r <= 32) return launch_lora<ep_lora_kernel<T, 4>>(a, smem(4), copy, st);
-    return a.r <= 64 ? launch_lora<ep_lora_kernel<T, 8>>(a, smem(8), copy, st) : launch_lora<ep_lora_kernel<T, 16>>(a, smem(16), copy, st);
+    if (a.r <= 16) return launch_lora<ep_lora_kernel<T, 2>>(a, kThreads, smem(2), st);
+    if (a.r <= 32) return launch_lora<ep_lora_kernel<T, 4>>(a, kThreads, smem(4), st);
+    return a.r <= 64 ? launch_lora<ep_lora_kernel<T, 8>>(a, kThreads, smem(8), st) : launch_lora<ep_lora_kernel<T, 16>>(a, kThreads, smem(16), st);
 }
+
+// Tiles of 128 rows begin slowly (their sums cross the cluster, 19 us at least) and then read A and B an eighth as often as tiles of
+// 16 rows, whose time is about 3.2e-7 us per 16 rows, column of x or y, and (r + 25).  The border is at 50 us of that.  16 / 128 rows:
+// 1024 tokens, 4 adapters of rank 16, 4096 -> 4096: 8.2 / 21 us; 2048, 16 of rank 64, 2048 -> 2048: 17 / 43; 8192, 1 of rank 16,
+// 4096 -> 4096: 55 / 50; 4096, 32 of rank 128: 91 / 82; 8192, 5 of rank 64: 119 / 58; 16384, 8 of rank 16, 2048 -> 6144: 133 / 95.
+bool takes_tiles(long long rows, int H, int N, int rank) { return rows * (H + N) * (rank + 25) >= 2500000000ll; }
 
 bool lora_stride_ok(long long ld, int cols) { return ld >= cols && ld % 8 == 0; }
 
@@ -626,17 +695,16 @@ extern "C" int ep_lora_add(const void *y, long long y_stride, const void *x, lon
     p.out = (uint16_t *)out;
     if (p.R_max == 0) p.R_max = 1;
     // a tile's rows: about as many as an adapter has; then as many CTAs to a tile as two to an SM allow
-    const long long per = (long long)L->T * L->K / p.G;
+    const long long all = rows_max(L->T, L->K, L->fused_shared), per = all / p.G;
     const int sms = std::max(device_sm_count(), 1);
     p.rows = 1;
     while (p.rows < 16 && p.rows < per) p.rows *= 2;
-    if (per >= 64) p.rows = kTileRows;
+    if (per >= kTileRows && takes_tiles(all, H, N, rank)) p.rows = kTileRows;
     p.tiles = (p.R_max + p.rows - 1) / p.rows;
     p.heads = p.rows > 1 ? p.G : 0;
     const long long groups = (long long)p.tiles + p.heads, stages = (std::max(H, N) + 63) / 64;
     p.C = (int)std::max(1ll, std::min({(long long)kMaxCluster, 2 * sms / groups, p.rows == kTileRows ? stages : (stages + 3) / 4}));
-    int copy = by_token && out != y ? std::min((L->T + kWarps - 1) / kWarps, 2 * sms) : 0;
-    copy = (copy + p.C - 1) / p.C * p.C;
+    p.copy = by_token && out != y;
     cudaStream_t st = as_stream(stream);
-    return dtype == EP_F16 ? launch_type<__half>(p, copy, st) : launch_type<__nv_bfloat16>(p, copy, st);
+    return dtype == EP_F16 ? launch_type<__half>(p, st) : launch_type<__nv_bfloat16>(p, st);
 }

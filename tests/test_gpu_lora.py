@@ -49,7 +49,10 @@ def check(ep, ids, y, x, a, b, scale, in_place=False):
 # (T, adapters, r, H, N): one token; every tile of rows; each width of the rank; odd sizes; one adapter for all
 CASES = [(1, 1, 8, 16, 16), (1, 32, 16, 2048, 2048), (7, 3, 24, 80, 48), (16, 1, 32, 256, 272), (33, 2, 40, 272, 96), (64, 48, 32, 1024, 512),
          (65, 1, 64, 144, 1040), (100, 5, 72, 528, 304), (300, 4, 128, 512, 160), (500, 7, 64, 384, 208), (130, 1000, 16, 64, 32),
-         (2000, 3, 16, 96, 64), (40, 2, 104, 32768, 16), (24, 8, 8, 7168, 4096)]
+         (2000, 3, 16, 96, 64), (40, 2, 104, 32768, 16), (24, 8, 8, 7168, 4096),
+         # enough of everything for tiles of 128 rows: each width of the rank, odd sizes, one adapter, ragged ends
+         (3000, 3, 72, 7168, 1456), (20000, 7, 24, 1040, 1520), (9000, 2, 128, 1136, 720), (70000, 5, 8, 512, 608), (8200, 1, 16, 4096, 4112),
+         (14000, 9, 64, 48, 2064), (12000, 2, 40, 3200, 32)]
 
 
 @pytest.mark.parametrize("T,G,r,H,N", CASES)
