@@ -5,12 +5,23 @@
 //   grad_x      out[r, k] = sum over n of grad[r, n] w[g, n, k]              (or, through the gate, that of gate and up)
 //   grad_w      out[g, n, k] = sum over the rows r of g of grad[r, n] x[r, k]
 //
-// One persistent kernel, templated on the form.  The weights' rows (or columns) are M of the tensor cores' product and the layout's
-// rows are N, in steps of 32: a group of any number of rows then costs about what its rows cost, and weights, which have
-// hundreds of rows or more, fill M.  A pair of CTAs shares a product of 256 x 256: each loads 128 of M and half of N by TMA and
-// keeps the sums of its 128 of M in tensor memory, twice, so that one tile's results leave while the next one's
-// are added up.  Warp 0 loads, warp 1 of the first CTA issues the products, warps 4 to 11 take results out, four at a time 32
-// columns; warp 2 (grad_w) clears the rows behind a group's last one in shared memory, since there they are summed over.
+// One kernel, templated on the form, of CTA pairs that stay: a pair takes the places of pairs that have not begun until none is left,
+// so that pairs which drew long tiles take fewer.  The weights' rows (or columns) are M of the tensor cores' product and the
+// layout's rows are N, in steps of 32: a group of any number of rows then costs about what its rows cost, and weights, which have
+// hundreds of rows or more, fill M.  A pair shares a product of 256 x 256: each CTA loads 128 of M and half of N by TMA, one copy for
+// an operand, and keeps the sums of its 128 of M in tensor memory, twice, so that one tile's results leave while the next one's are
+// added up.  Warp 0 loads, warp 1 of the first CTA issues the products, warp 3 looks tiles up ahead of the others, warps 4 to 11 take
+// results out, four at a time 32 columns; warp 2 (grad_w) clears the rows behind a group's last one in shared memory, since
+// there they are summed over.  No atomics: the order of every sum is fixed.
+//
+// 4864 rows of one group, 4096 -> 4096: 83 us, 1970 TFLOP/s (0.98 of the measured cuBLAS burst), and so the gated form and grad_x; K = 16384:
+// 332 us, where the power limit lowers the clock.  Many groups of few rows are bound by HBM (256 tokens, top-8 of 64 and a shared
+// expert, 7168 -> 2 x 2048 gated: 560 us, 6.7 TB/s), those between by the way from L2, which has to bring 32 KB for 512 cycles of
+// products at 256 rows and as much for half the work at 128, while outputs leave: 8192 tokens, top-8 of 128, 2048 -> 2 x 768
+// gated with gate and up saved 287 us (floor 205), its down product 148 (115), grad_x through the gate 181 (160), grad_w 180 (115).
+// Without its loads / its outputs the first of them took 207 / 276 us of 324 then; fetching the next tile's operands into L2
+// ahead (by TMA, or in bulk) cost 10 to 150 % everywhere, eviction hints changed nothing, and taking several groups at a time, less read
+// at the same moment by several pairs, cost 4 to 60 %.
 #include <limits.h>
 #include <math.h>
 
@@ -26,6 +37,7 @@ namespace {
 
 enum Form { kPlain, kGlu, kGradX, kGradGate, kGradW };
 
+constexpr int kPair = 2;                      // CTAs that work on one product
 constexpr int kThreads = 384;
 constexpr int kOutGroups = 2;                // of four warps that take results out
 constexpr int kBlockK = 64;                  // of the summed dimension in a stage: 128 bytes, one swizzle row
@@ -81,9 +93,9 @@ struct LinearArgs {
 };
 
 // What tile number `tile` is.
-template <Form FORM, int CG> struct Tiles {
-    static constexpr int kM = FORM == kGlu ? 64 * CG : 128 * CG, kN = 128 * CG;
-    static constexpr int kUnit = 16 * CG;    // of N in a product
+template <Form FORM> struct Tiles {
+    static constexpr int kM = FORM == kGlu ? 64 * kPair : 128 * kPair, kN = 128 * kPair;
+    static constexpr int kUnit = 16 * kPair;    // of N in a product
     const LinearArgs &a;
     const Control &c;
 
@@ -131,8 +143,8 @@ template <Form FORM, int CG> struct Tiles {
             w.last = a.sum - (w.kb - 1) * kBlockK;
         }
         // whole blocks of 64 where one copy brings them
-        const int unit = FORM == kGradW && a.whole_b ? 64 : kUnit / CG;
-        w.half = (w.n + unit * CG - 1) / (unit * CG) * unit;
+        const int unit = FORM == kGradW && a.whole_b ? 64 : kUnit / kPair;
+        w.half = (w.n + unit * kPair - 1) / (unit * kPair) * unit;
         return true;
     }
     // grad_w: the next chunk of the same tile.
@@ -201,14 +213,14 @@ struct Sigmoid {
 };
 
 // Into a stage in shared memory.
-template <int CG> struct Load {
+struct Load {
     uint32_t stage, bar;
-    template <int DIMS> __device__ void operator()(int at, const CUtensorMap &m, const int (&c)[DIMS]) const { tma_load<CG, DIMS>(stage + at, &m, c, bar); }
+    template <int DIMS> __device__ void operator()(int at, const CUtensorMap &m, const int (&c)[DIMS]) const { tma_load<DIMS>(stage + at, &m, c, bar); }
 };
 
 // The copies of block b of a tile, whose m and n begin at these for the CTA.  One for an operand where its map allows it: each takes
 // the issuing thread some 50 cycles of the 512 that the products of a block last.
-template <Form FORM, int CG> struct Copies {
+template <Form FORM> struct Copies {
     const CUtensorMap &map_a, &map_b, &map_c;
     const LinearArgs &a;
     template <typename To> __device__ __forceinline__ void block(const Work &w, int b, int m, int n, int half, const To &to, bool take_a, bool take_b) const {
@@ -249,7 +261,7 @@ template <Form FORM, int CG> struct Copies {
     }
 };
 
-template <Form FORM, int CG>
+template <Form FORM>
 __global__ void __launch_bounds__(kThreads, 1)
 ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ CUtensorMap map_c, const LinearArgs a) {
@@ -258,23 +270,23 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     uint8_t *const staging = smem + kStages * kStageBytes;
     Control &c = *reinterpret_cast<Control *>(staging + kOutGroups * kStaging);
     const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
-    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const uint32_t rank = cluster_rank();
 
-    if (CG == 2) cluster_arrive();
+    cluster_arrive();
     if (tid == 0) {
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_b);
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_u32(&c.full[s]), CG);         // each CTA's loader (or its clearing warp)
+            mbar_init(smem_u32(&c.full[s]), kPair);         // each CTA's loader (or its clearing warp)
             mbar_init(smem_u32(&c.empty[s]), 1);
             mbar_init(smem_u32(&c.landed[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&c.sums_full[b]), 1);
-            mbar_init(smem_u32(&c.sums_empty[b]), 4 * kOutGroups * CG);
+            mbar_init(smem_u32(&c.sums_empty[b]), 4 * kOutGroups * kPair);
         }
         mbar_init(smem_u32(&c.drawn), 1);
-        mbar_init(smem_u32(&c.read), CG);
+        mbar_init(smem_u32(&c.read), kPair);
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(smem_u32(&c.work_full[s]), 1);
             // loads, results, products in the first CTA, rows to clear
@@ -282,15 +294,15 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         }
         mbar_init_done();
     }
-    if (warp == 2) tmem_alloc<CG>(smem_u32(&c.tmem), 2 * kCols);
+    if (warp == 2) tmem_alloc<kPair>(smem_u32(&c.tmem), 2 * kCols);
     pdl_begin();
-    if (CG == 2) cluster_wait();                         // the other CTA has begun
+    cluster_wait();                         // the other CTA has begun
     if (tid == 0 && rank == 0) {                         // the pair acts on one reading of the status
         const uint32_t st = (uint32_t)load_status(a.status);
         c.skip = st;
-        if (CG == 2) st_cluster(at_rank(smem_u32(&c.skip), 1), st);
+        st_cluster(at_rank(smem_u32(&c.skip), 1), st);
     }
-    const Tiles<FORM, CG> tiles{a, c};
+    const Tiles<FORM> tiles{a, c};
     if (kBoundsCheck) {
         for (int i = tid; i <= a.G; i += kThreads)
             if (a.row_offsets[i] != tiles.off(i)) bounds_fail(a.status);
@@ -328,7 +340,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_all();
+    cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     bool ok = true;                                      // false: a wait ran out
@@ -340,7 +352,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                 int s = 0, used = 0;
                 uint32_t round = 0;
                 while (ok && feed.next<false>(w, rank, ok)) {
-                    const int half = w.half, m = w.m + (int)rank * (Tiles<FORM, CG>::kM / CG);
+                    const int half = w.half, m = w.m + (int)rank * (Tiles<FORM>::kM / kPair);
                     const int n = (FORM == kGradW ? w.col : w.row) + (int)rank * half;
                     const uint32_t bytes = kTileA + (FORM == kGradW || half > 96 ? kTileB : ((half + 31) >> 5) * 4096);
                     for (int b = 0; b < w.kb; ++b) {
@@ -349,7 +361,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         const bool clear = FORM == kGradW && b == w.kb - 1 && (w.last & 15) != 0;
                         const uint32_t bar = clear ? smem_u32(&c.landed[s]) : at_rank(smem_u32(&c.full[s]), 0);
                         mbar_arrive_expect(clear ? at_rank(bar, rank) : bar, bytes);
-                        Copies<FORM, CG>{map_a, map_b, map_c, a}.block(w, b, m, n, half, Load<CG>{smem_u32(smem + s * kStageBytes), bar}, true, true);
+                        Copies<FORM>{map_a, map_b, map_c, a}.block(w, b, m, n, half, Load{smem_u32(smem + s * kStageBytes), bar}, true, true);
                         if (++s == kStages) s = 0, ++round;
                         used = min(used + 1, kStages);
                     }
@@ -369,13 +381,13 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             if (rank == 0) {                             // the whole warp keeps step, one lane issues
                 int s = 0, buf = 0;
                 uint32_t round = 0, done = 0;
-                const uint32_t idesc = mma_desc(a.f16 != 0, 128 * CG, 0, kAmn, kBmn);
+                const uint32_t idesc = mma_desc(a.f16 != 0, 128 * kPair, 0, kAmn, kBmn);
                 const uint64_t desc = smem_desc(smem_u32(smem), 8192);
                 while (ok && feed.next<true>(w, rank, ok)) {
                     if (w.kb == 0) continue;
                     if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_empty[buf]), ((done >> 1) & 1) ^ 1)))) break;
                     tc_fence_after();
-                    const uint32_t id = idesc | (uint32_t)(w.half * CG >> 4) << 18;
+                    const uint32_t id = idesc | (uint32_t)(w.half * kPair >> 4) << 18;
                     const uint32_t d = tmem + buf * kCols;
                     for (int b = 0; b < w.kb; ++b) {
                         const bool last = b == w.kb - 1, cleared = FORM == kGradW && last && (w.last & 15) != 0;
@@ -387,9 +399,9 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                             const int steps = last ? (w.last + 15) >> 4 : kBlockK / 16;
 #pragma unroll
                             for (int i = 0; i < kBlockK / 16; ++i)
-                                if (i < steps) tc_mma<CG>(d, da + i * (kAmn ? 128 : 2), db + i * (kBmn ? 128 : 2), id, b > 0 || i > 0);
-                            tc_commit<CG>(smem_u32(&c.empty[s]));
-                            if (last) tc_commit<CG>(smem_u32(&c.sums_full[buf]));
+                                if (i < steps) tc_mma<kPair>(d, da + i * (kAmn ? 128 : 2), db + i * (kBmn ? 128 : 2), id, b > 0 || i > 0);
+                            tc_commit<kPair>(smem_u32(&c.empty[s]));
+                            if (last) tc_commit<kPair>(smem_u32(&c.sums_full[buf]));
                         }
                         __syncwarp();
                         if (++s == kStages) s = 0, ++round;
@@ -423,7 +435,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         } else if (warp == 3) {                          // ------------------------------------------------ tiles
             if (elect_one()) {
                 const uint32_t read = at_rank(smem_u32(&c.read), 0);
-                int tile = blockIdx.x / CG, slot = 0;
+                int tile = blockIdx.x / kPair, slot = 0;
                 uint32_t round = 0;
                 auto hand_over = [&]() {
                     if (round > 0 && !(ok = mbar_wait(smem_u32(&c.work_empty[slot]), (round & 1) ^ 1))) return;
@@ -447,7 +459,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                     if (!ok || tile < 0) break;
                     if (!(ok = mbar_wait(smem_u32(&c.drawn), i & 1))) break;
                     tile = next_cluster_block(smem_u32(&c.answer));
-                    if (tile >= 0) tile /= CG;
+                    if (tile >= 0) tile /= kPair;
                     fence_proxy_async_smem();
                     mbar_arrive(read);
                 }
@@ -464,9 +476,10 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             constexpr int kWide = FORM == kGradW ? kCols / 32 / kOutGroups : 1;
             float total[kWide][32];                      // an fp32 gradient's sums over the chunks so far
             while (ok && feed.next<true>(w, rank, ok)) {
-                const int m0 = w.m + (int)rank * (Tiles<FORM, CG>::kM / CG);          // first feature of this CTA
+                const int m0 = w.m + (int)rank * (Tiles<FORM>::kM / kPair);          // first feature of this CTA
                 const uint32_t sums = lanes + buf * kCols;
                 if constexpr (FORM == kGradW) {
+                    if (w.kb == 0 && a.add) continue;    // nothing to add
                     if (w.kb > 0) {
                         if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_full[buf]), (done >> 1) & 1)))) break;
                         tc_fence_after();
@@ -650,9 +663,9 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_all();
+    cluster_sync_all();
     tc_fence_after();
-    if (warp == 2) tmem_free<CG>(tmem, 2 * kCols);
+    if (warp == 2) tmem_free<kPair>(tmem, 2 * kCols);
 }
 
 // ------------------------------------------------------------------------------------------------------------ host
@@ -700,17 +713,17 @@ bool encode_columns(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows,
     return whole ? encode(m, p, 2, {{64, 1, 64}, {rows, ld, kBlockK}, {cols / 64, 64, 2}}) : encode(m, p, 2, {{cols, 1, 64}, {rows, ld, kBlockK}});
 }
 
-template <Form FORM, int CG>
+template <Form FORM>
 int launch_form(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mc, const LinearArgs &a, cudaStream_t st) {
-    constexpr auto kern = ep_linear_kernel<FORM, CG>;
+    constexpr auto kern = ep_linear_kernel<FORM>;
     const int rc = allow_smem<kern>(kSmem);
     if (rc != EP_OK) return rc;
-    constexpr int kM = Tiles<FORM, CG>::kM, kN = Tiles<FORM, CG>::kN;
+    constexpr int kM = Tiles<FORM>::kM, kN = Tiles<FORM>::kN;
     const long long m_tiles = (a.M + kM - 1) / kM;
     const long long tiles = m_tiles * (FORM == kGradW ? (long long)a.G * ((a.sum + kN - 1) / kN) : (long long)a.R_max / kN + std::min(a.G, a.R_max));
     cudaLaunchConfig_t cfg = {};
-    if (tiles > INT_MAX / CG) return EP_ERR_INVALID_ARG;
-    cfg.gridDim = dim3((unsigned)std::max(1ll, tiles) * CG);        // the most there can be; clusters that run take them in turn
+    if (tiles > INT_MAX / kPair) return EP_ERR_INVALID_ARG;
+    cfg.gridDim = dim3((unsigned)std::max(1ll, tiles) * kPair);        // the most there can be; clusters that run take them in turn
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
@@ -718,7 +731,7 @@ int launch_form(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = kPair;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -768,7 +781,7 @@ extern "C" int ep_expert_linear(const void *x, long long x_stride, const void *w
     else ok = ok && encode(&ma, w, 2, {{k, 1, kBlockK}, {16, k, 16}, {2, f * k, 2}, {f / 16, 16 * k, 4}, {g, each, 1}});     // 16 gates, their 16 ups
     if (!ok) return EP_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    return swiglu ? launch_form<kGlu, 2>(ma, mb, mc, a, st) : launch_form<kPlain, 2>(ma, mb, mc, a, st);
+    return swiglu ? launch_form<kGlu>(ma, mb, mc, a, st) : launch_form<kPlain>(ma, mb, mc, a, st);
 }
 
 extern "C" int ep_expert_linear_bwd(const void *grad, long long grad_stride, const void *x, long long x_stride, const void *w,
@@ -799,7 +812,7 @@ extern "C" int ep_expert_linear_bwd(const void *grad, long long grad_stride, con
         const bool ok = a.whole_a ? encode(&ma, w, 2, {{64, 1, 64}, {n, k, kBlockK}, {k / 64, 64, 2}, {g, each, 1}})
                                   : encode(&ma, w, 2, {{k, 1, 64}, {n, k, kBlockK}, {g, each, 1}});
         if (!ok || !encode_rows(&mb, grad, N, a.R_max, grad_stride, 128) || !encode_rows(&mc, grad, N, a.R_max, grad_stride, 32)) return EP_ERR_CUDA;
-        const int rc = gate_up ? launch_form<kGradGate, 2>(ma, mb, mc, a, st) : launch_form<kGradX, 2>(ma, mb, mc, a, st);
+        const int rc = gate_up ? launch_form<kGradGate>(ma, mb, mc, a, st) : launch_form<kGradX>(ma, mb, mc, a, st);
         if (rc != EP_OK) return rc;
     }
     if (!grad_w) return EP_OK;
@@ -816,5 +829,5 @@ extern "C" int ep_expert_linear_bwd(const void *grad, long long grad_stride, con
         !encode_columns(&mb, none ? grad_w : x, k, rows, none ? k : x_stride, a.whole_b) ||
         !encode(&mc, grad_w, a.wide ? 4 : 2, {{k, 1, a.wide ? 32u : 64u}, {n, k, 32}, {g, each, 1}}))
         return EP_ERR_CUDA;
-    return launch_form<kGradW, 2>(ma, mb, mc, a, st);
+    return launch_form<kGradW>(ma, mb, mc, a, st);
 }

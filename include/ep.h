@@ -77,8 +77,8 @@ typedef enum {
  */
 #define EP_STATUS_BOUNDS     8
 /*
- * Set by ep_expert_linear and ep_expert_linear_bwd when a wait between the warps of their kernel has
- * lasted two seconds, which means a fault in the kernel: it ends then, its outputs incomplete.
+ * Set by ep_expert_linear, ep_expert_linear_bwd and ep_lora_add when a wait between the warps of their
+ * kernel has lasted two seconds, which means a fault in the kernel: it ends then, its outputs incomplete.
  */
 #define EP_STATUS_TIMEOUT   16
 

@@ -137,16 +137,51 @@ def test_rows_do_not_mix():
     assert out.isfinite().all()
 
 
+@pytest.mark.parametrize("T,N", [(40, 96), (18000, 144)])                # tiles of 16 rows, and of 128
 @pytest.mark.parametrize("size", [1e-6, 1.0, 3000.0])
-def test_size_of_the_low_rank_values(size):
+def test_size_of_the_low_rank_values(size, T, N):
     """A x from below fp16's normal numbers to above its largest, brought back by B."""
     import combine_topk_ids_histogram_gb300 as ep
-    ids, y, x, a, b, scale = make(40, 3, 16, 4096, 96, F16, 2)
+    ids, y, x, a, b, scale = make(T, 3, 16, 4096, N, F16, 2)
     ids[:] = ids.abs() % 3
     x = (x.abs() * 10 * min(size, 1.0)).half()
     a = (a.abs() * max(size, 1.0)).half()
     b = (b / 64 / max(size, 1.0)).half()
     check(ep, ids, y, x, a, b, scale)
+
+
+def test_tiles_of_128_rows():
+    """What the tests above ask of few rows: strides, in place, rows with NaN, a status, a CUDA graph on other ids."""
+    import combine_topk_ids_histogram_gb300 as ep
+    T, G, r, H, N = 9000, 3, 40, 3200, 1136
+    ids, _, _, a, b, scale = make(T, G, r, H, N, BF16, 1)
+    ywide, xwide = normal(1, T, N + 64), normal(2, T, H + 16)
+    y, x = ywide[:, 24:24 + N], xwide[:, 8:8 + H]
+    want = check(ep, ids, y.contiguous(), x.contiguous(), a, b, scale)
+    guard = ywide.clone()
+    assert torch.equal(check(ep, ids, y, x, a, b, scale, in_place=True), want)
+    assert torch.equal(ywide[:, :24], guard[:, :24]) and torch.equal(ywide[:, 24 + N:], guard[:, 24 + N:])
+    y = guard[:, 24:24 + N]
+    x2 = x.clone()
+    at = [0, 77, 4000, T - 1]
+    x2[at] = float("nan")
+    out = ep.lora_add(y, x2, a, b, ep.dispatch_layout(ids, G), scale=scale)
+    others = torch.ones(T, dtype=torch.bool, device="cuda")
+    others[at] = False
+    assert torch.equal(out[others], want[others])
+    for t in at:
+        assert out[t].isnan().all() or ids[t, 0] < 0
+    L = ep.dispatch_layout(ids.clamp(min=0), G, capacity=10)
+    kept = torch.full_like(want, 7.0)
+    ep.lora_add(y, x, a, b, L, out=kept)
+    assert ep.read_status(L) == ep.STATUS_OVERFLOW and (kept == 7).all()
+    graph, ids_s = torch.cuda.CUDAGraph(), ids.clone()
+    with torch.cuda.graph(graph):
+        held = ep.lora_add(y, x, a, b, ep.dispatch_layout(ids_s, G), scale=scale)
+    for new in (ids, ids.flip(0), torch.full_like(ids, 2), torch.full_like(ids, -1)):
+        ids_s.copy_(new)
+        graph.replay()
+        assert torch.equal(held, ep.lora_add(y, x, a, b, ep.dispatch_layout(ids_s, G), scale=scale))
 
 
 def test_status_graph_and_streams():
