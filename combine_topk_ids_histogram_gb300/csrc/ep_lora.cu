@@ -56,6 +56,9 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void st_cluster_x4(uint32_t addr, const uint32_t (&v)[4]) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
     uint8_t *const smem = s_raw + (1024 - (smem_u32(s_raw) & 1023)) % 1024;
     __shared__ __align__(8) uint64_t s_full[kRing], s_free[kRing], s_done[2];
     __shared__ uint32_t s_tmem;
-    __shared__ float s_most[2][kTileRows];
+    __shared__ float s_scale[kTileRows];
     __shared__ int s_at[kTileRows];
     const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
     pdl_begin_if(one_wave);
@@ -465,76 +468,53 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         for (int j = 0; j < 8; ++j) *reinterpret_cast<float4 *>(mine + k0 + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     }
     cluster_sync_all();                                      // (a barrier of the CTA where it is alone)
-    // Lanes side by side read a row side by side: 16-byte reads of 32 rows of another CTA's took 60,000 cycles for what takes
-    // 4,000 so.  The sums pass through the operand's place, a row's pieces exchanged so that a thread reads its row without conflicts.
-    float4 *const all = reinterpret_cast<float4 *>(smem + kRing * S::kStage);
-    const int pieces = n1 / 4;
-    constexpr int kBatch = 4;                                // loads on their way together: each takes some 700 cycles
-    for (int i0 = tid; i0 < kTileRows * pieces; i0 += kBatch * kTileThreads) {
-        uint32_t from[kBatch];
-        float4 v[kBatch] = {};
+    // Every CTA adds up its share of the rows and hands them to all.  8 * RB lanes side by side read a row side by side (16-byte
+    // reads of 32 different rows took 60,000 cycles for what takes a few thousand so), 8 columns each.
+    const int share = (kTileRows + a.C - 1) / a.C, last = min(kTileRows, (rank + 1) * share);
+    for (int i = tid; !issuer && rank * share + i / (8 * RB) < last; i += kThreads) {
+        const int r = rank * share + i / (8 * RB), k = i % (8 * RB);
+        const uint32_t from = smem_u32(reinterpret_cast<float *>(smem) + r * S::kPitch + 8 * k);
+        float t[8] = {};
+        if (8 * k < n1)
+            for (int o = 0; o < a.C; o += 4) {               // loads on their way together: each takes some 700 cycles
+                float4 u[4][2];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int i = min(i0 + j * kTileThreads, kTileRows * pieces - 1);
-            from[j] = smem_u32(reinterpret_cast<float *>(smem) + i / pieces * S::kPitch + i % pieces * 4);
+                for (int h = 0; h < 8; ++h) u[h >> 1][h & 1] = ld_cluster_f32x4(at_rank(from + (h & 1) * 16, min(o + (h >> 1), a.C - 1)));
+#pragma unroll
+                for (int h = 0; h < 8; ++h)
+                    if (o + (h >> 1) < a.C) {
+                        const float4 v = u[h >> 1][h & 1];
+                        float *const p = t + 4 * (h & 1);
+                        p[0] += v.x;
+                        p[1] += v.y;
+                        p[2] += v.z;
+                        p[3] += v.w;
+                    }
+            }
+        float f = 1.0f;                                      // a power of two per row keeps the sums in fp16's range
+        if (f16) {
+            float most = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(t[j]));
+            const uint32_t mates = (RB == 1 ? 0xffu : 0xffffu) << (lane & ~(8 * RB - 1));
+#pragma unroll
+            for (int o = 4 * RB; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(mates, most, o));
+            f = fp16_scale(most);
         }
-        for (int o = 0; o < a.C; o += 2) {
-            float4 u[2][kBatch];
+        uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) u[h][j] = ld_cluster_f32x4(at_rank(from[j], min(o + h, a.C - 1)));
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j)
-                    if (o + h < a.C) v[j] = make_float4(v[j].x + u[h][j].x, v[j].y + u[h][j].y, v[j].z + u[h][j].z, v[j].w + u[h][j].w);
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * kTileThreads, r = i / pieces, k = i % pieces;
-            if (i < kTileRows * pieces) all[r * 16 * RB + (k ^ (r & 15))] = v[j];
-        }
-    }
-    __syncthreads();
-    float t[RB][32], most = 0.0f;
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int k = (half * RB + b) * 8 + j;
-            const float4 v = k < pieces ? all[row * 16 * RB + (k ^ (row & 15))] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            t[b][4 * j] = v.x;
-            t[b][4 * j + 1] = v.y;
-            t[b][4 * j + 2] = v.z;
-            t[b][4 * j + 3] = v.w;
-            most = fmaxf(most, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-        }
-    __syncthreads();
-    float f = 1.0f;                                          // a power of two per row keeps the sums in fp16's range
-    if (f16) {
-        if (!issuer) s_most[half][row] = most;
-        __syncthreads();
-        f = fp16_scale(fmaxf(most, s_most[half ^ 1][row]));
-    }
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-        const int k0 = (half * RB + b) * 32;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) split2<T>(t[b][8 * j + 2 * i] * f, t[b][8 * j + 2 * i + 1] * f, hi[i], lo[i]);
-            uint8_t *const p = smem + kRing * S::kStage + (k0 / 64) * kTileRows * 128 + swizzled(row, k0 % 64 / 8 + j);
-            if (issuer) continue;
-            *reinterpret_cast<uint4 *>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(p + S::kLow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int j = 0; j < 4; ++j) split2<T>(t[2 * j] * f, t[2 * j + 1] * f, hi[j], lo[j]);
+        const uint32_t to_op = low + (k >> 3) * kTileRows * 128 + swizzled(r, k & 7), to_f = smem_u32(s_scale + r);
+        for (int o = 0; o < a.C; ++o) {
+            st_cluster_x4(at_rank(to_op, o), hi);
+            st_cluster_x4(at_rank(to_op + S::kLow, o), lo);
+            if (k == 0) st_cluster(at_rank(to_f, o), __float_as_uint(f));
         }
     }
-    const float back = (a.scale ? a.scale[g] : 1.0f) / f;
     fence_proxy_async_smem();
     tc_fence_before();
-    cluster_sync_all();                                      // the sums have been read everywhere: the ring has their place again
+    cluster_sync_all();                                      // the operand is complete everywhere, and the ring has the sums' place again
+    const float back = (a.scale ? a.scale[g] : 1.0f) / s_scale[row];
     // ---- out = y + B (A x): every CTA its stages of N
 #pragma unroll
     for (int i = 0; i < 4; ++i) left[i] = a.y + (has[i] ? s_at[r0 + 32 * i] * a.ldy : 0) + 8 * piece;
