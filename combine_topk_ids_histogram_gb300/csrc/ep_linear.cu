@@ -20,7 +20,7 @@
 // products at 256 rows and as much for half the work at 128, while outputs leave: 8192 tokens, top-8 of 128, 2048 -> 2 x 768
 // gated with gate and up saved 287 us (floor 205), its down product 148 (115), grad_x through the gate 181 (160), grad_w 180 (115).
 // Without its loads / its outputs the first of them took 207 / 276 us of 324 then; fetching the next tile's operands into L2
-// ahead (by TMA, or in bulk) cost 10 to 150 % everywhere, eviction hints changed nothing, and taking several groups at a time, less read
+// ahead (by TMA, in bulk, or by lines) gained nothing in grad_w and cost up to 150 % elsewhere, eviction hints changed nothing, and taking several groups at a time, less read
 // at the same moment by several pairs, cost 4 to 60 %.
 #include <limits.h>
 #include <math.h>

@@ -9,10 +9,10 @@
 //               CTA's through shared memory, then the CTAs' through each other's, and split N for the second product,
 //               which takes y along.  The contraction may take its k in any order as long as both operands take the same one: a thread reads
 //               8 consecutive elements of a row, and the second product's columns are permuted so that a thread's sums are
-//               8 consecutive outputs.  One token, rank 16, 2048 -> 2048: 4.0 us; 64 tokens, 48 adapters of rank 32, 7168 -> 4096:
-//               10.2 us (floor 3.9).  Latency bounds it: the ids, A and x, the exchange, B, one after another.
-//   many rows   128, on tcgen05.  8192 tokens, 5 adapters of rank 64, 4096 -> 4096: 60 us (floor 29).  HBM bounds the second half
-//               (5 TB/s), the exchange of the sums between the CTAs (a sixth of the time) and the copies' latency the first.
+//               8 consecutive outputs.  One token, rank 16, 2048 -> 2048: 3.6 us; 64 tokens, 48 adapters of rank 32, 7168 -> 4096:
+//               9.2 us (floor 3.9).  Latency bounds it: the ids, A and x, the exchange, one after another.
+//   many rows   128, on tcgen05.  8192 tokens, 5 adapters of rank 64, 4096 -> 4096: 58 us (floor 29).  HBM bounds the second half
+//               (5 TB/s), the copies' latency and the exchange of the sums between the CTAs the first.
 #include <stddef.h>
 
 #include <algorithm>
@@ -166,6 +166,11 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane >> 2, q = lane & 3;
     pdl_begin_if(one_wave);
     const int tile = blockIdx.x / a.C, rank = blockIdx.x % a.C, part = rank * kWarps + warp, parts = a.C * kWarps;
+    int token[2] = {};                                       // comes along with the loads of Rows
+    if (a.by_token && tile < a.tiles) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) token[i] = a.src_info[2 * (size_t)min(tile * a.rows + c + 8 * i, a.R_max - 1)];
+    }
     const Rows rows(a, tile);
     if constexpr (kBoundsCheck) {                            // another CTA may set a bit meanwhile: the cluster acts on one reading
         __shared__ int s_status;
@@ -182,12 +187,13 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
         if (a.copy) copy_rows(a);
         return;
     }
-    const int g = rows.g;
-    int at[2];                                           // the row of x, y and out; -1: none
+    const int g = rows.g, cells = (rows.end - rows.first) * kR;
+    const float scale = a.scale ? a.scale[g] : 1.0f;
+    int at[2];                                               // the row of x, y and out; -1: none
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int j = rows.first + c + 8 * i;
-        at[i] = j < rows.end ? (a.by_token ? a.src_info[2 * (size_t)j] : j) : -1;
+        at[i] = j >= rows.end ? -1 : !a.by_token ? j : tile < a.tiles ? token[i] : a.src_info[2 * (size_t)j];
         if (a.by_token && at[i] >= a.T) {
             bounds_fail(a.status);
             at[i] = -1;
@@ -228,10 +234,10 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     for (int j = 0; j < RN; ++j) {
         float *const p = s_part + warp * kCells + c * kR + 8 * j + 2 * q;
         *reinterpret_cast<float2 *>(p) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2 *>(p + 8 * kR) = make_float2(acc[j][2], acc[j][3]);
+        if (cells > 8 * kR) *reinterpret_cast<float2 *>(p + 8 * kR) = make_float2(acc[j][2], acc[j][3]);
     }
     __syncthreads();
-    for (int i = tid; i < kCells; i += kThreads) {
+    for (int i = tid; i < cells; i += kThreads) {            // (rows without a token stay undefined, and go into no other)
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += s_part[w * kCells + i];
@@ -239,15 +245,20 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     }
     if (a.C > 1) {
         cluster_sync_all();
-        for (int i = tid; i < kCells; i += kThreads) {
-            float v = 0.0f;
-            for (int k = 0; k < a.C; ++k) v += ld_cluster_f32(at_rank(smem_u32(s_mine + i), k));
+        for (int i = tid; i < cells; i += kThreads) {
+            float u[kMaxCluster], v = 0.0f;                  // loads on their way together: each takes some 700 cycles
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k)
+                if (k < a.C) u[k] = ld_cluster_f32(at_rank(smem_u32(s_mine + i), k));
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k)
+                if (k < a.C) v += u[k];
             s_all[i] = v;
         }
     }
     __syncthreads();
     if constexpr (std::is_same_v<T, __half>) {           // a power of two per row keeps the sums in fp16's range
-        for (int i = warp; i < kRows; i += kWarps) {
+        for (int i = warp; i * kR < cells; i += kWarps) {
             float v = 0.0f;
             for (int k = lane; k < kR; k += 32) v = fmaxf(v, fabsf(s_all[i * kR + k]));
             v = warp_max(v);
@@ -257,8 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     }
     constexpr int kK = RN / 2;                       // steps of 16 of the second product
     uint32_t hi[kK][4], lo[kK][4];
-    float back[2];                                   // adapter's scale, over the row's
-    const float scale = a.scale ? a.scale[g] : 1.0f;
+    float back[2];                                           // adapter's scale, over the row's
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int j = c + 8 * i;
@@ -309,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
 // The same for tiles of 128 rows on tcgen05, where the bytes of x, y and out are what counts.  The rows are M; both products stream
 // through a ring in shared memory that cp.async fills ahead: 64 columns of x with 64 of A (N is r), then 64 of y with 64 rows of B
 // (K is r).  The CTAs of a cluster split H, add up A x through each other's shared memory, and split N.  (With mma.sync from
-// shared memory its products took half of the time: 71 us with 8192 tokens, 5 adapters of rank 64, 4096 -> 4096, where this takes 60.)
+// shared memory its products took half of the time: 71 us with 8192 tokens, 5 adapters of rank 64, 4096 -> 4096, where this takes 58.)
 constexpr int kTileRows = 128, kRing = 3, kTileThreads = kThreads + 32;           // the last warp issues the products
 
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gmem, bool valid) {
@@ -638,10 +648,11 @@ template <typename T> int launch_type(const LoraArgs &a, cudaStream_t st) {
     return a.r <= 64 ? launch_lora<ep_lora_kernel<T, 8>>(a, kThreads, smem(8), st) : launch_lora<ep_lora_kernel<T, 16>>(a, kThreads, smem(16), st);
 }
 
-// Tiles of 128 rows begin slowly (their sums cross the cluster, 19 us at least) and then read A and B an eighth as often as tiles of
-// 16 rows, whose time is about 3.2e-7 us per 16 rows, column of x or y, and (r + 25).  The border is at 50 us of that.  16 / 128 rows:
-// 1024 tokens, 4 adapters of rank 16, 4096 -> 4096: 8.2 / 21 us; 2048, 16 of rank 64, 2048 -> 2048: 17 / 43; 8192, 1 of rank 16,
-// 4096 -> 4096: 55 / 50; 4096, 32 of rank 128: 91 / 82; 8192, 5 of rank 64: 119 / 58; 16384, 8 of rank 16, 2048 -> 6144: 133 / 95.
+// Tiles of 128 rows begin slowly (19 us at least, of which their sums' way across the cluster is some) and then read A and B an
+// eighth as often as tiles of 16 rows, whose time is about 3.2e-7 us per 16 rows, column of x or y, and (r + 25).  The border is at 50 us
+// of that.  16 / 128 rows: 1024 tokens, 4 adapters of rank 16, 4096 -> 4096: 8.2 / 21 us; 2048, 16 of rank 64, 2048 -> 2048: 17 / 43;
+// 8192, 1 of rank 16, 4096 -> 4096: 55 / 47; 4096, 32 of rank 128: 91 / 74; 8192, 5 of rank 64: 119 / 54; 16384, 8 of rank 16,
+// 2048 -> 6144: 133 / 94.
 bool takes_tiles(long long rows, int H, int N, int rank) { return rows * (H + N) * (rank + 25) >= 2500000000ll; }
 
 bool lora_stride_ok(long long ld, int cols) { return ld >= cols && ld % 8 == 0; }
