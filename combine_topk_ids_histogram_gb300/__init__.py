@@ -784,6 +784,14 @@ def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ro
 _HALF = (torch.bfloat16, torch.float16)
 
 
+def _here(*tensors):
+    """The kernels run on the current device: refuse tensors of another one."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor on device {t.get_device()}, but the current device is {dev}")
+
+
 def _layout_rows(t: torch.Tensor, L: Layout, cols: int, dtype, what: str):
     """Pointer and row stride of a 2-D tensor with a row for each row of the layout's buffers."""
     p, rows, n, stride, _ = _matrix(t, what)
@@ -822,6 +830,7 @@ def expert_linear(x: torch.Tensor, w: torch.Tensor, L: Layout, swiglu: bool = Fa
         new = lambda n: torch.empty(max(L.R_max, 1), n, dtype=w.dtype, device=x.device)
         out = (new(n_out), new(N)) if save else new(n_out)
     y, gu = out if save else (out, None)
+    _here(x, w, y, gu)
     rc = _lib.ep_expert_linear(px, ld, pw, K, N, DTYPES[w.dtype], 1 if swiglu else 0, L.ref, _out_rows(y, L, n_out, w.dtype, "out"),
                                _out_rows(gu, L, N, w.dtype, "gate_up") if save else None, _stream(stream))
     _check(rc, "ep_expert_linear")
@@ -862,6 +871,7 @@ def expert_linear_bwd(grad: torch.Tensor, x: torch.Tensor | None, w: torch.Tenso
         if wdt not in (w.dtype, torch.float32) or (grad_w_dtype is not None and grad_w_dtype != wdt):
             raise TypeError(f"grad_w: dtype {wdt}")
         pgw = _buffer(gw, (G, N, K), (wdt,), "grad_w")
+    _here(grad, x if need_w else None, w, gate_up, gx if need_x else None, gw if need_w else None)
     rc = _lib.ep_expert_linear_bwd(pg, ldg, px, ldx, pw, K, N, DTYPES[w.dtype], pgu, L.ref, pgx, pgw, DTYPES[wdt],
                                    1 if accumulate else 0, _stream(stream))
     _check(rc, "ep_expert_linear_bwd")
@@ -887,6 +897,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
         raise TypeError(f"y {y.dtype}, x {x.dtype} and out {out.dtype}: expected {dt}")
     if wy != N or wx != H or wo != N or min(ly, lx, lo) < n or (by_token and max(ly, lx, lo) != n):
         raise ValueError(f"expected {n} rows: y and out of {N}, x of {H}; got {tuple(y.shape)}, {tuple(out.shape)}, {tuple(x.shape)}")
+    _here(y, x, a, b, scale, out)
     rc = _lib.ep_lora_add(py, ldy, px, ldx, pa, pb, None if scale is None else _buffer(scale, (L.G,), _F32, "scale"), H, N, r, ty,
                           1 if by_token else 0, L.ref, po, ldo, _stream(stream))
     _check(rc, "ep_lora_add")

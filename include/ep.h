@@ -541,8 +541,8 @@ int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t *codes, co
  * Sums are fp32 on the tensor cores, whose adder truncates (by up to 2^-23 of the sum every 16
  * products); every output is rounded once.  The rows [0, row_offsets[G]) are written; padding rows are
  * rows like others, and zero where x is.  No row takes part in another's result, whatever it holds.
- * Nothing is written while the layout's status word is non-zero.  No workspace, no atomics: the
- * same call gives the same bits.
+ * Nothing is written while the layout's status word is non-zero.  Outputs overlap no input.  No workspace,
+ * no atomics: the same call gives the same bits.
  */
 int ep_expert_linear(const void *x, long long x_stride, const void *w, int in_features, int out_rows,
                      int dtype, int swiglu, const ep_layout_t *L, void *out, void *gate_up,
@@ -562,7 +562,7 @@ int ep_expert_linear(const void *x, long long x_stride, const void *w, int in_fe
  * Rows as in the forward call; padding rows take part in grad_w, so x or grad has to be zero there (and
  * neither infinite nor NaN): ep_dispatch_bf16 and ep_combine_bwd write zeros.  Rows outside a group, or behind the last one, take no part
  * in its grad_w.  grad_x and grad_w may not both be NULL; w is not read without grad_x nor x without
- * grad_w, and they may be NULL then.
+ * grad_w, and they may be NULL then.  Outputs overlap no input.
  */
 int ep_expert_linear_bwd(const void *grad, long long grad_stride, const void *x, long long x_stride,
                          const void *w, int in_features, int out_rows, int dtype,

@@ -204,6 +204,35 @@ def test_extreme_gates():
     check_backward(ep, L, normal(1, 40, 48), x, normal(2, 1, 48, 16), gu, True)
 
 
+def test_refusals(monkeypatch):
+    """What the binding checks before the library sees it."""
+    import combine_topk_ids_histogram_gb300 as ep
+    L = ref.layout_of(ep, [30, 50])
+    x, w, g, a, b = normal(1, 80, 64), normal(2, 2, 96, 64), normal(3, 80, 96), normal(4, 2, 8, 64), normal(5, 2, 64, 8)
+    wrong = [lambda: ep.expert_linear(x[:79], w, L), lambda: ep.expert_linear(x[:, :48], w, L), lambda: ep.expert_linear(x, w[:1], L),
+             lambda: ep.expert_linear(x, w[0], L), lambda: ep.expert_linear(x, w, L, save=True), lambda: ep.expert_linear(x, w, L, out=x),
+             lambda: ep.expert_linear(x.cpu(), w, L), lambda: ep.expert_linear_bwd(g[:, :80], x, w, L),
+             lambda: ep.expert_linear_bwd(g, None, w, L), lambda: ep.expert_linear_bwd(g, x, w, L, accumulate=True),
+             lambda: ep.expert_linear_bwd(g, x, w, L, gate_up=x), lambda: ep.expert_linear_bwd(g, x, w, L, gate_up=x, need=(False, True)),
+             lambda: ep.lora_add(x, x[:70], a, b, L, by_token=False),
+             lambda: ep.lora_add(x, x, a, b[:1], L, by_token=False), lambda: ep.lora_add(x, x, a, a, L, by_token=False)]
+    for i, f in enumerate(wrong):
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: ep.expert_linear(x.half(), w, L), lambda: ep.expert_linear(x.float(), w.float(), L),
+              lambda: ep.expert_linear_bwd(g, x, w, L, grad_w_dtype=F16), lambda: ep.lora_add(x, x.half(), a, b, L, by_token=False)):
+        with pytest.raises(TypeError):
+            f()
+    with pytest.raises(ep.EPError):
+        ep.expert_linear_bwd(g, x, w, L, need=(False, False))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for f in (lambda: ep.expert_linear(x, w, L, stream=s), lambda: ep.expert_linear_bwd(g, x, w, L, stream=s),
+              lambda: ep.lora_add(x, x, a, b, L, by_token=False, stream=s)):
+        s = torch.cuda.Stream(device=0)
+        with pytest.raises(ValueError, match="current device"):
+            f()
+
+
 def test_one_of_the_gradients():
     import combine_topk_ids_histogram_gb300 as ep
     L = ref.layout_of(ep, [30, 50])
