@@ -784,35 +784,56 @@ def expert_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, ro
 _HALF = (torch.bfloat16, torch.float16)
 
 
-def _here(*tensors):
-    """The kernels run on the current device: refuse tensors of another one."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor on device {t.get_device()}, but the current device is {dev}")
-
-
-def _layout_rows(t: torch.Tensor, L: Layout, cols: int, dtype, what: str):
-    """Pointer and row stride of a 2-D tensor with a row for each row of the layout's buffers."""
-    p, rows, n, stride, _ = _matrix(t, what)
-    if t.dtype != dtype:
+# The checks of the calls below, with few attribute look-ups: a call's host time is what a decode step of one token waits for.
+def _plane(t: torch.Tensor, cols: int, dtype, dev: int, what: str):
+    """Pointer, rows and row stride of a 2-D tensor of the current device whose rows are contiguous."""
+    if t.dtype is not dtype:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if n != cols or rows < L.R_max:
-        raise ValueError(f"{what}: needs at least {L.R_max} rows of {cols}, got {tuple(t.shape)}")
-    return p, stride
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{dev}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols:
+        raise ValueError(f"{what}: expected [*, {cols}], got {tuple(shape)}")
+    rows = shape[0]
+    stride, step = t.stride()
+    if rows <= 1:
+        stride = cols
+    if (step != 1 and cols > 1) or stride < cols:
+        raise ValueError(f"{what}: rows must be contiguous and not overlap, got strides {t.stride()}")
+    return t.data_ptr(), rows, stride
 
 
-def _out_rows(t: torch.Tensor, L: Layout, cols: int, dtype, what: str) -> int:
+def _dense(t: torch.Tensor, shape: tuple, dtypes, dev: int, what: str) -> int:
+    """Pointer of a contiguous tensor of this shape (a first size of None: any) on the current device."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: dtype {t.dtype} not in {dtypes}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _of_layout(rows: int, L: Layout, what: str):
+    if rows < L.R_max:
+        raise ValueError(f"{what}: needs at least {L.R_max} rows, got {rows}")
+
+
+def _out_rows(t: torch.Tensor, L: Layout, cols: int, dtype, dev: int, what: str) -> int:
     """Pointer of a contiguous tensor of at least the layout's rows."""
-    if t.dim() != 2 or t.shape[0] < L.R_max:
-        raise ValueError(f"{what}: needs at least {L.R_max} rows of {cols}, got {tuple(t.shape)}")
-    return _buffer(t, (t.shape[0], cols), (dtype,), what)
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected [*, {cols}], got {tuple(t.shape)}")
+    _of_layout(t.shape[0], L, what)
+    return _dense(t, (t.shape[0], cols), (dtype,), dev, what)
 
 
-def _weights(w: torch.Tensor, L: Layout):
-    if w.dim() != 3:
-        raise ValueError(f"w: expected [{L.G}, N, K], got {tuple(w.shape)}")
-    return _buffer(w, (L.G, w.shape[1], w.shape[2]), _HALF, "w")
+def _three(t: torch.Tensor, G: int, what: str):
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != G:
+        raise ValueError(f"{what}: expected [{G}, *, *], got {tuple(shape)}")
+    return shape
 
 
 def expert_linear(x: torch.Tensor, w: torch.Tensor, L: Layout, swiglu: bool = False, save: bool = False, out=None, stream=None):
@@ -820,19 +841,22 @@ def expert_linear(x: torch.Tensor, w: torch.Tensor, L: Layout, swiglu: bool = Fa
     order (what ``dispatch_bf16`` returns; rows may have a stride, a multiple of 8), w [G, N, K], both bf16 or both fp16 ->
     out [R_max, N].  With ``swiglu`` w holds N/2 gate rows, then N/2 up rows, and out [R_max, N/2] is silu(gate) * up; with
     ``save`` too the call returns (out, gate_up [R_max, N]) for ``expert_linear_bwd``.  ``out``: the buffer, or both."""
-    pw = _weights(w, L)
-    G, N, K = w.shape
-    px, ld = _layout_rows(x, L, K, w.dtype, "x")
+    dev = torch.cuda.current_device()
+    shape = _three(w, L.G, "w")
+    N, K = shape[1], shape[2]
+    dt = w.dtype
+    pw = _dense(w, shape, _HALF, dev, "w")
+    px, rows, ld = _plane(x, K, dt, dev, "x")
+    _of_layout(rows, L, "x")
     if save and not swiglu:
         raise ValueError("save keeps the gate and up values of swiglu")
     n_out = N // 2 if swiglu else N
     if out is None:
-        new = lambda n: torch.empty(max(L.R_max, 1), n, dtype=w.dtype, device=x.device)
+        new = lambda n: torch.empty(max(L.R_max, 1), n, dtype=dt, device=x.device)
         out = (new(n_out), new(N)) if save else new(n_out)
     y, gu = out if save else (out, None)
-    _here(x, w, y, gu)
-    rc = _lib.ep_expert_linear(px, ld, pw, K, N, DTYPES[w.dtype], 1 if swiglu else 0, L.ref, _out_rows(y, L, n_out, w.dtype, "out"),
-                               _out_rows(gu, L, N, w.dtype, "gate_up") if save else None, _stream(stream))
+    rc = _lib.ep_expert_linear(px, ld, pw, K, N, DTYPES[dt], 1 if swiglu else 0, L.ref, _out_rows(y, L, n_out, dt, dev, "out"),
+                               _out_rows(gu, L, N, dt, dev, "gate_up") if save else None, _stream(stream))
     _check(rc, "ep_expert_linear")
     return out
 
@@ -844,36 +868,40 @@ def expert_linear_bwd(grad: torch.Tensor, x: torch.Tensor | None, w: torch.Tenso
     instead, which is ``grad`` for that call's weights.  ``need``: which of the two to compute (None for the other).
     grad_w is in w's dtype or ``grad_w_dtype`` = torch.float32, and with ``accumulate`` (fp32, with ``out``) it is added to what
     is there.  ``out``: the two buffers."""
-    pw = _weights(w, L)
-    G, N, K = w.shape
-    pg, ldg = _layout_rows(grad, L, N, w.dtype, "grad")
+    dev = torch.cuda.current_device()
+    shape = _three(w, L.G, "w")
+    N, K = shape[1], shape[2]
+    dt = w.dtype
+    pw = _dense(w, shape, _HALF, dev, "w")
+    pg, rows, ldg = _plane(grad, N, dt, dev, "grad")
+    _of_layout(rows, L, "grad")
     need_x, need_w = need
     gx, gw = out if out is not None else (None, None)
     cols = K if gate_up is None else 2 * K
     px = pgx = pgu = pgw = None
-    ldx, wdt = K, w.dtype
+    ldx, wdt = K, dt
     if need_x:
         if gx is None:
-            gx = torch.empty(max(L.R_max, 1), cols, dtype=w.dtype, device=grad.device)
-        pgx = _out_rows(gx, L, cols, w.dtype, "grad_x")
-        pgu = None if gate_up is None else _out_rows(gate_up, L, cols, w.dtype, "gate_up")
+            gx = torch.empty(max(L.R_max, 1), cols, dtype=dt, device=grad.device)
+        pgx = _out_rows(gx, L, cols, dt, dev, "grad_x")
+        pgu = None if gate_up is None else _out_rows(gate_up, L, cols, dt, dev, "gate_up")
     elif gate_up is not None:
         raise ValueError("gate_up is for the gradient of the rows")
     if need_w:
         if x is None:
             raise ValueError("the gradient of the weights needs x")
-        px, ldx = _layout_rows(x, L, K, w.dtype, "x")
+        px, rows, ldx = _plane(x, K, dt, dev, "x")
+        _of_layout(rows, L, "x")
         if gw is None:
             if accumulate:
                 raise ValueError("accumulate adds to a buffer: pass out=")
-            gw = torch.empty(G, N, K, dtype=grad_w_dtype or w.dtype, device=grad.device)
+            gw = torch.empty(shape, dtype=grad_w_dtype or dt, device=grad.device)
         wdt = gw.dtype
-        if wdt not in (w.dtype, torch.float32) or (grad_w_dtype is not None and grad_w_dtype != wdt):
-            raise TypeError(f"grad_w: dtype {wdt}")
-        pgw = _buffer(gw, (G, N, K), (wdt,), "grad_w")
-    _here(grad, x if need_w else None, w, gate_up, gx if need_x else None, gw if need_w else None)
-    rc = _lib.ep_expert_linear_bwd(pg, ldg, px, ldx, pw, K, N, DTYPES[w.dtype], pgu, L.ref, pgx, pgw, DTYPES[wdt],
-                                   1 if accumulate else 0, _stream(stream))
+        if grad_w_dtype is not None and grad_w_dtype != wdt:
+            raise TypeError(f"grad_w: dtype {wdt}, expected {grad_w_dtype}")
+        pgw = _dense(gw, shape, (dt, torch.float32), dev, "grad_w")
+    rc = _lib.ep_expert_linear_bwd(pg, ldg, px, ldx, pw, K, N, DTYPES[dt], pgu, L.ref, pgx, pgw, DTYPES[wdt], 1 if accumulate else 0,
+                                   _stream(stream))
     _check(rc, "ep_expert_linear_bwd")
     return gx if need_x else None, gw if need_w else None
 
@@ -885,20 +913,19 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     stride, a multiple of 8), a [G, r, H] and b [G, N, r], all bf16 or all fp16; scale fp32 [G], None for 1.  Without
     ``by_token`` y, x and out are in the layout's row order [R_max, *], for any layout (adapters of experts).  ``out`` may be
     y, which is then added to in place."""
-    if a.dim() != 3 or b.dim() != 3:
-        raise ValueError(f"expected a [{L.G}, r, H] and b [{L.G}, N, r], got {tuple(a.shape)} and {tuple(b.shape)}")
-    (_, r, H), N, dt = a.shape, b.shape[1], a.dtype
-    pa, pb = _buffer(a, (L.G, r, H), _HALF, "a"), _buffer(b, (L.G, N, r), (dt,), "b")
-    n = L.T if by_token else L.R_max
+    dev = torch.cuda.current_device()
+    G, dt = L.G, a.dtype
+    shape = _three(a, G, "a")
+    r, H, N = shape[1], shape[2], _three(b, G, "b")[1]
+    pa, pb = _dense(a, shape, _HALF, dev, "a"), _dense(b, (G, N, r), (dt,), dev, "b")
     if out is None:
         out = torch.empty(y.shape, dtype=dt, device=y.device)
-    (py, ly, wy, ldy, ty), (px, lx, wx, ldx, tx), (po, lo, wo, ldo, to) = _matrix(y, "y"), _matrix(x, "x"), _matrix(out, "out")
-    if ty != tx or ty != to or y.dtype != dt:
-        raise TypeError(f"y {y.dtype}, x {x.dtype} and out {out.dtype}: expected {dt}")
-    if wy != N or wx != H or wo != N or min(ly, lx, lo) < n or (by_token and max(ly, lx, lo) != n):
-        raise ValueError(f"expected {n} rows: y and out of {N}, x of {H}; got {tuple(y.shape)}, {tuple(out.shape)}, {tuple(x.shape)}")
-    _here(y, x, a, b, scale, out)
-    rc = _lib.ep_lora_add(py, ldy, px, ldx, pa, pb, None if scale is None else _buffer(scale, (L.G,), _F32, "scale"), H, N, r, ty,
+    py, ly, ldy = _plane(y, N, dt, dev, "y")
+    px, lx, ldx = _plane(x, H, dt, dev, "x")
+    po, lo, ldo = (py, ly, ldy) if out is y else _plane(out, N, dt, dev, "out")
+    if not (ly == lx == lo == L.T if by_token else min(ly, lx, lo) >= L.R_max):
+        raise ValueError(f"expected {L.T if by_token else L.R_max} rows of y, x and out, got {ly}, {lx} and {lo}")
+    rc = _lib.ep_lora_add(py, ldy, px, ldx, pa, pb, None if scale is None else _dense(scale, (G,), _F32, dev, "scale"), H, N, r, DTYPES[dt],
                           1 if by_token else 0, L.ref, po, ldo, _stream(stream))
     _check(rc, "ep_lora_add")
     return out
