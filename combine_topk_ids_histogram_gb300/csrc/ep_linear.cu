@@ -88,6 +88,7 @@ struct LinearArgs {
     int M;                                   // of the output: features of a row (gated: F), rows of a weight gradient
     int sum;                                 // length of the sums (forms that sum over rows: columns of the output)
     int f16, wide, add;                      // operands fp16; grad_w: fp32 output, added to what is there
+    int beside;                              // grad_w behind grad_x in the same call
     int whole_a, whole_b;                    // whether the operand's map has the blocks of 64 as a dimension
     uint16_t *out, *gate_up;                 // gate_up: saved by kGlu, read by kGradGate
 };
@@ -295,8 +296,11 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         mbar_init_done();
     }
     if (warp == 2) tmem_alloc<kPair>(smem_u32(&c.tmem), 2 * kCols);
-    pdl_begin();
-    cluster_wait();                         // the other CTA has begun
+    // The weights' gradient needs nothing of the rows' in front of it: it begins as that one's CTAs leave, and waits for its end at its
+    // own.  What came before both was complete when the CTAs in front let this launch begin.
+    if (a.beside) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    else pdl_begin();
+    cluster_wait();                                      // the other CTA has begun
     if (tid == 0 && rank == 0) {                         // the pair acts on one reading of the status
         const uint32_t st = (uint32_t)load_status(a.status);
         c.skip = st;
@@ -666,6 +670,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     cluster_sync_all();
     tc_fence_after();
     if (warp == 2) tmem_free<kPair>(tmem, 2 * kCols);
+    if (a.beside) pdl_wait();
 }
 
 // ------------------------------------------------------------------------------------------------------------ host
@@ -816,6 +821,7 @@ extern "C" int ep_expert_linear_bwd(const void *grad, long long grad_stride, con
         if (rc != EP_OK) return rc;
     }
     if (!grad_w) return EP_OK;
+    a.beside = grad_x && L->T > 0;
     a.M = N;
     a.sum = K;
     a.wide = grad_w_dtype == EP_F32;
