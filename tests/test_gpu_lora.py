@@ -150,6 +150,17 @@ def test_size_of_the_low_rank_values(size, T, N):
     check(ep, ids, y, x, a, b, scale)
 
 
+@pytest.mark.parametrize("T,G,r,H,N", [(50, 4, 24, 80, 48), (9000, 2, 72, 2560, 496)])
+def test_padded_layouts_by_token(T, G, r, H, N):
+    """Padding rows have no token and change nothing."""
+    import combine_topk_ids_histogram_gb300 as ep
+    ids, y, x, a, b, scale = make(T, G, r, H, N, BF16, 6)
+    want, tol = expected(y, x, a, b, scale, [(ids[:, 0] == g).nonzero()[:, 0] for g in range(G)])
+    for pad, capacity in ((16, None), (128, T + 300 * G)):
+        L = ep.dispatch_layout_routed(G, topk_ids=ids, pad_multiple=pad, num_permuted_tokens=capacity)[0]
+        ref.assert_within(ep.lora_add(y, x, a, b, L, scale=scale), want, tol, f"padded to {pad}")
+
+
 def test_tiles_of_128_rows():
     """What the tests above ask of few rows: strides, in place, rows with NaN, a status, a CUDA graph on other ids."""
     import combine_topk_ids_histogram_gb300 as ep
