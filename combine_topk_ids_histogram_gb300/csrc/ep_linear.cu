@@ -9,7 +9,7 @@
 // so that pairs which drew long tiles take fewer.  The weights' rows (or columns) are M of the tensor cores' product and the
 // layout's rows are N, in steps of 32: a group of any number of rows then costs about what its rows cost, and weights, which have
 // hundreds of rows or more, fill M.  A pair shares a product of 256 x 256: each CTA loads 128 of M and half of N by TMA, one copy for
-// an operand, and keeps the sums of its 128 of M in tensor memory, twice, so that one tile's results leave while the next one's are
+// an operand, and keeps the sums of its 128 of M in tensor memory, twice, so that one chunk's sums leave while the next one's are
 // added up.  Warp 0 loads, warp 1 of the first CTA issues the products, warp 3 looks tiles up ahead of the others, warps 4 to 11 take
 // results out, four at a time 32 columns; warp 2 (grad_w) clears the rows behind a group's last one in shared memory, since
 // there they are summed over.  No atomics: the order of every sum is fixed.
@@ -40,6 +40,7 @@ enum Form { kPlain, kGlu, kGradX, kGradGate, kGradW };
 constexpr int kPair = 2;                      // CTAs that work on one product
 constexpr int kThreads = 384;
 constexpr int kOutGroups = 2;                // of four warps that take results out
+constexpr int kFewRegs = 48, kManyRegs = 208;   // of a thread of the first four warps, and of the others (launched with 168 each)
 constexpr int kBlockK = 64;                  // of the summed dimension in a stage: 128 bytes, one swizzle row
 constexpr int kTileA = 128 * kBlockK * 2;    // bytes a CTA loads of each operand per stage
 constexpr int kTileB = 128 * kBlockK * 2;
@@ -51,19 +52,20 @@ constexpr int kMaxGroups = kMaxE + 1;
 constexpr int kStages = 6;
 constexpr int kStaging = 16384;              // bytes in which a group of four warps turns its results into rows
 constexpr int kSuper = 8;                    // grad_w: tiles of N that go through all of K before the next
-// The tensor cores' adder truncates, by up to 2^-23 of the sum per 16 products, all to one side: sums of an fp32 gradient leave them
-// every 512 rows and are added up in registers, rounded to nearest.  Normal operands lose 4.7e-7 of the sums' norm then (of one sign
-// 9e-7) whatever the number of rows; with 256 / 1024 / 2048 rows 2.3e-7 / 1.0e-6 / 1.9e-6, and 8 x 28672 x 4096 gradients of 8192
-// rows took 1520 / 1390 / 1340 us where these take 1430.
-constexpr int kChunkRows = 512;
+// The tensor cores' adder truncates, by up to 2^-23 of the sum per 16 products, all to one side: sums leave them every 8 blocks, 512
+// products, and are added up in registers, rounded to nearest.  A sum of n normal products loses 4.7e-7 of its norm then, whatever n is, and
+// one of one sign 3e-6; sums that stayed for 32768 / 65536 products of one sign lost 2e-4 / 4e-4, visible in fp16.  With 256 products fp32
+// gradients of 8192 rows lost 2.3e-7 and took 1506 us (8 x 28672 x 4096) where they take 1320.  For rows the first two chunks are
+// longer, so that products get further ahead while a tile's results leave: 8192 tokens, top-8 of 128, 2048 -> 2 x 768 with gate and up kept
+// take 330 us with chunks of 8 blocks, 298 so, and 285 with sums that stay; grad_x through the gate 230, 200 and 182.
+constexpr int kChunk = 8, kFirstChunk = 12;
 
 // A tile: rows or features, and what is summed over.
 struct Work {
     int g, m, row, n;                        // group (-1: no more tiles); first of M of the pair; first row; valid of N
-    int col, end;                            // grad_w: first column; row behind the group's last
+    int col;                                 // grad_w: first column
     int kb, last;                            // blocks of 64 to sum over, and the valid of the last
     int half;                                // of N, what each CTA loads
-    int first, final;                        // grad_w: whether it is the first chunk of the tile's rows, and the last
 };
 
 constexpr int kSlots = 3;                    // tiles that the roles may be apart, and be taken ahead
@@ -97,6 +99,9 @@ struct LinearArgs {
 template <Form FORM> struct Tiles {
     static constexpr int kM = FORM == kGlu ? 64 * kPair : 128 * kPair, kN = 128 * kPair;
     static constexpr int kUnit = 16 * kPair;    // of N in a product
+    static constexpr int kFirst = FORM == kGradW ? kChunk : kFirstChunk;
+    // Blocks of the chunk that begins at block b.
+    static __device__ __forceinline__ int chunk_blocks(int b) { return b < 2 * kFirst ? kFirst : kChunk; }
     const LinearArgs &a;
     const Control &c;
 
@@ -115,9 +120,7 @@ template <Form FORM> struct Tiles {
             w.col = at / wide * kN;
             w.n = min(kN, a.sum - w.col);
             w.row = off(w.g);
-            w.end = off(w.g + 1);
-            w.first = 1;
-            blocks(w);
+            sum_over(w, max(off(w.g + 1) - w.row, 0));
         } else {
             int p = 0, hi = (a.G + 1) / 2;   // the last two groups that begin at or before the tile
             if (tile >= c.start[hi]) return false;
@@ -140,28 +143,16 @@ template <Form FORM> struct Tiles {
             w.m = in / n * kM;
             w.row = begin + at;
             w.n = min(part, rows - at);
-            w.kb = (a.sum + kBlockK - 1) / kBlockK;
-            w.last = a.sum - (w.kb - 1) * kBlockK;
+            sum_over(w, a.sum);
         }
         // whole blocks of 64 where one copy brings them
         const int unit = FORM == kGradW && a.whole_b ? 64 : kUnit / kPair;
         w.half = (w.n + unit * kPair - 1) / (unit * kPair) * unit;
         return true;
     }
-    // grad_w: the next chunk of the same tile.
-    __device__ bool next_chunk(Work &w) const {
-        if (FORM != kGradW || !a.wide || w.row + kChunkRows >= w.end) return false;
-        w.row += kChunkRows;
-        w.first = 0;
-        blocks(w);
-        return true;
-    }
-    __device__ void blocks(Work &w) const {
-        int left = max(w.end - w.row, 0);
-        if (a.wide) left = min(left, kChunkRows);
-        w.kb = (left + kBlockK - 1) / kBlockK;
-        w.last = left - (w.kb - 1) * kBlockK;
-        w.final = !a.wide || w.row + kChunkRows >= w.end;
+    __device__ void sum_over(Work &w, int n) const {
+        w.kb = (n + kBlockK - 1) / kBlockK;
+        w.last = n - (w.kb - 1) * kBlockK;
     }
 };
 
@@ -190,6 +181,9 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, int f16) {
 __device__ __forceinline__ float wide16(uint16_t v, int f16) {
     return f16 ? __half2float(__ushort_as_half(v)) : __uint_as_float((uint32_t)v << 16);
 }
+// Of all warps of a group of four.
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 // And whether `v` holds for all of them.
 __device__ __forceinline__ bool bar_all(int id, int threads, bool v) {
@@ -351,143 +345,77 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     if (c.skip == 0) {
         Feed feed{c, 0};
         Work w = {};
-        if (warp == 0) {                                 // ------------------------------------------------ loads
-            if (elect_one()) {
-                int s = 0, used = 0;
-                uint32_t round = 0;
-                while (ok && feed.next<false>(w, rank, ok)) {
-                    const int half = w.half, m = w.m + (int)rank * (Tiles<FORM>::kM / kPair);
-                    const int n = (FORM == kGradW ? w.col : w.row) + (int)rank * half;
-                    const uint32_t bytes = kTileA + (FORM == kGradW || half > 96 ? kTileB : ((half + 31) >> 5) * 4096);
-                    for (int b = 0; b < w.kb; ++b) {
-                        if (used == kStages && !(ok = mbar_wait(smem_u32(&c.empty[s]), (round & 1) ^ 1))) break;
-                        // a block that ends inside 16 rows lands here first and is cleared behind its end
-                        const bool clear = FORM == kGradW && b == w.kb - 1 && (w.last & 15) != 0;
-                        const uint32_t bar = clear ? smem_u32(&c.landed[s]) : at_rank(smem_u32(&c.full[s]), 0);
-                        mbar_arrive_expect(clear ? at_rank(bar, rank) : bar, bytes);
-                        Copies<FORM>{map_a, map_b, map_c, a}.block(w, b, m, n, half, Load{smem_u32(smem + s * kStageBytes), bar}, true, true);
-                        if (++s == kStages) s = 0, ++round;
-                        used = min(used + 1, kStages);
-                    }
-                }
-                // Nothing of the pair may still be on its way to this CTA when it ends.
-                for (int i = 0; ok && i < used; ++i) {
-                    s = s == 0 ? kStages - 1 : s - 1;
-                    if (s == kStages - 1) --round;
-                    ok = mbar_wait(smem_u32(&c.empty[s]), round & 1);
-                }
-                if (!ok) {
-                    const unsigned long long t = global_ns();
-                    while (global_ns() - t < 1000000ull) {}
-                }
-            }
-        } else if (warp == 1) {                          // ------------------------------------------------ products
-            if (rank == 0) {                             // the whole warp keeps step, one lane issues
-                int s = 0, buf = 0;
-                uint32_t round = 0, done = 0;
-                const uint32_t idesc = mma_desc(a.f16 != 0, 128 * kPair, 0, kAmn, kBmn);
-                const uint64_t desc = smem_desc(smem_u32(smem), 8192);
-                while (ok && feed.next<true>(w, rank, ok)) {
-                    if (w.kb == 0) continue;
-                    if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_empty[buf]), ((done >> 1) & 1) ^ 1)))) break;
-                    tc_fence_after();
-                    const uint32_t id = idesc | (uint32_t)(w.half * kPair >> 4) << 18;
-                    const uint32_t d = tmem + buf * kCols;
-                    for (int b = 0; b < w.kb; ++b) {
-                        const bool last = b == w.kb - 1, cleared = FORM == kGradW && last && (w.last & 15) != 0;
-                        const uint32_t full = smem_u32(&c.full[s]);
-                        if (!(ok = __all_sync(kFullMask, cleared ? mbar_wait<true>(full, round & 1) : mbar_wait(full, round & 1)))) break;
-                        tc_fence_after();
-                        const uint64_t da = desc + s * (kStageBytes >> 4), db = da + (kTileA >> 4);
-                        if (elect_one()) {
-                            const int steps = last ? (w.last + 15) >> 4 : kBlockK / 16;
-#pragma unroll
-                            for (int i = 0; i < kBlockK / 16; ++i)
-                                if (i < steps) tc_mma<kPair>(d, da + i * (kAmn ? 128 : 2), db + i * (kBmn ? 128 : 2), id, b > 0 || i > 0);
-                            tc_commit<kPair>(smem_u32(&c.empty[s]));
-                            if (last) tc_commit<kPair>(smem_u32(&c.sums_full[buf]));
-                        }
-                        __syncwarp();
-                        if (++s == kStages) s = 0, ++round;
-                    }
-                    buf ^= 1;
-                    ++done;
-                }
-            }
-        } else if (warp == 2) {                          // ------------------------------------------------ rows to clear
-            if constexpr (FORM == kGradW) {
-                int s = 0;
-                uint32_t seen = 0;                       // parity of landed[s]
-                while (ok && feed.next<true>(w, rank, ok)) {
-                    s = (s + max(w.kb - 1, 0)) % kStages;
-                    if (w.kb == 0) continue;
-                    if (w.last & 15) {
-                        if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.landed[s]), seen >> s & 1)))) break;
-                        seen ^= 1u << s;
-                        // rows last to the next multiple of 16, of two blocks of 64 columns of each operand
-                        uint8_t *const st = smem + s * kStageBytes + w.last * 128;
-                        const int rows = 16 - (w.last & 15);
-                        for (int i = lane; i < 4 * rows * 8; i += 32)
-                            *reinterpret_cast<uint4 *>(st + i / (rows * 8) * 8192 + i % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
-                        asm volatile("fence.proxy.async;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_release(at_rank(smem_u32(&c.full[s]), 0));
-                    }
-                    if (++s == kStages) s = 0;
-                }
-            }
-        } else if (warp == 3) {                          // ------------------------------------------------ tiles
-            if (elect_one()) {
-                const uint32_t read = at_rank(smem_u32(&c.read), 0);
-                int tile = blockIdx.x / kPair, slot = 0;
-                uint32_t round = 0;
-                auto hand_over = [&]() {
-                    if (round > 0 && !(ok = mbar_wait(smem_u32(&c.work_empty[slot]), (round & 1) ^ 1))) return;
-                    c.work[slot] = w;
-                    mbar_arrive(at_rank(smem_u32(&c.work_full[slot]), rank));
-                    if (++slot == kSlots) slot = 0, ++round;
-                };
-                for (uint32_t i = 0; ok; ++i) {
-                    const bool some = tile >= 0 && tiles.look_up(tile, w);
-                    if (tile >= 0) {                     // ask for the next one, once both CTAs have read the last answer
-                        mbar_arrive_expect(at_rank(smem_u32(&c.drawn), rank), 16);
-                        if (rank == 0) {
-                            if (i > 0 && !(ok = mbar_wait(smem_u32(&c.read), (i & 1) ^ 1))) break;
-                            next_cluster_request(smem_u32(&c.answer), smem_u32(&c.drawn));
-                        }
-                    }
-                    if (some) {
-                        hand_over();
-                        while (ok && tiles.next_chunk(w)) hand_over();
-                    }
-                    if (!ok || tile < 0) break;
-                    if (!(ok = mbar_wait(smem_u32(&c.drawn), i & 1))) break;
-                    tile = next_cluster_block(smem_u32(&c.answer));
-                    if (tile >= 0) tile /= kPair;
-                    fence_proxy_async_smem();
-                    mbar_arrive(read);
-                }
-                w.g = -1;
-                if (ok) hand_over();
-            }
-        } else if (warp >= 4) {                          // ------------------------------------------------ results
+        if (warp >= 4) {                                 // ------------------------------------------------ results
+            regs_up<kManyRegs>();
             const int q = warp & 3, part = (warp - 4) >> 2, et = tid & 127, bar = 1 + part;
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
             int buf = 0;
             uint32_t done = 0;
             uint8_t *const own = staging + part * kStaging;
             uint16_t *const st16 = reinterpret_cast<uint16_t *>(own);
-            constexpr int kWide = FORM == kGradW ? kCols / 32 / kOutGroups : 1;
-            float total[kWide][32];                      // an fp32 gradient's sums over the chunks so far
+            constexpr int kOwn = kCols / 32 / kOutGroups;
+            float total[kOwn][32];                       // this thread's sums over the chunks so far, in blocks of 32 columns (rows of the output)
+            // A block's first column: the two groups take turns, by 64 where the output has 16 bits and lines of 64 columns.
+            auto column = [&](int i) {
+                return FORM == kGradW && !a.wide ? ((i >> 1) * kOutGroups + part) * 64 + (i & 1) * 32 : (i * kOutGroups + part) * 32;
+            };
+            auto load = [&](int i, float(&v)[32]) {
+                tmem_ld32(lanes + buf * kCols + column(i), v);
+                tmem_wait_ld();
+            };
+            auto take = [&](int i, bool add) {
+                float v[32];
+                load(i, v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    total[i][j] = add ? total[i][j] + v[j] : v[j];
+                    asm volatile("" : "+f"(total[i][j]));        // before the next reading begins, which needs the registers of v
+                }
+            };
+            auto taken = [&]() {                         // the products may have the buffer again
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(at_rank(smem_u32(&c.sums_empty[buf]), 0));
+                buf ^= 1;
+                ++done;
+            };
             while (ok && feed.next<true>(w, rank, ok)) {
+                if (FORM == kGradW && w.kb == 0 && a.add) continue;      // nothing to add
                 const int m0 = w.m + (int)rank * (Tiles<FORM>::kM / kPair);          // first feature of this CTA
-                const uint32_t sums = lanes + buf * kCols;
-                if constexpr (FORM == kGradW) {
-                    if (w.kb == 0 && a.add) continue;    // nothing to add
-                    if (w.kb > 0) {
-                        if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_full[buf]), (done >> 1) & 1)))) break;
-                        tc_fence_after();
+                const bool one = w.kb <= Tiles<FORM>::kFirst;        // the only chunk stays in tensor memory until the output needs it
+                auto prefetch = [&](int s) {             // kGradGate: the saved gate and up of 16 rows, half of a block
+                    uint16_t *const st = st16 + (s & 1) * 4096;
+                    for (int i = et; i < 256; i += 128) {
+                        const int t = column(s >> 1) + (s & 1) * 16 + (i >> 4), f = m0 + (i & 15) * 8;
+                        if (t < w.n && f < a.M) {
+                            const uint16_t *src = a.gate_up + (size_t)(w.row + t) * 2 * a.M + f;
+                            cp_async16(st + i * 8, src);
+                            cp_async16(st + 2048 + i * 8, src + a.M);
+                        }
                     }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                };
+                if constexpr (FORM != kGradW) bar_sync(bar, 128);        // the last tile has left the staging buffers
+                if constexpr (FORM == kGradGate) prefetch(0);
+                auto arrived = [&]() {
+                    ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_full[buf]), (done >> 1) & 1));
+                    tc_fence_after();
+                };
+                if (w.kb > 0) arrived();
+                if (!one) {
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i) take(i, false);
+                    taken();
+                    for (int b = Tiles<FORM>::kFirst; ok && b < w.kb; b += Tiles<FORM>::chunk_blocks(b)) {
+                        arrived();
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i)
+                            if (column(i) < w.n) take(i, true);
+                        taken();
+                    }
+                }
+                if constexpr (FORM == kGradW) {
+                    if (!ok) break;
                     // 32 rows of 128 bytes per warp at a time, swizzled as TMA reads them: 32 columns of fp32 or 64 of 16 bits
                     uint8_t *const line = own + q * 4096 + lane * 128;
                     auto store = [&](int col) {
@@ -504,79 +432,55 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                         if (lane == 0) bulk_wait_read_all();
                         __syncwarp();
                     };
-                    if (a.wide) {
+                    auto wide_out = [&](int i, const float(&v)[32]) {
+                        left();
 #pragma unroll
-                        for (int i = 0; i < kWide; ++i) {
-                            const int col = (i * kOutGroups + part) * 32;
-                            if (col >= w.n) continue;
-                            if (w.first) {
-                                if (w.kb > 0) tmem_ld32(sums + col, total[i]);
-                                else
-                                    for (int j = 0; j < 32; ++j) total[i][j] = 0.0f;
-                                tmem_wait_ld();
-                            } else {
-                                float v[32];
-                                tmem_ld32(sums + col, v);
-                                tmem_wait_ld();
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4 *>(line + ((j ^ (lane & 7)) << 4)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                        store(column(i));
+                    };
+                    auto half_out = [&](int i, const float(&v)[32]) {
+                        const int h = i & 1;             // half of a line
+                        if (h == 0) left();
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) total[i][j] += v[j];
-                            }
-                            if (!w.final) continue;
-                            left();
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4 *>(line + (((4 * h + j) ^ (lane & 7)) << 4)) =
+                                make_uint4(pack16(v[8 * j], v[8 * j + 1], a.f16), pack16(v[8 * j + 2], v[8 * j + 3], a.f16),
+                                           pack16(v[8 * j + 4], v[8 * j + 5], a.f16), pack16(v[8 * j + 6], v[8 * j + 7], a.f16));
+                        if (h == 1) store(column(i & ~1));
+                    };
+                    auto more = [&](int i) { return column(a.wide ? i : i & ~1) < w.n; };
+                    if (one && !a.wide) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                *reinterpret_cast<float4 *>(line + ((j ^ (lane & 7)) << 4)) =
-                                    make_float4(total[i][4 * j], total[i][4 * j + 1], total[i][4 * j + 2], total[i][4 * j + 3]);
-                            store(col);
-                        }
-                    } else {
-                        for (int col = part * 64; col < w.n; col += kOutGroups * 64) {
-                            left();
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
+                        for (int i = 0; i < kOwn; ++i)
+                            if (more(i)) {
                                 float v[32] = {};
-                                if (w.kb > 0) {
-                                    tmem_ld32(sums + col + 32 * h, v);
-                                    tmem_wait_ld();
-                                }
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    *reinterpret_cast<uint4 *>(line + (((4 * h + i) ^ (lane & 7)) << 4)) =
-                                        make_uint4(pack16(v[8 * i], v[8 * i + 1], a.f16), pack16(v[8 * i + 2], v[8 * i + 3], a.f16),
-                                                   pack16(v[8 * i + 4], v[8 * i + 5], a.f16), pack16(v[8 * i + 6], v[8 * i + 7], a.f16));
+                                if (w.kb > 0) load(i, v);
+                                half_out(i, v);
                             }
-                            store(col);
+                    } else if (one) {
+                        for (int i = 0; i < kOwn && more(i); ++i) {
+                            float v[32] = {};
+                            if (w.kb > 0) load(i, v);
+                            wide_out(i, v);
                         }
+                    } else if (a.wide) {
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i)
+                            if (more(i)) wide_out(i, total[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i)
+                            if (more(i)) half_out(i, total[i]);
                     }
-                    if (w.kb == 0) continue;
+                    if (one && w.kb > 0) taken();
                 } else {
                     const int F = a.M;
-                    constexpr int kRows = FORM == kGradGate ? 16 : 32;          // of the output at a time
-                    const int chunks = (w.n + kRows - 1) / kRows;
-                    auto prefetch = [&](int ch) {        // the saved gate and up of 16 rows
-                        uint16_t *const st = st16 + (ch / kOutGroups & 1) * 4096;
-                        for (int i = et; i < 256; i += 128) {
-                            const int t = ch * kRows + (i >> 4), f = m0 + (i & 15) * 8;
-                            if (t < w.n && f < F) {
-                                const uint16_t *src = a.gate_up + (size_t)(w.row + t) * 2 * F + f;
-                                cp_async16(st + i * 8, src);
-                                cp_async16(st + 2048 + i * 8, src + F);
-                            }
-                        }
-                        asm volatile("cp.async.commit_group;" ::: "memory");
-                    };
-                    bar_sync(bar, 128);                    // the last tile has left the staging buffers
-                    if constexpr (FORM == kGradGate) prefetch(part);
-                    if (!(ok = bar_all(bar, 128, mbar_wait(smem_u32(&c.sums_full[buf]), (done >> 1) & 1)))) break;
-                    tc_fence_after();
-                    for (int ch = part; ch < chunks; ch += kOutGroups) {
-                        const int at = ch / kOutGroups & 1;  // of the two staging buffers
-                        float v[kRows];
-                        if constexpr (kRows == 16) tmem_ld16(sums + ch * kRows, v);
-                        else tmem_ld32(sums + ch * kRows, v);
-                        tmem_wait_ld();
-                        const size_t row0 = (size_t)w.row + ch * kRows;
-                        const int rows = min(kRows, w.n - ch * kRows);
+                    if (!(ok = bar_all(bar, 128, ok))) break;
+                    auto rows_out = [&](int i, const float(&v)[32]) {
+                        const int at = i & 1;            // of the two staging buffers
+                        const size_t row0 = (size_t)w.row + column(i);
+                        const int rows = min(32, w.n - column(i));
                         if constexpr (FORM == kPlain || FORM == kGradX) {
                             uint16_t *const st = st16 + at * 4096;
 #pragma unroll
@@ -591,25 +495,32 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                                 if (f < F) *reinterpret_cast<uint4 *>(a.out + (row0 + (i >> 4)) * F + f) = *reinterpret_cast<const uint4 *>(st + i * 8);
                             }
                         } else if constexpr (FORM == kGradGate) {
-                            asm volatile("cp.async.wait_group 0;" ::: "memory");
-                            bar_sync(bar, 128);            // everyone's pieces of this chunk; the other buffer is free
-                            if (ch + kOutGroups < chunks) prefetch(ch + kOutGroups);
-                            uint16_t *const st = st16 + at * 4096;
 #pragma unroll
-                            for (int j = 0; j < kRows; ++j) {
-                                const float gate = wide16(st[j * 128 + et], a.f16), up = wide16(st[2048 + j * 128 + et], a.f16);
-                                const Sigmoid sig(gate);
-                                const uint32_t p = pack16(v[j] * up * (sig.s * (1.0f + gate * sig.rest)), v[j] * (gate * sig.s), a.f16);
-                                st[j * 128 + et] = (uint16_t)p;
-                                st[2048 + j * 128 + et] = (uint16_t)(p >> 16);
-                            }
-                            bar_sync(bar, 128);
-                            for (int i = et; i < rows * 16; i += 128) {
-                                const int f = m0 + (i & 15) * 8;
-                                if (f < F) {
-                                    uint16_t *const dst = a.out + (row0 + (i >> 4)) * 2 * F + f;
-                                    *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(st + i * 8);
-                                    *reinterpret_cast<uint4 *>(dst + F) = *reinterpret_cast<const uint4 *>(st + 2048 + i * 8);
+                            for (int h = 0; h < 2; ++h) {
+                                if (h * 16 >= rows) break;
+                                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                                bar_sync(bar, 128);        // everyone's pieces of these rows; the other buffer is free
+                                if (h == 0 ? 16 < rows : column(i + 1) < w.n) prefetch(2 * i + h + 1);
+                                uint16_t *const st = st16 + h * 4096;
+                                uint16_t gs[16], us[16];                 // all read before the first is needed
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) gs[j] = st[j * 128 + et], us[j] = st[2048 + j * 128 + et];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    const float gate = wide16(gs[j], a.f16), up = wide16(us[j], a.f16), d = v[16 * h + j];
+                                    const Sigmoid sig(gate);
+                                    const uint32_t p = pack16(d * up * (sig.s * (1.0f + gate * sig.rest)), d * (gate * sig.s), a.f16);
+                                    st[j * 128 + et] = (uint16_t)p;
+                                    st[2048 + j * 128 + et] = (uint16_t)(p >> 16);
+                                }
+                                bar_sync(bar, 128);
+                                for (int i = et; i < min(16, rows - 16 * h) * 16; i += 128) {
+                                    const int f = m0 + (i & 15) * 8;
+                                    if (f < F) {
+                                        uint16_t *const dst = a.out + (row0 + 16 * h + (i >> 4)) * 2 * F + f;
+                                        *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(st + i * 8);
+                                        *reinterpret_cast<uint4 *>(dst + F) = *reinterpret_cast<const uint4 *>(st + 2048 + i * 8);
+                                    }
                                 }
                             }
                         } else {
@@ -618,7 +529,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                             const int f = q * 16 + (lane & 15);
                             uint16_t *const act = st16 + at * 2048, *const gu = st16 + 4096;
                             if (a.gate_up) {
-                                if (ch != part) bar_sync(bar, 128);      // the rows before have left
+                                if (i > 0) bar_sync(bar, 128);           // the rows before have left
 #pragma unroll
                                 for (int j = 0; j < 32; j += 2) {
                                     const uint32_t p = pack16(v[j], v[j + 1], a.f16);
@@ -630,10 +541,10 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                             for (int j = 0; j < 16; j += 2) {
                                 float y[2];
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const float other = __shfl_xor_sync(kFullMask, up ? v[j + i] : v[16 + j + i], 16), own = up ? v[16 + j + i] : v[j + i];
+                                for (int k = 0; k < 2; ++k) {
+                                    const float other = __shfl_xor_sync(kFullMask, up ? v[j + k] : v[16 + j + k], 16), own = up ? v[16 + j + k] : v[j + k];
                                     const float gate = up ? other : own;
-                                    y[i] = gate * Sigmoid(gate).s * (up ? own : other);
+                                    y[k] = gate * Sigmoid(gate).s * (up ? own : other);
                                 }
                                 const uint32_t p = pack16(y[0], y[1], a.f16);
                                 act[(up * 16 + j) * 64 + f] = (uint16_t)p;
@@ -652,15 +563,155 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                                 }
                             }
                         }
+                    };
+                    if (FORM != kGradGate && one) {
+                        for (int i = 0; column(i) < w.n; ++i) {
+                            float v[32];
+                            load(i, v);
+                            rows_out(i, v);
+                        }
+                    } else if constexpr (FORM == kGradGate) {
+                        // One copy of the code for all blocks, whose sums move up instead: four of them would have to be fetched at every launch
+                        // (a call of 1332 rows took 47 us with them, and 39 so).
+#pragma unroll 1
+                        for (int i = 0; column(i) < w.n; ++i) {
+                            if (one) load(i, total[0]);
+                            rows_out(i, total[0]);
+#pragma unroll
+                            for (int k = 0; k + 1 < kOwn; ++k)
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) total[k][j] = total[k + 1][j];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i)
+                            if (column(i) < w.n) rows_out(i, total[i]);
                     }
+                    if (one) taken();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(at_rank(smem_u32(&c.sums_empty[buf]), 0));
-                buf ^= 1;
-                ++done;
             }
             if (FORM == kGradW && lane == 0) bulk_wait_all();
+        } else {
+            regs_down<kFewRegs>();
+            if (warp == 0) {                                 // ------------------------------------------------ loads
+                if (elect_one()) {
+                    int s = 0, used = 0;
+                    uint32_t round = 0;
+                    while (ok && feed.next<false>(w, rank, ok)) {
+                        const int half = w.half, m = w.m + (int)rank * (Tiles<FORM>::kM / kPair);
+                        const int n = (FORM == kGradW ? w.col : w.row) + (int)rank * half;
+                        const uint32_t bytes = kTileA + (FORM == kGradW || half > 96 ? kTileB : ((half + 31) >> 5) * 4096);
+                        for (int b = 0; b < w.kb; ++b) {
+                            if (used == kStages && !(ok = mbar_wait(smem_u32(&c.empty[s]), (round & 1) ^ 1))) break;
+                            // a block that ends inside 16 rows lands here first and is cleared behind its end
+                            const bool clear = FORM == kGradW && b == w.kb - 1 && (w.last & 15) != 0;
+                            const uint32_t bar = clear ? smem_u32(&c.landed[s]) : at_rank(smem_u32(&c.full[s]), 0);
+                            mbar_arrive_expect(clear ? at_rank(bar, rank) : bar, bytes);
+                            Copies<FORM>{map_a, map_b, map_c, a}.block(w, b, m, n, half, Load{smem_u32(smem + s * kStageBytes), bar}, true, true);
+                            if (++s == kStages) s = 0, ++round;
+                            used = min(used + 1, kStages);
+                        }
+                    }
+                    // Nothing of the pair may still be on its way to this CTA when it ends.
+                    for (int i = 0; ok && i < used; ++i) {
+                        s = s == 0 ? kStages - 1 : s - 1;
+                        if (s == kStages - 1) --round;
+                        ok = mbar_wait(smem_u32(&c.empty[s]), round & 1);
+                    }
+                    if (!ok) {
+                        const unsigned long long t = global_ns();
+                        while (global_ns() - t < 1000000ull) {}
+                    }
+                }
+            } else if (warp == 1) {                          // ------------------------------------------------ products
+                if (rank == 0) {                             // the whole warp keeps step, one lane issues
+                    int s = 0, buf = 0;
+                    uint32_t round = 0, done = 0;
+                    const uint32_t idesc = mma_desc(a.f16 != 0, 128 * kPair, 0, kAmn, kBmn);
+                    const uint64_t desc = smem_desc(smem_u32(smem), 8192);
+                    while (ok && feed.next<true>(w, rank, ok)) {
+                        const uint32_t id = idesc | (uint32_t)(w.half * kPair >> 4) << 18;
+                        for (int b = 0, first = 0, next = 0; b < w.kb; ++b) {
+                            if (b == next) {                 // a chunk begins
+                                first = b;
+                                next = b + Tiles<FORM>::chunk_blocks(b);
+                                if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.sums_empty[buf]), ((done >> 1) & 1) ^ 1)))) break;
+                                tc_fence_after();
+                            }
+                            const uint32_t d = tmem + buf * kCols;
+                            const bool last = b == w.kb - 1, ends = last || b + 1 == next, cleared = FORM == kGradW && last && (w.last & 15) != 0;
+                            const uint32_t full = smem_u32(&c.full[s]);
+                            if (!(ok = __all_sync(kFullMask, cleared ? mbar_wait<true>(full, round & 1) : mbar_wait(full, round & 1)))) break;
+                            tc_fence_after();
+                            const uint64_t da = desc + s * (kStageBytes >> 4), db = da + (kTileA >> 4);
+                            if (elect_one()) {
+                                const int steps = last ? (w.last + 15) >> 4 : kBlockK / 16;
+#pragma unroll
+                                for (int i = 0; i < kBlockK / 16; ++i)
+                                    if (i < steps) tc_mma<kPair>(d, da + i * (kAmn ? 128 : 2), db + i * (kBmn ? 128 : 2), id, b > first || i > 0);
+                                tc_commit<kPair>(smem_u32(&c.empty[s]));
+                                if (ends) tc_commit<kPair>(smem_u32(&c.sums_full[buf]));
+                            }
+                            __syncwarp();
+                            if (ends) buf ^= 1, ++done;
+                            if (++s == kStages) s = 0, ++round;
+                        }
+                    }
+                }
+            } else if (warp == 2) {                          // ------------------------------------------------ rows to clear
+                if constexpr (FORM == kGradW) {
+                    int s = 0;
+                    uint32_t seen = 0;                       // parity of landed[s]
+                    while (ok && feed.next<true>(w, rank, ok)) {
+                        s = (s + max(w.kb - 1, 0)) % kStages;
+                        if (w.kb == 0) continue;
+                        if (w.last & 15) {
+                            if (!(ok = __all_sync(kFullMask, mbar_wait(smem_u32(&c.landed[s]), seen >> s & 1)))) break;
+                            seen ^= 1u << s;
+                            // rows last to the next multiple of 16, of two blocks of 64 columns of each operand
+                            uint8_t *const st = smem + s * kStageBytes + w.last * 128;
+                            const int rows = 16 - (w.last & 15);
+                            for (int i = lane; i < 4 * rows * 8; i += 32)
+                                *reinterpret_cast<uint4 *>(st + i / (rows * 8) * 8192 + i % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
+                            asm volatile("fence.proxy.async;" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_release(at_rank(smem_u32(&c.full[s]), 0));
+                        }
+                        if (++s == kStages) s = 0;
+                    }
+                }
+            } else if (warp == 3) {                          // ------------------------------------------------ tiles
+                if (elect_one()) {
+                    const uint32_t read = at_rank(smem_u32(&c.read), 0);
+                    int tile = blockIdx.x / kPair, slot = 0;
+                    uint32_t round = 0;
+                    auto hand_over = [&]() {
+                        if (round > 0 && !(ok = mbar_wait(smem_u32(&c.work_empty[slot]), (round & 1) ^ 1))) return;
+                        c.work[slot] = w;
+                        mbar_arrive(at_rank(smem_u32(&c.work_full[slot]), rank));
+                        if (++slot == kSlots) slot = 0, ++round;
+                    };
+                    for (uint32_t i = 0; ok; ++i) {
+                        const bool some = tile >= 0 && tiles.look_up(tile, w);
+                        if (tile >= 0) {                     // ask for the next one, once both CTAs have read the last answer
+                            mbar_arrive_expect(at_rank(smem_u32(&c.drawn), rank), 16);
+                            if (rank == 0) {
+                                if (i > 0 && !(ok = mbar_wait(smem_u32(&c.read), (i & 1) ^ 1))) break;
+                                next_cluster_request(smem_u32(&c.answer), smem_u32(&c.drawn));
+                            }
+                        }
+                        if (some) hand_over();
+                        if (!ok || tile < 0) break;
+                        if (!(ok = mbar_wait(smem_u32(&c.drawn), i & 1))) break;
+                        tile = next_cluster_block(smem_u32(&c.answer));
+                        if (tile >= 0) tile /= kPair;
+                        fence_proxy_async_smem();
+                        mbar_arrive(read);
+                    }
+                    w.g = -1;
+                    if (ok) hand_over();
+                }
+            }
         }
     }
     if (!ok) atomicOr(a.status, EP_STATUS_TIMEOUT);
@@ -723,6 +774,11 @@ int launch_form(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap 
     constexpr auto kern = ep_linear_kernel<FORM>;
     const int rc = allow_smem<kern>(kSmem);
     if (rc != EP_OK) return rc;
+    static const bool has_regs = [] {                // what the warps take over from one another has to be there, or they would wait for it
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kern) == cudaSuccess && f.numRegs * kThreads >= kFewRegs * 128 + kManyRegs * kOutGroups * 128;
+    }();
+    if (!has_regs) return EP_ERR_CUDA;
     constexpr int kM = Tiles<FORM>::kM, kN = Tiles<FORM>::kN;
     const long long m_tiles = (a.M + kM - 1) / kM;
     const long long tiles = m_tiles * (FORM == kGradW ? (long long)a.G * ((a.sum + kN - 1) / kN) : (long long)a.R_max / kN + std::min(a.G, a.R_max));

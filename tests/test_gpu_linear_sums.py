@@ -1,0 +1,91 @@
+"""How exactly the grouped 16-bit products sum.
+
+The tensor cores' adder truncates, by up to 2^-23 of the running sum with every 16 products.  Sums leave it every 512 products (those of
+rows: after 768, 768 and then every 512) and are added up in fp32, so that terms of one sign lose at most 32 (48) * 2^-23 of the sum there and
+2^-24 of it with each addition; sums that stay lose length / 32 * 2^-23 of it on average, several times as much at these lengths.  A 16-bit output hides that behind its own
+rounding, but roundings average out: over M outputs to 6 * u / sqrt(3 M) (six standard deviations of M roundings, each uniform
+within u)."""
+import pytest
+import torch
+
+import linear_ref as ref
+from operator_ref import U
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+def lost(n, chunk=768):
+    """Of a sum of n terms of one sign."""
+    return chunk / 16 * 2.0 ** -23 + n / 512 * 2.0 ** -24
+
+
+def one_sign(seed, scale, *shape, dtype=F16):
+    """Between scale / 2 and 2 * scale: values of the columns in [1/2, 1), times a factor in [1, 2) for each row."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    v = 0.5 + 0.5 * torch.rand(*shape, generator=g, device="cuda")
+    return (v * (1 + torch.rand(*shape[:-1], 1, generator=g, device="cuda")) * scale).to(dtype)
+
+
+def assert_unbiased(got, want, n, dtype, factor=1.0, chunk=768):
+    bias = ((got.double() - want) / want).mean().item()
+    print(f"bias over {n}: {bias}")
+    assert abs(bias) <= factor * lost(n, chunk) + 6 * U[dtype] / (3 * want.numel()) ** 0.5, bias
+
+
+@pytest.mark.parametrize("K", [4096, 32768])
+def test_rows(K):
+    import combine_topk_ids_histogram_gb300 as ep
+    R, N = 512, 1024
+    L = ref.layout_of(ep, [R])
+    x, w = one_sign(1, 2.0 ** -6, R, K), one_sign(2, 2.0 ** -5 if K == 4096 else 2.0 ** -8, 1, N, K)
+    want = x.double() @ w[0].double().t()
+    assert_unbiased(ep.expert_linear(x, w, L), want, K, F16)
+    act, gu = ep.expert_linear(x, w, L, swiglu=True, save=True)
+    assert_unbiased(gu, want, K, F16)
+    gate, up = want[:, :N // 2], want[:, N // 2:]
+    # the product follows up, and gate by 1 + gate (1 - s) <= 1.28; the sigmoid is off by 2^-20 at most
+    assert_unbiased(act, gate * torch.sigmoid(gate) * up, K, F16, 2.28 + 2.0 ** -20 / lost(K))
+
+
+@pytest.mark.parametrize("N", [4096, 65536])
+def test_gradient_of_rows(N):
+    import combine_topk_ids_histogram_gb300 as ep
+    R, K = 1024, 512
+    L = ref.layout_of(ep, [R])
+    g, w = one_sign(3, 2.0 ** -6, R, N), one_sign(4, 2.0 ** -8, 1, N, K)
+    want = g.double() @ w[0].double()
+    gx, _ = ep.expert_linear_bwd(g, None, w, L, need=(True, False))
+    assert_unbiased(gx, want, N, F16)
+    gu = torch.cat([torch.zeros(R, K), torch.full((R, K), 4.0)], 1).half().cuda()      # silu'(0) = 1/2
+    gx, _ = ep.expert_linear_bwd(g, None, w, L, gate_up=gu, need=(True, False))
+    assert_unbiased(gx[:, :K], 2 * want, N, F16)
+
+
+@pytest.mark.parametrize("R", [4096, 33000])
+def test_gradient_of_weights(R):
+    import combine_topk_ids_histogram_gb300 as ep
+    L = ref.layout_of(ep, [100, R])
+    x, g, w = one_sign(5, 2.0 ** -7, R + 100, 512), one_sign(6, 2.0 ** -7, R + 100, 1024), torch.zeros(2, 1024, 512, dtype=F16, device="cuda")
+    want = g[100:].double().t() @ x[100:].double()
+    _, gw = ep.expert_linear_bwd(g, x, w, L, need=(False, True))
+    assert_unbiased(gw[1], want, R, F16, chunk=512)
+    _, gw = ep.expert_linear_bwd(g, x, w, L, need=(False, True), grad_w_dtype=torch.float32)
+    assert ((gw[1].double() - want).abs() <= (lost(R, 512) + 2.0 ** -24) * want).all()
+    before = torch.full((2, 1024, 512), 3.0, device="cuda")
+    ep.expert_linear_bwd(g, x, w, L, need=(False, True), accumulate=True, out=(None, before))
+    assert ((before[1].double() - 3 - want).abs() <= (lost(R, 512) + 2.0 ** -24) * want + 2.0 ** -24 * (want + 3)).all()
+
+
+def test_norm_of_the_weights_gradient():
+    """Of normal operands.  The running sums of a chunk have the size of sqrt(16 t) after t steps, and lose 2^-23 of that at most: 483 * 2^-23
+    in 32 steps, of a chunk's sqrt(512).  Chunks' errors are as independent as their sums, and the additions in fp32 lose less."""
+    import combine_topk_ids_histogram_gb300 as ep
+    R = 16384
+    L = ref.layout_of(ep, [R])
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x, g = (torch.randn(R, 512, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    _, gw = ep.expert_linear_bwd(g, x, torch.zeros(1, 512, 512, dtype=BF16, device="cuda"), L, need=(False, True), grad_w_dtype=torch.float32)
+    want = g.double().t() @ x.double()
+    assert (gw[0].double() - want).norm() <= (483 / 512 ** 0.5 * 2.0 ** -23 + R / 512 * 2.0 ** -24) * want.norm()
