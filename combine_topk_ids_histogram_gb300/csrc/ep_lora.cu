@@ -19,6 +19,7 @@
 
 #include "ep_async.cuh"
 #include "ep_host.h"
+#include "ep_ring.h"
 #include "ep_tensor.cuh"
 #include "ep_types.cuh"
 
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
 // through a ring in shared memory that cp.async fills ahead: 64 columns of x with 64 of A (N is r), then 64 of y with 64 rows of B
 // (K is r).  The CTAs of a cluster split H, add up A x through each other's shared memory, and split N.  (With mma.sync from
 // shared memory its products took half of the time: 71 us with 8192 tokens, 5 adapters of rank 64, 4096 -> 4096, where this takes 58.)
-constexpr int kTileRows = 128, kRing = 3, kTileThreads = kThreads + 32;           // the last warp issues the products
+constexpr int kTileRows = 128, kTileThreads = kThreads + 32;           // the last warp issues the products
 
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gmem, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(valid ? 16 : 0) : "memory");
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
     constexpr uint32_t kTmem = 128;                          // columns: the sums of A x, then of 64 outputs
     extern __shared__ __align__(16) uint8_t s_raw[];
     uint8_t *const smem = s_raw + (1024 - (smem_u32(s_raw) & 1023)) % 1024;
-    __shared__ __align__(8) uint64_t s_full[kRing], s_free[kRing], s_done[2];
+    __shared__ __align__(8) uint64_t s_full[kRing], s_free[kRing], s_done[kRing];
     __shared__ uint32_t s_tmem;
     __shared__ float s_scale[kTileRows];
     __shared__ int s_at[kTileRows];
@@ -388,9 +389,8 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_u32(&s_full[i]), kThreads);
             mbar_init(smem_u32(&s_free[i]), kWarps);
+            mbar_init(smem_u32(&s_done[i]), 1);
         }
-        mbar_init(smem_u32(&s_done[0]), 1);
-        mbar_init(smem_u32(&s_done[1]), 1);
         mbar_init_done();
     }
     tc_fence_before();
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         }
         cp_async_arrive(smem_u32(&s_full[slot]));
     };
-    // ---- A x: every CTA sums its stages of H.  Stage i is in slot i % kRing; barriers' phases count on through both parts.
+    // ---- A x: every CTA sums its stages of H.  Barriers' phases count on through both parts.
     const int first2 = (a.N + 63) / 64 * rank / a.C, stages1 = (a.H + 63) / 64 * (rank + 1) / a.C - first1, stages2 = (a.N + 63) / 64 * (rank + 1) / a.C - first2;
     auto wait = [&](uint64_t &bar, int phase) {
         if (ok) ok = mbar_wait(smem_u32(&bar), phase & 1);
@@ -438,15 +438,15 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
     if (issuer) {
         const uint32_t id1 = mma_desc(f16, 128, n1, false, false);
         for (int i = 0; i < stages1; ++i) {
-            const int slot = i % kRing;
-            wait(s_full[slot], i / kRing);
+            const int slot = ring_slot(i);
+            wait(s_full[slot], ring_phase(i));
             fence_proxy_async_smem();
             if (elect_one()) {
                 tc_fence_after();
                 const uint64_t da = smem_desc(ring + slot * S::kStage, 0), db = smem_desc(ring + slot * S::kStage + S::kLeft, 0);
                 const int steps = min(4, (a.H - (first1 + i) * 64 + 15) / 16);
                 for (int k = 0; k < steps; ++k) tc_mma<1>(tmem, da + 2 * k, db + 2 * k, id1, i > 0 || k > 0);
-                tc_commit<1>(smem_u32(&s_done[i & 1]));
+                tc_commit<1>(smem_u32(&s_done[slot]));
             }
             __syncwarp();
         }
@@ -454,10 +454,10 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         for (int i = 0; i < kRing - 1 && i < stages1; ++i) fill_first(i, i);
         if (a.copy) copy_rows(a);                            // while they are on their way
         for (int i = 0; i < stages1; ++i) {
-            if (i > 0) wait(s_done[(i - 1) & 1], (i - 1) >> 1);          // the products of stage i - 1 have read its slot
-            if (i + kRing - 1 < stages1) fill_first(i + kRing - 1, (i + kRing - 1) % kRing);
+            if (i > 0) wait(s_done[ring_slot(i - 1)], ring_phase(i - 1));        // the products of stage i - 1 have read its slot
+            if (i + kRing - 1 < stages1) fill_first(i + kRing - 1, ring_slot(i + kRing - 1));
         }
-        if (stages1 > 0) wait(s_done[(stages1 - 1) & 1], (stages1 - 1) >> 1);
+        if (stages1 > 0) wait(s_done[ring_slot(stages1 - 1)], ring_phase(stages1 - 1));
     }
     tc_fence_after();
     __syncthreads();
@@ -549,16 +549,13 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         cp_async_arrive(smem_u32(&s_full[slot]));
     };
     tc_fence_after();
-    // Barriers have gone through these many phases: s_full by slot, s_done by parity.
-    auto full_phase = [&](int i) { return (stages1 - i % kRing + kRing - 1) / kRing + i / kRing; };
-    auto done_phase = [&](int i) { return (stages1 + 1 - (i & 1)) / 2 + (i >> 1); };
     if (issuer) {
         const uint32_t id2 = mma_desc(f16, 128, 64, false, false);
         for (int i = 0; i < stages2; ++i) {
-            const int slot = i % kRing;
-            wait(s_full[slot], full_phase(i));
+            const int slot = ring_slot(i);
+            wait(s_full[slot], ring_phase(i, stages1));
             // (twice 64 columns of sums: those of stage i - 2 have been read when its slot's successor is filled)
-            if (i >= 2) wait(s_free[(i - 2) % kRing], (i - 2) / kRing);
+            if (i >= 2) wait(s_free[ring_slot(i - 2)], ring_phase(i - 2));
             fence_proxy_async_smem();
             if (elect_one()) {
                 tc_fence_after();
@@ -568,18 +565,18 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
                     tc_mma<1>(tmem + (i & 1) * 64, da + S::kLow / 16 + ka, db + kb, id2, k > 0);
                     tc_mma<1>(tmem + (i & 1) * 64, da + ka, db + kb, id2, true);
                 }
-                tc_commit<1>(smem_u32(&s_done[i & 1]));
+                tc_commit<1>(smem_u32(&s_done[slot]));
             }
             __syncwarp();
         }
     } else {
         for (int i = 0; i < kRing - 1 && i < stages2; ++i) fill_second(i, i);
         for (int i = 0; i < stages2; ++i) {
-            const int slot = i % kRing, col = (first2 + i) * 64;
-            if (i > 0) wait(s_free[(i - 1) % kRing], (i - 1) / kRing);   // every warp has written stage i - 1
-            if (i + kRing - 1 < stages2) fill_second(i + kRing - 1, (i + kRing - 1) % kRing);
-            wait(s_full[slot], full_phase(i));
-            wait(s_done[i & 1], done_phase(i));
+            const int slot = ring_slot(i), col = (first2 + i) * 64;
+            if (i > 0) wait(s_free[ring_slot(i - 1)], ring_phase(i - 1));        // every warp has written stage i - 1
+            if (i + kRing - 1 < stages2) fill_second(i + kRing - 1, ring_slot(i + kRing - 1));
+            wait(s_full[slot], ring_phase(i, stages1));
+            wait(s_done[slot], ring_phase(i, stages1));
             __syncwarp();
             tc_fence_after();
             uint8_t *const st = smem + slot * S::kStage;

@@ -1,0 +1,159 @@
+// Every order in which two copying warps, the issuing warp and the tensor cores can pass a ring's barriers, as the adapters' kernel for
+// many rows uses them in its two products.  argv: stages of the first product, of the second, and optionally "two" for a model with
+// two barriers for finished products, by the parity of the stage, in place of a slot's own.  Prints "ok" or what went wrong.
+#include <algorithm>
+#include <array>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <set>
+#include <string>
+#include <vector>
+
+#include "ep_ring.h"
+
+using namespace ep;
+
+constexpr int kWarps = 2;
+bool two = false;
+int stages[2];
+
+enum Kind { kFill, kWaitDone, kWaitFull, kWaitFree, kRead, kIssue, kSync };
+struct Op {
+    Kind kind;
+    int part, stage;
+};
+std::vector<Op> copier, issuer;
+
+int done_bar(int stage) { return two ? stage & 1 : ring_slot(stage); }
+int done_phase(int part, int stage) {
+    if (!two) return ring_phase(stage, part ? stages[0] : 0);
+    return (part ? (stages[0] + 1 - (stage & 1)) / 2 : 0) + (stage >> 1);
+}
+int full_phase(int part, int stage) { return ring_phase(stage, part ? stages[0] : 0); }
+
+void programs() {
+    for (int i = 0; i < kRing - 1 && i < stages[0]; ++i) copier.push_back({kFill, 0, i});
+    for (int i = 0; i < stages[0]; ++i) {
+        if (i > 0) copier.push_back({kWaitDone, 0, i - 1});
+        if (i + kRing - 1 < stages[0]) copier.push_back({kFill, 0, i + kRing - 1});
+    }
+    if (stages[0] > 0) copier.push_back({kWaitDone, 0, stages[0] - 1});
+    copier.push_back({kSync, 0, 0});
+    for (int i = 0; i < kRing - 1 && i < stages[1]; ++i) copier.push_back({kFill, 1, i});
+    for (int i = 0; i < stages[1]; ++i) {
+        if (i > 0) copier.push_back({kWaitFree, 1, i - 1});
+        if (i + kRing - 1 < stages[1]) copier.push_back({kFill, 1, i + kRing - 1});
+        copier.push_back({kWaitFull, 1, i});
+        copier.push_back({kWaitDone, 1, i});
+        copier.push_back({kRead, 1, i});
+    }
+    for (int i = 0; i < stages[0]; ++i) {
+        issuer.push_back({kWaitFull, 0, i});
+        issuer.push_back({kIssue, 0, i});
+    }
+    issuer.push_back({kSync, 0, 0});
+    for (int i = 0; i < stages[1]; ++i) {
+        issuer.push_back({kWaitFull, 1, i});
+        if (i >= 2) issuer.push_back({kWaitFree, 1, i - 2});
+        issuer.push_back({kIssue, 1, i});
+    }
+}
+
+// Where each warp and the issuer are, and how many products have been finished; everything else follows from that.
+using State = std::array<int, kWarps + 2>;
+
+int count(const std::vector<Op> &prog, int pc, Kind kind, int part, int stage_at_most, int (*key)(int), int k) {
+    int n = 0;
+    for (int i = 0; i < pc; ++i)
+        if (prog[i].kind == kind && prog[i].part <= part && (prog[i].part < part || prog[i].stage <= stage_at_most) && key(prog[i].stage) == k) ++n;
+    return n;
+}
+bool passed(const std::vector<Op> &prog, int pc, const Op &op) {
+    for (int i = 0; i < pc; ++i)
+        if (prog[i].kind == op.kind && prog[i].part == op.part && prog[i].stage == op.stage) return true;
+    return false;
+}
+
+int ended(const State &s, Kind kind, int bar) {          // phases that a barrier has ended
+    if (kind == kWaitDone) {
+        int n = 0, at = 0;
+        for (const Op &op : issuer)
+            if (op.kind == kIssue && at++ < s[kWarps + 1] && done_bar(op.stage) == bar) ++n;
+        return n;
+    }
+    int least = 1 << 30;
+    for (int w = 0; w < kWarps; ++w) least = std::min(least, count(copier, s[w], kind == kWaitFull ? kFill : kRead, 1, 1 << 30, ring_slot, bar));
+    return least;
+}
+
+// 1: may go on, 0: has to wait, -1: goes on or waits wrongly
+int wait(const State &s, const Op &op) {
+    const int bar = op.kind == kWaitDone ? done_bar(op.stage) : ring_slot(op.stage);
+    const int phase = op.kind == kWaitDone ? done_phase(op.part, op.stage) : op.kind == kWaitFull ? full_phase(op.part, op.stage) : ring_phase(op.stage);
+    const int n = ended(s, op.kind, bar);
+    const bool sees = ((n ^ phase) & 1) != 0, is = n > phase;
+    if (sees != is) return -1;
+    return is;
+}
+
+std::string explore() {
+    std::set<State> seen;
+    std::vector<State> todo{State{}};
+    seen.insert(todo[0]);
+    while (!todo.empty()) {
+        const State s = todo.back();
+        todo.pop_back();
+        bool moved = false, all = true;
+        auto go = [&](int who) {
+            State t = s;
+            ++t[who];
+            moved = true;
+            if (seen.insert(t).second) todo.push_back(t);
+        };
+        for (int who = 0; who <= kWarps; ++who) {
+            const std::vector<Op> &prog = who < kWarps ? copier : issuer;
+            if (s[who] == (int)prog.size()) continue;
+            all = false;
+            const Op op = prog[s[who]];
+            if (op.kind == kFill) {
+                // what the slot held before has been multiplied (and, of the second product, read by everyone)
+                if (op.stage >= kRing) {
+                    int at = 0, when = 0;
+                    for (const Op &q : issuer)
+                        if (q.kind == kIssue && ++at && q.part == op.part && q.stage == op.stage - kRing) when = at;
+                    if (s[kWarps + 1] < when) return "a slot is filled before its products are done";
+                    if (op.part == 1)
+                        for (int w = 0; w < kWarps; ++w)
+                            if (!passed(copier, s[w], {kRead, 1, op.stage - kRing})) return "a slot is filled before it has been read";
+                }
+                go(who);
+            } else if (op.kind == kRead || op.kind == kIssue) {
+                go(who);
+            } else if (op.kind == kSync) {
+                bool here = true;
+                for (int o = 0; o <= kWarps; ++o) here = here && s[o] >= 0 && passed(o < kWarps ? copier : issuer, s[o] + 1, {kSync, 0, 0});
+                if (here) go(who);
+            } else {
+                const int r = wait(s, op);
+                if (r < 0) return "a wait sees the parity of another phase";
+                if (r) go(who);
+            }
+        }
+        int issued = 0;
+        for (int i = 0; i < s[kWarps]; ++i) issued += issuer[i].kind == kIssue;
+        if (s[kWarps + 1] < issued) all = false, go(kWarps + 1);
+        if (!moved && !all) return "nobody can go on";
+    }
+    return "ok";
+}
+
+int main(int argc, char **argv) {
+    stages[0] = atoi(argv[1]);
+    stages[1] = atoi(argv[2]);
+    two = argc > 3 && !strcmp(argv[3], "two");
+    programs();
+    const std::string r = explore();
+    printf("%s\n", r.c_str());
+    return r == "ok" ? 0 : 1;
+}
