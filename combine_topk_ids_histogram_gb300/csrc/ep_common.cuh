@@ -62,14 +62,15 @@ __device__ __forceinline__ int load_status(const int32_t *status) {
 #endif
 constexpr bool kBoundsCheck = EP_BOUNDS_CHECK != 0;
 
-// The status word as one value for the whole CTA; every thread of the CTA must call it.  Only
-// the layout writes the word, and it completes before any kernel that reads it starts, so in
-// the default build every thread reads the same value.  In the bounds-checked build another CTA
-// of the running kernel may set EP_STATUS_BOUNDS meanwhile, so the CTA agrees on one reading
-// (one barrier) before it acts on it.
+// The status word as one value for the whole CTA; every thread of the CTA must call it.  The
+// layout writes the word, and completes before any kernel that reads it starts; but a kernel that
+// runs beside this one on another stream with the same layout may set EP_STATUS_TIMEOUT (the
+// kernels with bounded waits, ep_linear.cu and ep_lora.cu, whose clusters act on one reading too),
+// and in the bounds-checked build any CTA may set EP_STATUS_BOUNDS.  So the CTA agrees on one
+// reading (one barrier) before it acts on it: a thread that left alone would leave the others its
+// part of shared memory unwritten.
 __device__ __forceinline__ int cta_status(const int32_t *status) {
-    if (kBoundsCheck) return __syncthreads_or(load_status(status));
-    return load_status(status);
+    return __syncthreads_or(load_status(status));
 }
 
 // Records a failed check in the status word (checked build only).

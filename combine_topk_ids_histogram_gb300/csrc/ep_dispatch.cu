@@ -374,9 +374,11 @@ ep_dispatch_nvfp4_staged_kernel(const uint16_t *__restrict__ x, int T, int H, in
     const int tb = (int)((long long)blockIdx.x * T / tok_ctas);
     const int te = (int)((long long)(blockIdx.x + 1) * T / tok_ctas);
     bool waited = false;
+    int stop = 0;                   // the status, read once, before any copy is issued
     if (!early) {
         pdl_begin();
         waited = true;
+        stop = cta_status(status);
     }
     const uint4 *xv = reinterpret_cast<const uint4 *>(x);
     uint4 v[4], vn[4];
@@ -432,10 +434,11 @@ ep_dispatch_nvfp4_staged_kernel(const uint16_t *__restrict__ x, int T, int H, in
         if (!waited) {              // from here on the layout's outputs are needed
             pdl_begin();
             waited = true;
+            stop = cta_status(status);
         }
         const int shared_base = S ? row_offsets[E] : 0;
         const int nrows = K + S;
-        if (cta_status(status)) {         // constant per call: no copy was issued before
+        if (stop) {
             if (write_meta)                // no payload, but every row's metadata
                 for (int t = tb + warp; t < te; t += nwarps)
                     for (int k = lane; k < nrows; k += 32) {

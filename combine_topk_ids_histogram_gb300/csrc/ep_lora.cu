@@ -51,6 +51,11 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -91,7 +96,7 @@ struct Rows {
             end = min(R, first + a.rows);
             if (first >= R) return;
             if (g < 0 || g >= a.G) {
-                bounds_fail(a.status);
+                if (kBoundsCheck && load_status(a.status) == 0) bounds_fail(a.status);
                 end = first;
             } else if (a.rows > 1) {
                 end = min(end, a.row_offsets[g + 1]);
@@ -173,19 +178,12 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
         for (int i = 0; i < 2; ++i) token[i] = a.src_info[2 * (size_t)min(tile * a.rows + c + 8 * i, a.R_max - 1)];
     }
     const Rows rows(a, tile);
-    if constexpr (kBoundsCheck) {                            // another CTA may set a bit meanwhile: the cluster acts on one reading
-        __shared__ int s_status;
-        if (tid == 0) s_status = load_status(a.status);
-        cluster_sync_all();
-        int st;
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(st) : "r"(at_rank(smem_u32(&s_status), 0)) : "memory");
-        cluster_sync_all();
-        if (st) return;
-    } else if (load_status(a.status)) {
-        return;
-    }
+    // Another kernel that uses the layout may set a bit meanwhile, and so may this one: the cluster acts on one reading, the first
+    // CTA's, once it meets.  Until then nothing is written, and whatever a layout with a status holds is checked like any other.
+    __shared__ int s_status;
+    const int status = load_status(a.status);
     if (rows.end <= rows.first) {
-        if (a.copy) copy_rows(a);
+        if (a.copy && status == 0) copy_rows(a);
         return;
     }
     const int g = rows.g, cells = (rows.end - rows.first) * kR;
@@ -196,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
         const int j = rows.first + c + 8 * i;
         at[i] = j >= rows.end ? -1 : !a.by_token ? j : tile < a.tiles ? token[i] : a.src_info[2 * (size_t)j];
         if (a.by_token && at[i] >= a.T) {
-            bounds_fail(a.status);
+            if (status == 0) bounds_fail(a.status);
             at[i] = -1;
         }
     }
@@ -237,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
         *reinterpret_cast<float2 *>(p) = make_float2(acc[j][0], acc[j][1]);
         if (cells > 8 * kR) *reinterpret_cast<float2 *>(p + 8 * kR) = make_float2(acc[j][2], acc[j][3]);
     }
+    if (tid == 0) s_status = status;
     __syncthreads();
     for (int i = tid; i < cells; i += kThreads) {            // (rows without a token stay undefined, and go into no other)
         float v = 0.0f;
@@ -244,8 +243,10 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
         for (int w = 0; w < kWarps; ++w) v += s_part[w * kCells + i];
         s_mine[i] = v;
     }
+    int one_status = s_status;
     if (a.C > 1) {
         cluster_sync_all();
+        one_status = ld_cluster_s32(at_rank(smem_u32(&s_status), 0));
         for (int i = tid; i < cells; i += kThreads) {
             float u[kMaxCluster], v = 0.0f;                  // loads on their way together: each takes some 700 cycles
 #pragma unroll
@@ -256,6 +257,10 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
                 if (k < a.C) v += u[k];
             s_all[i] = v;
         }
+    }
+    if (one_status) {
+        if (a.C > 1) cluster_sync_all();                     // (read everywhere)
+        return;
     }
     __syncthreads();
     if constexpr (std::is_same_v<T, __half>) {           // a power of two per row keeps the sums in fp16's range
@@ -359,27 +364,19 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
     pdl_begin_if(one_wave);
     const int tile = blockIdx.x / a.C, rank = blockIdx.x % a.C;
     const Rows rows(a, tile);
-    if constexpr (kBoundsCheck) {
-        __shared__ int s_status;
-        if (tid == 0) s_status = load_status(a.status);
-        cluster_sync_all();
-        int st;
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(st) : "r"(at_rank(smem_u32(&s_status), 0)) : "memory");
-        cluster_sync_all();
-        if (st) return;
-    } else if (load_status(a.status)) {
-        return;
-    }
+    __shared__ int s_status;                                 // as above
+    const int status = load_status(a.status);
     if (rows.end <= rows.first) {
-        if (a.copy) copy_rows(a);
+        if (a.copy && status == 0) copy_rows(a);
         return;
     }
+    if (tid == 0) s_status = status;
     const int g = rows.g;
     if (tid < kTileRows) {
         const int row = rows.first + tid;
         int at = row < rows.end ? (a.by_token ? a.src_info[2 * (size_t)row] : row) : -1;
         if (a.by_token && at >= a.T) {
-            bounds_fail(a.status);
+            if (status == 0) bounds_fail(a.status);
             at = -1;
         }
         s_at[tid] = at;
@@ -452,7 +449,7 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         }
     } else {
         for (int i = 0; i < kRing - 1 && i < stages1; ++i) fill_first(i, i);
-        if (a.copy) copy_rows(a);                            // while they are on their way
+        if (a.copy && s_status == 0) copy_rows(a);           // while they are on their way
         for (int i = 0; i < stages1; ++i) {
             if (i > 0) wait(s_done[ring_slot(i - 1)], ring_phase(i - 1));        // the products of stage i - 1 have read its slot
             if (i + kRing - 1 < stages1) fill_first(i + kRing - 1, ring_slot(i + kRing - 1));
@@ -478,6 +475,13 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         for (int j = 0; j < 8; ++j) *reinterpret_cast<float4 *>(mine + k0 + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     }
     cluster_sync_all();                                      // (a barrier of the CTA where it is alone)
+    if (ld_cluster_s32(at_rank(smem_u32(&s_status), 0))) {
+        tc_fence_before();
+        cluster_sync_all();                                  // (read everywhere)
+        tc_fence_after();
+        if (warp == 4) tmem_free<1>(tmem, kTmem);
+        return;
+    }
     // Every CTA adds up its share of the rows and hands them to all.  8 * RB lanes side by side read a row side by side (16-byte
     // reads of 32 different rows took 60,000 cycles for what takes a few thousand so), 8 columns each.
     const int share = (kTileRows + a.C - 1) / a.C, last = min(kTileRows, (rank + 1) * share);

@@ -79,6 +79,7 @@ typedef enum {
 /*
  * Set by ep_expert_linear, ep_expert_linear_bwd and ep_lora_add when a wait between the warps of their
  * kernel has lasted two seconds, which means a fault in the kernel: it ends then, its outputs incomplete.
+ * Calls that use the layout on other streams meanwhile act on the word as each of their CTAs reads it.
  */
 #define EP_STATUS_TIMEOUT   16
 
