@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
     const uint32_t tmem = s_tmem, ring = smem_u32(smem), low = ring + kRing * S::kStage;
     const bool f16 = std::is_same_v<T, __half>;
     const int n1 = (a.r + 15) & ~15;                         // r in steps of the tensor cores
-    bool ok = true;                                          // false: a wait ran out, and no other is begun
+    bool ok = true;                                          // false: a wait ran out, and the warp does no more of the loop it is in, nor of the next
     // This thread copies a 16-byte piece of rows tid / 8 + 32 i of both tiles.
     const int piece = tid & 7, r0 = (tid & (kThreads - 1)) >> 3;
     const uint32_t to = swizzled(r0, piece);
@@ -429,14 +429,15 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
     // ---- A x: every CTA sums its stages of H.  Barriers' phases count on through both parts.
     const int first2 = (a.N + 63) / 64 * rank / a.C, stages1 = (a.H + 63) / 64 * (rank + 1) / a.C - first1, stages2 = (a.N + 63) / 64 * (rank + 1) / a.C - first2;
     auto wait = [&](uint64_t &bar, int phase) {
-        if (ok) ok = mbar_wait(smem_u32(&bar), phase & 1);
+        if (ok) ok = __all_sync(kFullMask, mbar_wait(smem_u32(&bar), phase & 1));
+        return ok;
     };
     const bool issuer = warp == kWarps;
     if (issuer) {
         const uint32_t id1 = mma_desc(f16, 128, n1, false, false);
         for (int i = 0; i < stages1; ++i) {
             const int slot = ring_slot(i);
-            wait(s_full[slot], ring_phase(i));
+            if (!wait(s_full[slot], ring_phase(i))) break;
             fence_proxy_async_smem();
             if (elect_one()) {
                 tc_fence_after();
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         for (int i = 0; i < kRing - 1 && i < stages1; ++i) fill_first(i, i);
         if (a.copy && s_status == 0) copy_rows(a);           // while they are on their way
         for (int i = 0; i < stages1; ++i) {
-            if (i > 0) wait(s_done[ring_slot(i - 1)], ring_phase(i - 1));        // the products of stage i - 1 have read its slot
+            if (i > 0 && !wait(s_done[ring_slot(i - 1)], ring_phase(i - 1))) break;      // the products of stage i - 1 have read its slot
             if (i + kRing - 1 < stages1) fill_first(i + kRing - 1, ring_slot(i + kRing - 1));
         }
         if (stages1 > 0) wait(s_done[ring_slot(stages1 - 1)], ring_phase(stages1 - 1));
@@ -555,11 +556,11 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
     tc_fence_after();
     if (issuer) {
         const uint32_t id2 = mma_desc(f16, 128, 64, false, false);
-        for (int i = 0; i < stages2; ++i) {
+        for (int i = 0; ok && i < stages2; ++i) {
             const int slot = ring_slot(i);
-            wait(s_full[slot], ring_phase(i, stages1));
+            if (!wait(s_full[slot], ring_phase(i, stages1))) break;
             // (twice 64 columns of sums: those of stage i - 2 have been read when its slot's successor is filled)
-            if (i >= 2) wait(s_free[ring_slot(i - 2)], ring_phase(i - 2));
+            if (i >= 2 && !wait(s_free[ring_slot(i - 2)], ring_phase(i - 2))) break;
             fence_proxy_async_smem();
             if (elect_one()) {
                 tc_fence_after();
@@ -574,13 +575,12 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
             __syncwarp();
         }
     } else {
-        for (int i = 0; i < kRing - 1 && i < stages2; ++i) fill_second(i, i);
-        for (int i = 0; i < stages2; ++i) {
+        for (int i = 0; ok && i < kRing - 1 && i < stages2; ++i) fill_second(i, i);
+        for (int i = 0; ok && i < stages2; ++i) {
             const int slot = ring_slot(i), col = (first2 + i) * 64;
-            if (i > 0) wait(s_free[ring_slot(i - 1)], ring_phase(i - 1));        // every warp has written stage i - 1
+            if (i > 0 && !wait(s_free[ring_slot(i - 1)], ring_phase(i - 1))) break;      // every warp has written stage i - 1
             if (i + kRing - 1 < stages2) fill_second(i + kRing - 1, ring_slot(i + kRing - 1));
-            wait(s_full[slot], ring_phase(i, stages1));
-            wait(s_done[slot], ring_phase(i, stages1));
+            if (!wait(s_full[slot], ring_phase(i, stages1)) || !wait(s_done[slot], ring_phase(i, stages1))) break;
             __syncwarp();
             tc_fence_after();
             uint8_t *const st = smem + slot * S::kStage;
@@ -613,7 +613,12 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
             if (lane == 0) mbar_arrive(at_rank(smem_u32(&s_free[slot]), cluster_rank()));
         }
     }
-    if (!ok) atomicOr(const_cast<int32_t *>(a.status), EP_STATUS_TIMEOUT);
+    if (!ok) {                                               // copies and products that are still on their way get the time to arrive
+        atomicOr(const_cast<int32_t *>(a.status), EP_STATUS_TIMEOUT);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        const unsigned long long t = global_ns();
+        while (global_ns() - t < 1000000ull) {}
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -1,6 +1,9 @@
 // Every order in which two copying warps, the issuing warp and the tensor cores can pass a ring's barriers, as the adapters' kernel for
-// many rows uses them in its two products.  argv: stages of the first product, of the second, and optionally "two" for a model with
-// two barriers for finished products, by the parity of the stage, in place of a slot's own.  Prints "ok" or what went wrong.
+// many rows uses them in its two products.  argv: stages of the first product, of the second, and optionally
+//   two          a model with two barriers for finished products, by the parity of the stage, in place of a slot's own
+//   lost N [on]  the products numbered N and later never finish: when nobody can go on, the waits run out.  Who waited leaves the loop and the
+//                next one ("on": goes on in it).
+// Prints "ok" or what went wrong.
 #include <algorithm>
 #include <array>
 #include <cstdio>
@@ -15,7 +18,8 @@
 using namespace ep;
 
 constexpr int kWarps = 2;
-bool two = false;
+bool two = false, on = false;
+int lost = 1 << 30;
 int stages[2];
 
 enum Kind { kFill, kWaitDone, kWaitFull, kWaitFree, kRead, kIssue, kSync };
@@ -60,8 +64,9 @@ void programs() {
     }
 }
 
-// Where each warp and the issuer are, and how many products have been finished; everything else follows from that.
-using State = std::array<int, kWarps + 2>;
+// Where each warp and the issuer are, how many products have been finished, and who has had a wait run out.
+using State = std::array<int, 2 * kWarps + 3>;
+constexpr int kFailed = kWarps + 2;
 
 int count(const std::vector<Op> &prog, int pc, Kind kind, int part, int stage_at_most, int (*key)(int), int k) {
     int n = 0;
@@ -113,7 +118,7 @@ std::string explore() {
         };
         for (int who = 0; who <= kWarps; ++who) {
             const std::vector<Op> &prog = who < kWarps ? copier : issuer;
-            if (s[who] == (int)prog.size()) continue;
+            if (s[who] == (int)prog.size() || (s[kFailed + who] && !on)) continue;       // it has left its loops: done, and at the barrier between
             all = false;
             const Op op = prog[s[who]];
             if (op.kind == kFill) {
@@ -132,7 +137,7 @@ std::string explore() {
                 go(who);
             } else if (op.kind == kSync) {
                 bool here = true;
-                for (int o = 0; o <= kWarps; ++o) here = here && s[o] >= 0 && passed(o < kWarps ? copier : issuer, s[o] + 1, {kSync, 0, 0});
+                for (int o = 0; o <= kWarps; ++o) here = here && (s[kFailed + o] || passed(o < kWarps ? copier : issuer, s[o] + 1, {kSync, 0, 0}));
                 if (here) go(who);
             } else {
                 const int r = wait(s, op);
@@ -142,8 +147,21 @@ std::string explore() {
         }
         int issued = 0;
         for (int i = 0; i < s[kWarps]; ++i) issued += issuer[i].kind == kIssue;
-        if (s[kWarps + 1] < issued) all = false, go(kWarps + 1);
-        if (!moved && !all) return "nobody can go on";
+        if (s[kWarps + 1] < std::min(issued, lost)) all = false, go(kWarps + 1);
+        if (!moved && !all) {
+            if (lost == 1 << 30) return "nobody can go on";
+            State t = s;
+            bool waits = false;
+            for (int who = 0; who <= kWarps; ++who) {
+                const std::vector<Op> &prog = who < kWarps ? copier : issuer;
+                if (s[who] == (int)prog.size() || (s[kFailed + who] && !on) || prog[s[who]].kind == kSync) continue;
+                waits = true;
+                t[kFailed + who] = 1;
+                if (on) ++t[who];
+            }
+            if (!waits) return "nobody can go on";
+            if (seen.insert(t).second) todo.push_back(t);
+        }
     }
     return "ok";
 }
@@ -152,6 +170,8 @@ int main(int argc, char **argv) {
     stages[0] = atoi(argv[1]);
     stages[1] = atoi(argv[2]);
     two = argc > 3 && !strcmp(argv[3], "two");
+    if (argc > 4 && !strcmp(argv[3], "lost")) lost = atoi(argv[4]);
+    on = argc > 5;
     programs();
     const std::string r = explore();
     printf("%s\n", r.c_str());

@@ -30,6 +30,15 @@ def test_the_model_finds_a_phase_that_is_passed_over(model):
     assert model(6, 3, "two") == "a wait sees the parity of another phase"
 
 
+@pytest.mark.parametrize("first,second", [(1, 1), (4, 3), (6, 6)])
+def test_a_wait_that_runs_out(model, first, second):
+    """Products that never finish: everyone comes to the end, and nobody fills a slot that they may still read.  Going on in the loop, as if
+    the wait had ended, would."""
+    for n in range(first + second + 1):
+        assert model(first, second, "lost", n) == "ok"
+    assert model(6, 6, "lost", 1, "on") == "a slot is filled before its products are done"
+
+
 def test_the_kernel_goes_by_the_ring(model):
     """The kernel's barriers and phases are the ones that the model goes through."""
     with open(os.path.join(ROOT, "combine_topk_ids_histogram_gb300", "csrc", "ep_lora.cu")) as f:
@@ -38,3 +47,5 @@ def test_the_kernel_goes_by_the_ring(model):
     for line in src.splitlines():
         if "wait(s_" in line or "tc_commit" in line:
             assert "slot" in line, line
+        if "wait(s_" in line and "if (stages1 > 0)" not in line:     # (the last one of the first product, behind its loop)
+            assert "break;" in line, line
