@@ -71,17 +71,34 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     return v;
 }
 
-// The power of two that brings a largest magnitude to [2^14, 2^15), in fp16's range: from its exponent (1 for 0, infinities and NaN).
+// The magnitude that counts for a row's scale: infinities are theirs whatever it is.
+__device__ __forceinline__ float finite_abs(float v) { return fabsf(v) <= FLT_MAX ? fabsf(v) : 0.0f; }
+// The power of two that brings a largest magnitude to [2^14, 2^15), in fp16's range: from its exponent (1 for 0).
 __device__ __forceinline__ float fp16_scale(float most) {
     const int e = (int)(__float_as_uint(most) >> 23) - 127;
-    return most > 0.0f && e < 128 ? __uint_as_float((uint32_t)(min(14 - e, 126) + 127) << 23) : 1.0f;
+    return most > 0.0f ? __uint_as_float((uint32_t)(min(14 - e, 126) + 127) << 23) : 1.0f;
 }
 
-// A sum v of A x as two 16-bit numbers, hi + lo: their products with B are exact in fp32, and v keeps 16 bits (bf16) or 22 (fp16).
+// Two values rounded towards zero.
+__device__ __forceinline__ uint32_t towards_zero(float v0, float v1, __nv_bfloat16) { return __byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x7632); }
+__device__ __forceinline__ uint32_t towards_zero(float v0, float v1, __half) {
+    uint32_t w;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(v1), "f"(v0));
+    return w;
+}
+// v as two 16-bit numbers: its products with B are exact in fp32, and it keeps 16 bits (bf16) or 22 (fp16).  hi is rounded towards zero, which
+// no finite value leaves, and both have the sign of v and are no zeros unless it is one (the smallest number, 2^-133 or 2^-24, stands
+// in), so that infinities of v and of B give what they give with v itself: their parts' products never cancel or vanish.
 template <typename T> __device__ __forceinline__ void split2(float v0, float v1, uint32_t &hi, uint32_t &lo) {
-    hi = f32_to_word(v0, v1, T());
+    hi = towards_zero(v0, v1, T());
     const float2 h = word_to_f32(hi, T());
     lo = f32_to_word(v0 - h.x, v1 - h.y, T());
+    const uint32_t least = (v0 != 0.0f ? __float_as_uint(v0) >> 31 << 15 | 1u : 0u) | (v1 != 0.0f ? __float_as_uint(v1) >> 31 << 31 | 0x10000u : 0u);
+    const bool inf0 = fabsf(v0) > FLT_MAX, inf1 = fabsf(v1) > FLT_MAX;   // (not NaN, which stays one in lo)
+    if ((hi & 0x7fffu) == 0) hi |= least & 0xffffu;
+    if ((hi & 0x7fff0000u) == 0) hi |= least & 0xffff0000u;
+    if ((lo & 0x7fffu) == 0 || inf0) lo = (lo & 0xffff0000u) | (least & 0xffffu);
+    if ((lo & 0x7fff0000u) == 0 || inf1) lo = (lo & 0xffffu) | (least & 0xffff0000u);
 }
 
 // The rows of a cluster, all of one adapter: of tile t those from its first row to the end of that row's adapter, and of tile
@@ -241,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += s_part[w * kCells + i];
-        s_mine[i] = v;
+        s_mine[i] = (i & (kR - 1)) < a.r ? v : 0.0f;         // (an infinite x times the zeros behind A's rows is NaN)
     }
     int one_status = s_status;
     if (a.C > 1) {
@@ -266,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     if constexpr (std::is_same_v<T, __half>) {           // a power of two per row keeps the sums in fp16's range
         for (int i = warp; i * kR < cells; i += kWarps) {
             float v = 0.0f;
-            for (int k = lane; k < kR; k += 32) v = fmaxf(v, fabsf(s_all[i * kR + k]));
+            for (int k = lane; k < kR; k += 32) v = fmaxf(v, finite_abs(s_all[i * kR + k]));
             v = warp_max(v);
             if (lane == 0) s_scale[i] = fp16_scale(v);
         }
@@ -490,7 +507,7 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         const int r = rank * share + i / (8 * RB), k = i % (8 * RB);
         const uint32_t from = smem_u32(reinterpret_cast<float *>(smem) + r * S::kPitch + 8 * k);
         float t[8] = {};
-        if (8 * k < n1)
+        if (8 * k < a.r)                                     // (an infinite x times the zeros behind A's rows is NaN)
             for (int o = 0; o < a.C; o += 4) {               // loads on their way together: each takes some 700 cycles
                 float4 u[4][2];
 #pragma unroll
@@ -510,7 +527,7 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         if (f16) {
             float most = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(t[j]));
+            for (int j = 0; j < 8; ++j) most = fmaxf(most, finite_abs(t[j]));
             const uint32_t mates = (RB == 1 ? 0xffu : 0xffffu) << (lane & ~(8 * RB - 1));
 #pragma unroll
             for (int o = 4 * RB; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(mates, most, o));

@@ -587,8 +587,10 @@ int ep_expert_linear_bwd(const void *grad, long long grad_stride, const void *x,
  *              same stride: added in place, rows without an adapter untouched), and overlaps nothing else.
  *   dtype      EP_BF16 or EP_F16, of y, x, a, b and out.
  * Both sums are fp32.  a[g] x goes into the second one as the sum of two 16-bit numbers (16 bits of it
- * with EP_BF16, 22 with EP_F16); out is rounded once.  Nothing is written while the layout's status word is
- * non-zero.  No workspace, no atomics: the same call gives the same bits.
+ * with EP_BF16, 22 with EP_F16); out is rounded once.  Infinities in x, a and b give what the formula
+ * gives: infinities, and NaN with a zero or with one of the other sign in the same sum.  Nothing is
+ * written while the layout's status word is non-zero.  No workspace, no atomics: the same call gives the
+ * same bits.
  */
 int ep_lora_add(const void *y, long long y_stride, const void *x, long long x_stride, const void *a,
                 const void *b, const float *scale, int in_features, int out_features, int rank,
