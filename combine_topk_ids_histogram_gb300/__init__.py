@@ -236,6 +236,7 @@ class Layout:
             raise EPError(EP_ERR_INVALID_ARG, "layout sizes")
         self.workspace = torch.zeros(nb, dtype=torch.uint8, device=dev)
         self.capacity = T
+        self.device_index = self.status.get_device()
         self.matvec_bytes = {}                   # H -> expert_matvec_workspace_bytes
         self.c = _Layout(
             row_offsets=self.row_offsets.data_ptr(), expert_ids=self.expert_ids.data_ptr(),
@@ -816,6 +817,11 @@ def _dense(t: torch.Tensor, shape: tuple, dtypes, dev: int, what: str) -> int:
     return t.data_ptr()
 
 
+def _layout_on(L: Layout, dev: int):
+    if L.device_index != dev:
+        raise ValueError(f"layout: on {L.status.device}, but the current device is cuda:{dev}")
+
+
 def _of_layout(rows: int, L: Layout, what: str):
     if rows < L.R_max:
         raise ValueError(f"{what}: needs at least {L.R_max} rows, got {rows}")
@@ -842,6 +848,7 @@ def expert_linear(x: torch.Tensor, w: torch.Tensor, L: Layout, swiglu: bool = Fa
     out [R_max, N].  With ``swiglu`` w holds N/2 gate rows, then N/2 up rows, and out [R_max, N/2] is silu(gate) * up; with
     ``save`` too the call returns (out, gate_up [R_max, N]) for ``expert_linear_bwd``.  ``out``: the buffer, or both."""
     dev = torch.cuda.current_device()
+    _layout_on(L, dev)
     shape = _three(w, L.G, "w")
     N, K = shape[1], shape[2]
     dt = w.dtype
@@ -869,6 +876,7 @@ def expert_linear_bwd(grad: torch.Tensor, x: torch.Tensor | None, w: torch.Tenso
     grad_w is in w's dtype or ``grad_w_dtype`` = torch.float32, and with ``accumulate`` (fp32, with ``out``) it is added to what
     is there.  ``out``: the two buffers."""
     dev = torch.cuda.current_device()
+    _layout_on(L, dev)
     shape = _three(w, L.G, "w")
     N, K = shape[1], shape[2]
     dt = w.dtype
@@ -914,6 +922,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     ``by_token`` y, x and out are in the layout's row order [R_max, *], for any layout (adapters of experts).  ``out`` may be
     y, which is then added to in place."""
     dev = torch.cuda.current_device()
+    _layout_on(L, dev)
     G, dt = L.G, a.dtype
     shape = _three(a, G, "a")
     r, H, N = shape[1], shape[2], _three(b, G, "b")[1]
