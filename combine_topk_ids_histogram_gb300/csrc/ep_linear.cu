@@ -207,51 +207,45 @@ struct Sigmoid {
     }
 };
 
-// Into a stage in shared memory.
-struct Load {
-    uint32_t stage, bar;
-    template <int DIMS> __device__ void operator()(int at, const CUtensorMap &m, const int (&c)[DIMS]) const { tma_load<DIMS>(stage + at, &m, c, bar); }
-};
-
-// The copies of block b of a tile, whose m and n begin at these for the CTA.  One for an operand where its map allows it: each takes
-// the issuing thread some 50 cycles of the 512 that the products of a block last.
+// The copies of block b of a tile, whose m and n begin at these for the CTA, into a stage.  One for an operand where its map allows it: each
+// takes the issuing thread some 50 cycles of the 512 that the products of a block last.
 template <Form FORM> struct Copies {
     const CUtensorMap &map_a, &map_b, &map_c;
     const LinearArgs &a;
-    template <typename To> __device__ __forceinline__ void block(const Work &w, int b, int m, int n, int half, const To &to, bool take_a, bool take_b) const {
+    uint32_t stage, bar;
+    template <int DIMS> __device__ __forceinline__ void load(int at, const CUtensorMap &m, const int (&c)[DIMS]) const {
+        tma_load<DIMS>(stage + at, &m, c, bar);
+    }
+    __device__ __forceinline__ void block(const Work &w, int b, int m, int n, int half) const {
         const int k = b * kBlockK;
-        if (take_a) {
-            if constexpr (FORM == kGradW) {
-                if (a.whole_a) {
-                    to(0, map_a, {0, w.row + k, m >> 6});
-                } else {
-                    to(0, map_a, {m, w.row + k});
-                    to(8192, map_a, {m + 64, w.row + k});
-                }
-            } else if constexpr (FORM == kPlain) {
-                to(0, map_a, {k, m, w.g});
-            } else if constexpr (FORM == kGlu) {
-                to(0, map_a, {k, 0, 0, m >> 4, w.g});
-            } else if (a.whole_a) {
-                to(0, map_a, {0, k, m >> 6, w.g});
+        if constexpr (FORM == kGradW) {
+            if (a.whole_a) {
+                load(0, map_a, {0, w.row + k, m >> 6});
             } else {
-                to(0, map_a, {m, k, w.g});
-                to(8192, map_a, {m + 64, k, w.g});
+                load(0, map_a, {m, w.row + k});
+                load(8192, map_a, {m + 64, w.row + k});
             }
+        } else if constexpr (FORM == kPlain) {
+            load(0, map_a, {k, m, w.g});
+        } else if constexpr (FORM == kGlu) {
+            load(0, map_a, {k, 0, 0, m >> 4, w.g});
+        } else if (a.whole_a) {
+            load(0, map_a, {0, k, m >> 6, w.g});
+        } else {
+            load(0, map_a, {m, k, w.g});
+            load(8192, map_a, {m + 64, k, w.g});
         }
-        if (take_b) {
-            if constexpr (FORM == kGradW) {
-                if (a.whole_b) {
-                    to(kTileA, map_b, {0, w.row + k, n >> 6});
-                } else {
-                    to(kTileA, map_b, {n, w.row + k});
-                    to(kTileA + 8192, map_b, {n + 64, w.row + k});
-                }
-            } else if (half > 96) {
-                to(kTileA, map_b, {k, n});
+        if constexpr (FORM == kGradW) {
+            if (a.whole_b) {
+                load(kTileA, map_b, {0, w.row + k, n >> 6});
             } else {
-                for (int i = 0; i < half; i += 32) to(kTileA + i * 128, map_c, {k, n + i});
+                load(kTileA, map_b, {n, w.row + k});
+                load(kTileA + 8192, map_b, {n + 64, w.row + k});
             }
+        } else if (half > 96) {
+            load(kTileA, map_b, {k, n});
+        } else {
+            for (int i = 0; i < half; i += 32) load(kTileA + i * 128, map_c, {k, n + i});
         }
     }
 };
@@ -607,7 +601,7 @@ ep_linear_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
                             const bool clear = FORM == kGradW && b == w.kb - 1 && (w.last & 15) != 0;
                             const uint32_t bar = clear ? smem_u32(&c.landed[s]) : at_rank(smem_u32(&c.full[s]), 0);
                             mbar_arrive_expect(clear ? at_rank(bar, rank) : bar, bytes);
-                            Copies<FORM>{map_a, map_b, map_c, a}.block(w, b, m, n, half, Load{smem_u32(smem + s * kStageBytes), bar}, true, true);
+                            Copies<FORM>{map_a, map_b, map_c, a, smem_u32(smem + s * kStageBytes), bar}.block(w, b, m, n, half);
                             if (++s == kStages) s = 0, ++round;
                             used = min(used + 1, kStages);
                         }

@@ -707,7 +707,6 @@ extern "C" int ep_lora_add(const void *y, long long y_stride, const void *x, lon
     p.H = H; p.N = N; p.r = rank; p.T = L->T; p.G = L->E + L->fused_shared; p.R_max = layout_rows(L); p.by_token = by_token;
     p.row_offsets = L->row_offsets; p.expert_ids = L->expert_ids; p.src_info = L->src_info; p.row_of = L->row_of; p.status = L->status;
     p.out = (uint16_t *)out;
-    if (p.R_max == 0) p.R_max = 1;
     // a tile's rows: about as many as an adapter has; then as many CTAs to a tile as two to an SM allow
     const long long all = rows_max(L->T, L->K, L->fused_shared), per = all / p.G;
     const int sms = std::max(device_sm_count(), 1);
