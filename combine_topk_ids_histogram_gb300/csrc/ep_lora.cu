@@ -86,13 +86,25 @@ __device__ __forceinline__ uint32_t towards_zero(float v0, float v1, __half) {
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(v1), "f"(v0));
     return w;
 }
+// The smaller magnitude, NaN if one is.
+__device__ __forceinline__ float least_abs(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
 // v as two 16-bit numbers: its products with B are exact in fp32, and it keeps 16 bits (bf16) or 22 (fp16).  hi is rounded towards zero, which
 // no finite value leaves, and both have the sign of v and are no zeros unless it is one (the smallest number, 2^-133 or 2^-24, stands
 // in), so that infinities of v and of B give what they give with v itself: their parts' products never cancel or vanish.
-template <typename T> __device__ __forceinline__ void split2(float v0, float v1, uint32_t &hi, uint32_t &lo) {
+// False: a zero, an infinity or NaN may be among them, and amend2 has to follow.
+template <typename T> __device__ __forceinline__ bool split2(float v0, float v1, uint32_t &hi, uint32_t &lo) {
+    constexpr float kLeast = std::is_same_v<T, __half> ? 0x1p-24f : 0x1p-133f;
     hi = towards_zero(v0, v1, T());
     const float2 h = word_to_f32(hi, T());
-    lo = f32_to_word(v0 - h.x, v1 - h.y, T());
+    const float d0 = v0 - h.x, d1 = v1 - h.y;
+    lo = f32_to_word(d0, d1, T());
+    return least_abs(d0, d1) >= kLeast;
+}
+__device__ __forceinline__ void amend2(float v0, float v1, uint32_t &hi, uint32_t &lo) {
     const uint32_t least = (v0 != 0.0f ? __float_as_uint(v0) >> 31 << 15 | 1u : 0u) | (v1 != 0.0f ? __float_as_uint(v1) >> 31 << 31 | 0x10000u : 0u);
     const bool inf0 = fabsf(v0) > FLT_MAX, inf1 = fabsf(v1) > FLT_MAX;   // (not NaN, which stays one in lo)
     if ((hi & 0x7fffu) == 0) hi |= least & 0xffffu;
@@ -292,21 +304,30 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     constexpr int kK = RN / 2;                       // steps of 16 of the second product
     uint32_t hi[kK][4], lo[kK][4];
     float back[2];                                           // adapter's scale, over the row's
+    bool plain = true;
+    auto each = [&](auto &&with) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int j = c + 8 * i;
-        float f = 1.0f;
-        if constexpr (std::is_same_v<T, __half>) f = s_scale[j];
-        back[i] = scale / f;
+        for (int i = 0; i < 2; ++i) {
+            const int j = min(c + 8 * i, rows.end - rows.first - 1);     // (a lane without a row takes the last one's)
+            float f = 1.0f;
+            if constexpr (std::is_same_v<T, __half>) f = s_scale[j];
+            back[i] = scale / f;
 #pragma unroll
-        for (int s = 0; s < kK; ++s)
+            for (int s = 0; s < kK; ++s)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = RN == 2 ? 4 * q + 2 * h : s / 2 * 32 + 8 * q + s % 2 * 4 + 2 * h;
-                const float2 v = *reinterpret_cast<const float2 *>(s_all + j * kR + k);
-                split2<T>(v.x * f, v.y * f, hi[s][i + 2 * h], lo[s][i + 2 * h]);
-            }
-    }
+                for (int h = 0; h < 2; ++h) {
+                    const int k = RN == 2 ? 4 * q + 2 * h : s / 2 * 32 + 8 * q + s % 2 * 4 + 2 * h;
+                    const float2 v = *reinterpret_cast<const float2 *>(s_all + j * kR + k);
+                    with(v.x * f, v.y * f, hi[s][i + 2 * h], lo[s][i + 2 * h]);
+                }
+        }
+    };
+    each([&](float v0, float v1, uint32_t &x, uint32_t &y) {
+        const bool p = split2<T>(v0, v1, x, y);
+        if constexpr (RN <= 8) plain &= p;
+        else if (!p) amend2(v0, v1, x, y);                   // (registers for both passes are not left)
+    });
+    if (!plain) each([&](float v0, float v1, uint32_t &x, uint32_t &y) { amend2(v0, v1, x, y); });
     for (int n0 = part * 32; n0 < a.N; n0 += parts * 32) {
         Block<RN> now;
         if (kAhead && n0 == part * 32) now = ahead;
@@ -535,7 +556,8 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         }
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) split2<T>(t[2 * j] * f, t[2 * j + 1] * f, hi[j], lo[j]);
+        for (int j = 0; j < 4; ++j)
+            if (!split2<T>(t[2 * j] * f, t[2 * j + 1] * f, hi[j], lo[j])) amend2(t[2 * j] * f, t[2 * j + 1] * f, hi[j], lo[j]);
         const uint32_t to_op = low + (k >> 3) * kTileRows * 128 + swizzled(r, k & 7), to_f = smem_u32(s_scale + r);
         for (int o = 0; o < a.C; ++o) {
             st_cluster_x4(at_rank(to_op, o), hi);
