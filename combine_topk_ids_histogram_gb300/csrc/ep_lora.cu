@@ -29,6 +29,9 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxRank = 128;
 constexpr int kMaxCluster = 8;
+// The tensor cores' adder truncates, to one side: sums of A x leave it after so many products and go on in fp32, rounded to nearest.
+// (Of 32768 products of one sign 2e-4 would be lost.  The second product has 128 at most.)
+constexpr int kLongest = 512;
 
 struct LoraArgs {
     const uint16_t *y, *x, *a, *b;
@@ -231,7 +234,28 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     if (kAhead) ahead.load(a, g, part * 32, at, c, q);
     float acc[RN][4] = {};
     const uint4 zero = make_uint4(0, 0, 0, 0);
+    // The warp's sums so far, to the thread's own places in shared memory.
+    auto put = [&](bool first) {
+#pragma unroll
+        for (int j = 0; j < RN; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (i == 1 && cells <= 8 * kR) break;
+                float2 *const p = reinterpret_cast<float2 *>(s_part + warp * kCells + (c + 8 * i) * kR + 8 * j + 2 * q);
+                float2 v = make_float2(acc[j][2 * i], acc[j][2 * i + 1]);
+                if (!first) v = make_float2(p->x + v.x, p->y + v.y);
+                *p = v;
+                acc[j][2 * i] = acc[j][2 * i + 1] = 0.0f;
+            }
+    };
+    int until = kLongest / (kSteps * 32);                    // turns until the sums leave the tensor cores
+    bool first = true;
     for (int k0 = part * kSteps * 32; k0 < a.H; k0 += parts * kSteps * 32) {
+        if (until-- == 0) {
+            put(first);
+            first = false;
+            until = kLongest / (kSteps * 32) - 1;
+        }
         uint4 xv[kSteps][2];
 #pragma unroll
         for (int u = 0; u < kSteps; ++u)
@@ -258,12 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
             }
         }
     }
-#pragma unroll
-    for (int j = 0; j < RN; ++j) {
-        float *const p = s_part + warp * kCells + c * kR + 8 * j + 2 * q;
-        *reinterpret_cast<float2 *>(p) = make_float2(acc[j][0], acc[j][1]);
-        if (cells > 8 * kR) *reinterpret_cast<float2 *>(p + 8 * kR) = make_float2(acc[j][2], acc[j][3]);
-    }
+    put(first);
     if (tid == 0) s_status = status;
     __syncthreads();
     for (int i = tid; i < cells; i += kThreads) {            // (rows without a token stay undefined, and go into no other)
@@ -389,12 +408,12 @@ template <int RB> struct TileSmem {
 // Eight warps copy, add up and write; the ninth waits for what they copied and issues the products.  It fences as well: the
 // fence between copies and tensor cores waits for all copies of the thread that issues it, those of later stages too.
 template <typename T, int RB>
-__global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraArgs a, int one_wave) {
+__global__ void __launch_bounds__(kTileThreads, RB == 1 ? 2 : 1) ep_lora_tile_kernel(const LoraArgs a, int one_wave) {
     using S = TileSmem<RB>;
-    constexpr uint32_t kTmem = 128;                          // columns: the sums of A x, then of 64 outputs
+    constexpr uint32_t kTmem = 128 * RB;                     // columns: twice the sums of A x, then of 64 outputs
     extern __shared__ __align__(16) uint8_t s_raw[];
     uint8_t *const smem = s_raw + (1024 - (smem_u32(s_raw) & 1023)) % 1024;
-    __shared__ __align__(8) uint64_t s_full[kRing], s_free[kRing], s_done[kRing];
+    __shared__ __align__(8) uint64_t s_full[kRing], s_free[kRing], s_done[kRing], s_taken[2];
     __shared__ uint32_t s_tmem;
     __shared__ float s_scale[kTileRows];
     __shared__ int s_at[kTileRows];
@@ -426,6 +445,7 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
             mbar_init(smem_u32(&s_free[i]), kWarps);
             mbar_init(smem_u32(&s_done[i]), 1);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&s_taken[i]), kWarps);
         mbar_init_done();
     }
     tc_fence_before();
@@ -471,17 +491,39 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         return ok;
     };
     const bool issuer = warp == kWarps;
+    // Sums: rows q * 32 + lane, 32 * RB columns.  They leave tensor memory after every chunk of stages.
+    const int q = warp & 3, half = (warp >> 2) & 1, row = q * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    float total[RB][32] = {};
+    auto take = [&](int chunk) {
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            const int k0 = (half * RB + b) * 32;
+            if (k0 >= n1) continue;
+            float v[32];
+            tmem_ld32(lanes + chunk_buffer(chunk) * 64 * RB + k0, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) total[b][j] += v[j];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(at_rank(smem_u32(&s_taken[chunk_buffer(chunk)]), cluster_rank()));
+    };
     if (issuer) {
         const uint32_t id1 = mma_desc(f16, 128, n1, false, false);
         for (int i = 0; i < stages1; ++i) {
             const int slot = ring_slot(i);
             if (!wait(s_full[slot], ring_phase(i))) break;
+            const int chunk = stage_chunk(i);
+            if (chunk_begins(i) && chunk >= 2 && !wait(s_taken[chunk_buffer(chunk)], chunk_phase(chunk - 2))) break;
             fence_proxy_async_smem();
             if (elect_one()) {
                 tc_fence_after();
                 const uint64_t da = smem_desc(ring + slot * S::kStage, 0), db = smem_desc(ring + slot * S::kStage + S::kLeft, 0);
                 const int steps = min(4, (a.H - (first1 + i) * 64 + 15) / 16);
-                for (int k = 0; k < steps; ++k) tc_mma<1>(tmem, da + 2 * k, db + 2 * k, id1, i > 0 || k > 0);
+                for (int k = 0; k < steps; ++k) tc_mma<1>(tmem + chunk_buffer(chunk) * 64 * RB, da + 2 * k, db + 2 * k, id1, !chunk_begins(i) || k > 0);
                 tc_commit<1>(smem_u32(&s_done[slot]));
             }
             __syncwarp();
@@ -492,24 +534,18 @@ __global__ void __launch_bounds__(kTileThreads) ep_lora_tile_kernel(const LoraAr
         for (int i = 0; i < stages1; ++i) {
             if (i > 0 && !wait(s_done[ring_slot(i - 1)], ring_phase(i - 1))) break;      // the products of stage i - 1 have read its slot
             if (i + kRing - 1 < stages1) fill_first(i + kRing - 1, ring_slot(i + kRing - 1));
+            if (i > 0 && chunk_begins(i)) take(stage_chunk(i - 1));
         }
-        if (stages1 > 0) wait(s_done[ring_slot(stages1 - 1)], ring_phase(stages1 - 1));
+        if (stages1 > 0 && wait(s_done[ring_slot(stages1 - 1)], ring_phase(stages1 - 1))) take(stage_chunk(stages1 - 1));
     }
-    tc_fence_after();
     __syncthreads();
     // ---- the cluster's sums, as 16-bit operand
-    const int q = warp & 3, half = (warp >> 2) & 1, row = q * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     float *const mine = reinterpret_cast<float *>(smem) + row * S::kPitch;
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
         const int k0 = (half * RB + b) * 32;
         if (issuer || k0 >= n1) continue;
-        float v[32] = {};
-        if (stages1 > 0) {
-            tmem_ld32(lanes + k0, v);
-            tmem_wait_ld();
-        }
+        const float(&v)[32] = total[b];
 #pragma unroll
         for (int j = 0; j < 8; ++j) *reinterpret_cast<float4 *>(mine + k0 + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     }

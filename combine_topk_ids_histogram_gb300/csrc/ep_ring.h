@@ -19,4 +19,11 @@ EP_HOST_DEVICE constexpr int ring_slot(int stage) { return stage % kRing; }
 // Phases that such a barrier has ended before that of `stage`, where `before` stages of an earlier pass went through the ring.
 EP_HOST_DEVICE constexpr int ring_phase(int stage, int before = 0) { return (before - stage % kRing + kRing - 1) / kRing + stage / kRing; }
 
+// Sums over many stages leave the tensor cores after every chunk of them, from one of two buffers.
+constexpr int kChunkStages = 8;
+EP_HOST_DEVICE constexpr int stage_chunk(int stage) { return stage / kChunkStages; }
+EP_HOST_DEVICE constexpr bool chunk_begins(int stage) { return stage % kChunkStages == 0; }
+EP_HOST_DEVICE constexpr int chunk_buffer(int chunk) { return chunk & 1; }
+EP_HOST_DEVICE constexpr int chunk_phase(int chunk) { return chunk >> 1; }
+
 }  // namespace ep

@@ -22,7 +22,7 @@ bool two = false, on = false;
 int lost = 1 << 30;
 int stages[2];
 
-enum Kind { kFill, kWaitDone, kWaitFull, kWaitFree, kRead, kIssue, kSync };
+enum Kind { kFill, kWaitDone, kWaitFull, kWaitFree, kRead, kIssue, kTake, kWaitTaken, kSync };      // (the stage of the last but one: its chunk)
 struct Op {
     Kind kind;
     int part, stage;
@@ -41,8 +41,12 @@ void programs() {
     for (int i = 0; i < stages[0]; ++i) {
         if (i > 0) copier.push_back({kWaitDone, 0, i - 1});
         if (i + kRing - 1 < stages[0]) copier.push_back({kFill, 0, i + kRing - 1});
+        if (i > 0 && chunk_begins(i)) copier.push_back({kTake, 0, stage_chunk(i - 1)});
     }
-    if (stages[0] > 0) copier.push_back({kWaitDone, 0, stages[0] - 1});
+    if (stages[0] > 0) {
+        copier.push_back({kWaitDone, 0, stages[0] - 1});
+        copier.push_back({kTake, 0, stage_chunk(stages[0] - 1)});
+    }
     copier.push_back({kSync, 0, 0});
     for (int i = 0; i < kRing - 1 && i < stages[1]; ++i) copier.push_back({kFill, 1, i});
     for (int i = 0; i < stages[1]; ++i) {
@@ -54,6 +58,7 @@ void programs() {
     }
     for (int i = 0; i < stages[0]; ++i) {
         issuer.push_back({kWaitFull, 0, i});
+        if (chunk_begins(i) && stage_chunk(i) >= 2) issuer.push_back({kWaitTaken, 0, stage_chunk(i) - 2});
         issuer.push_back({kIssue, 0, i});
     }
     issuer.push_back({kSync, 0, 0});
@@ -88,14 +93,18 @@ int ended(const State &s, Kind kind, int bar) {          // phases that a barrie
         return n;
     }
     int least = 1 << 30;
+    if (kind == kWaitTaken) {
+        for (int w = 0; w < kWarps; ++w) least = std::min(least, count(copier, s[w], kTake, 1, 1 << 30, chunk_buffer, bar));
+        return least;
+    }
     for (int w = 0; w < kWarps; ++w) least = std::min(least, count(copier, s[w], kind == kWaitFull ? kFill : kRead, 1, 1 << 30, ring_slot, bar));
     return least;
 }
 
 // 1: may go on, 0: has to wait, -1: goes on or waits wrongly
 int wait(const State &s, const Op &op) {
-    const int bar = op.kind == kWaitDone ? done_bar(op.stage) : ring_slot(op.stage);
-    const int phase = op.kind == kWaitDone ? done_phase(op.part, op.stage) : op.kind == kWaitFull ? full_phase(op.part, op.stage) : ring_phase(op.stage);
+    const int bar = op.kind == kWaitDone ? done_bar(op.stage) : op.kind == kWaitTaken ? chunk_buffer(op.stage) : ring_slot(op.stage);
+    const int phase = op.kind == kWaitTaken ? chunk_phase(op.stage) : op.kind == kWaitDone ? done_phase(op.part, op.stage) : op.kind == kWaitFull ? full_phase(op.part, op.stage) : ring_phase(op.stage);
     const int n = ended(s, op.kind, bar);
     const bool sees = ((n ^ phase) & 1) != 0, is = n > phase;
     if (sees != is) return -1;
@@ -133,7 +142,14 @@ std::string explore() {
                             if (!passed(copier, s[w], {kRead, 1, op.stage - kRing})) return "a slot is filled before it has been read";
                 }
                 go(who);
-            } else if (op.kind == kRead || op.kind == kIssue) {
+            } else if (op.kind == kRead || op.kind == kIssue || op.kind == kTake) {
+                // a chunk's buffer has been read by everyone before the next but one begins in it, and is read before that
+                if (op.kind == kIssue && op.part == 0 && chunk_begins(op.stage) && stage_chunk(op.stage) >= 2)
+                    for (int w = 0; w < kWarps; ++w)
+                        if (!passed(copier, s[w], {kTake, 0, stage_chunk(op.stage) - 2})) return "a buffer of sums is written before it has been read";
+                if (op.kind == kIssue && op.part == 1 && stages[0] > 0)
+                    for (int w = 0; w < kWarps; ++w)
+                        if (!passed(copier, s[w], {kTake, 0, stage_chunk(stages[0] - 1)}) && !s[kFailed + w]) return "sums are written over before they have been read";
                 go(who);
             } else if (op.kind == kSync) {
                 bool here = true;

@@ -30,7 +30,12 @@ def test_the_model_finds_a_phase_that_is_passed_over(model):
     assert model(6, 3, "two") == "a wait sees the parity of another phase"
 
 
-@pytest.mark.parametrize("first,second", [(1, 1), (4, 3), (6, 6)])
+@pytest.mark.parametrize("first", [15, 16, 17, 24, 25, 33, 41])
+def test_chunks_of_sums(model, first):
+    assert model(first, 2) == "ok"
+
+
+@pytest.mark.parametrize("first,second", [(1, 1), (4, 3), (6, 6), (18, 2)])
 def test_a_wait_that_runs_out(model, first, second):
     """Products that never finish: everyone comes to the end, and nobody fills a slot that they may still read.  Going on in the loop, as if
     the wait had ended, would."""
@@ -43,9 +48,9 @@ def test_the_kernel_goes_by_the_ring(model):
     """The kernel's barriers and phases are the ones that the model goes through."""
     with open(os.path.join(ROOT, "combine_topk_ids_histogram_gb300", "csrc", "ep_lora.cu")) as f:
         src = f.read()
-    assert "s_full[kRing], s_free[kRing], s_done[kRing];" in src
+    assert "s_full[kRing], s_free[kRing], s_done[kRing], s_taken[2];" in src
     for line in src.splitlines():
         if "wait(s_" in line or "tc_commit" in line:
-            assert "slot" in line, line
-        if "wait(s_" in line and "if (stages1 > 0)" not in line:     # (the last one of the first product, behind its loop)
+            assert "slot" in line or "chunk_phase" in line, line
+        if "wait(s_" in line and "stages1 > 0" not in line:     # (the last one of the first product, behind its loop)
             assert "break;" in line, line
