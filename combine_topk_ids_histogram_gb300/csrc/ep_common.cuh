@@ -23,7 +23,9 @@ __device__ __forceinline__ void st_stream(void *p, uint4 v) { __stcs(reinterpret
 
 // Programmatic dependent launch.  Every kernel first waits (griddepcontrol.wait) until the
 // kernel before it in the stream has completed and its memory is visible, so it never reads
-// anything before all earlier work in the stream is done.
+// anything before all earlier work in the stream is done.  (One exception: the gradient of the
+// experts' weights behind that of their rows in the same call, which needs nothing of it.  The kernel in front
+// has waited before it lets this one begin, and this one waits before it ends.)
 //   pdl_begin: grids whose CTAs are all resident at once (persistent grids, the layout) then
 //              let the next kernel start launching, so its launch and ramp-up overlap this
 //              kernel's run.

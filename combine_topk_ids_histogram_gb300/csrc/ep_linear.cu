@@ -11,17 +11,18 @@
 // hundreds of rows or more, fill M.  A pair shares a product of 256 x 256: each CTA loads 128 of M and half of N by TMA, one copy for
 // an operand, and keeps the sums of its 128 of M in tensor memory, twice, so that one chunk's sums leave while the next one's are
 // added up.  Warp 0 loads, warp 1 of the first CTA issues the products, warp 3 looks tiles up ahead of the others, warps 4 to 11 take
-// results out, four at a time 32 columns; warp 2 (grad_w) clears the rows behind a group's last one in shared memory, since
+// results out, four at a time 32 columns, with registers that the others hand over; warp 2 (grad_w) clears the rows behind a group's last one in shared memory, since
 // there they are summed over.  No atomics: the order of every sum is fixed.
 //
-// 4864 rows of one group, 4096 -> 4096: 83 us, 1970 TFLOP/s (0.98 of the measured cuBLAS burst), and so the gated form and grad_x; K = 16384:
-// 332 us, where the power limit lowers the clock.  Many groups of few rows are bound by HBM (256 tokens, top-8 of 64 and a shared
-// expert, 7168 -> 2 x 2048 gated: 560 us, 6.7 TB/s), those between by the way from L2, which has to bring 32 KB for 512 cycles of
-// products at 256 rows and as much for half the work at 128, while outputs leave: 8192 tokens, top-8 of 128, 2048 -> 2 x 768
-// gated with gate and up saved 287 us (floor 205), its down product 148 (115), grad_x through the gate 181 (160), grad_w 180 (115).
-// Without its loads / its outputs the first of them took 207 / 276 us of 324 then; fetching the next tile's operands into L2
-// ahead (by TMA, in bulk, or by lines) gained nothing in grad_w and cost up to 150 % elsewhere, eviction hints changed nothing, and taking several groups at a time, less read
-// at the same moment by several pairs, cost 4 to 60 %.
+// 4864 rows of one group, 4096 -> 4096: 84 us, 1940 TFLOP/s (0.97 of the measured cuBLAS burst), and so the gated form and grad_x; K = 16384:
+// 332 to 340 us, where the power limit lowers the clock.  Many groups of few rows are bound by HBM (256 tokens, top-8 of 64 and a shared
+// expert, 7168 -> 2 x 2048 gated: 576 us, 6.7 TB/s), those between by the way from L2, which has to bring 32 KB for 512 cycles of
+// products at 256 rows and as much for half the work at 128, while outputs leave: 65536 rows, drawn log-normally over 128 groups, 2048 ->
+// 2 x 768 gated with gate and up saved 294 us (floor 205), the down product 148 (115), grad_x through the gate 200 (160), grad_w 178
+// (115), each kernel by itself on inputs that stay the same; calls on changing inputs take 342, 171 and, both gradients, 406.
+// Without its loads / its outputs the first of them took 207 / 276 us of 324 in an earlier form; fetching the next tile's operands into
+// L2 ahead (by TMA, in bulk, or by lines) gained nothing in grad_w and cost up to 150 % elsewhere, eviction hints changed nothing,
+// and taking several groups at a time, less read at the same moment by several pairs, cost 4 to 60 %.
 #include <limits.h>
 #include <math.h>
 
@@ -47,17 +48,18 @@ constexpr int kTileB = 128 * kBlockK * 2;
 constexpr int kStageBytes = kTileA + kTileB;
 constexpr int kCols = 256;                   // columns of tensor memory per tile's sums
 constexpr int kMaxGroups = kMaxE + 1;
-// As many stages as fit.  What they hide is the way from L2: with 3 / 4 / 5 of them the gated products of 8192 tokens, top-8 of 128,
-// 2048 -> 2 x 768 took 327 / 294 / 272 us, the down products 188 / 172 / 156.
+// As many stages as fit.  What they hide is the way from L2: in an earlier form, with 3 / 4 / 5 of them the gated products of 65536 rows
+// in 128 groups, 2048 -> 2 x 768 took 327 / 294 / 272 us, the down products 188 / 172 / 156.
 constexpr int kStages = 6;
 constexpr int kStaging = 16384;              // bytes in which a group of four warps turns its results into rows
 constexpr int kSuper = 8;                    // grad_w: tiles of N that go through all of K before the next
-// The tensor cores' adder truncates, by up to 2^-23 of the sum per 16 products, all to one side: sums leave them every 8 blocks, 512
-// products, and are added up in registers, rounded to nearest.  A sum of n normal products loses 4.7e-7 of its norm then, whatever n is, and
-// one of one sign 3e-6; sums that stayed for 32768 / 65536 products of one sign lost 2e-4 / 4e-4, visible in fp16.  With 256 products fp32
-// gradients of 8192 rows lost 2.3e-7 and took 1506 us (8 x 28672 x 4096) where they take 1320.  For rows the first two chunks are
-// longer, so that products get further ahead while a tile's results leave: 8192 tokens, top-8 of 128, 2048 -> 2 x 768 with gate and up kept
-// take 330 us with chunks of 8 blocks, 298 so, and 285 with sums that stay; grad_x through the gate 230, 200 and 182.
+// The tensor cores' adder cuts off what it adds, all to one side: terms of one sign lose 2^-22 of the running sum with every 16 products
+// (fp16; a third of that in bf16, whose products have fewer digits).  So sums leave them every 8 blocks, 512 products, and are added up in
+// registers, rounded to nearest.  Whatever the number of products, sums of normal ones lose 4.7e-7 of their norm then (fp16 6.5e-7) and of one
+// sign 9e-7 (2.8e-6); fp16 sums that stayed for 32768 / 65536 products lost 2e-4 / 4e-4, half an ulp and more.  With 256 products
+// bf16 lost 2.3e-7, and fp32 gradients of 8192 rows took 1506 us (8 x 28672 x 4096) where they take 1320.  For rows the first two chunks are
+// longer, so that products get further ahead while a tile's results leave: 65536 rows in 128 groups, 2048 -> 2 x 768 with gate and up kept
+// take 330 us with chunks of 8 blocks, 294 so, and 285 with sums that stay; grad_x through the gate 230, 200 and 182.
 constexpr int kChunk = 8, kFirstChunk = 12;
 
 // A tile: rows or features, and what is summed over.

@@ -9,9 +9,9 @@
 //               CTA's through shared memory, then the CTAs' through each other's, and split N for the second product,
 //               which takes y along.  The contraction may take its k in any order as long as both operands take the same one: a thread reads
 //               8 consecutive elements of a row, and the second product's columns are permuted so that a thread's sums are
-//               8 consecutive outputs.  One token, rank 16, 2048 -> 2048: 3.6 us; 64 tokens, 48 adapters of rank 32, 7168 -> 4096:
-//               9.2 us (floor 3.9).  Latency bounds it: the ids, A and x, the exchange, one after another.
-//   many rows   128, on tcgen05.  8192 tokens, 5 adapters of rank 64, 4096 -> 4096: 58 us (floor 29).  HBM bounds the second half
+//               8 consecutive outputs.  One token, rank 16, 2048 -> 2048: 3.7 us; 64 tokens, 48 adapters of rank 32, 7168 -> 4096:
+//               9.4 us (floor 3.9).  Latency bounds it: the ids, A and x, the exchange, one after another.
+//   many rows   128, on tcgen05.  8192 tokens, 5 adapters of rank 64, 4096 -> 4096: 57 us (floor 29).  HBM bounds the second half
 //               (5 TB/s), the copies' latency and the exchange of the sums between the CTAs the first.
 #include <stddef.h>
 
@@ -29,8 +29,8 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxRank = 128;
 constexpr int kMaxCluster = 8;
-// The tensor cores' adder truncates, to one side: sums of A x leave it after so many products and go on in fp32, rounded to nearest.
-// (Of 32768 products of one sign 2e-4 would be lost.  The second product has 128 at most.)
+// The tensor cores' adder cuts off what it adds, to one side: sums of A x leave it after so many products and go on in fp32, rounded to
+// nearest.  (Of 32768 fp16 products of one sign 2e-4 would be lost, of 512 3e-6.  The second product has 128 at most.)
 constexpr int kLongest = 512;
 
 struct LoraArgs {
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
 // The same for tiles of 128 rows on tcgen05, where the bytes of x, y and out are what counts.  The rows are M; both products stream
 // through a ring in shared memory that cp.async fills ahead: 64 columns of x with 64 of A (N is r), then 64 of y with 64 rows of B
 // (K is r).  The CTAs of a cluster split H, add up A x through each other's shared memory, and split N.  (With mma.sync from
-// shared memory its products took half of the time: 71 us with 8192 tokens, 5 adapters of rank 64, 4096 -> 4096, where this takes 58.)
+// shared memory its products took half of the time: 71 us with 8192 tokens, 5 adapters of rank 64, 4096 -> 4096, where this takes 57.)
 constexpr int kTileRows = 128, kTileThreads = kThreads + 32;           // the last warp issues the products
 
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void *gmem, bool valid) {
@@ -731,7 +731,7 @@ template <typename T> int launch_type(const LoraArgs &a, cudaStream_t st) {
 
 // Tiles of 128 rows begin slowly (19 us at least, of which their sums' way across the cluster is some) and then read A and B an
 // eighth as often as tiles of 16 rows, whose time is about 3.2e-7 us per 16 rows, column of x or y, and (r + 25).  The border is at 50 us
-// of that.  16 / 128 rows: 1024 tokens, 4 adapters of rank 16, 4096 -> 4096: 8.2 / 21 us; 2048, 16 of rank 64, 2048 -> 2048: 17 / 43;
+// of that.  16 / 128 rows, every token with an adapter, in a CUDA graph: 1024 tokens, 4 adapters of rank 16, 4096 -> 4096: 8.2 / 21 us; 2048, 16 of rank 64, 2048 -> 2048: 17 / 43;
 // 8192, 1 of rank 16, 4096 -> 4096: 55 / 47; 4096, 32 of rank 128: 91 / 74; 8192, 5 of rank 64: 119 / 54; 16384, 8 of rank 16,
 // 2048 -> 6144: 133 / 94.
 bool takes_tiles(long long rows, int H, int N, int rank) { return rows * (H + N) * (rank + 25) >= 2500000000ll; }

@@ -539,9 +539,9 @@ int ep_expert_matvec(const uint16_t *x, int x_by_token, const uint8_t *codes, co
  *              1: w holds N/2 gate rows, then N/2 up rows (N a multiple of 32), and out [R_max * N/2] is
  *              silu(gate) * up, silu(v) = v / (1 + exp(-v)).
  *   gate_up    with swiglu [R_max * N] or NULL: gate and up of every row, for the backward pass.
- * Sums are fp32 on the tensor cores, whose adder truncates (by up to 2^-23 of the sum every 16
- * products), and leave them every 512 products (the first two times 768) to be added up rounded to
- * nearest; every output is rounded once.  The rows [0, row_offsets[G]) are written; padding rows are
+ * Sums are fp32 on the tensor cores, whose adder truncates, and leave them every 512 products (the
+ * first two times 768) to be added up rounded to nearest: terms of one sign lose 1e-6 (EP_BF16) or 4e-6
+ * (EP_F16) of a sum, whatever its length.  Every output is rounded once.  The rows [0, row_offsets[G]) are written; padding rows are
  * rows like others, and zero where x is.  No row takes part in another's result, whatever it holds.
  * Nothing is written while the layout's status word is non-zero.  Outputs overlap no input.  No workspace,
  * no atomics: the same call gives the same bits.
@@ -560,8 +560,7 @@ int ep_expert_linear(const void *x, long long x_stride, const void *w, int in_fe
  *              d * up * s * (1 + gate * (1 - s)), and d * gate * s.
  *   -> grad_w  NULL, or [G * N * K] in grad_w_dtype (dtype or EP_F32): grad_w[g, n, k] = sum over the rows
  *              of g of grad[r, n] x[r, k]; zeros for a group without rows.  accumulate 1 (EP_F32 only)
- *              adds to what is there.  Its sums leave the tensor cores every 512 rows: terms of
- *              one sign lose at most 2^-18 there, and 2^-24 with each addition.
+ *              adds to what is there.  Its sums leave the tensor cores every 512 rows.
  * Rows as in the forward call; padding rows take part in grad_w, so x or grad has to be zero there (and
  * neither infinite nor NaN): ep_dispatch_bf16 and ep_combine_bwd write zeros.  Rows outside a group, or behind the last one, take no part
  * in its grad_w.  grad_x and grad_w may not both be NULL; w is not read without grad_x nor x without

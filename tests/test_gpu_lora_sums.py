@@ -1,6 +1,6 @@
-"""How exactly the adapters sum A x: the tensor cores' adder truncates, by up to 2^-23 of the running sum with every 16 products, so sums
-leave it after 512 of them and go on in fp32.  Terms of one sign then lose at most 32 * 2^-23 of a sum, and 2^-24 with each of its
-additions: those of the chunks, of eight warps and of eight CTAs.  A x keeps 16 bits (bf16) or 22 (fp16) on its way into the
+"""How exactly the adapters sum A x: the tensor cores' adder cuts off up to 2^-22 of the running sum with every 16 products of one sign, so
+sums leave it after 512 of them and go on in fp32.  The running sum is half of a chunk's on average: 32 * 2^-23 of a sum are lost, and 2^-24 with each of
+its additions: those of the chunks, of eight warps and of eight CTAs.  A x keeps 16 bits (bf16) or 22 (fp16) on its way into the
 second product, cut off, so a half of the last is lost on average; that product has at most 128 terms.  Roundings of the output average out to 6 * u / sqrt(3 M)
 over M outputs (six standard deviations of M roundings, each uniform within u)."""
 import pytest
