@@ -10,12 +10,13 @@
 //               which takes y along.  The contraction may take its k in any order as long as both operands take the same one: a thread reads
 //               8 consecutive elements of a row, and the second product's columns are permuted so that a thread's sums are
 //               8 consecutive outputs.  One token, rank 16, 2048 -> 2048: 3.7 us; 64 tokens, 48 adapters of rank 32, 7168 -> 4096:
-//               9.4 us (floor 3.9).  Latency bounds it: the ids, A and x, the exchange, one after another.
+//               9.5 us (floor 3.9).  Latency bounds it: the ids, A and x, the exchange, one after another.
 //   many rows   128, on tcgen05.  8192 tokens, 5 adapters of rank 64, 4096 -> 4096: 57 us (floor 29).  HBM bounds the second half
 //               (5 TB/s), the copies' latency and the exchange of the sums between the CTAs the first.
 #include <stddef.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ep_async.cuh"
 #include "ep_host.h"
@@ -82,38 +83,40 @@ __device__ __forceinline__ float fp16_scale(float most) {
     return most > 0.0f ? __uint_as_float((uint32_t)(min(14 - e, 126) + 127) << 23) : 1.0f;
 }
 
-// Two values rounded towards zero.
-__device__ __forceinline__ uint32_t towards_zero(float v0, float v1, __nv_bfloat16) { return __byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x7632); }
-__device__ __forceinline__ uint32_t towards_zero(float v0, float v1, __half) {
-    uint32_t w;
-    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(v1), "f"(v0));
-    return w;
-}
-// The smaller magnitude, NaN if one is.
-__device__ __forceinline__ float least_abs(float a, float b) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
-    return r;
-}
-// v as two 16-bit numbers: its products with B are exact in fp32, and it keeps 16 bits (bf16) or 22 (fp16).  hi is rounded towards zero, which
-// no finite value leaves, and both have the sign of v and are no zeros unless it is one (the smallest number, 2^-133 or 2^-24, stands
-// in), so that infinities of v and of B give what they give with v itself: their parts' products never cancel or vanish.
-// False: a zero, an infinity or NaN may be among them, and amend2 has to follow.
-template <typename T> __device__ __forceinline__ bool split2(float v0, float v1, uint32_t &hi, uint32_t &lo) {
-    constexpr float kLeast = std::is_same_v<T, __half> ? 0x1p-24f : 0x1p-133f;
-    hi = towards_zero(v0, v1, T());
+// A sum v of A x as two 16-bit numbers, hi + lo: their products with B are exact in fp32, and v keeps 16 bits (bf16) or 22 (fp16).
+// Where v, hi or an element of B is infinite, those products may cancel to NaN: sums that are not finite are added up anew from v.
+template <typename T> __device__ __forceinline__ void split2(float v0, float v1, uint32_t &hi, uint32_t &lo) {
+    hi = f32_to_word(v0, v1, T());
     const float2 h = word_to_f32(hi, T());
-    const float d0 = v0 - h.x, d1 = v1 - h.y;
-    lo = f32_to_word(d0, d1, T());
-    return least_abs(d0, d1) >= kLeast;
+    lo = f32_to_word(v0 - h.x, v1 - h.y, T());
 }
-__device__ __forceinline__ void amend2(float v0, float v1, uint32_t &hi, uint32_t &lo) {
-    const uint32_t least = (v0 != 0.0f ? __float_as_uint(v0) >> 31 << 15 | 1u : 0u) | (v1 != 0.0f ? __float_as_uint(v1) >> 31 << 31 | 0x10000u : 0u);
-    const bool inf0 = fabsf(v0) > FLT_MAX, inf1 = fabsf(v1) > FLT_MAX;   // (not NaN, which stays one in lo)
-    if ((hi & 0x7fffu) == 0) hi |= least & 0xffffu;
-    if ((hi & 0x7fff0000u) == 0) hi |= least & 0xffff0000u;
-    if ((lo & 0x7fffu) == 0 || inf0) lo = (lo & 0xffff0000u) | (least & 0xffffu);
-    if ((lo & 0x7fff0000u) == 0 || inf1) lo = (lo & 0xffffu) | (least & 0xffff0000u);
+// The same where v has to be found again in hi + lo: an infinite one has no lo, and a finite one whose hi is infinite (above bf16's largest
+// number) the largest number as hi.
+template <typename T> __device__ __forceinline__ void split2_whole(float v0, float v1, uint32_t &hi, uint32_t &lo) {
+    split2<T>(v0, v1, hi, lo);
+    const float2 h = word_to_f32(hi, T());
+    if (fmaxf(fabsf(h.x), fabsf(h.y)) <= FLT_MAX) return;
+    constexpr uint32_t kInf = std::is_same_v<T, __half> ? 0x7c00u : 0x7f80u;
+    const float v[2] = {v0, v1};
+    uint32_t w[2] = {hi & 0xffffu, hi >> 16}, l[2] = {lo & 0xffffu, lo >> 16};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if ((w[i] & 0x7fffu) == kInf) {
+            if (fabsf(v[i]) <= FLT_MAX) {
+                w[i] -= 1;
+                l[i] = f32_to_word(v[i] - word_to_f32(w[i], T()).x, 0.0f, T()) & 0xffffu;
+            } else {
+                l[i] = 0;
+            }
+        }
+    hi = w[0] | w[1] << 16;
+    lo = l[0] | l[1] << 16;
+}
+// Whether one of these is NaN or infinite.
+template <typename... Vs> __device__ __forceinline__ bool not_finite(Vs... v) {
+    float z = 0.0f;
+    ((z = fmaf(v, 0.0f, z)), ...);
+    return !(z == 0.0f);
 }
 
 // The rows of a cluster, all of one adapter: of tile t those from its first row to the end of that row's adapter, and of tile
@@ -323,47 +326,61 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     constexpr int kK = RN / 2;                       // steps of 16 of the second product
     uint32_t hi[kK][4], lo[kK][4];
     float back[2];                                           // adapter's scale, over the row's
-    bool plain = true;
-    auto each = [&](auto &&with) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int j = min(c + 8 * i, rows.end - rows.first - 1);     // (a lane without a row takes the last one's)
-            float f = 1.0f;
-            if constexpr (std::is_same_v<T, __half>) f = s_scale[j];
-            back[i] = scale / f;
+    for (int i = 0; i < 2; ++i) {
+        const int j = c + 8 * i;
+        float f = 1.0f;
+        if constexpr (std::is_same_v<T, __half>) f = s_scale[j];
+        back[i] = scale / f;
 #pragma unroll
-            for (int s = 0; s < kK; ++s)
+        for (int s = 0; s < kK; ++s)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int k = RN == 2 ? 4 * q + 2 * h : s / 2 * 32 + 8 * q + s % 2 * 4 + 2 * h;
-                    const float2 v = *reinterpret_cast<const float2 *>(s_all + j * kR + k);
-                    with(v.x * f, v.y * f, hi[s][i + 2 * h], lo[s][i + 2 * h]);
-                }
-        }
-    };
-    each([&](float v0, float v1, uint32_t &x, uint32_t &y) {
-        const bool p = split2<T>(v0, v1, x, y);
-        if constexpr (RN <= 8) plain &= p;
-        else if (!p) amend2(v0, v1, x, y);                   // (registers for both passes are not left)
-    });
-    if (!plain) each([&](float v0, float v1, uint32_t &x, uint32_t &y) { amend2(v0, v1, x, y); });
-    for (int n0 = part * 32; n0 < a.N; n0 += parts * 32) {
-        Block<RN> now;
-        if (kAhead && n0 == part * 32) now = ahead;
-        else now.load(a, g, n0, at, c, q);
-        float sum[4][4] = {};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int s = 0; s < kK; ++s) {
-                mma16<T>(sum[j], lo[s][0], lo[s][1], lo[s][2], lo[s][3], now.b[j][2 * s], now.b[j][2 * s + 1]);
-                mma16<T>(sum[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], now.b[j][2 * s], now.b[j][2 * s + 1]);
+            for (int h = 0; h < 2; ++h) {
+                const int k = RN == 2 ? 4 * q + 2 * h : s / 2 * 32 + 8 * q + s % 2 * 4 + 2 * h;
+                const float2 v = *reinterpret_cast<const float2 *>(s_all + j * kR + k);
+                split2<T>(v.x * f, v.y * f, hi[s][i + 2 * h], lo[s][i + 2 * h]);
             }
-        const int n = n0 + 8 * q;
-        if (n >= a.N) continue;
+    }
+    // The second product from column n0 on.  The first time up to a block with a sum that is not finite (nearly never), of which it
+    // writes nothing, and then with care: such outputs are added up from A x, B and y in memory.
+    auto second = [&](auto with_care, int n0) {
+        constexpr bool careful = decltype(with_care)::value;
+        for (; n0 < a.N; n0 += parts * 32) {
+            Block<RN> now;
+            if (kAhead && !careful && n0 == part * 32) now = ahead;
+            else now.load(a, g, n0, at, c, q);
+            float sum[4][4] = {};
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (at[i] >= 0) {
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < kK; ++s) {
+                    mma16<T>(sum[j], lo[s][0], lo[s][1], lo[s][2], lo[s][3], now.b[j][2 * s], now.b[j][2 * s + 1]);
+                    mma16<T>(sum[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], now.b[j][2 * s], now.b[j][2 * s + 1]);
+                }
+            bool odd[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                odd[i] = at[i] >= 0 && not_finite(sum[0][2 * i], sum[0][2 * i + 1], sum[1][2 * i], sum[1][2 * i + 1], sum[2][2 * i], sum[2][2 * i + 1],
+                                                  sum[3][2 * i], sum[3][2 * i + 1]);
+            if (!careful && __any_sync(kFullMask, odd[0] || odd[1])) break;
+            const int n = n0 + 8 * q;
+            if (n >= a.N) continue;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (at[i] < 0) continue;
+                uint16_t *const out = a.out + at[i] * a.ldo + n;
+                if (careful && odd[i]) {
+                    const float *const t = s_all + (c + 8 * i) * kR;
+                    const uint16_t *bp = a.b + ((size_t)g * a.N + n) * a.r;
+#pragma unroll 1
+                    for (int e = 0; e < 8; ++e) {
+                        float v = 0.0f;
+#pragma unroll 1
+                        for (int k = 0; k < a.r; ++k) v = fmaf(t[k], word_to_f32(*bp++, T()).x, v);
+                        out[e] = (uint16_t)f32_to_word(fmaf(scale, v, word_to_f32(a.y[at[i] * a.ldy + n + e], T()).x), 0.0f, T());
+                    }
+                    continue;
+                }
                 const uint32_t w[4] = {now.y[i].x, now.y[i].y, now.y[i].z, now.y[i].w};
                 uint32_t o[4];
 #pragma unroll
@@ -371,9 +388,13 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
                     const float2 v = word_to_f32(w[j], T());
                     o[j] = f32_to_word(fmaf(back[i], sum[j][2 * i], v.x), fmaf(back[i], sum[j][2 * i + 1], v.y), T());
                 }
-                *reinterpret_cast<uint4 *>(a.out + at[i] * a.ldo + n) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(out) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-    }
+        }
+        return n0;
+    };
+    const int rest = second(std::false_type{}, part * 32);
+    if (rest < a.N) second(std::true_type{}, rest);
     if (a.copy) copy_rows(a);
     if (a.C > 1) cluster_sync_all();                         // the sums have been read everywhere
 }
@@ -592,8 +613,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 1 ? 2 : 1) ep_lora_tile_ke
         }
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (!split2<T>(t[2 * j] * f, t[2 * j + 1] * f, hi[j], lo[j])) amend2(t[2 * j] * f, t[2 * j + 1] * f, hi[j], lo[j]);
+        for (int j = 0; j < 4; ++j) split2_whole<T>(t[2 * j] * f, t[2 * j + 1] * f, hi[j], lo[j]);
         const uint32_t to_op = low + (k >> 3) * kTileRows * 128 + swizzled(r, k & 7), to_f = smem_u32(s_scale + r);
         for (int o = 0; o < a.C; ++o) {
             st_cluster_x4(at_rank(to_op, o), hi);
@@ -663,6 +683,9 @@ __global__ void __launch_bounds__(kTileThreads, RB == 1 ? 2 : 1) ep_lora_tile_ke
             tmem_ld32(lanes + (i & 1) * 64 + half * 32, v);
             tmem_wait_ld();
             tc_fence_before();
+            bool odd = false;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) odd |= not_finite(v[j], v[j + 1], v[j + 2], v[j + 3], v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint4 *const p = reinterpret_cast<uint4 *>(st + swizzled(row, half * 4 + j));
@@ -675,6 +698,26 @@ __global__ void __launch_bounds__(kTileThreads, RB == 1 ? 2 : 1) ep_lora_tile_ke
                     o[k] = f32_to_word(fmaf(back, v[8 * j + 2 * k], yv.x), fmaf(back, v[8 * j + 2 * k + 1], yv.y), T());
                 }
                 *p = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            if (odd) {                                       // nearly never: outputs that are NaN, from the parts of A x, B and y in memory
+                const auto number = [&](uint32_t tile, int r, int k) {       // k of row r of an operand's blocks of 64 columns
+                    return word_to_f32(*reinterpret_cast<const uint16_t *>(smem + tile + swizzled(r, k >> 3 & 7) + (k & 7) * 2), T()).x;
+                };
+                const int at = s_at[row];
+#pragma unroll 1
+                for (int n = half * 32; at >= 0 && n < half * 32 + 32 && col + n < a.N; ++n) {
+                    uint16_t *const out = reinterpret_cast<uint16_t *>(st + swizzled(row, n >> 3) + (n & 7) * 2);
+                    const float was = word_to_f32(*out, T()).x;
+                    if (was == was) continue;
+                    float sum = 0.0f;
+#pragma unroll 1
+                    for (int k = 0; k < a.r; ++k) {
+                        const uint32_t t = kRing * S::kStage + (k >> 6) * kTileRows * 128;
+                        sum = fmaf(number(t, row, k & 63) + number(t + S::kLow, row, k & 63),
+                                   number(slot * S::kStage + S::kLeft + (k >> 6) * 8192, n, k & 63), sum);
+                    }
+                    *out = (uint16_t)f32_to_word(fmaf(back, sum, word_to_f32(a.y[at * a.ldy + col + n], T()).x), 0.0f, T());
+                }
             }
             __syncwarp();
             // this warp's 32 rows and 32 columns, four lanes to a row

@@ -1,7 +1,7 @@
 """How exactly the adapters sum A x: the tensor cores' adder cuts off up to 2^-22 of the running sum with every 16 products of one sign, so
 sums leave it after 512 of them and go on in fp32.  The running sum is half of a chunk's on average: 32 * 2^-23 of a sum are lost, and 2^-24 with each of
-its additions: those of the chunks, of eight warps and of eight CTAs.  A x keeps 16 bits (bf16) or 22 (fp16) on its way into the
-second product, cut off, so a half of the last is lost on average; that product has at most 128 terms.  Roundings of the output average out to 6 * u / sqrt(3 M)
+its additions: those of the chunks, of eight warps and of eight CTAs.  A x keeps 22 bits (fp16) on its way into the second
+product, rounded to nearest, and that product has at most 128 terms: 8 steps.  Roundings of the output average out to 6 * u / sqrt(3 M)
 over M outputs (six standard deviations of M roundings, each uniform within u)."""
 import pytest
 import torch
@@ -35,3 +35,24 @@ def test_long_sums(T, G, r, H, N):
             m += want.numel()
     lost = 32 * 2.0 ** -23 + (H / 512 + 16) * 2.0 ** -24 + 2.0 ** -23 + 8 * 2.0 ** -23
     assert abs(off / m) <= lost + 6 * U[torch.float16] / (3 * m) ** 0.5, off / m
+
+
+@pytest.mark.parametrize("T,N", [(64, 16), (30000, 2048)])               # tiles of few rows, and of 128
+@pytest.mark.parametrize("dtype,bits", [(torch.bfloat16, 8), (torch.float16, 11)])
+def test_digits_of_the_sums(T, N, dtype, bits):
+    """out = y + A x with y the nearest 16-bit number below or above -A x: what is left are the digits behind it.  The second part of A x is at
+    most half a step of the first, 2^-bits of the binade, and off by half a step of its own: 2^-(2 bits + 1) of A x's binade."""
+    import combine_topk_ids_histogram_gb300 as ep
+    gen = torch.Generator(device="cuda").manual_seed(bits)
+    H, r = 1024, 32
+    x, a, b = torch.zeros(T, H, dtype=dtype, device="cuda"), torch.zeros(1, r, H, dtype=dtype, device="cuda"), torch.zeros(1, N, r, dtype=dtype, device="cuda")
+    x[:, 0], x[:, 1] = 1 + torch.rand(T, generator=gen, device="cuda"), torch.rand(T, generator=gen, device="cuda") * 2.0 ** -6
+    a[0, :, 0], a[0, :, 1] = 1 + torch.rand(r, generator=gen, device="cuda"), torch.rand(r, generator=gen, device="cuda") * 2.0 ** -6
+    b[0, torch.arange(N), torch.arange(N) % r] = 1
+    t = (x.double() @ a[0].double().t())[:, torch.arange(N) % r]
+    y = (-t).to(dtype)
+    out = ep.lora_add(y, x, a, b, ep.dispatch_layout(torch.zeros(T, 1, dtype=torch.int32, device="cuda"), 1))
+    left = t + y.double()
+    binade = 2.0 ** t.log2().floor()
+    sums = 2 * 2.0 ** -22 * t                            # two products, and the sums of both contractions
+    assert ((out.double() - left).abs() <= binade * 2.0 ** (-2 * bits - 1) + sums + U[dtype] * left.abs()).all()
