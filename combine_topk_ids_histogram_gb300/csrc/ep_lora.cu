@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2) ep_lora_kernel(const LoraArgs a, 
     auto second = [&](auto with_care, int n0) {
         constexpr bool careful = decltype(with_care)::value;
         for (; n0 < a.N; n0 += parts * 32) {
+            if (careful) __syncwarp();
             Block<RN> now;
             if (kAhead && !careful && n0 == part * 32) now = ahead;
             else now.load(a, g, n0, at, c, q);
